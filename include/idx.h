@@ -282,6 +282,123 @@ IDX_API int idx_score_topk_perrow(const void* q, const float* q_scale, int q_dty
                           int32_t* out_ids, float* out_scores,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Key-value cache of an attention layer: two planes (keys, values) of the pool layout
+ * above with kv_heads heads.  Page p of head h is head page p * kv_heads + h, so token
+ * t of head h of a page lies in plane row (page * kv_heads + h) * 64 + t % 64 and each
+ * head page is one contiguous tile; an idx_pool of num_pages * kv_heads pages holds one
+ * plane, and with one head the layout is an index pool's.  bf16 and e4m3 planes.
+ */
+
+/*
+ * idx_store_kv — write new keys (and values) into the cache.  bf16 planes take the bits;
+ * e4m3 planes take, per row of 128, a = max(max |x|, 2^-96), scale = a / 448 and codes
+ * e4m3(x * (448 * (1 / a))), each quotient and product rounded once in fp32, the code half
+ * to even and saturating.  A NaN makes its row's scale and codes NaN.
+ *   k_src, v_src (device): bf16 [num_tokens][kv_heads][128], k_stride / v_stride elements
+ *                          between tokens (a slice of a fused projection is fine): multiples
+ *                          of 8, 16-byte aligned.  v_src NULL with v_pool NULL: keys only
+ *                          (an index pool's bf16 or e4m3 keys, with kv_heads = 1).
+ *   slot_mapping (device): int64 [num_tokens], page * 64 + offset of each token; negative or
+ *                          >= num_pages * 64 skips the token.  Slots must differ: of two
+ *                          tokens with one slot either may stay.
+ *   k_pool, v_pool (host): planes of num_pages * kv_heads head pages, the same dtype.
+ * Asynchronous on stream; allocates nothing; capturable.  IDX_ERR_INVALID for arguments out of range;
+ * IDX_ERR_UNSUPPORTED for an NVFP4 pool (idx_store_nvfp4 writes those).  num_tokens == 0 is
+ * a no-op.
+ */
+IDX_API int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
+                         const int64_t* slot_mapping, int64_t num_tokens, int kv_heads,
+                         const idx_pool* k_pool, const idx_pool* v_pool, void* stream);
+
+/*
+ * idx_attn_workspace_bytes — device scratch of idx_attn_paged (lists 0) and idx_attn_blocks:
+ * the header, and the partial results of the units that several CTAs share.  It does not
+ * depend on the number of requests or the context.  0 for arguments that do not fit together.
+ */
+IDX_API size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_heads, int lists);
+
+/*
+ * idx_attn_paged — attention of the newest tokens (one, or P = packed_queries draft rows, a
+ * request) over the whole paged cache.  Row (r, p, head) sees the tokens t < row_lens[r][p] of
+ * its request: out = softmax(sm_scale * q . k_t) v_t, lse = ln sum exp(sm_scale * q . k_t).
+ * The work is split evenly over the GPU along the caches' length and joined in a fixed order.
+ *   q (device):          bf16 [R][P][q_heads][128]; query head j goes by key head
+ *                        j / (q_heads / kv_heads)
+ *   k_payload .. v_scale (device): the planes; scales are fp32 [rows], e4m3 caches only
+ *   kv_dtype:            IDX_BF16 or IDX_FP8_E4M3
+ *   num_pages:           pages of the cache (a page holds all heads); a page id outside
+ *                        [0, num_pages) is not read, its tokens are left out and
+ *                        IDX_DEVERR_BAD_PAGE is set
+ *   page_table, slot_ids, row_lens: as for idx_score_topk; a pad request or a row of length
+ *                        <= 0 gives out = 0, lse = -inf; lengths past max_pages * 64 are
+ *                        clamped (IDX_DEVERR_LEN_CLAMPED)
+ *   out (device):        bf16 [R][P][q_heads][128];  out_lse (device): fp32 [R][P][q_heads],
+ *                        natural log, or NULL.  Partial results over context shards join by
+ *                        it: out = sum_w out_w exp(lse_w - lse).
+ *   workspace (device):  >= idx_attn_workspace_bytes(P, q_heads, kv_heads, 0), 256-byte
+ *                        aligned, no clearing needed; not shared by calls that may overlap.
+ *                        idx_workspace_errors reads its flags.
+ * What lies in the cache past a row's length (uninitialised pages, NaN) does not reach the row.
+ * Sums and softmax statistics are fp32; for the product with the values the weights are
+ * held as two bf16 (bf16 cache, 16 bits) or one f16 (e4m3 cache).  Asynchronous on stream; allocates nothing;
+ * capturable.  R <= IDX_MAX_REQUESTS, P * q_heads <= IDX_MAX_ROWS_PER_REQUEST, num_pages *
+ * kv_heads < 2^31 / 64; q_heads a multiple of kv_heads.
+ */
+IDX_API int idx_attn_paged(const void* q, const void* k_payload, const void* k_scale,
+                           const void* v_payload, const void* v_scale, int kv_dtype,
+                           int64_t num_pages, int kv_heads, const int32_t* page_table, int n_slots,
+                           int max_pages, const int32_t* slot_ids, const int32_t* row_lens,
+                           int num_requests, int packed_queries, int q_heads, float sm_scale,
+                           void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * idx_attn_blocks — the same over the 128-token blocks that the index step chose: row
+ * (r, p, head) sees the tokens t < row_lens[r][p] whose block t / 128 is in its list.
+ *   block_ids (device):  int32 [R][P][lists][topk], idx_score_topk's out_ids with gqa = lists.
+ *                        Query head j goes by list j / (q_heads / lists).  A list is a set: its
+ *                        order does not matter, a block listed twice counts once, and ids < 0
+ *                        or at or past the row's own blocks are left out.
+ *   lists:               q_heads must be a multiple of it, and lists and kv_heads one a multiple
+ *                        of the other;  topk: 1 .. IDX_MAX_TOPK
+ * The draft rows of a request that share a list position are packed: their lists are joined,
+ * and a block that several of them chose is read once.  Everything else is as above, with the
+ * workspace of idx_attn_workspace_bytes(P, q_heads, kv_heads, lists).
+ */
+IDX_API int idx_attn_blocks(const void* q, const void* k_payload, const void* k_scale,
+                            const void* v_payload, const void* v_scale, int kv_dtype,
+                            int64_t num_pages, int kv_heads, const int32_t* page_table,
+                            int n_slots, int max_pages, const int32_t* slot_ids,
+                            const int32_t* row_lens, const int32_t* block_ids, int lists, int topk,
+                            int num_requests, int packed_queries, int q_heads, float sm_scale,
+                            void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * idx_add_rmsnorm_fp8 — residual addition, root-mean-square norm, e4m3 result.  Per row, in
+ * fp32: h = x + residual; out_residual = bf16(h); y = h / sqrt(mean(h^2) + eps) * weight; then
+ * codes and scales of y by idx_store_kv's rule, per group of IDX_NORM_GROUP elements (the last
+ * one may be shorter) or per row.
+ *   x (device):            bf16 [num_rows][dim], x_stride elements between rows
+ *   residual (device):     the same with residual_stride, or NULL: h = x
+ *   weight (device):       bf16 [dim];  group: IDX_NORM_GROUP, or 0 for the whole row
+ *   out (device):          e4m3 codes [num_rows][dim]
+ *   out_scale (device):    fp32 [num_rows][ceil(dim / group)], or [num_rows] with group 0
+ *   out_residual (device): bf16 [num_rows][dim], or NULL; may be residual itself (when its
+ *                          stride is dim)
+ * With dim = 128 and group 0 the result is an e4m3 query or key of idx_score_topk with its
+ * scale.  Any dim in [1, IDX_MAX_NORM_DIM] and any alignment of the elements; rows of a
+ * multiple of 8 elements on 16-byte boundaries are faster.  Asynchronous on stream; allocates
+ * nothing; capturable.  num_rows == 0 is a no-op.
+ */
+#define IDX_NORM_GROUP 128
+#define IDX_MAX_NORM_DIM 32768
+IDX_API int idx_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual,
+                                int64_t residual_stride, const void* weight, int64_t num_rows,
+                                int dim, int group, float eps, void* out, float* out_scale,
+                                void* out_residual, void* stream);
+
 /* idx_set_kernel_events — instrumentation for timing.  Arms, for the next
  * idx_score_topk / idx_score_topk_perrow call on the calling host thread only, up
  * to three cudaEvent_t (passed as void*, NULL to skip) that the call records on its
@@ -348,7 +465,7 @@ IDX_API int idx_score_topk_noalloc(const void* q, const float* q_scale, int q_dt
 IDX_API int idx_noalloc_errors(void* stream, uint32_t* flags);
 
 /* idx_set_wait_limit_ns — limit (nanoseconds, process-wide) of every pipeline wait in
- * the score kernels; 0 restores the default of 2 s.  A wait that runs past it ends
+ * the score and attention kernels; 0 restores the default of 2 s.  A wait that runs past it ends
  * its role: the CTA waits for its own copies in flight, frees its tensor memory,
  * sets IDX_DEVERR_TIMEOUT in the workspace header and exits, so the context stays
  * usable.  The limit is read at each call (a captured graph keeps the one of its
@@ -367,7 +484,8 @@ IDX_API int idx_set_stall_test(int on);
 /* idx_set_grid_limit — cap the number of CTAs the score kernel launches (process-
  * wide; 0 restores the default of one CTA per SM).  Results do not depend on it:
  * each block max is computed whole by one warp, so any split of the work gives the
- * same bits.  Meant for tests and tuning. */
+ * same bits.  The attention kernels obey it too; there the split decides where partial
+ * sums are joined, so their results agree to rounding.  Meant for tests and tuning. */
 IDX_API int idx_set_grid_limit(int max_ctas);
 
 /* idx_workspace_errors — read the device error flags of the last call that used this

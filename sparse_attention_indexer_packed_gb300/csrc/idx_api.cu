@@ -12,8 +12,11 @@
 #include <string>
 
 #include "../../include/idx.h"
+#include "idx_attn.cuh"
 #include "idx_internal.cuh"
+#include "idx_ops.cuh"
 
+static_assert(idx::kMaxNormDim == IDX_MAX_NORM_DIM, "norm limit mismatch");
 static_assert(idx::kHeaderBytes == IDX_WORKSPACE_HEADER_BYTES, "header size mismatch");
 
 namespace {
@@ -185,6 +188,131 @@ int make_q_map(int q_dtype, const void* q, int64_t rows, CUtensorMap* map) {
   if (r != CUDA_SUCCESS)
     return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled (query rows) failed (%d)", (int)r);
   g_maps.put(1, q_dtype, q, rows, *map);
+  return IDX_OK;
+}
+
+// Tensor map over one plane of a key-value cache for 32-token pieces: bf16 rows
+// as two 64-column boxes, e4m3 rows as one 128-byte box, 32 rows high, 128-byte
+// swizzle.  Encoded at each call: it is a fraction of a launch's host time.
+int make_plane_map(int dtype, const void* payload, int64_t rows, CUtensorMap* map) {
+  auto fn = encode_fn();
+  if (!fn) return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const bool bf16 = dtype == IDX_BF16;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 256 : 128)};
+  const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : 128), (cuuint32_t)idx::attn::kItem};
+  const cuuint32_t estride[2] = {1, 1};
+  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                  const_cast<void*>(payload), dims, strides, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled (cache plane) failed (%d)", (int)r);
+  return IDX_OK;
+}
+
+// Heads of a unit: the query heads of a request that go by the same key head and
+// the same block list.  0: the counts do not fit together.
+int unit_heads(int q_heads, int kv_heads, int lists) {
+  const int hi = kv_heads > lists ? kv_heads : lists, lo = kv_heads > lists ? lists : kv_heads;
+  if (q_heads < 1 || kv_heads < 1 || lists < 1 || hi % lo != 0 || q_heads % hi != 0) return 0;
+  return hi;
+}
+
+// Whole-cache attention (block_ids NULL, lists 0) or over block lists.
+int attn_impl(const void* q, const void* k_payload, const void* k_scale, const void* v_payload,
+              const void* v_scale, int kv_dtype, int64_t num_pages, int kv_heads,
+              const int32_t* page_table, int n_slots, int max_pages, const int32_t* slot_ids,
+              const int32_t* row_lens, bool blocks, const int32_t* block_ids, int lists, int topk,
+              int R, int P, int q_heads, float sm_scale, void* out, float* out_lse,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  if (R < 0 || R > IDX_MAX_REQUESTS)
+    return fail(IDX_ERR_INVALID, "num_requests must be in [0, %d] (got %d)", IDX_MAX_REQUESTS, R);
+  if (P < 1 || q_heads < 1 || (long long)P * q_heads > IDX_MAX_ROWS_PER_REQUEST)
+    return fail(IDX_ERR_INVALID, "packed_queries * q_heads must be in [1, %d] (got %d x %d)",
+                IDX_MAX_ROWS_PER_REQUEST, P, q_heads);
+  const int heads = unit_heads(q_heads, kv_heads, blocks ? lists : 1);
+  if (heads == 0)
+    return fail(IDX_ERR_INVALID,
+                "q_heads must be a multiple of kv_heads and of the lists, and one of those two a "
+                "multiple of the other (got %d, %d, %d)",
+                q_heads, kv_heads, blocks ? lists : 1);
+  if (blocks && (topk < 1 || topk > IDX_MAX_TOPK))
+    return fail(IDX_ERR_INVALID, "topk must be in [1, %d] (got %d)", IDX_MAX_TOPK, topk);
+  if (kv_dtype != IDX_BF16 && kv_dtype != IDX_FP8_E4M3)
+    return fail(IDX_ERR_UNSUPPORTED, "the attention reads bf16 and e4m3 caches (got dtype %d)",
+                kv_dtype);
+  if (!(sm_scale > 0.f) || !(sm_scale < 1e30f))
+    return fail(IDX_ERR_INVALID, "sm_scale must be positive and finite (got %g)", (double)sm_scale);
+  if (n_slots < 1 || max_pages < 1 || max_pages > 65536)
+    return fail(IDX_ERR_INVALID, "need n_slots >= 1 and 1 <= max_pages <= 65536 (got %d, %d)",
+                n_slots, max_pages);
+  if (num_pages < 1 || num_pages > 0x7fffffffLL / idx::kPage / kv_heads)
+    return fail(IDX_ERR_INVALID, "num_pages * kv_heads must be in [1, 2^31 / 64) (got %lld x %d)",
+                (long long)num_pages, kv_heads);
+  if (!workspace) return fail(IDX_ERR_INVALID, "workspace is NULL");
+  if (!aligned(workspace, 256)) return fail(IDX_ERR_INVALID, "workspace must be 256-byte aligned");
+  const size_t need = idx_attn_workspace_bytes(P, q_heads, kv_heads, blocks ? lists : 0);
+  if (workspace_bytes < need)
+    return fail(IDX_ERR_INVALID, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R == 0) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the workspace header");
+    return IDX_OK;
+  }
+  if (!q || !k_payload || !v_payload || !page_table || !slot_ids || !row_lens || !out ||
+      (blocks && !block_ids))
+    return fail(IDX_ERR_INVALID, "a required pointer is NULL");
+  if (kv_dtype == IDX_FP8_E4M3 && (!k_scale || !v_scale))
+    return fail(IDX_ERR_INVALID, "an e4m3 cache needs k_scale and v_scale");
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_payload, 16) || !aligned(v_payload, 16) ||
+      !aligned(k_scale, 16) || !aligned(v_scale, 16))
+    return fail(IDX_ERR_INVALID, "q, out and the cache planes must be 16-byte aligned");
+
+  idx::AttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_payload = static_cast<const uint8_t*>(k_payload);
+  a.k_scale = static_cast<const float*>(k_scale);
+  a.v_payload = static_cast<const uint8_t*>(v_payload);
+  a.v_scale = static_cast<const float*>(v_scale);
+  a.page_table = page_table;
+  a.slot_ids = slot_ids;
+  a.row_lens = row_lens;
+  a.block_ids = blocks ? block_ids : nullptr;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = out_lse;
+  a.num_pages = num_pages;
+  a.n_slots = n_slots;
+  a.max_pages = max_pages;
+  a.R = R;
+  a.P = P;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.lists = blocks ? lists : 1;
+  a.topk = blocks ? topk : 0;
+  a.heads = heads;
+  a.nq = q_heads / heads;
+  a.group_rows = idx::attn::group_rows(P, a.nq);
+  a.groups = (P * a.nq + a.group_rows - 1) / a.group_rows;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.wait_ns = idx::wait_limit_ns();
+  a.stall_test = idx::stall_test();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.err_count = reinterpret_cast<uint32_t*>(ws);
+  a.err_bytes = ws + idx::kFlagBytesOff;
+  a.records = reinterpret_cast<idx::attn::SplitRecord*>(ws + IDX_WORKSPACE_HEADER_BYTES);
+  ws += IDX_WORKSPACE_HEADER_BYTES + idx::attn::records_bytes();
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  ws += idx::attn::part_ml_bytes(idx::attn::kMaxCtas, a.group_rows);
+  a.part_o = reinterpret_cast<float*>(ws);
+  CUtensorMap k_map, v_map;
+  int rc = make_plane_map(kv_dtype, k_payload, num_pages * kv_heads * idx::kPage, &k_map);
+  if (rc == IDX_OK)
+    rc = make_plane_map(kv_dtype, v_payload, num_pages * kv_heads * idx::kPage, &v_map);
+  if (rc != IDX_OK) return rc;
+  const cudaError_t e = idx::launch_attn(kv_dtype, a, k_map, v_map, st);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the attention kernels");
   return IDX_OK;
 }
 
@@ -621,6 +749,137 @@ int idx_topk_merge(const int32_t* cand_ids, const float* cand_scores, int world,
   m.topk = topk;
   cudaError_t e = idx::launch_merge(m, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the merge kernel");
+  return IDX_OK;
+}
+
+int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
+                 const int64_t* slot_mapping, int64_t num_tokens, int kv_heads,
+                 const idx_pool* k_pool, const idx_pool* v_pool, void* stream) {
+  if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
+  if ((v_src != nullptr) != (v_pool != nullptr))
+    return fail(IDX_ERR_INVALID, "v_src and v_pool come together or not at all");
+  if (kv_heads < 1) return fail(IDX_ERR_INVALID, "kv_heads must be >= 1 (got %d)", kv_heads);
+  const int dtype = k_pool->dtype;
+  if (dtype != IDX_BF16 && dtype != IDX_FP8_E4M3)
+    return fail(IDX_ERR_UNSUPPORTED, "the store writes bf16 and e4m3 pools (got dtype %d)", dtype);
+  const idx_pool* pools[2] = {k_pool, v_pool};
+  for (const idx_pool* p : pools) {
+    if (!p) continue;
+    if (p->dtype != dtype || p->page_size != IDX_PAGE_SIZE || p->dim != IDX_DIM ||
+        p->payload_row_bytes != payload_row_bytes(dtype) ||
+        p->scale_row_bytes != scale_row_bytes(dtype) || p->num_pages != k_pool->num_pages)
+      return fail(IDX_ERR_INVALID,
+                  "the pools must have the same dtype and pages, 64-token pages and dim 128");
+    if (p->num_pages < 1 || p->num_pages % kv_heads != 0)
+      return fail(IDX_ERR_INVALID,
+                  "a pool of kv_heads heads holds a multiple of kv_heads head pages (got %lld, %d)",
+                  (long long)p->num_pages, kv_heads);
+  }
+  if (num_tokens < 0) return fail(IDX_ERR_INVALID, "num_tokens must be >= 0");
+  if (num_tokens == 0) return IDX_OK;
+  if (num_tokens > ((int64_t)1 << 34) / kv_heads / 2)
+    return fail(IDX_ERR_INVALID, "num_tokens too large");
+  if (!k_src || !slot_mapping) return fail(IDX_ERR_INVALID, "a required pointer is NULL");
+  if (k_stride < (int64_t)kv_heads * IDX_DIM || k_stride % 8 != 0 ||
+      (v_src && (v_stride < (int64_t)kv_heads * IDX_DIM || v_stride % 8 != 0)))
+    return fail(IDX_ERR_INVALID,
+                "token strides must be multiples of 8 elements and at least kv_heads * 128");
+  if (!aligned(k_src, 16) || !aligned(v_src, 16))
+    return fail(IDX_ERR_INVALID, "k_src and v_src must be 16-byte aligned");
+  for (const idx_pool* p : pools) {
+    if (!p) continue;
+    if (!p->payload || (dtype == IDX_FP8_E4M3 && !p->scale))
+      return fail(IDX_ERR_INVALID, "a pool's plane is NULL");
+    if (!aligned(p->payload, 16) || !aligned(p->scale, 4))
+      return fail(IDX_ERR_INVALID, "payload planes must be 16-byte, scale planes 4-byte aligned");
+  }
+  idx::StoreArgs s;
+  s.src[0] = static_cast<const uint16_t*>(k_src);
+  s.src[1] = static_cast<const uint16_t*>(v_src);
+  s.stride[0] = k_stride;
+  s.stride[1] = v_stride;
+  s.payload[0] = static_cast<uint8_t*>(k_pool->payload);
+  s.payload[1] = v_pool ? static_cast<uint8_t*>(v_pool->payload) : nullptr;
+  s.scale[0] = static_cast<float*>(k_pool->scale);
+  s.scale[1] = v_pool ? static_cast<float*>(v_pool->scale) : nullptr;
+  s.slots = slot_mapping;
+  s.tokens = num_tokens;
+  s.num_slots = k_pool->num_pages / kv_heads * IDX_PAGE_SIZE;
+  s.heads = kv_heads;
+  s.planes = v_pool ? 2 : 1;
+  const cudaError_t e = idx::launch_store_kv(dtype, s, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "launching the key-value store kernel");
+  return IDX_OK;
+}
+
+size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_heads, int lists) {
+  const int heads = unit_heads(q_heads, kv_heads, lists > 0 ? lists : 1);
+  if (packed_queries < 1 || lists < 0 || heads == 0) return 0;
+  const int rows = idx::attn::group_rows(packed_queries, q_heads / heads);
+  return IDX_WORKSPACE_HEADER_BYTES + idx::attn::records_bytes() +
+         idx::attn::part_ml_bytes(idx::attn::kMaxCtas, rows) +
+         idx::attn::part_o_bytes(idx::attn::kMaxCtas, rows);
+}
+
+int idx_attn_paged(const void* q, const void* k_payload, const void* k_scale,
+                   const void* v_payload, const void* v_scale, int kv_dtype, int64_t num_pages,
+                   int kv_heads, const int32_t* page_table, int n_slots, int max_pages,
+                   const int32_t* slot_ids, const int32_t* row_lens, int num_requests,
+                   int packed_queries, int q_heads, float sm_scale, void* out, float* out_lse,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  return attn_impl(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, num_pages, kv_heads,
+                   page_table, n_slots, max_pages, slot_ids, row_lens, false, nullptr, 0, 0,
+                   num_requests, packed_queries, q_heads, sm_scale, out, out_lse, workspace,
+                   workspace_bytes, stream);
+}
+
+int idx_attn_blocks(const void* q, const void* k_payload, const void* k_scale,
+                    const void* v_payload, const void* v_scale, int kv_dtype, int64_t num_pages,
+                    int kv_heads, const int32_t* page_table, int n_slots, int max_pages,
+                    const int32_t* slot_ids, const int32_t* row_lens, const int32_t* block_ids,
+                    int lists, int topk, int num_requests, int packed_queries, int q_heads,
+                    float sm_scale, void* out, float* out_lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  return attn_impl(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, num_pages, kv_heads,
+                   page_table, n_slots, max_pages, slot_ids, row_lens, true, block_ids, lists, topk,
+                   num_requests, packed_queries, q_heads, sm_scale, out, out_lse, workspace,
+                   workspace_bytes, stream);
+}
+
+int idx_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, const void* weight, int64_t num_rows, int dim,
+                        int group, float eps, void* out, float* out_scale, void* out_residual,
+                        void* stream) {
+  if (num_rows < 0 || num_rows > 0x7fffffffLL)
+    return fail(IDX_ERR_INVALID, "num_rows must be in [0, 2^31) (got %lld)", (long long)num_rows);
+  if (dim < 1 || dim > IDX_MAX_NORM_DIM)
+    return fail(IDX_ERR_INVALID, "dim must be in [1, %d] (got %d)", IDX_MAX_NORM_DIM, dim);
+  if (group != 0 && group != IDX_NORM_GROUP)
+    return fail(IDX_ERR_INVALID, "group must be 0 (the whole row) or %d (got %d)", IDX_NORM_GROUP,
+                group);
+  if (!(eps >= 0.f)) return fail(IDX_ERR_INVALID, "eps must be >= 0 (got %g)", (double)eps);
+  if (num_rows == 0) return IDX_OK;
+  if (!x || !weight || !out || !out_scale) return fail(IDX_ERR_INVALID, "a required pointer is NULL");
+  if (x_stride < dim || (residual && residual_stride < dim))
+    return fail(IDX_ERR_INVALID, "row strides must be at least dim");
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(out_residual, 2) ||
+      !aligned(out_scale, 4))
+    return fail(IDX_ERR_INVALID, "bf16 pointers must be 2-byte, out_scale 4-byte aligned");
+  idx::NormArgs n;
+  n.x = static_cast<const uint16_t*>(x);
+  n.residual = static_cast<const uint16_t*>(residual);
+  n.weight = static_cast<const uint16_t*>(weight);
+  n.out = static_cast<uint8_t*>(out);
+  n.out_scale = out_scale;
+  n.out_residual = static_cast<uint16_t*>(out_residual);
+  n.rows = num_rows;
+  n.x_stride = x_stride;
+  n.residual_stride = residual ? residual_stride : 0;
+  n.dim = dim;
+  n.group = group;
+  n.eps = eps;
+  const cudaError_t e = idx::launch_add_rmsnorm(n, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "launching the norm kernel");
   return IDX_OK;
 }
 

@@ -1,0 +1,909 @@
+// Attention of the newest tokens over the paged cache: the whole cache, or the
+// 128-token blocks of the index step's lists.
+//
+// What it computes: for packed row i of a unit (idx_attn.cuh), with query q_i
+// and visible tokens T_i = { t < the row's length [, t / 128 in the row's list] },
+//   s_t = scale * q_i . k_t,   lse = ln sum_T e^{s_t},   out = sum_T e^{s_t - lse} v_t
+// in one pass over the keys and values, with the running maximum m and sum l of
+// the softmax: a token piece with maximum m' rescales what was summed so far by
+// e^{m - max(m, m')}.  A row with no visible token gives out = 0, lse = -inf.
+//
+// What bounds it: the cache's bytes.  16 rows cost 16 flop a byte of a bf16
+// cache (32 of an e4m3 one), far below the ridge, so the tiles of a unit are
+// read once for all of its rows and the work is the stream from HBM.
+//
+// How (sm_103a):
+//  * a persistent grid, one CTA per SM; every CTA takes an equal stretch of the
+//    units' 32-token pieces (idx_attn.cuh), so one long request is split over
+//    many CTAs and many short ones share a CTA;
+//  * a warp owns one shared-memory stage of one piece (keys and values, by TMA
+//    through the page table) and refills it as soon as it has been used; no
+//    stage is shared between warps, so there is no "empty" barrier;
+//  * a piece is two chains of m16n8k16 products on the registers: scores from
+//    ldmatrix'ed keys, then the weights, still in the accumulators' layout,
+//    against transposed-ldmatrix values.  An e4m3 piece is decoded to exact f16
+//    in registers;
+//  * warps keep softmax states of their own; they are joined through shared
+//    memory at a unit's end.  A unit inside one CTA is written at once; one
+//    that was cut leaves (m, l, out) in the workspace for the join kernel;
+//  * every wait is bounded, as in the score kernels.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "idx_attn.cuh"
+#include "idx_ptx.cuh"
+
+namespace idx {
+
+namespace {
+
+using namespace attn;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 16;                              // packed rows of a group here
+constexpr int kMaxList = kMaxTopk * kMaxDrafts;        // joined block list of a group
+constexpr int kMaxBlockWords = 65536 / 2 / 32;         // bits for every block of a request
+constexpr int kMergeStride = kDim + 8;                 // floats: keeps row writes off one bank
+
+template <int KF>
+struct ACfg;
+template <>
+struct ACfg<kBf16> {
+  static constexpr int kRowBytes = 256;
+  static constexpr int kWarps = 8;
+};
+template <>
+struct ACfg<kFp8> {
+  static constexpr int kRowBytes = 128;
+  static constexpr int kWarps = 10;
+};
+
+template <int KF>
+struct ALayout {
+  static constexpr int NW = ACfg<KF>::kWarps;
+  static constexpr int kThreads = 32 * NW;
+  static constexpr int kTileBytes = kItem * ACfg<KF>::kRowBytes;  // keys or values of a piece
+  static constexpr int kStage = 2 * kTileBytes;
+  static constexpr int kScaleBytes = KF == kFp8 ? 2 * kItem * 4 : 0;
+  static constexpr int kScaleOff = NW * kStage;
+  static constexpr int kMergeOff = kScaleOff + NW * kScaleBytes;
+  static constexpr int kMlOff = kMergeOff + NW * kTile * kMergeStride * 4;
+  static constexpr int kBarOff = kMlOff + NW * kTile * 8;
+  static constexpr int kCtlOff = kBarOff + (NW + 1) * 8;
+  static constexpr int kPreOff = (kCtlOff + 32 + 15) & ~15;
+  static constexpr int kListOff = kPreOff + (kMaxGroups + 4) * 4;
+  static constexpr int kBytes = kListOff + kMaxList * 4;
+  // the block bits are only held while a list is joined: in the merge area,
+  // which is free between two units
+  static constexpr int kBitsOff = kMergeOff;
+  static_assert(2 * kMaxBlockWords * 4 <= kMlOff - kMergeOff, "block bits");
+  static constexpr int kSmem = kBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {
+  const int L = __ldg(a.row_lens + r * a.P + p), cap = a.max_pages * kPage;
+  return L < 0 ? 0 : (L > cap ? cap : L);
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, uint32_t& r1,
+                                                  uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The 16 query rows in A-fragment order.
+//  bf16: a[ks] = {row g: d 16ks+2t,+1; row g+8: same; row g: +8,+9; row g+8: +8,+9}
+//  e4m3 keys: the queries as f16, scaled a row by the power of two that brings
+//  the row's largest magnitude into [2^14, 2^15) (exact for every element within
+//  2^24 of it, undone by post): e4m3 values are exact in f16, so each product is
+//  exact.  k order: step c takes d = 16c + 4t + {0,1} and + {2,3}, the order in
+//  which a lane's four bytes of an ldmatrix'ed key arrive.
+template <int KF>
+struct QRows {
+  uint32_t a[8][4];
+  float post0, post1;
+  __device__ void load(const uint16_t* r0, const uint16_t* r1, float scale_log2, int lane) {
+    const int t = lane & 3;
+    if (KF == kBf16) {
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const int o = 16 * ks + 2 * t;
+        a[ks][0] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o)) : 0u;
+        a[ks][1] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o)) : 0u;
+        a[ks][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o + 8)) : 0u;
+        a[ks][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o + 8)) : 0u;
+      }
+      post0 = post1 = scale_log2;
+    } else {
+      load_f16(r0, 0, post0, t);
+      load_f16(r1, 1, post1, t);
+      post0 *= scale_log2;
+      post1 *= scale_log2;
+    }
+  }
+  __device__ void load_f16(const uint16_t* row, int half, float& post, int t) {
+    uint2 u[8];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      u[c] = row ? __ldg(reinterpret_cast<const uint2*>(row + 16 * c + 4 * t)) : make_uint2(0, 0);
+      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(bf16_lo(u[c].x)), fabsf(bf16_hi(u[c].x)))),
+                   fmaxf(fabsf(bf16_lo(u[c].y)), fabsf(bf16_hi(u[c].y))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    int e = 0;
+    if (amax > 0.f) e = 14 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
+    e = max(-100, min(100, e));
+    const float up = ldexpf(1.f, e);
+    post = ldexpf(1.f, -e);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      a[c][half] = pack_f16(bf16_lo(u[c].x) * up, bf16_hi(u[c].x) * up);
+      a[c][2 + half] = pack_f16(bf16_lo(u[c].y) * up, bf16_hi(u[c].y) * up);
+    }
+  }
+};
+
+// Softmax state of the two rows a lane holds (g and g + 8), and its part of the
+// unnormalised output.  m in log2 units, the same in the four lanes of a row;
+// l is the lane's own part of the sum.  e4m3 values: o is held in units of mv, a
+// power of two at or above every value scale so far, so that weight times
+// scale / mv fits f16.
+struct State {
+  float m0, m1, l0, l1, mv;
+  float o[16][4];
+  __device__ __forceinline__ void reset() {
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+    mv = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
+};
+
+// The smallest power of two above x (x finite, >= 0; at least 2^-100).
+__device__ __forceinline__ float pow2_above(float x) {
+  const int e = max(27, (int)(__float_as_uint(x) >> 23));
+  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
+}
+
+// One 32-token piece.  kMask: some token of the piece lies outside some row
+// (len0, len1: the rows' visible lengths, 0 for a row that does not list the
+// block) or at or past glen, where the cache holds anything: such values are
+// dropped by selection, not by a product with zero.
+template <int KF, bool kMask>
+__device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t stage,
+                                      const float* scales, int lane, int tb, int len0, int len1,
+                                      int glen) {
+  const int t = lane & 3, m = lane >> 3, rr = lane & 7;
+  constexpr int TB = ALayout<KF>::kTileBytes;
+  float s[4][4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    const uint32_t row = stage + (uint32_t)((nt * 8 + rr) * 128);
+    if (KF == kBf16) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int ch = 4 * c + m;
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4(row + (uint32_t)((ch >> 3) * (TB / 2)) + (uint32_t)(((ch ^ rr) & 7) << 4), b0,
+                    b1, b2, b3);
+        mma_bf16_16816(s[nt], q.a[2 * c], b0, b1);
+        mma_bf16_16816(s[nt], q.a[2 * c + 1], b2, b3);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[4];
+        ldmatrix_x4(row + (uint32_t)((((4 * c + m) ^ rr) & 7) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t lo, hi;
+          e4m3x4_to_f16x2x2(w[e], lo, hi);
+          mma_f16_16816(s[nt], q.a[4 * c + e], lo, hi);
+        }
+      }
+    }
+  }
+  // scores in log2 units, their row maxima
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    float f0 = q.post0, f1 = q.post0, f2 = q.post1, f3 = q.post1;
+    if (KF == kFp8) {
+      const float2 ks = *reinterpret_cast<const float2*>(scales + nt * 8 + 2 * t);
+      f0 *= ks.x, f1 *= ks.y, f2 *= ks.x, f3 *= ks.y;
+    }
+    s[nt][0] *= f0, s[nt][1] *= f1, s[nt][2] *= f2, s[nt][3] *= f3;
+    if (kMask) {
+      const int t0 = tb + nt * 8 + 2 * t;
+      if (t0 >= len0) s[nt][0] = -INFINITY;
+      if (t0 + 1 >= len0) s[nt][1] = -INFINITY;
+      if (t0 >= len1) s[nt][2] = -INFINITY;
+      if (t0 + 1 >= len1) s[nt][3] = -INFINITY;
+    }
+    mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
+    mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+  }
+  const float mn0 = fmaxf(st.m0, mx0), mn1 = fmaxf(st.m1, mx1);
+  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
+  float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
+  st.m0 = mn0, st.m1 = mn1;
+  float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    s[nt][0] = ex2_approx(s[nt][0] - ref0);
+    s[nt][1] = ex2_approx(s[nt][1] - ref0);
+    s[nt][2] = ex2_approx(s[nt][2] - ref1);
+    s[nt][3] = ex2_approx(s[nt][3] - ref1);
+    l0 += s[nt][0] + s[nt][1];
+    l1 += s[nt][2] + s[nt][3];
+  }
+  st.l0 = fmaf(st.l0, c0, l0);
+  st.l1 = fmaf(st.l1, c1, l1);
+  if (KF == kFp8) {
+    // weights times value scales, in units of mv
+    float vs[4][2], top = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const float2 v = *reinterpret_cast<const float2*>(scales + kItem + nt * 8 + 2 * t);
+      vs[nt][0] = v.x, vs[nt][1] = v.y;
+      if (kMask) {
+        const int t0 = tb + nt * 8 + 2 * t;
+        if (t0 >= glen) vs[nt][0] = 0.f;
+        if (t0 + 1 >= glen) vs[nt][1] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = fabsf(vs[nt][e]);
+        if (x < INFINITY) top = fmaxf(top, x);
+      }
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float mv = fmaxf(st.mv, pow2_above(top));
+    const float inv = 1.f / mv;   // a power of two: exact
+    const float shrink = st.mv * inv;
+    st.mv = mv;
+    c0 *= shrink, c1 *= shrink;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const float r0 = vs[nt][0] * inv, r1 = vs[nt][1] * inv;
+      s[nt][0] *= r0, s[nt][1] *= r1, s[nt][2] *= r0, s[nt][3] *= r1;
+      if (kMask) {   // a masked token's scale may be anything
+        const int t0 = tb + nt * 8 + 2 * t;
+        if (t0 >= len0) s[nt][0] = 0.f;
+        if (t0 + 1 >= len0) s[nt][1] = 0.f;
+        if (t0 >= len1) s[nt][2] = 0.f;
+        if (t0 + 1 >= len1) s[nt][3] = 0.f;
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      st.o[j][0] *= c0, st.o[j][1] *= c0;
+      st.o[j][2] *= c1, st.o[j][3] *= c1;
+    }
+  }
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    uint32_t p[4], plo[4];
+    if (KF == kBf16) {
+      // a weight as the sum of two bf16 (together 16 bits): rounded to one, the
+      // weights would cost as much precision as the result's own rounding
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = s[2 * ks + (e >> 1)][2 * (e & 1)], y = s[2 * ks + (e >> 1)][2 * (e & 1) + 1];
+        p[e] = pack_bf16(x, y);
+        plo[e] = pack_bf16(x - bf16_lo(p[e]), y - bf16_hi(p[e]));
+      }
+    } else {
+      p[0] = pack_f16(s[2 * ks][0], s[2 * ks][1]);
+      p[1] = pack_f16(s[2 * ks][2], s[2 * ks][3]);
+      p[2] = pack_f16(s[2 * ks + 1][0], s[2 * ks + 1][1]);
+      p[3] = pack_f16(s[2 * ks + 1][2], s[2 * ks + 1][3]);
+    }
+    uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;   // which of the lane's tokens exist
+    if (kMask) {
+      const int t0 = tb + ks * 16 + 2 * t;
+      k0 = (t0 < glen ? 0xffffu : 0u) | (t0 + 1 < glen ? 0xffff0000u : 0u);
+      k1 = (t0 + 8 < glen ? 0xffffu : 0u) | (t0 + 9 < glen ? 0xffff0000u : 0u);
+    }
+    const uint32_t row = stage + TB + (uint32_t)((ks * 16 + (m & 1) * 8 + rr) * 128);
+#pragma unroll
+    for (int j = 0; j < (KF == kBf16 ? 8 : 4); ++j) {
+      const int ch = 2 * j + (m >> 1);
+      uint32_t v0, v1, v2, v3;
+      ldmatrix_x4_trans(row + (KF == kBf16 ? (uint32_t)((ch >> 3) * (TB / 2)) : 0u) +
+                            (uint32_t)(((ch ^ rr) & 7) << 4),
+                        v0, v1, v2, v3);
+      if (kMask) v0 &= k0, v1 &= k1, v2 &= k0, v3 &= k1;
+      if (KF == kBf16) {
+        mma_bf16_16816(st.o[2 * j], p, v0, v1);
+        mma_bf16_16816(st.o[2 * j + 1], p, v2, v3);
+        mma_bf16_16816(st.o[2 * j], plo, v0, v1);
+        mma_bf16_16816(st.o[2 * j + 1], plo, v2, v3);
+      } else {
+        // a register holds two dims (even, odd) of two tokens: split into the
+        // even and the odd dims' operand
+        uint32_t a0, a1, b0, b1;
+        e4m3x4_to_f16x2x2(v0, a0, a1);
+        e4m3x4_to_f16x2x2(v1, b0, b1);
+        mma_f16_16816(st.o[4 * j], p, prmt(a0, a1, 0x5410), prmt(b0, b1, 0x5410));
+        mma_f16_16816(st.o[4 * j + 1], p, prmt(a0, a1, 0x7632), prmt(b0, b1, 0x7632));
+        e4m3x4_to_f16x2x2(v2, a0, a1);
+        e4m3x4_to_f16x2x2(v3, b0, b1);
+        mma_f16_16816(st.o[4 * j + 2], p, prmt(a0, a1, 0x5410), prmt(b0, b1, 0x5410));
+        mma_f16_16816(st.o[4 * j + 3], p, prmt(a0, a1, 0x7632), prmt(b0, b1, 0x7632));
+      }
+    }
+  }
+}
+
+// Four consecutive dims of a plane row as fp32.
+template <int KF>
+__device__ __forceinline__ float4 plane_f32(const uint8_t* payload, const float* scale,
+                                            long long row, int lane) {
+  if (KF == kBf16) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(payload + row * 256) + lane);
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2x2(__ldg(reinterpret_cast<const uint32_t*>(payload + row * 128) + lane), lo, hi);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float s = __ldg(scale + row);
+  return make_float4(x.x * s, x.y * s, y.x * s, y.y * s);
+}
+
+// A stretch of one unit: which tokens its items are.
+struct Items {
+  int r, head, slot, glen, kv_head;
+  int i0, i1;
+};
+
+// Item i of the stretch: its first token, and for block lists the drafts that
+// list its block (bit p - p0).  False: nothing there.
+template <bool kBlocks>
+__device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
+                                            uint32_t& members) {
+  if (kBlocks) {
+    const uint32_t e = list[i >> 2];
+    tb = (int)(e & 0xffffu) * kBlock + (i & 3) * kItem;
+    members = e >> 16;
+  } else {
+    tb = i * kItem;
+    members = 0xffffffffu;
+  }
+  return tb < it.glen;
+}
+
+// Plane row of the item's first token, -1 if its page id is out of range.
+__device__ __forceinline__ long long item_row(const AttnArgs& a, const Items& it, int tb) {
+  const int page = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
+  if (page < 0 || page >= a.num_pages) return -1;
+  return ((long long)page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
+}
+
+// One row of a stretch token by token (one warp, lane = four dims), for rows
+// whose joined output is not finite: the tiled products put 0 * NaN into a row
+// that does not see the NaN, this does not.
+template <int KF, bool kBlocks>
+__device__ __noinline__ void careful_row(const AttnArgs& a, const Items& it, const uint32_t* list,
+                                         const uint16_t* q, int len, int draft_bit, int lane,
+                                         float& m, float& l, float4& o) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(q) + lane);
+  const float4 qv = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  m = -INFINITY;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = it.i0; i < it.i1; ++i) {
+    int tb;
+    uint32_t members;
+    if (!item_tokens<kBlocks>(it, list, i, tb, members) || !((members >> draft_bit) & 1u)) continue;
+    const long long row = item_row(a, it, tb);
+    if (row < 0) continue;
+    for (int e = 0; e < kItem && tb + e < len; ++e) {
+      const float4 k = plane_f32<KF>(a.k_payload, a.k_scale, row + e, lane);
+      float x = qv.x * k.x + qv.y * k.y + qv.z * k.z + qv.w * k.w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      x *= a.scale_log2;
+      if (x == -INFINITY) continue;
+      const float mn = fmaxf(m, x), c = ex2_approx(m - mn), p = ex2_approx(x - mn);
+      const float4 v = plane_f32<KF>(a.v_payload, a.v_scale, row + e, lane);
+      l = l * c + p;
+      o = make_float4(o.x * c + p * v.x, o.y * c + p * v.y, o.z * c + p * v.z, o.w * c + p * v.w);
+      m = mn;
+    }
+  }
+}
+
+__device__ __forceinline__ bool finite4(float4 o) {
+  return isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
+}
+
+// Write a finished row: lane = four dims.
+__device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, float m, float l, float4 o,
+                                          int lane) {
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  uint2 u;
+  u.x = m == -INFINITY ? 0u : pack_bf16(o.x * inv, o.y * inv);
+  u.y = m == -INFINITY ? 0u : pack_bf16(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.out + row * kDim)[lane] = u;
+  if (lane == 0 && a.lse) a.lse[row] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+}
+
+template <int KF, bool kBlocks>
+__global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map) {
+  using L = ALayout<KF>;
+  constexpr int NW = L::NW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
+  int* pre = reinterpret_cast<int*>(smem + L::kPreOff);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
+  uint32_t* rank = bits + kMaxBlockWords;
+  float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
+  float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  if (lane == 0) {
+    mbar_init(sbase + L::kBarOff + warp * 8, 1);
+    if (warp == 0) mbar_init(sbase + L::kBarOff + NW * 8, 1);  // the stall test's barrier
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- prefix of the requests' unit weights --------------------------------
+  if (warp == 0) {
+    int run = 0;
+    bool clamped = false;
+    for (int v0 = 0; v0 < a.R; v0 += 32) {
+      const int v = v0 + lane;
+      int wt = 0;
+      if (v < a.R) {
+        const int slot = __ldg(a.slot_ids + v);
+        int n = 0;
+        if (slot >= 0 && slot < a.n_slots) {
+          for (int p = 0; p < a.P; ++p) {
+            n = max(n, row_len(a, v, p));
+            clamped |= __ldg(a.row_lens + v * a.P + p) > a.max_pages * kPage;
+          }
+        }
+        if (kBlocks) {
+          const int nb = (n + kBlock - 1) / kBlock;
+          const int drafts = min(a.P, (kTile + a.nq - 2) / a.nq + 1);
+          n = min(nb, a.topk * drafts) * (kBlock / kItem);
+        } else {
+          n = (n + kItem - 1) / kItem;
+        }
+        wt = n + kUnitCost;
+      }
+      int incl = wt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (v < a.R) pre[v] = run + incl - wt;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    clamped = __any_sync(0xffffffffu, clamped);
+    if (lane == 0) {
+      pre[a.R] = run;
+      *cta_flags = (clamped && blockIdx.x == 0) ? kErrLenClamped : 0u;
+    }
+  }
+  __syncthreads();
+
+  const int per = a.heads * a.groups;
+  const long long W = (long long)pre[a.R] * per;
+  // no CTA takes less than about one piece a warp
+  const long long want = (W + NW - 1) / NW;
+  const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
+  const int c = blockIdx.x;
+  const long long begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
+  SplitRecord record = {-1, 0};
+
+  auto items_of = [&](const Segment& s, int n) {
+    Items it;
+    it.r = s.r;
+    it.head = s.head;
+    it.kv_head = s.head * a.kv_heads / a.heads;
+    const int slot = __ldg(a.slot_ids + s.r);
+    it.slot = slot;
+    it.glen = 0;
+    if (slot >= 0 && slot < a.n_slots)
+      for (int p = 0; p < a.P; ++p) it.glen = max(it.glen, row_len(a, s.r, p));
+    if (kBlocks) {
+      it.i0 = s.cap ? (int)((long long)n * s.o0 / s.cap) : 0;
+      it.i1 = s.cap ? (int)((long long)n * s.o1 / s.cap) : 0;
+    } else {
+      it.i0 = s.o0;
+      it.i1 = s.o1;
+    }
+    return it;
+  };
+
+  // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
+  struct Next {
+    int unit;      // -1: nothing left
+    int tb;
+    uint32_t members;
+    int row;
+  };
+  long long fpos = begin;
+  Items fit = {};
+  int funit = -1, fi = 0;
+  fit.i1 = 0;
+  bool dead = false;
+  auto feed = [&]() -> Next {
+    Next n = {-1, 0, 0u, 0};
+    while (!dead) {
+      if (fi >= fit.i1) {
+        if (kBlocks || fpos >= end) break;
+        const Segment s = next_segment(pre, a.R, a.heads, a.groups, fpos, end);
+        if (!s.live) continue;
+        fit = items_of(s, 0);
+        funit = s.unit;
+        fi = fit.i0 + warp;
+        continue;
+      }
+      const int i = fi;
+      fi += NW;
+      if (!item_tokens<kBlocks>(fit, list, i, n.tb, n.members)) continue;
+      const long long row = item_row(a, fit, n.tb);
+      if (row < 0) {
+        if (lane == 0) atomicOr(cta_flags, kErrBadPage);
+        continue;
+      }
+      n.row = (int)row;
+      n.unit = funit;
+      break;
+    }
+    return n;
+  };
+  const uint32_t stage = sbase + warp * L::kStage;
+  const uint32_t bar = sbase + L::kBarOff + warp * 8;
+  const float* scales = reinterpret_cast<const float*>(smem + L::kScaleOff + warp * L::kScaleBytes);
+  auto issue = [&](const Next& n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, L::kStage + L::kScaleBytes);
+      if (KF == kBf16) {
+        tma_load_2d(stage, &k_map, 0, n.row, bar);
+        tma_load_2d(stage + L::kTileBytes / 2, &k_map, 64, n.row, bar);
+        tma_load_2d(stage + L::kTileBytes, &v_map, 0, n.row, bar);
+        tma_load_2d(stage + L::kTileBytes + L::kTileBytes / 2, &v_map, 64, n.row, bar);
+      } else {
+        const uint32_t sc = sbase + L::kScaleOff + warp * L::kScaleBytes;
+        tma_load_2d(stage, &k_map, 0, n.row, bar);
+        bulk_load(sc, a.k_scale + n.row, kItem * 4, bar);
+        tma_load_2d(stage + L::kTileBytes, &v_map, 0, n.row, bar);
+        bulk_load(sc + kItem * 4, a.v_scale + n.row, kItem * 4, bar);
+      }
+    }
+  };
+
+  Next cur = {-1, 0, 0u, 0}, nxt = {-1, 0, 0u, 0};
+  int used = 0;           // pieces this warp has waited for
+  bool primed = false;
+  long long pos = begin;
+  while (pos < end) {
+    const Segment s = next_segment(pre, a.R, a.heads, a.groups, pos, end);
+    if (!s.live) continue;
+    const int row_first = s.group * kTile;
+    const int nrows = min(kTile, a.P * a.nq - row_first);
+    const int p0 = row_first / a.nq;
+    int n_items = 0;
+    if (kBlocks) {
+      // ---- the drafts' lists joined: one entry a block, with its drafts -----
+      const int p1 = (row_first + nrows - 1) / a.nq;
+      const int ldx = s.head * a.lists / a.heads;
+      const int slot = __ldg(a.slot_ids + s.r);
+      const bool pad = slot < 0 || slot >= a.n_slots;
+      const int words = (a.max_pages + 63) / 64;
+      for (int w = threadIdx.x; w < words; w += L::kThreads) bits[w] = 0u;
+      __syncthreads();
+      const int entries = pad ? 0 : (p1 - p0 + 1) * a.topk;
+      for (int e = threadIdx.x; e < entries; e += L::kThreads) {
+        const int p = p0 + e / a.topk, j = e % a.topk;
+        const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + ldx) * a.topk + j);
+        if (id >= 0 && (long long)id * kBlock < row_len(a, s.r, p))
+          atomicOr(&bits[id >> 5], 1u << (id & 31));
+      }
+      __syncthreads();
+      if (warp == 0) {
+        int run = 0;
+        for (int w0 = 0; w0 < words; w0 += 32) {
+          const int w = w0 + lane;
+          const int cnt = w < words ? __popc(bits[w]) : 0;
+          int incl = cnt;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          if (w < words) rank[w] = (uint32_t)(run + incl - cnt);
+          run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) cta_flags[1] = (unsigned int)run;
+      }
+      __syncthreads();
+      n_items = (int)cta_flags[1] * (kBlock / kItem);
+      for (int w = threadIdx.x; w < n_items / 4; w += L::kThreads) list[w] = 0u;
+      __syncthreads();
+      for (int e = threadIdx.x; e < entries; e += L::kThreads) {
+        const int p = p0 + e / a.topk, j = e % a.topk;
+        const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + ldx) * a.topk + j);
+        if (id >= 0 && (long long)id * kBlock < row_len(a, s.r, p)) {
+          const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
+          atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
+        }
+      }
+      __syncthreads();
+      fit = items_of(s, n_items);
+      funit = s.unit;
+      fi = fit.i0 + warp;
+      primed = false;
+    }
+    if (!primed) {
+      primed = true;
+      cur = feed();
+      if (cur.unit >= 0) {
+        issue(cur);
+        nxt = feed();
+      }
+    }
+    const Items it = kBlocks ? fit : items_of(s, 0);
+    // ---- the unit's rows ----------------------------------------------------
+    const bool pad = it.slot < 0 || it.slot >= a.n_slots;
+    auto q_index = [&](int i) {
+      const int pk = row_first + i, p = pk / a.nq;
+      return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
+    };
+    auto len_of = [&](int i) { return i < nrows && !pad ? row_len(a, s.r, (row_first + i) / a.nq) : 0; };
+    const int L0 = len_of(g), L1 = len_of(g + 8);
+    const int d0 = (row_first + min(g, nrows - 1)) / a.nq - p0;
+    const int d1 = (row_first + min(g + 8, nrows - 1)) / a.nq - p0;
+    QRows<KF> q;
+    q.load(g < nrows ? a.q + q_index(g) * kDim : nullptr,
+           g + 8 < nrows ? a.q + q_index(g + 8) * kDim : nullptr, a.scale_log2, lane);
+    State st;
+    st.reset();
+    // ---- its pieces -----------------------------------------------------------
+    while (cur.unit == s.unit) {
+      const bool stall = a.stall_test && warp == 0 && used == 0;
+      if (!mbar_wait_bounded(stall ? sbase + L::kBarOff + NW * 8 : bar,
+                             stall ? 0u : (uint32_t)(used & 1), a.wait_ns)) {
+        if (lane == 0) atomicOr(cta_flags, kErrTimeout);
+        dead = true;
+        break;
+      }
+      ++used;
+      __syncwarp();
+      const int e0 = (cur.members >> d0) & 1u ? L0 : 0, e1 = (cur.members >> d1) & 1u ? L1 : 0;
+      const bool whole = __all_sync(0xffffffffu, (g >= nrows || cur.tb + kItem <= e0) &&
+                                                     (g + 8 >= nrows || cur.tb + kItem <= e1));
+      if (whole)
+        piece<KF, false>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
+      else
+        piece<KF, true>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
+      // every lane's reads of the stage come before the copies that refill it
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      cur = nxt;
+      if (cur.unit >= 0) {
+        issue(cur);
+        nxt = feed();
+      }
+    }
+    if (dead) {
+      // let the copies in flight land, take no more
+      if (cur.unit >= 0 && lane == 0) (void)mbar_wait_bounded(bar, (uint32_t)(used & 1), 200000000ull);
+      cur.unit = nxt.unit = -1;
+    }
+    // ---- join the warps ---------------------------------------------------------
+    {
+      float l0 = st.l0, l1 = st.l1;
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+      }
+      if (t == 0) {
+        ml[warp * kTile + g] = make_float2(st.m0, l0);
+        ml[warp * kTile + g + 8] = make_float2(st.m1, l1);
+      }
+      float* w0 = merge + (size_t)(warp * kTile + g) * kMergeStride;
+      float* w1 = w0 + 8 * kMergeStride;
+      if (KF == kBf16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          *reinterpret_cast<float2*>(w0 + 8 * j + 2 * t) = make_float2(st.o[j][0], st.o[j][1]);
+          *reinterpret_cast<float2*>(w1 + 8 * j + 2 * t) = make_float2(st.o[j][2], st.o[j][3]);
+        }
+      } else {
+        const float f = st.mv;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const float* e = st.o[2 * ch];
+          const float* d = st.o[2 * ch + 1];
+          *reinterpret_cast<float4*>(w0 + 16 * ch + 4 * t) = make_float4(e[0] * f, d[0] * f, e[1] * f, d[1] * f);
+          *reinterpret_cast<float4*>(w1 + 16 * ch + 4 * t) = make_float4(e[2] * f, d[2] * f, e[3] * f, d[3] * f);
+        }
+      }
+    }
+    __syncthreads();
+    const bool complete = s.o0 == 0 && s.o1 == s.cap;
+    const int slot_out = 2 * c + (s.o0 == 0 ? 1 : 0);
+    if (s.o0 == 0 && !complete) {
+      record.unit = s.unit;
+      record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
+    }
+    for (int i = warp; i < nrows; i += NW) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, ml[w * kTile + i].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 x = ml[w * kTile + i];
+          const float f = ex2_approx(x.x - m);
+          if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
+          const float4 v = *reinterpret_cast<const float4*>(merge + (size_t)(w * kTile + i) * kMergeStride + 4 * lane);
+          l = fmaf(x.y, f, l);
+          o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+        }
+      }
+      if (__any_sync(0xffffffffu, !finite4(o)))
+        careful_row<KF, kBlocks>(a, it, list, a.q + q_index(i) * kDim, len_of(i),
+                                 (row_first + i) / a.nq - p0, lane, m, l, o);
+      if (complete) {
+        write_row(a, q_index(i), m, l, o, lane);
+      } else {
+        const size_t at = (size_t)slot_out * kTile + i;
+        if (lane == 0) a.part_ml[at] = make_float2(m, l);
+        reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    a.records[c] = record;
+    a.err_bytes[c] = (uint8_t)*cta_flags;
+    if (c == 0) *a.err_count = gridDim.x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The join of units that several CTAs shared.  Block (c, i): row i of the unit
+// that CTA c started and did not end.  Its parts are CTA c's second slot and the
+// first slots of the CTAs behind it, added in that order in each of four warps'
+// shares, so the result does not depend on timing.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+  __shared__ float2 sml[4];
+  __shared__ float so[4][kDim];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x / a.group_rows, i = blockIdx.x - c * a.group_rows;
+  const SplitRecord rec = a.records[c];
+  if (rec.unit < 0) return;
+  const int per = a.heads * a.groups;
+  const int r = rec.unit / per, k = rec.unit - r * per;
+  const int head = k / a.groups, pk = (k - head * a.groups) * a.group_rows + i;
+  if (pk >= a.P * a.nq) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = warp; s < rec.splits; s += 4) {
+    const size_t at = (size_t)slot(s) * a.group_rows + i;
+    const float2 x = a.part_ml[at];
+    if (x.x == -INFINITY) continue;
+    const float4 v = reinterpret_cast<const float4*>(a.part_o + at * kDim)[lane];
+    const float mn = fmaxf(m, x.x), f = ex2_approx(m - mn), h = ex2_approx(x.x - mn);
+    l = fmaf(l, f, x.y * h);
+    o = make_float4(fmaf(o.x, f, v.x * h), fmaf(o.y, f, v.y * h), fmaf(o.z, f, v.z * h), fmaf(o.w, f, v.w * h));
+    m = mn;
+  }
+  if (lane == 0) sml[warp] = make_float2(m, l);
+  reinterpret_cast<float4*>(so[warp])[lane] = o;
+  __syncthreads();
+  if (warp) return;
+  for (int w = 1; w < 4; ++w) {
+    const float2 x = sml[w];
+    if (x.x == -INFINITY) continue;
+    const float4 v = reinterpret_cast<const float4*>(so[w])[lane];
+    const float mn = fmaxf(m, x.x), f = ex2_approx(m - mn), h = ex2_approx(x.x - mn);
+    l = fmaf(l, f, x.y * h);
+    o = make_float4(fmaf(o.x, f, v.x * h), fmaf(o.y, f, v.y * h), fmaf(o.z, f, v.z * h), fmaf(o.w, f, v.w * h));
+    m = mn;
+  }
+  const int p = pk / a.nq;
+  write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, lane);
+}
+
+template <int KF, bool kBlocks>
+cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                      int grid, int dev, cudaStream_t stream) {
+  using L = ALayout<KF>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_limit_once(attn_kernel<KF, kBlocks>, L::kSmem, dev, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_kernel<KF, kBlocks>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_ctas() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = cached_sm_count(dev);
+  const int lim = grid_limit();
+  if (lim > 0 && lim < n) n = lim;
+  return n > attn::kMaxCtas ? attn::kMaxCtas : n;
+}
+
+cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_map,
+                        const CUtensorMap& v_map, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int grid = attn_ctas();
+  if (grid <= 0) return cudaErrorInvalidDevice;
+  const bool blocks = a.block_ids != nullptr;
+  if (key_format == kBf16)
+    e = blocks ? launch_kf<kBf16, true>(a, k_map, v_map, grid, dev, stream)
+               : launch_kf<kBf16, false>(a, k_map, v_map, grid, dev, stream);
+  else
+    e = blocks ? launch_kf<kFp8, true>(a, k_map, v_map, grid, dev, stream)
+               : launch_kf<kFp8, false>(a, k_map, v_map, grid, dev, stream);
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(a, grid, stream);
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(attn_join_kernel, ctas * a.group_rows, 128, 0, stream, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace idx

@@ -1,0 +1,144 @@
+// Shared pieces of the attention kernels: the call's arguments, the split of the
+// work over CTAs, and the layout of the partial results in the workspace.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "idx_internal.cuh"
+
+namespace idx {
+namespace attn {
+
+constexpr int kItem = 32;          // tokens of one work item (half a page)
+constexpr int kMaxCtas = 256;      // CTAs of one call (the grid is one per SM)
+constexpr int kMaxDrafts = 16;     // draft rows whose block lists one row group joins
+
+constexpr uint32_t kErrBadPage = 1u;
+constexpr uint32_t kErrTimeout = 2u;
+constexpr uint32_t kErrLenClamped = 4u;
+
+// Where a unit that several CTAs share begins: written by the CTA that starts
+// it, read by the join.  unit < 0: this CTA starts no shared unit.
+struct SplitRecord {
+  int unit, splits;
+};
+
+}  // namespace attn
+
+// Arguments of one attention call.  A "unit" is what shares one read of the
+// keys and values: the query heads of one request that go by the same key head
+// and the same block list, cut into groups of `group_rows` packed rows.  Packed
+// row i of a unit is (draft row i / nq, query head unit_head * nq + i % nq).
+struct AttnArgs {
+  const uint16_t* q;           // bf16 [R][P][q_heads][128]
+  const uint8_t* k_payload;    // plane rows (page * kv_heads + head) * 64 + token % 64
+  const float* k_scale;        // one a row (fp8) or nullptr
+  const uint8_t* v_payload;
+  const float* v_scale;
+  const int32_t* page_table;   // [n_slots][max_pages]
+  const int32_t* slot_ids;     // [R]
+  const int32_t* row_lens;     // [R][P]
+  const int32_t* block_ids;    // [R][P][lists][topk], or nullptr: every block
+  uint16_t* out;               // bf16 [R][P][q_heads][128]
+  float* lse;                  // [R][P][q_heads] or nullptr
+  attn::SplitRecord* records;  // [CTAs]
+  float2* part_ml;             // [2 * CTAs][group_rows]: running max (log2 units) and sum
+  float* part_o;               // [2 * CTAs][group_rows][128]: unnormalised output
+  uint8_t* err_bytes;          // one flag byte per CTA
+  uint32_t* err_count;         // CTAs that wrote a flag byte
+  int64_t num_pages;
+  int n_slots, max_pages;
+  int R, P, q_heads, kv_heads, lists, topk;
+  int heads;                   // unit heads of a request: max(kv_heads, lists)
+  int nq;                      // query heads of a unit head
+  int group_rows;              // packed rows of a group (16, or up to 128)
+  int groups;                  // row groups of a unit head
+  float scale_log2;            // softmax scale times log2(e)
+  unsigned long long wait_ns;
+  int stall_test;
+};
+
+namespace attn {
+
+// Packed rows of a group: what one read of the keys serves.
+inline int group_rows(int /*drafts*/, int /*nq*/) { return 16; }
+
+// Bytes of the workspace after the header: records, then the partials.
+inline size_t records_bytes() { return (size_t)kMaxCtas * sizeof(SplitRecord); }
+inline size_t part_ml_bytes(int ctas, int group_rows) {
+  return (size_t)2 * ctas * group_rows * sizeof(float2);
+}
+inline size_t part_o_bytes(int ctas, int group_rows) {
+  return (size_t)2 * ctas * group_rows * kDim * sizeof(float);
+}
+
+// ---------------------------------------------------------------------------
+// The split.  Every unit of request r has weight wt(r) = items(r) + kUnitCost,
+// items(r) = its 32-token pieces (with block lists: an upper bound of them).
+// The units' weights lie end to end on a line of W positions, in the order
+// (request, unit head, row group); CTA c of C takes [W c / C, W (c + 1) / C).
+// A CTA's part of a unit is its items inside that range; the last kUnitCost
+// positions of a unit stand for the cost of ending it and hold no item, except
+// that a unit with no items is ended by the CTA that holds its first position.
+// ---------------------------------------------------------------------------
+constexpr int kUnitCost = 8;
+
+struct Segment {
+  int unit;          // (r * heads + unit head) * groups + group
+  int r, head, group;
+  int o0, o1, cap;   // items [o0, o1) of cap
+  long long start;   // the unit's first position
+  bool live;         // false: nothing to do in this stretch
+};
+
+// Largest r with pre[r] <= x.
+__device__ __forceinline__ int find_request(const int* pre, int R, int x) {
+  int lo = 0, hi = R - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The stretch that begins at `pos`; pos moves behind it.
+__device__ __forceinline__ Segment next_segment(const int* pre, int R, int heads, int groups,
+                                                long long& pos, long long end) {
+  Segment s;
+  const int per = heads * groups;
+  s.r = find_request(pre, R, (int)(pos / per));
+  const int wt = pre[s.r + 1] - pre[s.r];
+  const long long base = (long long)pre[s.r] * per;
+  const int k = (int)((pos - base) / wt);
+  const int o = (int)(pos - base - (long long)k * wt);
+  s.head = k / groups;
+  s.group = k - s.head * groups;
+  s.unit = s.r * per + k;
+  s.start = pos - o;
+  s.cap = wt - kUnitCost;
+  const long long left = end - pos;
+  const int take = left < wt - o ? (int)left : wt - o;
+  s.o0 = o < s.cap ? o : s.cap;
+  s.o1 = o + take < s.cap ? o + take : s.cap;
+  s.live = s.o1 > s.o0 || (s.cap == 0 && o == 0);
+  pos += take;
+  return s;
+}
+
+// The CTA that holds position x.
+__device__ __forceinline__ int owner(long long x, long long W, int C) {
+  return (int)(((x + 1) * C + W - 1) / W) - 1;
+}
+
+}  // namespace attn
+
+cudaError_t launch_attn(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
+                        const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnArgs& args, int ctas, cudaStream_t stream);
+// CTAs launch_attn uses on the current device (0: the device cannot be asked).
+int attn_ctas();
+
+}  // namespace idx

@@ -1,0 +1,339 @@
+"""idx_attn_paged / idx_attn_blocks against a 64-bit reference (needs a GPU): shapes, lengths
+and masks where a split, packed, paged kernel can go wrong, with NaN in every place of the
+cache that no row sees."""
+import pytest
+import torch
+
+import _attn
+import sparse_attention_indexer_packed_gb300 as idx
+
+pytestmark = pytest.mark.gpu
+DTYPES = ["bf16", "fp8_e4m3"]
+
+
+def draws(R, P, Hq, seed, scale=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (scale * torch.randn((R, P, Hq, 128), generator=g)).to(torch.bfloat16)
+
+
+def run(c, q, sm_scale=128 ** -0.5, block_ids=None, lists=0, lse=True, ws=None):
+    d = _attn.to_device(c)
+    R, P, Hq, _ = q.shape
+    out = torch.full((R, P, Hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    l = torch.full((R, P, Hq), 7.0, device="cuda") if lse else None
+    if ws is None:
+        ws = idx.alloc_attn_workspace(P, Hq, c.kv_heads, lists)
+        ws.fill_(0xff)      # no clearing is needed
+    if block_ids is None:
+        idx.idx_attn_paged(q.cuda(), *d.args(), c.kv_heads, sm_scale, out, l, ws)
+    else:
+        idx.idx_attn_blocks(q.cuda(), *d.args(), block_ids.cuda(), lists, c.kv_heads, sm_scale, out, l, ws)
+    flags = idx.idx_workspace_errors(ws)
+    return out, l, flags
+
+
+def drafts(L, P):
+    return [max(0, L - (P - 1) + p) for p in range(P)]
+
+
+LENS = [0, 1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 1000]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,Hq,Hkv", [(1, 1, 1), (1, 16, 2), (1, 4, 4), (2, 6, 2), (4, 16, 1),
+                                      (4, 8, 2), (3, 10, 2), (1, 40, 1), (7, 24, 1), (8, 16, 1)])
+def test_whole_cache(dtype, P, Hq, Hkv):
+    lens = [drafts(L, P) for L in LENS]
+    c = _attn.make(dtype, lens, Hkv, 11 + P + Hq, pads=(3, 8))
+    q = draws(len(lens), P, Hq, 5)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ctas", [1, 2, 7, 0])
+@pytest.mark.parametrize("P,Hq,Hkv", [(1, 8, 2), (4, 16, 1)])
+def test_splits_of_a_long_cache(dtype, ctas, P, Hq, Hkv):
+    lens = [drafts(L, P) for L in (5000, 3, 2049, 0, 777)]
+    c = _attn.make(dtype, lens, Hkv, 21)
+    q = draws(len(lens), P, Hq, 6)
+    idx.idx_set_grid_limit(ctas)
+    try:
+        out, l, flags = run(c, q)
+        again, l2, _ = run(c, q)
+    finally:
+        idx.idx_set_grid_limit(0)
+    assert flags == 0
+    assert torch.equal(out, again) and torch.equal(l, l2)      # the split's order is fixed
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_rows_of_very_different_lengths():
+    lens = [[1, 700, 0, 64], [129, 128, 2000, 1]]
+    for dtype in DTYPES:
+        c = _attn.make(dtype, lens, 2, 31)
+        q = draws(2, 4, 8, 7)
+        out, l, flags = run(c, q)
+        assert flags == 0
+        _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def lists_for(lens, n_lists, topk, seed, P):
+    g = torch.Generator().manual_seed(seed)
+    R = len(lens)
+    ids = torch.full((R, P * n_lists, topk), -1, dtype=torch.int32)
+    for r in range(R):
+        for p in range(P):
+            nb = -(-max(lens[r]) // 128)
+            for li in range(n_lists):
+                pick = torch.randperm(max(1, nb), generator=g)[:topk].to(torch.int32)
+                ids[r, p * n_lists + li, :len(pick)] = pick
+    return ids
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,Hq,Hkv,lists,topk", [
+    (1, 16, 1, 4, 8), (4, 16, 1, 4, 16), (4, 16, 4, 4, 5), (4, 16, 4, 2, 5), (2, 12, 2, 6, 3),
+    (16, 4, 1, 4, 4), (5, 40, 1, 2, 6), (1, 1, 1, 1, 256), (17, 2, 1, 2, 3), (8, 16, 1, 1, 4)])
+def test_blocks(dtype, P, Hq, Hkv, lists, topk):
+    lens = [drafts(L, P) for L in (0, 1, 64, 129, 1000, 2500, 4097)]
+    c = _attn.make(dtype, lens, Hkv, 41 + P, pads=(2,))
+    q = draws(len(lens), P, Hq, 8)
+    ids = lists_for(lens, lists, topk, 9, P)
+    # what a list may hold besides: a block twice, no block, blocks past the row's own
+    ids[4, 0, 0] = ids[4, 0, topk // 2]
+    ids[5, 1 % (P * lists), -1] = -7
+    ids[5, 0, 0] = 40 if topk > 1 else 0
+    ids[6, P * lists - 1] = -1
+    out, l, flags = run(c, q, block_ids=ids, lists=lists)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, lists))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_ids_of_any_value_are_left_out(dtype):
+    lens = [[300], [128]]
+    c = _attn.make(dtype, lens, 1, 51)
+    q = draws(2, 1, 4, 10)
+    ids = torch.tensor([[[2 ** 31 - 1, -2 ** 31, 2, 3, 0, 2 ** 24, 32768, 65536 * 3]],
+                        [[1, 1, -1, 5, 9, 2 ** 25, 2 ** 30, 7]]], dtype=torch.int32)
+    out, l, flags = run(c, q, block_ids=ids, lists=1)
+    assert flags == 0
+    keep = torch.tensor([[[2, 0]], [[-1, -1]]], dtype=torch.int32)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, keep, 1))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_lists_of_every_block_are_the_whole_cache(dtype):
+    lens = [drafts(L, 2) for L in (1, 500, 1025)]
+    c = _attn.make(dtype, lens, 1, 61)
+    q = draws(3, 2, 8, 11)
+    ids = torch.arange(9, dtype=torch.int32).flip(0).expand(3, 4, 9).contiguous()
+    ref = _attn.reference(c, q, 128 ** -0.5)
+    out, l, _ = run(c, q, block_ids=ids, lists=2)
+    _attn.check(out, l, ref)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_token_that_one_draft_row_sees_does_not_reach_the_others(dtype, bad):
+    """The rows of a unit share one product with the values: 0 * NaN must not leak."""
+    lens = [drafts(130, 4), drafts(64, 4)]
+    c = _attn.make(dtype, lens, 1, 71)
+    clean = _attn.reference(c, draws(2, 4, 4, 12), 128 ** -0.5)
+    page = c.page_table[int(c.slot_ids[0])]
+    row = int(page[129 // 64]) * 64 + 129 % 64        # the newest token: only the last row sees it
+    if dtype == "bf16":
+        c.v[0][row, 5] = bad
+        c.k[0][row, 3] = bad
+    else:
+        c.v[1][row] = bad
+        c.k[1][row] = bad
+    q = draws(2, 4, 4, 12)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    out, l = out.cpu(), l.cpu()
+    keep = torch.ones((2, 4, 4), dtype=torch.bool)
+    keep[0, 3] = False
+    d = (out.double() - clean[0]).abs()
+    assert (d[keep] <= clean[2][keep]).all()
+    assert ((l.double() - clean[1]).abs()[keep] <= clean[3][keep]).all()
+    if bad != -float("inf"):
+        # a NaN or +inf score makes the row that sees it not finite (-inf may be a weight of zero)
+        assert not torch.isfinite(out[0, 3].float()).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_block_that_one_draft_row_lists_does_not_reach_the_others(dtype):
+    lens = [[640, 640]]
+    c = _attn.make(dtype, lens, 1, 73)
+    ids = torch.tensor([[[0, 1, 2], [0, 3, 2]]], dtype=torch.int32)
+    q = draws(1, 2, 4, 13)
+    clean = _attn.reference(c, q, 128 ** -0.5, ids, 1)
+    page = c.page_table[int(c.slot_ids[0])]
+    row = int(page[3 * 128 // 64]) * 64 + 7            # in block 3
+    if dtype == "bf16":
+        c.v[0][row] = float("nan")
+    else:
+        c.v[0][row] = 0x7f
+    out, l, _ = run(c, q, block_ids=ids, lists=1)
+    d = (out.cpu().double() - clean[0]).abs()
+    assert (d[0, 0] <= clean[2][0, 0]).all()
+    assert torch.isnan(out[0, 1].float()).all()
+    assert ((l.cpu().double() - clean[1]).abs() <= clean[3]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scores_far_apart_and_value_scales_far_apart(dtype):
+    """A running maximum that grows late, weights that vanish, values over many powers of two."""
+    lens = [drafts(900, 2)]
+    c = _attn.make(dtype, lens, 1, 81, spread=True)
+    q = draws(1, 2, 8, 14, scale=40.0)
+    out, l, flags = run(c, q)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_zero_scales_and_zero_queries():
+    lens = [[200]]
+    c = _attn.make("fp8_e4m3", lens, 1, 83)
+    c.v[1].zero_()
+    q = draws(1, 1, 4, 15)
+    q[:, :, 1] = 0
+    out, l, _ = run(c, q)
+    assert torch.equal(out, torch.zeros_like(out))
+    ref = _attn.reference(c, q, 128 ** -0.5)
+    assert ((l.cpu().double() - ref[1]).abs() <= ref[3]).all()
+
+
+def test_no_lse_and_no_requests():
+    c = _attn.make("bf16", [[100]], 1, 85)
+    q = draws(1, 1, 4, 16)
+    a, l, _ = run(c, q)
+    b, none, _ = run(c, q, lse=False)
+    assert none is None and torch.equal(a, b)
+    d = _attn.to_device(c)
+    ws = idx.alloc_attn_workspace(1, 4, 1)
+    ws.fill_(0xff)
+    idx.idx_attn_paged(q[:0].cuda(), d.k[0], None, d.v[0], None, "bf16", d.page_table,
+                       d.slot_ids[:0], d.row_lens[:0], 1, 1.0, a[:0], None, ws)
+    assert idx.idx_workspace_errors(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("blocks", [False, True])
+def test_bad_pages_are_left_out_and_flagged(dtype, blocks):
+    lens = [[500], [300]]
+    c = _attn.make(dtype, lens, 2, 87)
+    s = int(c.slot_ids[0])
+    c.page_table[s, 2] = c.num_pages           # past the pool
+    c.page_table[s, 5] = -3
+    q = draws(2, 1, 4, 17)
+    ids = torch.arange(4, dtype=torch.int32).expand(2, 1, 4).contiguous() if blocks else None
+    out, l, flags = run(c, q, block_ids=ids, lists=1 if blocks else 0)
+    assert flags == idx._lib.DEVERR_BAD_PAGE
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, 1))
+
+
+def test_lengths_past_the_table_are_clamped_and_flagged():
+    c = _attn.make("bf16", [[200], [90]], 1, 89, max_pages=4)
+    c.row_lens[0] = 100000
+    c.page_table[int(c.slot_ids[0])] = torch.arange(4, dtype=torch.int32)
+    c.k[0].nan_to_num_(0.5)
+    c.v[0].nan_to_num_(0.5)
+    q = draws(2, 1, 4, 18)
+    out, l, flags = run(c, q)
+    assert flags == idx._lib.DEVERR_LEN_CLAMPED
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_negative_lengths_are_empty_rows():
+    c = _attn.make("bf16", [[200, 100]], 1, 91)
+    c.row_lens[0, 1] = -5
+    q = draws(1, 2, 4, 19)
+    out, l, _ = run(c, q)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_planes_past_32_bit_offsets():
+    """Pages near the end of 5 GB planes."""
+    pages, H = 300_000, 1
+    kp = torch.empty((pages * H * 64, 128), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    use = [pages - 1, pages - 7, 3, pages - 2]
+    c = _attn.make("bf16", [[250]], H, 93, garbage=False)
+    src = c.page_table[int(c.slot_ids[0])].tolist()
+    for i, p in enumerate(use):
+        kp[p * 64:(p + 1) * 64] = c.k[0][src[i] * 64:(src[i] + 1) * 64].cuda()
+        vp[p * 64:(p + 1) * 64] = c.v[0][src[i] * 64:(src[i] + 1) * 64].cuda()
+    q = draws(1, 1, 16, 20)
+    out = torch.empty((1, 1, 16, 128), dtype=torch.bfloat16, device="cuda")
+    l = torch.empty((1, 1, 16), device="cuda")
+    ws = idx.alloc_attn_workspace(1, 16, 1)
+    idx.idx_attn_paged(q.cuda(), kp, None, vp, None, "bf16",
+                       torch.tensor([use], dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, dtype=torch.int32, device="cuda"),
+                       torch.tensor([[250]], dtype=torch.int32, device="cuda"), H, 128 ** -0.5, out, l, ws)
+    assert idx.idx_workspace_errors(ws) == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_graph_replay_and_another_stream():
+    lens = [drafts(L, 2) for L in (900, 64)]
+    c = _attn.make("bf16", lens, 1, 95)
+    q = draws(2, 2, 8, 21)
+    want, wl, _ = run(c, q)
+    d = _attn.to_device(c)
+    qd = q.cuda()
+    out, l = torch.zeros_like(want), torch.zeros_like(wl)
+    ws = idx.alloc_attn_workspace(2, 8, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    idx.idx_attn_paged(qd, *d.args(), 1, 128 ** -0.5, out, l, ws, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(l, wl)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        idx.idx_attn_paged(qd, *d.args(), 1, 128 ** -0.5, out, l, ws)
+    d.row_lens[0] = torch.tensor([310, 311], dtype=torch.int32)
+    graph.replay()
+    torch.cuda.synchronize()
+    c.row_lens[0] = torch.tensor([310, 311], dtype=torch.int32)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,Hq", [(1, 8), (4, 16)])
+def test_a_wait_that_runs_out_is_flagged(dtype, P, Hq):
+    c = _attn.make(dtype, [drafts(3000, P)], 1, 97)
+    q = draws(1, P, Hq, 22)
+    idx.idx_set_wait_limit_ns(20_000_000)
+    idx.idx_set_stall_test(True)
+    try:
+        _, _, flags = run(c, q)
+    finally:
+        idx.idx_set_stall_test(False)
+        idx.idx_set_wait_limit_ns(0)
+    assert flags & idx._lib.DEVERR_TIMEOUT
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+def test_shards_join_by_lse():
+    """Two halves of a context, joined by their lse, are the whole."""
+    c = _attn.make("bf16", [[1024]], 1, 99, garbage=False)
+    q = draws(1, 1, 8, 23)
+    whole, wl, _ = run(c, q)
+    parts = []
+    table = c.page_table[int(c.slot_ids[0])].clone()
+    for half in range(2):
+        c.page_table[int(c.slot_ids[0]), :8] = table[8 * half:8 * half + 8]
+        c.row_lens[0, 0] = 512
+        parts.append(run(c, q)[:2])
+    l = torch.stack([p[1] for p in parts])
+    z = torch.logsumexp(l, 0)
+    out = sum(p[0].float() * torch.exp(p[1] - z)[..., None] for p in parts)
+    assert (z - wl).abs().max() <= 2e-5
+    # each side: a bf16 rounding of the weights and of the result
+    assert (out - whole.float()).abs().max() <= 2 * 2.0 ** -8 * whole.float().abs().max() + 2.0 ** -8
