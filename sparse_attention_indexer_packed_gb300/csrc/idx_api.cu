@@ -191,16 +191,15 @@ int make_q_map(int q_dtype, const void* q, int64_t rows, CUtensorMap* map) {
   return IDX_OK;
 }
 
-// Tensor map over one plane of a key-value cache for 32-token pieces: bf16 rows
-// as two 64-column boxes, e4m3 rows as one 128-byte box, 32 rows high, 128-byte
-// swizzle.  Encoded at each call: it is a fraction of a launch's host time.
-int make_plane_map(int dtype, const void* payload, int64_t rows, CUtensorMap* map) {
+// Tensor map over one plane of a key-value cache: bf16 rows as two 64-column
+// boxes, e4m3 rows as one 128-byte box, `box_rows` high, 128-byte swizzle.  Encoded at each call: it is a fraction of a launch's host time.
+int make_plane_map(int dtype, const void* payload, int64_t rows, int box_rows, CUtensorMap* map) {
   auto fn = encode_fn();
   if (!fn) return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const bool bf16 = dtype == IDX_BF16;
   const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 256 : 128)};
-  const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : 128), (cuuint32_t)idx::attn::kItem};
+  const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : 128), (cuuint32_t)box_rows};
   const cuuint32_t estride[2] = {1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                   const_cast<void*>(payload), dims, strides, box, estride,
@@ -293,7 +292,7 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   a.topk = blocks ? topk : 0;
   a.heads = heads;
   a.nq = q_heads / heads;
-  a.group_rows = idx::attn::group_rows(P, a.nq);
+  a.group_rows = idx::attn::group_rows(P, a.nq, blocks);
   a.groups = (P * a.nq + a.group_rows - 1) / a.group_rows;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.wait_ns = idx::wait_limit_ns();
@@ -307,9 +306,10 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   ws += idx::attn::part_ml_bytes(idx::attn::kMaxCtas, a.group_rows);
   a.part_o = reinterpret_cast<float*>(ws);
   CUtensorMap k_map, v_map;
-  int rc = make_plane_map(kv_dtype, k_payload, num_pages * kv_heads * idx::kPage, &k_map);
-  if (rc == IDX_OK)
-    rc = make_plane_map(kv_dtype, v_payload, num_pages * kv_heads * idx::kPage, &v_map);
+  const int64_t plane_rows = num_pages * kv_heads * idx::kPage;
+  const int box_rows = a.group_rows > 16 ? idx::kPage : idx::kPage / 2;
+  int rc = make_plane_map(kv_dtype, k_payload, plane_rows, box_rows, &k_map);
+  if (rc == IDX_OK) rc = make_plane_map(kv_dtype, v_payload, plane_rows, box_rows, &v_map);
   if (rc != IDX_OK) return rc;
   const cudaError_t e = idx::launch_attn(kv_dtype, a, k_map, v_map, st);
   if (e != cudaSuccess) return cuda_fail(e, "launching the attention kernels");
@@ -815,7 +815,7 @@ int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t
 size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_heads, int lists) {
   const int heads = unit_heads(q_heads, kv_heads, lists > 0 ? lists : 1);
   if (packed_queries < 1 || lists < 0 || heads == 0) return 0;
-  const int rows = idx::attn::group_rows(packed_queries, q_heads / heads);
+  const int rows = idx::attn::group_rows(packed_queries, q_heads / heads, lists > 0);
   return IDX_WORKSPACE_HEADER_BYTES + idx::attn::records_bytes() +
          idx::attn::part_ml_bytes(idx::attn::kMaxCtas, rows) +
          idx::attn::part_o_bytes(idx::attn::kMaxCtas, rows);

@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include "idx_attn.cuh"
+#include "idx_attn_rows.cuh"
 #include "idx_ptx.cuh"
 
 namespace idx {
@@ -41,10 +42,8 @@ namespace {
 
 using namespace attn;
 
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 16;                              // packed rows of a group here
-constexpr int kMaxList = kMaxTopk * kMaxDrafts;        // joined block list of a group
-constexpr int kMaxBlockWords = 65536 / 2 / 32;         // bits for every block of a request
+constexpr int kItem = 32;                              // tokens of a piece
 constexpr int kMergeStride = kDim + 8;                 // floats: keeps row writes off one bank
 
 template <int KF>
@@ -83,28 +82,12 @@ struct ALayout {
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {
-  const int L = __ldg(a.row_lens + r * a.P + p), cap = a.max_pages * kPage;
-  return L < 0 ? 0 : (L > cap ? cap : L);
-}
-
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, uint32_t& r1,
                                                   uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(addr));
 }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // The 16 query rows in A-fragment order.
 //  bf16: a[ks] = {row g: d 16ks+2t,+1; row g+8: same; row g: +8,+9; row g+8: +8,+9}
@@ -363,100 +346,6 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
   }
 }
 
-// Four consecutive dims of a plane row as fp32.
-template <int KF>
-__device__ __forceinline__ float4 plane_f32(const uint8_t* payload, const float* scale,
-                                            long long row, int lane) {
-  if (KF == kBf16) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(payload + row * 256) + lane);
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  }
-  uint32_t lo, hi;
-  e4m3x4_to_f16x2x2(__ldg(reinterpret_cast<const uint32_t*>(payload + row * 128) + lane), lo, hi);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  const float s = __ldg(scale + row);
-  return make_float4(x.x * s, x.y * s, y.x * s, y.y * s);
-}
-
-// A stretch of one unit: which tokens its items are.
-struct Items {
-  int r, head, slot, glen, kv_head;
-  int i0, i1;
-};
-
-// Item i of the stretch: its first token, and for block lists the drafts that
-// list its block (bit p - p0).  False: nothing there.
-template <bool kBlocks>
-__device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
-                                            uint32_t& members) {
-  if (kBlocks) {
-    const uint32_t e = list[i >> 2];
-    tb = (int)(e & 0xffffu) * kBlock + (i & 3) * kItem;
-    members = e >> 16;
-  } else {
-    tb = i * kItem;
-    members = 0xffffffffu;
-  }
-  return tb < it.glen;
-}
-
-// Plane row of the item's first token, -1 if its page id is out of range.
-__device__ __forceinline__ long long item_row(const AttnArgs& a, const Items& it, int tb) {
-  const int page = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
-  if (page < 0 || page >= a.num_pages) return -1;
-  return ((long long)page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
-}
-
-// One row of a stretch token by token (one warp, lane = four dims), for rows
-// whose joined output is not finite: the tiled products put 0 * NaN into a row
-// that does not see the NaN, this does not.
-template <int KF, bool kBlocks>
-__device__ __noinline__ void careful_row(const AttnArgs& a, const Items& it, const uint32_t* list,
-                                         const uint16_t* q, int len, int draft_bit, int lane,
-                                         float& m, float& l, float4& o) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(q) + lane);
-  const float4 qv = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-  m = -INFINITY;
-  l = 0.f;
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = it.i0; i < it.i1; ++i) {
-    int tb;
-    uint32_t members;
-    if (!item_tokens<kBlocks>(it, list, i, tb, members) || !((members >> draft_bit) & 1u)) continue;
-    const long long row = item_row(a, it, tb);
-    if (row < 0) continue;
-    for (int e = 0; e < kItem && tb + e < len; ++e) {
-      const float4 k = plane_f32<KF>(a.k_payload, a.k_scale, row + e, lane);
-      float x = qv.x * k.x + qv.y * k.y + qv.z * k.z + qv.w * k.w;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x *= a.scale_log2;
-      if (x == -INFINITY) continue;
-      const float mn = fmaxf(m, x), c = ex2_approx(m - mn), p = ex2_approx(x - mn);
-      const float4 v = plane_f32<KF>(a.v_payload, a.v_scale, row + e, lane);
-      l = l * c + p;
-      o = make_float4(o.x * c + p * v.x, o.y * c + p * v.y, o.z * c + p * v.z, o.w * c + p * v.w);
-      m = mn;
-    }
-  }
-}
-
-__device__ __forceinline__ bool finite4(float4 o) {
-  return isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
-}
-
-// Write a finished row: lane = four dims.
-__device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, float m, float l, float4 o,
-                                          int lane) {
-  const float inv = m == -INFINITY ? 0.f : 1.f / l;
-  uint2 u;
-  u.x = m == -INFINITY ? 0u : pack_bf16(o.x * inv, o.y * inv);
-  u.y = m == -INFINITY ? 0u : pack_bf16(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(a.out + row * kDim)[lane] = u;
-  if (lane == 0 && a.lse) a.lse[row] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
-}
-
 template <int KF, bool kBlocks>
 __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -471,7 +360,6 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   int* pre = reinterpret_cast<int*>(smem + L::kPreOff);
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
-  uint32_t* rank = bits + kMaxBlockWords;
   float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
 
@@ -489,46 +377,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- prefix of the requests' unit weights --------------------------------
-  if (warp == 0) {
-    int run = 0;
-    bool clamped = false;
-    for (int v0 = 0; v0 < a.R; v0 += 32) {
-      const int v = v0 + lane;
-      int wt = 0;
-      if (v < a.R) {
-        const int slot = __ldg(a.slot_ids + v);
-        int n = 0;
-        if (slot >= 0 && slot < a.n_slots) {
-          for (int p = 0; p < a.P; ++p) {
-            n = max(n, row_len(a, v, p));
-            clamped |= __ldg(a.row_lens + v * a.P + p) > a.max_pages * kPage;
-          }
-        }
-        if (kBlocks) {
-          const int nb = (n + kBlock - 1) / kBlock;
-          const int drafts = min(a.P, (kTile + a.nq - 2) / a.nq + 1);
-          n = min(nb, a.topk * drafts) * (kBlock / kItem);
-        } else {
-          n = (n + kItem - 1) / kItem;
-        }
-        wt = n + kUnitCost;
-      }
-      int incl = wt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (v < a.R) pre[v] = run + incl - wt;
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    clamped = __any_sync(0xffffffffu, clamped);
-    if (lane == 0) {
-      pre[a.R] = run;
-      *cta_flags = (clamped && blockIdx.x == 0) ? kErrLenClamped : 0u;
-    }
-  }
+  if (warp == 0) build_prefix<kItem, kBlocks>(a, pre, cta_flags, lane);
   __syncthreads();
 
   const int per = a.heads * a.groups;
@@ -539,26 +388,6 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   const int c = blockIdx.x;
   const long long begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
   SplitRecord record = {-1, 0};
-
-  auto items_of = [&](const Segment& s, int n) {
-    Items it;
-    it.r = s.r;
-    it.head = s.head;
-    it.kv_head = s.head * a.kv_heads / a.heads;
-    const int slot = __ldg(a.slot_ids + s.r);
-    it.slot = slot;
-    it.glen = 0;
-    if (slot >= 0 && slot < a.n_slots)
-      for (int p = 0; p < a.P; ++p) it.glen = max(it.glen, row_len(a, s.r, p));
-    if (kBlocks) {
-      it.i0 = s.cap ? (int)((long long)n * s.o0 / s.cap) : 0;
-      it.i1 = s.cap ? (int)((long long)n * s.o1 / s.cap) : 0;
-    } else {
-      it.i0 = s.o0;
-      it.i1 = s.o1;
-    }
-    return it;
-  };
 
   // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
   struct Next {
@@ -579,14 +408,14 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
         if (kBlocks || fpos >= end) break;
         const Segment s = next_segment(pre, a.R, a.heads, a.groups, fpos, end);
         if (!s.live) continue;
-        fit = items_of(s, 0);
+        fit = make_items<kBlocks>(a, s, 0);
         funit = s.unit;
         fi = fit.i0 + warp;
         continue;
       }
       const int i = fi;
       fi += NW;
-      if (!item_tokens<kBlocks>(fit, list, i, n.tb, n.members)) continue;
+      if (!item_tokens<kItem, kBlocks>(fit, list, i, n.tb, n.members)) continue;
       const long long row = item_row(a, fit, n.tb);
       if (row < 0) {
         if (lane == 0) atomicOr(cta_flags, kErrBadPage);
@@ -631,52 +460,9 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     const int p0 = row_first / a.nq;
     int n_items = 0;
     if (kBlocks) {
-      // ---- the drafts' lists joined: one entry a block, with its drafts -----
-      const int p1 = (row_first + nrows - 1) / a.nq;
-      const int ldx = s.head * a.lists / a.heads;
-      const int slot = __ldg(a.slot_ids + s.r);
-      const bool pad = slot < 0 || slot >= a.n_slots;
-      const int words = (a.max_pages + 63) / 64;
-      for (int w = threadIdx.x; w < words; w += L::kThreads) bits[w] = 0u;
-      __syncthreads();
-      const int entries = pad ? 0 : (p1 - p0 + 1) * a.topk;
-      for (int e = threadIdx.x; e < entries; e += L::kThreads) {
-        const int p = p0 + e / a.topk, j = e % a.topk;
-        const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + ldx) * a.topk + j);
-        if (id >= 0 && (long long)id * kBlock < row_len(a, s.r, p))
-          atomicOr(&bits[id >> 5], 1u << (id & 31));
-      }
-      __syncthreads();
-      if (warp == 0) {
-        int run = 0;
-        for (int w0 = 0; w0 < words; w0 += 32) {
-          const int w = w0 + lane;
-          const int cnt = w < words ? __popc(bits[w]) : 0;
-          int incl = cnt;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          if (w < words) rank[w] = (uint32_t)(run + incl - cnt);
-          run += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) cta_flags[1] = (unsigned int)run;
-      }
-      __syncthreads();
-      n_items = (int)cta_flags[1] * (kBlock / kItem);
-      for (int w = threadIdx.x; w < n_items / 4; w += L::kThreads) list[w] = 0u;
-      __syncthreads();
-      for (int e = threadIdx.x; e < entries; e += L::kThreads) {
-        const int p = p0 + e / a.topk, j = e % a.topk;
-        const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + ldx) * a.topk + j);
-        if (id >= 0 && (long long)id * kBlock < row_len(a, s.r, p)) {
-          const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
-          atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
-        }
-      }
-      __syncthreads();
-      fit = items_of(s, n_items);
+      n_items = join_lists(a, s, p0, (row_first + nrows - 1) / a.nq, list, bits, cta_flags + 1) *
+                (kBlock / kItem);
+      fit = make_items<kBlocks>(a, s, n_items);
       funit = s.unit;
       fi = fit.i0 + warp;
       primed = false;
@@ -689,7 +475,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
         nxt = feed();
       }
     }
-    const Items it = kBlocks ? fit : items_of(s, 0);
+    const Items it = kBlocks ? fit : make_items<kBlocks>(a, s, 0);
     // ---- the unit's rows ----------------------------------------------------
     const bool pad = it.slot < 0 || it.slot >= a.n_slots;
     auto q_index = [&](int i) {
@@ -792,7 +578,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
         }
       }
       if (__any_sync(0xffffffffu, !finite4(o)))
-        careful_row<KF, kBlocks>(a, it, list, a.q + q_index(i) * kDim, len_of(i),
+        careful_row<KF, kItem, kBlocks>(a, it, list, a.q + q_index(i) * kDim, len_of(i),
                                  (row_first + i) / a.nq - p0, lane, m, l, o);
       if (complete) {
         write_row(a, q_index(i), m, l, o, lane);
@@ -821,7 +607,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   __shared__ float2 sml[4];
   __shared__ float so[4][kDim];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x / a.group_rows, i = blockIdx.x - c * a.group_rows;
+  const int rows = min(a.group_rows, a.P * a.nq);
+  const int c = blockIdx.x / rows, i = blockIdx.x - c * rows;
   const SplitRecord rec = a.records[c];
   if (rec.unit < 0) return;
   const int per = a.heads * a.groups;
@@ -890,7 +677,9 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
   const int grid = attn_ctas();
   if (grid <= 0) return cudaErrorInvalidDevice;
   const bool blocks = a.block_ids != nullptr;
-  if (key_format == kBf16)
+  if (a.group_rows > kTile)
+    e = launch_attn_wide(key_format, a, k_map, v_map, grid, dev, stream);
+  else if (key_format == kBf16)
     e = blocks ? launch_kf<kBf16, true>(a, k_map, v_map, grid, dev, stream)
                : launch_kf<kBf16, false>(a, k_map, v_map, grid, dev, stream);
   else
@@ -901,7 +690,7 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(attn_join_kernel, ctas * a.group_rows, 128, 0, stream, a);
+  cudaError_t e = launch_pdl(attn_join_kernel, ctas * (a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows), 128, 0, stream, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

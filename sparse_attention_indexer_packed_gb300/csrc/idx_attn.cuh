@@ -11,8 +11,7 @@
 namespace idx {
 namespace attn {
 
-constexpr int kItem = 32;          // tokens of one work item (half a page)
-constexpr int kMaxCtas = 256;      // CTAs of one call (the grid is one per SM)
+constexpr int kMaxCtas = 192;      // CTAs of one call (the grid is one per SM)
 constexpr int kMaxDrafts = 16;     // draft rows whose block lists one row group joins
 
 constexpr uint32_t kErrBadPage = 1u;
@@ -62,8 +61,13 @@ struct AttnArgs {
 
 namespace attn {
 
-// Packed rows of a group: what one read of the keys serves.
-inline int group_rows(int /*drafts*/, int /*nq*/) { return 16; }
+// Packed rows of a group: what one read of the keys serves.  Up to 16 rows go to
+// the warp-level kernel, more to the tensor-memory one, 128 at most; a group of
+// block lists joins those of kMaxDrafts draft rows at most.
+inline int group_rows(int drafts, int nq, bool blocks) {
+  if ((long long)drafts * nq <= 16) return 16;
+  return blocks && nq * kMaxDrafts < 128 ? nq * kMaxDrafts : 128;
+}
 
 // Bytes of the workspace after the header: records, then the partials.
 inline size_t records_bytes() { return (size_t)kMaxCtas * sizeof(SplitRecord); }
@@ -76,7 +80,7 @@ inline size_t part_o_bytes(int ctas, int group_rows) {
 
 // ---------------------------------------------------------------------------
 // The split.  Every unit of request r has weight wt(r) = items(r) + kUnitCost,
-// items(r) = its 32-token pieces (with block lists: an upper bound of them).
+// items(r) = its pieces (with block lists: an upper bound of them).
 // The units' weights lie end to end on a line of W positions, in the order
 // (request, unit head, row group); CTA c of C takes [W c / C, W (c + 1) / C).
 // A CTA's part of a unit is its items inside that range; the last kUnitCost
@@ -137,6 +141,8 @@ __device__ __forceinline__ int owner(long long x, long long W, int C) {
 
 cudaError_t launch_attn(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
                         const CUtensorMap& v_map, cudaStream_t stream);
+cudaError_t launch_attn_wide(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
+                             const CUtensorMap& v_map, int grid, int dev, cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnArgs& args, int ctas, cudaStream_t stream);
 // CTAs launch_attn uses on the current device (0: the device cannot be asked).
 int attn_ctas();

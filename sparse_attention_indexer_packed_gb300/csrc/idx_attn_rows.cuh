@@ -1,0 +1,256 @@
+// Device code that both attention kernels use: lengths and items, the joined
+// block list of a row group, the token-by-token row, and the output row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "idx_attn.cuh"
+#include "idx_ptx.cuh"
+
+namespace idx {
+namespace attn {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxList = kMaxTopk * kMaxDrafts;  // joined block list of a group
+constexpr int kMaxBlockWords = 65536 / 2 / 32;   // bits for every block of a request
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Length of draft row p of request r, inside [0, max_pages * 64].
+__device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {
+  const int L = __ldg(a.row_lens + r * a.P + p), cap = a.max_pages * kPage;
+  return L < 0 ? 0 : (L > cap ? cap : L);
+}
+
+// pre[r] = sum of the unit weights of the requests before r, pre[R] the total
+// (one warp).  flags gets IDX_DEVERR_LEN_CLAMPED from the first CTA.
+template <int IT, bool kBlocks>
+__device__ __forceinline__ void build_prefix(const AttnArgs& a, int* pre, unsigned int* flags,
+                                             int lane) {
+  int run = 0;
+  bool clamped = false;
+  for (int v0 = 0; v0 < a.R; v0 += 32) {
+    const int v = v0 + lane;
+    int wt = 0;
+    if (v < a.R) {
+      const int slot = __ldg(a.slot_ids + v);
+      int n = 0;
+      if (slot >= 0 && slot < a.n_slots) {
+        for (int p = 0; p < a.P; ++p) {
+          n = max(n, row_len(a, v, p));
+          clamped |= __ldg(a.row_lens + v * a.P + p) > a.max_pages * kPage;
+        }
+      }
+      if (kBlocks) {
+        // at most: every draft row of a group lists other blocks
+        const int drafts = min(a.P, (a.group_rows + a.nq - 2) / a.nq + 1);
+        n = min((n + kBlock - 1) / kBlock, a.topk * drafts) * (kBlock / IT);
+      } else {
+        n = (n + IT - 1) / IT;
+      }
+      wt = n + kUnitCost;
+    }
+    int incl = wt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (v < a.R) pre[v] = run + incl - wt;
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  clamped = __any_sync(0xffffffffu, clamped);
+  if (lane == 0) {
+    pre[a.R] = run;
+    *flags = (clamped && blockIdx.x == 0) ? kErrLenClamped : 0u;
+  }
+}
+
+// The lists of draft rows p0 .. p1 (at most kMaxDrafts) of the segment's unit
+// joined in ascending order: list[i] = block id | drafts that list it << 16, bit
+// p - p0.  Every thread of the CTA; returns the number of blocks.  bits: 2 *
+// kMaxBlockWords words of scratch.  A set bit a block and a running count of them
+// give each entry its place, so a block listed twice takes one.
+__device__ __forceinline__ int join_lists(const AttnArgs& a, const Segment& s, int p0, int p1,
+                                          uint32_t* list, uint32_t* bits, unsigned int* count) {
+  uint32_t* rank = bits + kMaxBlockWords;
+  const int lane = threadIdx.x & 31, nt = blockDim.x;
+  const int which = s.head * a.lists / a.heads;
+  const int slot = __ldg(a.slot_ids + s.r);
+  const bool pad = slot < 0 || slot >= a.n_slots;
+  const int words = (a.max_pages + 63) / 64;
+  const int entries = pad ? 0 : (p1 - p0 + 1) * a.topk;
+  auto entry = [&](int e, int& p) {
+    p = p0 + e / a.topk;
+    const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + which) * a.topk + e % a.topk);
+    return id >= 0 && (long long)id * kBlock < row_len(a, s.r, p) ? id : -1;
+  };
+  for (int w = threadIdx.x; w < words; w += nt) bits[w] = 0u;
+  __syncthreads();
+  for (int e = threadIdx.x; e < entries; e += nt) {
+    int p;
+    const int id = entry(e, p);
+    if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const int w = w0 + lane;
+      const int cnt = w < words ? __popc(bits[w]) : 0;
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (w < words) rank[w] = (uint32_t)(run + incl - cnt);
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) *count = (unsigned int)run;
+  }
+  __syncthreads();
+  const int n = (int)*count;
+  for (int w = threadIdx.x; w < n; w += nt) list[w] = 0u;
+  __syncthreads();
+  for (int e = threadIdx.x; e < entries; e += nt) {
+    int p;
+    const int id = entry(e, p);
+    if (id >= 0) {
+      const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
+      atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
+    }
+  }
+  __syncthreads();
+  return n;
+}
+
+// Four consecutive dims of a plane row as fp32.
+template <int KF>
+__device__ __forceinline__ float4 plane_f32(const uint8_t* payload, const float* scale,
+                                            long long row, int lane) {
+  if (KF == kBf16) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(payload + row * 256) + lane);
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2x2(__ldg(reinterpret_cast<const uint32_t*>(payload + row * 128) + lane), lo, hi);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float s = __ldg(scale + row);
+  return make_float4(x.x * s, x.y * s, y.x * s, y.y * s);
+}
+
+// A stretch of one unit: which tokens its items are.
+struct Items {
+  int r, head, slot, glen, kv_head;
+  int i0, i1;
+};
+
+// The items of a stretch.  n: the unit's joined items (block lists), of which the
+// stretch takes the share that its positions have of the unit's.
+template <bool kBlocks>
+__device__ __forceinline__ Items make_items(const AttnArgs& a, const Segment& s, int n) {
+  Items it;
+  it.r = s.r;
+  it.head = s.head;
+  it.kv_head = s.head * a.kv_heads / a.heads;
+  it.slot = __ldg(a.slot_ids + s.r);
+  it.glen = 0;
+  if (it.slot >= 0 && it.slot < a.n_slots)
+    for (int p = 0; p < a.P; ++p) it.glen = max(it.glen, row_len(a, s.r, p));
+  if (kBlocks) {
+    it.i0 = s.cap ? (int)((long long)n * s.o0 / s.cap) : 0;
+    it.i1 = s.cap ? (int)((long long)n * s.o1 / s.cap) : 0;
+  } else {
+    it.i0 = s.o0;
+    it.i1 = s.o1;
+  }
+  return it;
+}
+
+// Item i of the stretch: its first token, and for block lists the drafts that
+// list its block (bit p - p0).  False: nothing there.
+template <int IT, bool kBlocks>
+__device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
+                                            uint32_t& members) {
+  if (kBlocks) {
+    constexpr int kPer = kBlock / IT;
+    const uint32_t e = list[i / kPer];
+    tb = (int)(e & 0xffffu) * kBlock + (i % kPer) * IT;
+    members = e >> 16;
+  } else {
+    tb = i * IT;
+    members = 0xffffffffu;
+  }
+  return tb < it.glen;
+}
+
+// Plane row of the item's first token, -1 if its page id is out of range.
+__device__ __forceinline__ long long item_row(const AttnArgs& a, const Items& it, int tb) {
+  const int page = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
+  if (page < 0 || page >= a.num_pages) return -1;
+  return ((long long)page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
+}
+
+// One row of a stretch token by token (one warp, lane = four dims), for rows
+// whose joined output is not finite: the tiled products put 0 * NaN into a row
+// that does not see the NaN, this does not.
+template <int KF, int IT, bool kBlocks>
+__device__ __noinline__ void careful_row(const AttnArgs& a, const Items& it, const uint32_t* list,
+                                         const uint16_t* q, int len, int draft_bit, int lane,
+                                         float& m, float& l, float4& o) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(q) + lane);
+  const float4 qv = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  m = -INFINITY;
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = it.i0; i < it.i1; ++i) {
+    int tb;
+    uint32_t members;
+    if (!item_tokens<IT, kBlocks>(it, list, i, tb, members) || !((members >> draft_bit) & 1u)) continue;
+    const long long row = item_row(a, it, tb);
+    if (row < 0) continue;
+    for (int e = 0; e < IT && tb + e < len; ++e) {
+      const float4 k = plane_f32<KF>(a.k_payload, a.k_scale, row + e, lane);
+      float x = qv.x * k.x + qv.y * k.y + qv.z * k.z + qv.w * k.w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      x *= a.scale_log2;
+      if (x == -INFINITY) continue;
+      const float mn = fmaxf(m, x), c = ex2_approx(m - mn), p = ex2_approx(x - mn);
+      const float4 v = plane_f32<KF>(a.v_payload, a.v_scale, row + e, lane);
+      l = l * c + p;
+      o = make_float4(o.x * c + p * v.x, o.y * c + p * v.y, o.z * c + p * v.z, o.w * c + p * v.w);
+      m = mn;
+    }
+  }
+}
+
+__device__ __forceinline__ bool finite4(float4 o) {
+  return isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w);
+}
+
+// Write a finished row: lane = four dims.
+__device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, float m, float l, float4 o,
+                                          int lane) {
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  uint2 u;
+  u.x = m == -INFINITY ? 0u : pack_bf16(o.x * inv, o.y * inv);
+  u.y = m == -INFINITY ? 0u : pack_bf16(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.out + row * kDim)[lane] = u;
+  if (lane == 0 && a.lse) a.lse[row] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+}
+
+}  // namespace attn
+}  // namespace idx

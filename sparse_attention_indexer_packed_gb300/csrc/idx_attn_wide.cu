@@ -1,0 +1,845 @@
+// Attention with more than 16 packed rows a unit (draft rows x query heads of one
+// key head), on the 5th-generation tensor cores.
+//
+// The mathematics is idx_attn.cu's; here up to 128 packed rows are the M = 128
+// rows of one tcgen05 product, and a tile is one page: S = Q K^T (N = 64 tokens,
+// K = 128 dims), then O += P V (N = 128 dims, K = 64 tokens), both accumulated in
+// fp32 in tensor memory.  The queries and the weights P are operands in tensor
+// memory, the keys and values go from TMA's tiles in shared memory straight into
+// the products: no key or value passes through registers.
+//
+// What bounds it: the cache's bytes.  A bf16 page is 32 KB, 1400 cycles of an
+// SM's share of the HBM rate; the products take ~400 of them and the weights'
+// arithmetic ~600 of each of the two softmax groups.
+//
+// How a row is laid out.  A lane of a softmax warp owns one tensor-memory lane,
+// so the softmax needs no shuffle.  With 64 rows or fewer each row is given F =
+// 128 / rows lanes, the query repeated in each, and each of the F lanes takes its
+// own 64 / F tokens of the page: it weighs those, leaves zeros for the others, and
+// so gathers an output and a (max, sum) of its own.  All 128 lanes work whatever
+// the row count; the F parts meet once, at the unit's end.
+//
+// Roles (one CTA per SM, the split of idx_attn.cuh in pages):
+//   warps 0-3, 4-7  two softmax groups; pages alternate between them, each with
+//               its own S, P and O in tensor memory, so one group's arithmetic
+//               runs under the other's products;
+//   warp 8      TMA producer (page table, keys, values, scales; a ring of pages);
+//   warp 9      issues the products, one elected lane.
+// The running maximum is only raised when a score passes it by 2^8 (weights up
+// to 2^8 are as exact as any): the output is rescaled then, which is rare.
+//
+// Precision.  bf16 cache: the weights are two bf16 (16 bits).  e4m3 cache: the
+// keys meet the queries as e4m3 codes, the query split into two e4m3 terms (its
+// 8 significant bits are 4 + 4; exact for elements within 2^10 of the row's
+// largest); the values are decoded to f16, exactly, by the group that uses them,
+// and the weights times the value's scale are one f16 (11 bits).
+//
+// Every wait is bounded, as in the score kernels.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "idx_attn.cuh"
+#include "idx_attn_rows.cuh"
+#include "idx_ptx.cuh"
+#include "idx_tc.cuh"
+
+namespace idx {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kTok = kPage;          // tokens of a tile
+constexpr int kLanes = 128;          // tensor-memory lanes, product rows
+constexpr float kSlack = 8.f;        // log2 units a score may pass the running maximum by
+// Tensor-memory columns: the queries; S then P of each group; O of each group.
+constexpr int kColQ = 0, kColS = 64, kColO = 256, kCols = 512;
+
+template <int KF>
+struct AWCfg;
+template <>
+struct AWCfg<kBf16> {
+  static constexpr int kRowBytes = 256;
+  static constexpr int kStages = 5;
+  // bit 16: the second operand (the values) runs along N
+  static constexpr uint32_t kIdQK = instr_desc(1u, kLanes, kTok);
+  static constexpr uint32_t kIdPV = instr_desc(1u, kLanes, kDim) | (1u << 16);
+};
+template <>
+struct AWCfg<kFp8> {
+  static constexpr int kRowBytes = 128;
+  static constexpr int kStages = 8;
+  static constexpr uint32_t kIdQK = instr_desc(0u, kLanes, kTok);                // e4m3
+  static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);   // f16
+};
+
+template <int KF>
+struct AWLayout {
+  static constexpr int NS = AWCfg<KF>::kStages;
+  static constexpr int kTile = kTok * AWCfg<KF>::kRowBytes;  // keys or values of a page
+  static constexpr int kV16 = KF == kFp8 ? kTok * 256 : 0;   // decoded values, one a group
+  static constexpr int kScale = KF == kFp8 ? kTok * 4 : 0;
+  static constexpr int kV16Off = NS * 2 * kTile;
+  static constexpr int kScaleOff = kV16Off + 2 * kV16;
+  static constexpr int kXchOff = kScaleOff + NS * 2 * kScale;  // [32 dims][128 rows] floats
+  static constexpr int kMlOff = kXchOff + 32 * kLanes * 4;
+  static constexpr int kInfoOff = kMlOff + 2 * kLanes * 8;     // valid tokens of each stage
+  // full_k full_v empty_k empty_v [NS], s_full p_full pv_done [2], q_full, stall, drain
+  static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
+  static constexpr int kNumBars = 4 * NS + 9;
+  static constexpr int kCtlOff = kBarOff + kNumBars * 8;       // flags, count, abort, tmem
+  static constexpr int kPreOff = (kCtlOff + 32 + 15) & ~15;
+  static constexpr int kListOff = kPreOff + (kMaxGroups + 4) * 4;
+  static constexpr int kBytes = kListOff + kMaxList * 4;
+  static constexpr int kSmem = kBytes + 1024;
+  static constexpr int kThreads = 320;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  // a list's bits are held in the exchange area, free between two units
+  static_assert(2 * kMaxBlockWords * 4 <= 32 * kLanes * 4, "block bits");
+  static_assert(kV16Off % 1024 == 0, "operand tiles on 1024 bytes");
+};
+
+// Shared-memory descriptor of an operand whose rows run along M or N: the
+// 128-byte swizzle, rows of 128 bytes (64 16-bit elements of the MN extent, one
+// row per K index), 8-row atoms of 1024 bytes along K; `lead` bytes to the next
+// 64 elements of MN.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lead >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// D (+)= A[tensor memory] * B[shared memory], the whole warp, one elected lane.
+__device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// N consecutive 32-bit columns of the warp's 32 lanes, to and from registers.
+template <int N>
+__device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t* v) {
+  if constexpr (N == 32) {
+    uint32_t(&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(v);
+    tc_ld_32cols(taddr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+  } else {
+    static_assert(N == 8, "8, 16 or 32 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t* v) {
+  if constexpr (N == 32) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+  } else {
+    static_assert(N == 4, "4, 8, 16 or 32 columns");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void group_sync() {   // the two softmax groups
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// Four e4m3 codes of four floats (round to nearest even, saturating), and what
+// they stand for taken off the floats.
+__device__ __forceinline__ uint32_t e4m3x4_take(float (&x)[4]) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h1, %4, %3;\n\t"
+      "mov.b32 %0, {h0, h1};\n\t}"
+      : "=r"(d)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2x2(d, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
+  return d;
+}
+
+// The smallest power of two above x (x finite, >= 0; at least 2^-100).
+__device__ __forceinline__ float pow2_above(float x) {
+  const int e = max(27, (int)(__float_as_uint(x) >> 23));
+  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
+}
+
+// F lanes a row (128 / F rows of a group, or fewer).
+template <int KF, int F, bool kBlocks>
+__global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
+    attn_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
+  using L = AWLayout<KF>;
+  constexpr int NS = L::NS;
+  constexpr int kPart = kTok / F;      // tokens of a lane
+  constexpr int kWarpRows = 32 / F;    // rows of a softmax warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* ctl = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);  // flags, count, abort, tmem
+  volatile unsigned int* abort_flag = ctl + 2;
+  int* pre = reinterpret_cast<int*>(smem + L::kPreOff);
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kXchOff);
+  float* xch = reinterpret_cast<float*>(smem + L::kXchOff);
+  float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+  volatile int* info = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
+  const uint32_t bars = sbase + L::kBarOff;
+  auto full_k = [&](int s) { return bars + 8 * s; };
+  auto full_v = [&](int s) { return bars + 8 * (NS + s); };
+  auto empty_k = [&](int s) { return bars + 8 * (2 * NS + s); };
+  auto empty_v = [&](int s) { return bars + 8 * (3 * NS + s); };
+  auto s_full = [&](int g) { return bars + 8 * (4 * NS + g); };
+  auto p_full = [&](int g) { return bars + 8 * (4 * NS + 2 + g); };
+  auto pv_done = [&](int g) { return bars + 8 * (4 * NS + 4 + g); };
+  const uint32_t q_full = bars + 8 * (4 * NS + 6), stall_bar = q_full + 8, drain = q_full + 16;
+  auto k_tile = [&](int s) { return sbase + s * 2 * L::kTile; };
+  auto v_tile = [&](int s) { return sbase + s * 2 * L::kTile + L::kTile; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full_k(s), 1);
+      mbar_init(full_v(s), 1);
+      mbar_init(empty_k(s), 1);
+      mbar_init(empty_v(s), KF == kFp8 ? 4 : 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(s_full(g), 1);
+      mbar_init(p_full(g), kLanes);
+      mbar_init(pv_done(g), 1);
+    }
+    mbar_init(q_full, kLanes);
+    mbar_init(stall_bar, 1);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    *abort_flag = 0;
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  if (warp == 9) {
+    tmem_alloc(sbase + L::kCtlOff + 12, kCols);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 8) build_prefix<kTok, kBlocks>(a, pre, ctl, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl[3];
+
+  const int per = a.heads * a.groups;
+  const long long W = (long long)pre[a.R] * per;
+  // no CTA takes less than about four pages
+  const long long want = (W + 3) / 4;
+  const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
+  const int c = blockIdx.x;
+  const long long begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
+  SplitRecord record = {-1, 0};
+
+  // A bounded wait of a whole warp; false once any role has given up.
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (dead) return false;
+    bool ok = mbar_try_wait(bar, parity);
+    const uint64_t t0 = ok ? 0 : global_timer_ns();
+    for (uint32_t it = 0; !ok; ++it) {
+      ok = mbar_try_wait(bar, parity);
+      if (ok) break;
+      if (it < 64u || (it & 63u) == 63u) {
+        if (*abort_flag) break;
+        if (global_timer_ns() - t0 > a.wait_ns) {
+          atomicOr(ctl, kErrTimeout);
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+    dead = !__all_sync(0xffffffffu, ok);   // a warp goes on, or stops, as one
+    return !dead;
+  };
+
+  int sent_k = 0, sent_v = 0;   // pages whose copies the producer has asked for
+  int tile0 = 0;            // pages of the CTA's earlier segments (producer, issuer, groups)
+  int segs = 0;             // segments with pages so far
+  int cnt0 = 0, cnt1 = 0;   // pages of group 0 / 1 so far
+  long long pos = begin;
+  while (pos < end) {
+    const Segment s = next_segment(pre, a.R, a.heads, a.groups, pos, end);
+    if (!s.live) continue;
+    const int row_first = s.group * a.group_rows;
+    const int nrows = min(a.group_rows, a.P * a.nq - row_first);
+    const int p0 = row_first / a.nq;
+    int n_items = 0;
+    if (kBlocks) {
+      __syncthreads();      // every role is done with the last unit's list
+      n_items = 2 * join_lists(a, s, p0, (row_first + nrows - 1) / a.nq, list, bits, ctl + 1);
+    }
+    const Items it = make_items<kBlocks>(a, s, n_items);
+    // the second page of a request's last block may not exist
+    int i1 = it.i1;
+    if (kBlocks && i1 == n_items && n_items > 0 &&
+        (int)(list[n_items / 2 - 1] & 0xffffu) * kBlock + kPage >= it.glen)
+      --i1;
+    const int n = max(0, i1 - it.i0);
+
+    if (warp == 8) {
+      // ---- producer ---------------------------------------------------------
+      // page ids 32 items at a time, one a lane
+      auto page_of = [&](int i) {
+        int tb = 0, pg = -1;
+        uint32_t m;
+        if (i < i1 && item_tokens<kTok, kBlocks>(it, list, i, tb, m))
+          pg = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
+        if (i < i1 && (pg < 0 || pg >= a.num_pages)) {
+          atomicOr(ctl, kErrBadPage);
+          pg = -1;
+        }
+        return pg;
+      };
+      int next_ids = dead ? -1 : page_of(it.i0 + lane), ids = -1;
+      for (int b = 0; b < n && !dead; ++b) {
+        if ((b & 31) == 0) {
+          ids = next_ids;
+          next_ids = page_of(it.i0 + b + 32 + lane);
+        }
+        const int pg = __shfl_sync(0xffffffffu, ids, b & 31);
+        const int tile = tile0 + b, st = tile % NS;
+        const uint32_t ph = (uint32_t)((tile / NS) & 1) ^ 1u;
+        int tb = 0;
+        uint32_t m;
+        item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, m);
+        const int row = (pg * a.kv_heads + it.kv_head) * kPage;
+        if (!wait(empty_k(st), ph)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile);
+          if (pg >= 0) {
+            tma_load_2d(k_tile(st), &k_map, 0, row, full_k(st));
+            if (KF == kBf16) tma_load_2d(k_tile(st) + L::kTile / 2, &k_map, 64, row, full_k(st));
+          }
+        }
+        ++sent_k;
+        if (!wait(empty_v(st), ph)) break;
+        if (lane == 0) {
+          info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
+          // both planes' scales come with the values: the group reads them, and
+          // it gives the values' stage back itself
+          mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + 2 * L::kScale);
+          if (pg >= 0) {
+            tma_load_2d(v_tile(st), &v_map, 0, row, full_v(st));
+            if (KF == kBf16) {
+              tma_load_2d(v_tile(st) + L::kTile / 2, &v_map, 64, row, full_v(st));
+            } else {
+              const uint32_t sc = sbase + L::kScaleOff + st * 2 * L::kScale;
+              bulk_load(sc, a.k_scale + row, L::kScale, full_v(st));
+              bulk_load(sc + L::kScale, a.v_scale + row, L::kScale, full_v(st));
+            }
+          }
+        }
+        ++sent_v;
+        __syncwarp();
+      }
+    } else if (warp == 9) {
+      // ---- product issuer -----------------------------------------------------
+      constexpr uint32_t kIdQK = AWCfg<KF>::kIdQK, kIdPV = AWCfg<KF>::kIdPV;
+      auto qk = [&](int b) -> bool {
+        const int tile = tile0 + b, st = tile % NS, g = b & 1;
+        if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + 64 * g;
+        if (KF == kBf16) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts_f16(d, tmem + kColQ + ks * 8,
+                       desc_kmajor_sw128(k_tile(st) + (ks >> 2) * (L::kTile / 2) + (ks & 3) * 32),
+                       kIdQK, ks > 0);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)   // the query's two terms, four steps of 32 each
+            mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32), kIdQK,
+                      ks > 0);
+        }
+        tc_commit_warp(empty_k(st));
+        tc_commit_warp(s_full(g));
+        return true;
+      };
+      bool ok = n > 0 && !dead;
+      if (ok && a.stall_test && segs == 0) ok = wait(stall_bar, 0);
+      ok = ok && wait(q_full, (uint32_t)(segs & 1));
+      tc_fence_after();
+      ok = ok && qk(0);
+      if (n > 1) ok = ok && qk(1);
+      int k0 = cnt0, k1 = cnt1;
+      for (int b = 0; b < n && ok; ++b) {
+        const int tile = tile0 + b, st = tile % NS, g = b & 1;
+        const uint32_t ph = (uint32_t)((g ? k1++ : k0++) & 1);
+        ok = wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + kColO + kDim * g, p = tmem + kColS + 64 * g;
+        const uint32_t v = KF == kBf16 ? v_tile(st) : sbase + L::kV16Off + g * L::kV16;
+#pragma unroll
+        for (int ks = 0; ks < kTok / 16; ++ks) {
+          const uint64_t vd = desc_mnmajor_sw128(v + ks * 2048, kTok * 128);
+          mma_ts_f16(d, p + ks * 8, vd, kIdPV, b >= 2 || ks > 0);
+          if (KF == kBf16) mma_ts_f16(d, p + 32 + ks * 8, vd, kIdPV, 1);
+        }
+        if (KF == kBf16) tc_commit_warp(empty_v(st));
+        tc_commit_warp(pv_done(g));
+        if (b + 2 < n) ok = qk(b + 2);
+      }
+    } else {
+      // ---- softmax group g: pages g, g + 2, ... ------------------------------
+      const int g = warp >> 2, quad = warp & 3;
+      const int part = lane / kWarpRows;
+      const int row = quad * kWarpRows + lane % kWarpRows;   // of the group
+      const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+      const bool live = row < nrows;
+      const int pk = row_first + (live ? row : 0), p = pk / a.nq;
+      const size_t q_row = ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
+      const bool pad = it.slot < 0 || it.slot >= a.n_slots;
+      const int len = live && !pad ? row_len(a, s.r, p) : 0;
+      const int bit = p - p0;
+      float post = a.scale_log2;
+      if (n > 0 && (g == 0 || KF == kFp8)) {
+        // the lane's query row; group 0 puts it into tensor memory
+        const uint4* qp = reinterpret_cast<const uint4*>(a.q + q_row * kDim);
+        uint32_t w[64];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint4 u = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
+          w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
+        }
+        if (KF == kFp8) {
+          // scaled by a power of two that brings the row's largest magnitude into
+          // [2^7, 2^8), then two e4m3 terms
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          int ex = 0;
+          if (amax > 0.f) ex = 7 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
+          ex = max(-100, min(100, ex));
+          const float up = ldexpf(1.f, ex);
+          post *= ldexpf(1.f, -ex);
+          if (g == 0) {
+            uint32_t lo[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
+                            bf16_hi(w[2 * e + 1]) * up};
+              w[e] = e4m3x4_take(x);
+              lo[e] = e4m3x4_take(x);
+            }
+            tm_st<32>(tl + kColQ, w);
+            tm_st<32>(tl + kColQ + 32, lo);
+          }
+        } else {
+          tm_st<32>(tl + kColQ, w);
+          tm_st<32>(tl + kColQ + 32, w + 32);
+        }
+        if (g == 0) {
+          tm_wait_st();
+          tc_fence_before();
+          mbar_arrive(q_full);
+        }
+      }
+      float m = -INFINITY, l = 0.f, mv = 0.f;
+      int cnt = g ? cnt1 : cnt0;
+      const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
+      for (int b = g; b < n; b += 2, ++cnt) {
+        const int tile = tile0 + b, st = tile % NS;
+        int tb;
+        uint32_t members;
+        item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, members);
+        if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
+        const int valid = info[st];
+        if (KF == kFp8) {
+          // this page's values as f16, rows past the request's tokens as zeros;
+          // the buffer is free once the group's last product has ended
+          if (cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
+          const int t = threadIdx.x & 127;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = t + 128 * e, tok = k >> 3, ch = k & 7;   // 16 codes
+            uint4 u = *reinterpret_cast<const uint4*>(smem + (v_tile(st) - sbase) + tok * 128 + ((ch ^ (tok & 7)) << 4));
+            if (tok >= valid) u = make_uint4(0, 0, 0, 0);
+            uint4 x, y;
+            e4m3x4_to_f16x2x2(u.x, x.x, x.y);
+            e4m3x4_to_f16x2x2(u.y, x.z, x.w);
+            e4m3x4_to_f16x2x2(u.z, y.x, y.y);
+            e4m3x4_to_f16x2x2(u.w, y.z, y.w);
+            // dims 16 ch .. +7 and +8 .. +15: two 16-byte chunks of a 64-dim half
+            uint8_t* base = smem + L::kV16Off + g * L::kV16 + (ch >> 2) * (kTok * 128) + tok * 128;
+            const int c0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = x;
+            *reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (tok & 7)) << 4)) = y;
+          }
+        } else if (valid < kTok) {
+          // whatever lies past the request's tokens must not meet a weight of zero
+          const int t = threadIdx.x & 127;
+          for (int k = valid * 16 + t; k < kTok * 16; k += 128) {
+            const int tok = k >> 4, ch = k & 15;
+            *reinterpret_cast<uint4*>(smem + (v_tile(st) - sbase) + (ch >> 3) * (kTok * 128) + tok * 128 + ((ch & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        if (!wait(s_full(g), (uint32_t)(cnt & 1))) break;
+        tc_fence_after();
+        // the lane's scores
+        uint32_t raw[kPart];
+        if constexpr (F == 1) {
+          tm_ld<32>(sp, raw);
+          tm_ld<32>(sp + 32, raw + 32);
+          tc_wait_ld();
+        } else {
+          uint32_t all[F][kPart];
+#pragma unroll
+          for (int f = 0; f < F; ++f) tm_ld<kPart>(sp + f * kPart, all[f]);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) {
+            raw[j] = all[0][j];
+#pragma unroll
+            for (int f = 1; f < F; ++f) raw[j] = part == f ? all[f][j] : raw[j];
+          }
+        }
+        float x[kPart];
+        const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * 2 * L::kScale) + part * kPart;
+#pragma unroll
+        for (int j = 0; j < kPart; j += 4) {
+          float4 f = make_float4(post, post, post, post);
+          if (KF == kFp8) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ks + j);
+            f = make_float4(post * k4.x, post * k4.y, post * k4.z, post * k4.w);
+          }
+          x[j] = __uint_as_float(raw[j]) * f.x;
+          x[j + 1] = __uint_as_float(raw[j + 1]) * f.y;
+          x[j + 2] = __uint_as_float(raw[j + 2]) * f.z;
+          x[j + 3] = __uint_as_float(raw[j + 3]) * f.w;
+        }
+        const int visible = min(min(len, tb + valid) - tb, (members >> bit) & 1u ? kTok : 0) - part * kPart;
+        const bool masked = __any_sync(0xffffffffu, visible < kPart);
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < kPart; ++j)
+            if (j >= visible) x[j] = -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j < kPart; ++j) top = fmaxf(top, x[j]);
+        float shrink = 1.f;     // what the output gathered so far is to be multiplied by
+        if (top > m + (m == -INFINITY ? 0.f : kSlack)) {
+          shrink = ex2_approx(m - top);
+          l *= shrink;
+          m = top;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPart; ++j) {
+          x[j] = ex2_approx(x[j] - ref);
+          sum += x[j];
+        }
+        l += sum;
+        if (KF == kFp8) {
+          // times the value scales, in units of mv: a power of two that the
+          // scales may pass by 2^6 (weights up to 2^8 stay inside f16)
+          const float* vs = ks + kTok;
+          float r[kPart], most = 0.f;
+#pragma unroll
+          for (int j = 0; j < kPart; j += 4) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vs + j);
+            r[j] = v4.x, r[j + 1] = v4.y, r[j + 2] = v4.z, r[j + 3] = v4.w;
+          }
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) {
+            const float y = fabsf(r[j]);
+            if (y < INFINITY && (!masked || j < visible)) most = fmaxf(most, y);
+          }
+          if (most > mv * 64.f || mv == 0.f) {
+            const float up = pow2_above(most);
+            shrink *= mv / up;      // mv = 0: nothing gathered yet
+            mv = up;
+          }
+          const float inv = 1.f / mv;
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) {
+            x[j] *= r[j] * inv;
+            if (masked && j >= visible) x[j] = 0.f;   // its scale may be anything
+          }
+        }
+        if (b >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll
+          for (int ch = 0; ch < kDim; ch += 32) {
+            uint32_t o[32];
+            tm_ld<32>(oc + ch, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+            tm_st<32>(oc + ch, o);
+          }
+        }
+        // the weights as operand rows: the lane's own tokens, zeros for the others
+        uint32_t hi[kPart / 2], lo[kPart / 2];
+#pragma unroll
+        for (int j = 0; j < kPart / 2; ++j) {
+          if (KF == kBf16) {
+            hi[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+            lo[j] = pack_bf16(x[2 * j] - bf16_lo(hi[j]), x[2 * j + 1] - bf16_hi(hi[j]));
+          } else {
+            hi[j] = pack_f16(x[2 * j], x[2 * j + 1]);
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          uint32_t z[kPart / 2];
+#pragma unroll
+          for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
+          tm_st<kPart / 2>(sp + f * (kPart / 2), z);
+          if (KF == kBf16) {
+#pragma unroll
+            for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
+            tm_st<kPart / 2>(sp + 32 + f * (kPart / 2), z);
+          }
+        }
+        tm_wait_st();
+        tc_fence_before();
+        if (KF == kFp8 || valid < kTok) fence_async();
+        mbar_arrive(p_full(g));
+        if (KF == kFp8) {
+          // codes and scales of the page have been read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty_v(st));
+        }
+      }
+      // ---- the unit's end: the parts and the groups meet ------------------------
+      if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
+      tc_fence_after();
+      ml[g * kLanes + quad * 32 + lane] = make_float2(m, l);
+      group_sync();
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int f = 0; f < 2 * F; ++f)
+        M = fmaxf(M, ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int f = 0; f < 2 * F; ++f) {
+        const float2 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
+        if (e.x != -INFINITY) sum = fmaf(e.y, ex2_approx(e.x - ref), sum);
+      }
+      const float mine = ex2_approx(m - ref) * (KF == kFp8 ? mv : 1.f);
+      const bool complete = s.o0 == 0 && s.o1 == s.cap;
+      const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
+      const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+      bool odd = false;
+      for (int ch = 0; ch < kDim; ch += 32) {
+        uint32_t o[32];
+        float v[32];
+        tm_ld<32>(oc + ch, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = m == -INFINITY ? 0.f : __uint_as_float(o[e]) * mine;   // no page: nothing gathered
+#pragma unroll
+          for (int d = kWarpRows; d < 32; d <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
+        }
+        if (g == 1 && part == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) xch[e * kLanes + row] = v[e];
+        }
+        group_sync();
+        if (g == 0 && part == 0 && live) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] += xch[e * kLanes + row];
+            odd |= !isfinite(v[e]);
+          }
+          if (complete) {
+            uint4* out = reinterpret_cast<uint4*>(a.out + q_row * kDim + ch);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 u;
+              u.x = pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv);
+              u.y = pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
+              u.z = pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv);
+              u.w = pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
+              out[e] = u;
+            }
+          } else {
+            float4* out = reinterpret_cast<float4*>(a.part_o + at * kDim + ch);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) out[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        }
+        group_sync();
+      }
+      if (g == 0 && part == 0 && live) {
+        if (complete) {
+          if (a.lse) a.lse[q_row] = M == -INFINITY ? M : (M + log2f(sum)) * kLn2;
+        } else {
+          a.part_ml[at] = make_float2(M, sum);
+        }
+      }
+      // rows that met something not finite: token by token, so that only the
+      // rows that see it keep it
+      uint32_t todo = g == 0 ? __ballot_sync(0xffffffffu, odd) : 0u;
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int r2 = __shfl_sync(0xffffffffu, row, src);
+        const int pk2 = row_first + r2, p2 = pk2 / a.nq;
+        const size_t q2 = ((size_t)s.r * a.P + p2) * a.q_heads + s.head * a.nq + (pk2 - p2 * a.nq);
+        float m2, l2;
+        float4 o2;
+        careful_row<KF, kTok, kBlocks>(a, it, list, a.q + q2 * kDim, __shfl_sync(0xffffffffu, len, src),
+                                       p2 - p0, lane, m2, l2, o2);
+        if (complete) {
+          write_row(a, q2, m2, l2, o2, lane);
+        } else {
+          const size_t at2 = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + r2;
+          if (lane == 0) a.part_ml[at2] = make_float2(m2, l2);
+          reinterpret_cast<float4*>(a.part_o + at2 * kDim)[lane] = o2;
+        }
+      }
+    }
+    if (s.o0 == 0 && s.o1 != s.cap) {
+      record.unit = s.unit;
+      record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
+    }
+    tile0 += n;
+    segs += n > 0;
+    cnt0 += (n + 1) / 2;
+    cnt1 += n / 2;
+  }
+
+  // after a timeout: the copies and products in flight end before the block does
+  if (warp == 8 && *abort_flag) {
+    __syncwarp();
+    for (int k = max(0, sent_k - NS); k < sent_k; ++k)
+      (void)mbar_wait_bounded(full_k(k % NS), (uint32_t)((k / NS) & 1), 200000000ull);
+    for (int k = max(0, sent_v - NS); k < sent_v; ++k)
+      (void)mbar_wait_bounded(full_v(k % NS), (uint32_t)((k / NS) & 1), 200000000ull);
+  }
+  if (warp == 9) {
+    __syncwarp();
+    tc_commit_warp(drain);
+    (void)mbar_wait_bounded(drain, 0, 200000000ull);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, kCols);
+  if (threadIdx.x == 0) {
+    a.records[c] = record;
+    a.err_bytes[c] = (uint8_t)ctl[0];
+    if (c == 0) *a.err_count = gridDim.x;
+  }
+}
+
+template <int KF, int F, bool kBlocks>
+cudaError_t launch_kfb(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                       int grid, int dev, cudaStream_t stream) {
+  using L = AWLayout<KF>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_limit_once(attn_wide_kernel<KF, F, kBlocks>, L::kSmem, dev, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_wide_kernel<KF, F, kBlocks>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int KF>
+cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                      int grid, int dev, cudaStream_t stream) {
+  const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
+  const bool blocks = a.block_ids != nullptr;
+#define IDX_LAUNCH(F)                                                              \
+  (blocks ? launch_kfb<KF, F, true>(a, k_map, v_map, grid, dev, stream)            \
+          : launch_kfb<KF, F, false>(a, k_map, v_map, grid, dev, stream))
+  if (rows <= 16) return IDX_LAUNCH(8);
+  if (rows <= 32) return IDX_LAUNCH(4);
+  if (rows <= 64) return IDX_LAUNCH(2);
+  return IDX_LAUNCH(1);
+#undef IDX_LAUNCH
+}
+
+}  // namespace
+
+cudaError_t launch_attn_wide(int key_format, const AttnArgs& a, const CUtensorMap& k_map,
+                             const CUtensorMap& v_map, int grid, int dev, cudaStream_t stream) {
+  return key_format == kBf16 ? launch_kf<kBf16>(a, k_map, v_map, grid, dev, stream)
+                             : launch_kf<kFp8>(a, k_map, v_map, grid, dev, stream);
+}
+
+}  // namespace idx
