@@ -123,6 +123,20 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+# torch.cuda.current_stream() builds a Stream object (~3 us); a decode step's small
+# calls ask torch for the bare handle where it has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor, stream) -> Optional[int]:
+    """The given stream's handle, or that of t's device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
+
+
 def pool_struct(dtype: str, payload: torch.Tensor, scale: Optional[torch.Tensor]) -> IdxPool:
     """Describe caller-owned planes (torch tensors) as an idx_pool."""
     rows, row_bytes = payload.shape[0], payload.shape[1] * payload.element_size()
@@ -329,40 +343,66 @@ def idx_noalloc_errors(stream=None) -> int:
     return int(v.value)
 
 
-def _want(t: torch.Tensor, name: str, dtype, shape=None) -> int:
-    """Device pointer of a contiguous CUDA tensor of this dtype (and shape)."""
-    if t.dtype != dtype:
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_ROW_BYTES = {"bf16": 256, "fp8_e4m3": 128, "nvfp4": 64}
+
+
+def _want(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Device pointer of a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise IdxError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise IdxError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    if t.shape != shape:
+        raise IdxError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     return _dev(t, name)
 
 
 def _rows_2d(t: torch.Tensor, name: str, rows: int, width: int):
     """Device pointer and row stride of a bf16 tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or tuple(t.shape) != (rows, width):
+    if t.dtype is not _BF16 or t.shape != (rows, width):
         raise IdxError(f"{name} must be bfloat16 [{rows}, {width}]")
     if not t.is_cuda:
         raise IdxError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if width > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if width > 1 and inner != 1:
         raise IdxError(f"{name}'s rows must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else width)
+    return t.data_ptr(), (stride if rows > 1 else width)
 
 
 def _plane(payload, scale, name: str, kv_dtype: str):
     """Pointers of a plane and its head pages, checked against the cache's dtype."""
-    if kv_dtype not in DTYPES:
+    want = _ROW_BYTES.get(kv_dtype)
+    if want is None:
         raise IdxError(f"unknown dtype {kv_dtype!r}")
-    want = {"bf16": 256, "fp8_e4m3": 128, "nvfp4": 64}[kv_dtype]
     if payload.dim() != 2 or payload.shape[1] * payload.element_size() != want:
         raise IdxError(f"{name}_payload must be [rows, {want} bytes] for a {kv_dtype} cache")
     rows = payload.shape[0]
     if rows % PAGE:
         raise IdxError(f"{name}_payload must hold whole pages of {PAGE} rows")
-    if kv_dtype == "fp8_e4m3" and (scale is None or scale.numel() * scale.element_size() != rows * 4):
-        raise IdxError(f"{name}_scale must hold one fp32 per row")
-    return (_dev(payload, f"{name}_payload"), _dev(scale, f"{name}_scale", required=False),
-            rows // PAGE)
+    if scale is not None or kv_dtype == "fp8_e4m3":
+        if kv_dtype == "fp8_e4m3" and (scale is None or scale.numel() * scale.element_size() != rows * 4):
+            raise IdxError(f"{name}_scale must hold one fp32 per row")
+        scale = _dev(scale, f"{name}_scale")
+    return _dev(payload, f"{name}_payload"), scale, rows // PAGE
+
+
+def _source(src, name: str, tokens: int, kv_heads: int):
+    """Pointer and token stride of new keys or values [tokens, kv_heads, 128]."""
+    if src.dtype is not _BF16 or src.shape != (tokens, kv_heads, DIM):
+        raise IdxError(f"{name} must be bfloat16 [{tokens}, {kv_heads}, {DIM}]")
+    if not src.is_cuda:
+        raise IdxError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    stride, head, inner = src.stride()
+    if tokens and (inner != 1 or (kv_heads > 1 and head != DIM)):
+        raise IdxError(f"{name}'s tokens must be contiguous [{kv_heads}, {DIM}]")
+    return src.data_ptr(), (stride if tokens > 1 else kv_heads * DIM)
+
+
+def _plane_struct(payload, scale, name: str, kv_dtype: str) -> IdxPool:
+    ptr, scale_ptr, pages = _plane(payload, scale, name, kv_dtype)
+    return IdxPool(DTYPES[kv_dtype], PAGE, DIM, 0, pages, ptr, scale_ptr, _ROW_BYTES[kv_dtype],
+                   {"bf16": 0, "fp8_e4m3": 4, "nvfp4": 8}[kv_dtype])
 
 
 def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
@@ -370,33 +410,20 @@ def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_sc
     """k_src, v_src: bf16 [tokens, kv_heads, 128], tokens any stride apart (a slice of a
     fused projection); v_src, v_payload, v_scale None: keys only.  Planes as for
     idx_attn_paged, or an index pool's (kv_heads 1)."""
-    pools, ptrs = [], []
-    T = int(slot_mapping.numel())
-    for src, payload, scale, name in ((k_src, k_payload, k_scale, "k"), (v_src, v_payload, v_scale, "v")):
-        if src is None and payload is None and name == "v":
-            pools.append(None)
-            ptrs.append((None, 0))
-            continue
-        if src is None or payload is None:
-            raise IdxError(f"{name}_src and {name}_payload come together")
-        if src.dtype != torch.bfloat16 or tuple(src.shape) != (T, kv_heads, DIM):
-            raise IdxError(f"{name}_src must be bfloat16 [{T}, {kv_heads}, {DIM}]")
-        if not src.is_cuda:
-            raise IdxError(f"{name}_src must be a CUDA tensor (the library has no CPU path)")
-        if T and (src.stride(2) != 1 or (kv_heads > 1 and src.stride(1) != DIM)):
-            raise IdxError(f"{name}_src's tokens must be contiguous [{kv_heads}, {DIM}]")
-        p = IdxPool()
-        p.dtype, p.page_size, p.dim = DTYPES.get(kv_dtype, -1), PAGE, DIM
-        p.payload, p.scale, p.num_pages = _plane(payload, scale, name, kv_dtype)
-        p.payload_row_bytes = payload.shape[1] * payload.element_size()
-        p.scale_row_bytes = {"fp8_e4m3": 4, "nvfp4": 8}.get(kv_dtype, 0)
-        pools.append(p)
-        ptrs.append((src.data_ptr(), src.stride(0) if T > 1 else kv_heads * DIM))
-    rc = lib().idx_store_kv(ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1],
-                            _want(slot_mapping, "slot_mapping", torch.int64), T, kv_heads,
-                            ctypes.byref(pools[0]), None if pools[1] is None else ctypes.byref(pools[1]),
-                            _stream_ptr(stream))
-    _check(rc, "idx_store_kv")
+    if k_src is None or k_payload is None or (v_src is None) != (v_payload is None):
+        raise IdxError("a source and its payload plane come together, and the keys always")
+    T = slot_mapping.numel()
+    k_ptr, k_stride = _source(k_src, "k_src", T, kv_heads)
+    k_pool = _plane_struct(k_payload, k_scale, "k", kv_dtype)
+    v_ptr, v_stride, v_pool = None, 0, None
+    if v_src is not None:
+        v_ptr, v_stride = _source(v_src, "v_src", T, kv_heads)
+        v_pool = ctypes.byref(_plane_struct(v_payload, v_scale, "v", kv_dtype))
+    rc = lib().idx_store_kv(k_ptr, v_ptr, k_stride, v_stride,
+                            _want(slot_mapping, "slot_mapping", torch.int64, (T,)), T, kv_heads,
+                            ctypes.byref(k_pool), v_pool, _stream_of(k_src, stream))
+    if rc:
+        _check(rc, "idx_store_kv")
 
 
 def idx_attn_workspace_bytes(packed_queries: int, q_heads: int, kv_heads: int, lists: int = 0) -> int:
@@ -412,33 +439,23 @@ def alloc_attn_workspace(packed_queries: int, q_heads: int, kv_heads: int, lists
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _attn(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, slot_ids, row_lens,
-          blocks, lists, kv_heads, sm_scale, out, out_lse, workspace, stream):
-    name = "idx_attn_paged" if blocks is None else "idx_attn_blocks"
+def _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, slot_ids,
+               row_lens, kv_heads):
+    """The arguments the two attention calls begin with, and R, P, q_heads."""
     if q.dim() != 4 or q.shape[3] != DIM:
         raise IdxError(f"q must be [requests, draft rows, q_heads, {DIM}]")
-    R, P, Hq = q.shape[:3]
+    R, P, Hq, _ = q.shape
     kp, ks, k_pages = _plane(k_payload, k_scale, "k", kv_dtype)
     vp, vs, v_pages = _plane(v_payload, v_scale, "v", kv_dtype)
     if kv_heads < 1 or k_pages != v_pages or k_pages % kv_heads:
         raise IdxError("the planes must hold the same whole pages of kv_heads heads")
     if page_table.dim() != 2:
         raise IdxError("page_table must be [n_slots, max_pages]")
-    head = (_want(q, "q", torch.bfloat16), kp, ks, vp, vs, DTYPES[kv_dtype], k_pages // kv_heads,
-            kv_heads, _want(page_table, "page_table", torch.int32), page_table.shape[0],
-            page_table.shape[1], _want(slot_ids, "slot_ids", torch.int32, (R,)),
-            _want(row_lens, "row_lens", torch.int32, (R, P)))
-    if blocks is not None:
-        if lists < 1 or blocks.dim() != 3:
-            raise IdxError("block_ids must be [requests, draft rows * lists, topk] and lists >= 1")
-        topk = blocks.shape[2]
-        head += (_want(blocks, "block_ids", torch.int32, (R, P * lists, topk)), lists, topk)
-    rc = getattr(lib(), name)(
-        *head, R, P, Hq, sm_scale, _want(out, "out", torch.bfloat16, (R, P, Hq, DIM)),
-        None if out_lse is None else _want(out_lse, "out_lse", torch.float32, (R, P, Hq)),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream))
-    _check(rc, name)
+    n_slots, max_pages = page_table.shape
+    return (_want(q, "q", _BF16, q.shape), kp, ks, vp, vs, DTYPES[kv_dtype], k_pages // kv_heads,
+            kv_heads, _want(page_table, "page_table", _I32, page_table.shape), n_slots, max_pages,
+            _want(slot_ids, "slot_ids", _I32, (R,)),
+            _want(row_lens, "row_lens", _I32, (R, P))), R, P, Hq
 
 
 def idx_attn_paged(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, page_table, slot_ids,
@@ -447,8 +464,14 @@ def idx_attn_paged(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, pag
     """Attention of q [R, P, q_heads, 128] over the whole paged cache into out (and
     out_lse, fp32 [R, P, q_heads], or None).  Planes: [num_pages * kv_heads * 64,
     128] rows with head page p * kv_heads + h; scales (fp8_e4m3 only) fp32 [rows]."""
-    _attn(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, slot_ids, row_lens,
-          None, 0, kv_heads, sm_scale, out, out_lse, workspace, stream)
+    head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table,
+                                slot_ids, row_lens, kv_heads)
+    rc = lib().idx_attn_paged(*head, R, P, Hq, sm_scale, _want(out, "out", _BF16, q.shape),
+                              None if out_lse is None else _want(out_lse, "out_lse", _F32, (R, P, Hq)),
+                              _dev(workspace, "workspace"), workspace.nbytes,
+                              _stream_of(q, stream))
+    if rc:
+        _check(rc, "idx_attn_paged")
 
 
 def idx_attn_blocks(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, page_table, slot_ids,
@@ -456,10 +479,18 @@ def idx_attn_blocks(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, pa
                     workspace, stream=None) -> None:
     """idx_attn_paged over the 128-token blocks of block_ids [R, P * lists, topk]
     (idx_score_topk's out_ids with gqa = lists)."""
-    if block_ids is None:
-        raise IdxError("block_ids is required")
-    _attn(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, slot_ids, row_lens,
-          block_ids, lists, kv_heads, sm_scale, out, out_lse, workspace, stream)
+    if block_ids is None or block_ids.dim() != 3 or lists < 1:
+        raise IdxError("block_ids must be [requests, draft rows * lists, topk] and lists >= 1")
+    head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table,
+                                slot_ids, row_lens, kv_heads)
+    topk = block_ids.shape[2]
+    rc = lib().idx_attn_blocks(*head, _want(block_ids, "block_ids", _I32, (R, P * lists, topk)), lists,
+                               topk, R, P, Hq, sm_scale, _want(out, "out", _BF16, q.shape),
+                               None if out_lse is None else _want(out_lse, "out_lse", _F32, (R, P, Hq)),
+                               _dev(workspace, "workspace"), workspace.nbytes,
+                               _stream_of(q, stream))
+    if rc:
+        _check(rc, "idx_attn_blocks")
 
 
 def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_scale,
@@ -472,15 +503,15 @@ def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_sc
     T, n = x.shape
     xp, xs = _rows_2d(x, "x", T, n)
     rp, rs = (None, 0) if residual is None else _rows_2d(residual, "residual", T, n)
-    if out.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(out.shape) != (T, n):
+    if out.dtype is not torch.float8_e4m3fn and out.dtype is not torch.uint8 or out.shape != (T, n):
         raise IdxError(f"out must be float8_e4m3fn or uint8 [{T}, {n}]")
     groups = -(-n // group) if group > 0 else 1
-    if out_scale.dtype != torch.float32 or out_scale.numel() != T * groups:
+    if out_scale.dtype is not _F32 or out_scale.numel() != T * groups:
         raise IdxError(f"out_scale must be float32 [{T}, {groups}]")
-    if out_residual is not None:
-        _want(out_residual, "out_residual", torch.bfloat16, (T, n))
-    rc = lib().idx_add_rmsnorm_fp8(xp, xs, rp, rs, _want(weight, "weight", torch.bfloat16, (n,)), T,
-                                   n, group, eps, _dev(out, "out"), _dev(out_scale, "out_scale"),
-                                   _dev(out_residual, "out_residual", required=False),
-                                   _stream_ptr(stream))
-    _check(rc, "idx_add_rmsnorm_fp8")
+    rc = lib().idx_add_rmsnorm_fp8(
+        xp, xs, rp, rs, _want(weight, "weight", _BF16, (n,)), T, n, group, eps, _dev(out, "out"),
+        _dev(out_scale, "out_scale"),
+        None if out_residual is None else _want(out_residual, "out_residual", _BF16, (T, n)),
+        _stream_of(x, stream))
+    if rc:
+        _check(rc, "idx_add_rmsnorm_fp8")
