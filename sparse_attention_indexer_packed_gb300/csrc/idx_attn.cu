@@ -52,27 +52,30 @@ template <>
 struct ACfg<kBf16> {
   static constexpr int kRowBytes = 256;
   static constexpr int kWarps = 8;
+  static constexpr int kDepth = 1;
 };
 template <>
 struct ACfg<kFp8> {
   static constexpr int kRowBytes = 128;
-  static constexpr int kWarps = 10;
+  static constexpr int kWarps = 8;
+  static constexpr int kDepth = 2;
 };
 
 template <int KF>
 struct ALayout {
   static constexpr int NW = ACfg<KF>::kWarps;
+  static constexpr int D = ACfg<KF>::kDepth;       // stages of a warp
   static constexpr int kThreads = 32 * NW;
   static constexpr int kTileBytes = kItem * ACfg<KF>::kRowBytes;  // keys or values of a piece
   static constexpr int kStage = 2 * kTileBytes;
   static constexpr int kScaleBytes = KF == kFp8 ? 2 * kItem * 4 : 0;
-  static constexpr int kScaleOff = NW * kStage;
-  static constexpr int kMergeOff = kScaleOff + NW * kScaleBytes;
-  static constexpr int kMlOff = kMergeOff + NW * kTile * kMergeStride * 4;
-  static constexpr int kBarOff = kMlOff + NW * kTile * 8;
-  static constexpr int kCtlOff = kBarOff + (NW + 1) * 8;
-  static constexpr int kPreOff = (kCtlOff + 32 + 15) & ~15;
-  static constexpr int kListOff = kPreOff + (kMaxGroups + 4) * 4;
+  static constexpr int kScaleOff = NW * D * kStage;
+  static constexpr int kMergeOff = kScaleOff + NW * D * kScaleBytes;
+  static constexpr int kMlOff = kMergeOff + NW / 2 * kTile * kMergeStride * 4;
+  static constexpr int kBarOff = kMlOff + NW / 2 * kTile * 8;
+  static constexpr int kCtlOff = kBarOff + (NW * D + 1) * 8;       // flags, count, one int a warp
+  static constexpr int kPreOff = (kCtlOff + 8 + NW * 4 + 15) & ~15;
+  static constexpr int kListOff = kPreOff + kRequestsBytes;
   static constexpr int kBytes = kListOff + kMaxList * 4;
   // the block bits are only held while a list is joined: in the merge area,
   // which is free between two units
@@ -92,10 +95,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, u
 // The 16 query rows in A-fragment order.
 //  bf16: a[ks] = {row g: d 16ks+2t,+1; row g+8: same; row g: +8,+9; row g+8: +8,+9}
 //  e4m3 keys: the queries as f16, scaled a row by the power of two that brings
-//  the row's largest magnitude into [2^14, 2^15) (exact for every element within
-//  2^24 of it, undone by post): e4m3 values are exact in f16, so each product is
+//  the row's largest magnitude into [2^7, 2^8) (exact for every element within
+//  2^21 of it, undone by post): e4m3 values are exact in f16, so each product is
 //  exact.  k order: step c takes d = 16c + 4t + {0,1} and + {2,3}, the order in
-//  which a lane's four bytes of an ldmatrix'ed key arrive.
+//  which a lane's four bytes of an ldmatrix'ed key arrive.  (Two e4m3 query terms
+//  on m16n8k32 would spare the keys' conversion; measured on the 16 x 131K decode
+//  134 us against 113: the warp-level e4m3 product is the slower one here.)
 template <int KF>
 struct QRows {
   uint32_t a[8][4];
@@ -113,33 +118,32 @@ struct QRows {
       }
       post0 = post1 = scale_log2;
     } else {
-      load_f16(r0, 0, post0, t);
-      load_f16(r1, 1, post1, t);
-      post0 *= scale_log2;
-      post1 *= scale_log2;
+      uint2 u[2][8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        u[0][c] = r0 ? __ldg(reinterpret_cast<const uint2*>(r0 + 16 * c + 4 * t)) : make_uint2(0, 0);
+        u[1][c] = r1 ? __ldg(reinterpret_cast<const uint2*>(r1 + 16 * c + 4 * t)) : make_uint2(0, 0);
+      }
+      post0 = scale_log2 * to_f16(u[0], 0);
+      post1 = scale_log2 * to_f16(u[1], 1);
     }
   }
-  __device__ void load_f16(const uint16_t* row, int half, float& post, int t) {
-    uint2 u[8];
+  __device__ float to_f16(const uint2 (&u)[8], int half) {
     float amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      u[c] = row ? __ldg(reinterpret_cast<const uint2*>(row + 16 * c + 4 * t)) : make_uint2(0, 0);
+    for (int c = 0; c < 8; ++c)
       amax = fmaxf(fmaxf(amax, fmaxf(fabsf(bf16_lo(u[c].x)), fabsf(bf16_hi(u[c].x)))),
                    fmaxf(fabsf(bf16_lo(u[c].y)), fabsf(bf16_hi(u[c].y))));
-    }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    int e = 0;
-    if (amax > 0.f) e = 14 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
-    e = max(-100, min(100, e));
+    const int e = to_2_7(amax);
     const float up = ldexpf(1.f, e);
-    post = ldexpf(1.f, -e);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       a[c][half] = pack_f16(bf16_lo(u[c].x) * up, bf16_hi(u[c].x) * up);
       a[c][2 + half] = pack_f16(bf16_lo(u[c].y) * up, bf16_hi(u[c].y) * up);
     }
+    return ldexpf(1.f, -e);
   }
 };
 
@@ -159,12 +163,6 @@ struct State {
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
 };
-
-// The smallest power of two above x (x finite, >= 0; at least 2^-100).
-__device__ __forceinline__ float pow2_above(float x) {
-  const int e = max(27, (int)(__float_as_uint(x) >> 23));
-  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
-}
 
 // One 32-token piece.  kMask: some token of the piece lies outside some row
 // (len0, len1: the rows' visible lengths, 0 for a row that does not list the
@@ -330,17 +328,17 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
         mma_bf16_16816(st.o[2 * j], plo, v0, v1);
         mma_bf16_16816(st.o[2 * j + 1], plo, v2, v3);
       } else {
-        // a register holds two dims (even, odd) of two tokens: split into the
-        // even and the odd dims' operand
-        uint32_t a0, a1, b0, b1;
-        e4m3x4_to_f16x2x2(v0, a0, a1);
-        e4m3x4_to_f16x2x2(v1, b0, b1);
-        mma_f16_16816(st.o[4 * j], p, prmt(a0, a1, 0x5410), prmt(b0, b1, 0x5410));
-        mma_f16_16816(st.o[4 * j + 1], p, prmt(a0, a1, 0x7632), prmt(b0, b1, 0x7632));
-        e4m3x4_to_f16x2x2(v2, a0, a1);
-        e4m3x4_to_f16x2x2(v3, b0, b1);
-        mma_f16_16816(st.o[4 * j + 2], p, prmt(a0, a1, 0x5410), prmt(b0, b1, 0x5410));
-        mma_f16_16816(st.o[4 * j + 3], p, prmt(a0, a1, 0x7632), prmt(b0, b1, 0x7632));
+        // a register holds two dims (even, odd) of two tokens: the even dims'
+        // bytes first, then the odd ones', each pair one operand register
+        uint32_t e0, o0, e1, o1;
+        e4m3x4_to_f16x2x2(prmt(v0, 0u, 0x3120), e0, o0);
+        e4m3x4_to_f16x2x2(prmt(v1, 0u, 0x3120), e1, o1);
+        mma_f16_16816(st.o[4 * j], p, e0, e1);
+        mma_f16_16816(st.o[4 * j + 1], p, o0, o1);
+        e4m3x4_to_f16x2x2(prmt(v2, 0u, 0x3120), e0, o0);
+        e4m3x4_to_f16x2x2(prmt(v3, 0u, 0x3120), e1, o1);
+        mma_f16_16816(st.o[4 * j + 2], p, e0, e1);
+        mma_f16_16816(st.o[4 * j + 3], p, o0, o1);
       }
     }
   }
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
-  int* pre = reinterpret_cast<int*>(smem + L::kPreOff);
+  const Requests rq = requests_at(smem + L::kPreOff);
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
   float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
@@ -366,8 +364,8 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   if (lane == 0) {
-    mbar_init(sbase + L::kBarOff + warp * 8, 1);
-    if (warp == 0) mbar_init(sbase + L::kBarOff + NW * 8, 1);  // the stall test's barrier
+    for (int d = 0; d < L::D; ++d) mbar_init(sbase + L::kBarOff + (warp * L::D + d) * 8, 1);
+    if (warp == 0) mbar_init(sbase + L::kBarOff + NW * L::D * 8, 1);  // the stall test's barrier
     fence_barrier_init();
   }
   if (threadIdx.x == 0) {
@@ -377,11 +375,10 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == 0) build_prefix<kItem, kBlocks>(a, pre, cta_flags, lane);
-  __syncthreads();
+  build_requests<kItem, kBlocks>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
 
   const int per = a.heads * a.groups;
-  const long long W = (long long)pre[a.R] * per;
+  const long long W = (long long)rq.pre[a.R] * per;
   // no CTA takes less than about one piece a warp
   const long long want = (W + NW - 1) / NW;
   const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
@@ -390,25 +387,28 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   SplitRecord record = {-1, 0};
 
   // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
+  // The page id is loaded here and looked at when the copy is issued, a piece
+  // later, so nothing waits for it.
   struct Next {
     int unit;      // -1: nothing left
     int tb;
     uint32_t members;
-    int row;
+    int page, kv_head;
   };
-  long long fpos = begin;
+  Walk walk, fwalk;
+  walk.begin(rq.pre, a.R, a.heads, a.groups, begin, end);
+  fwalk = walk;
   Items fit = {};
   int funit = -1, fi = 0;
-  fit.i1 = 0;
   bool dead = false;
   auto feed = [&]() -> Next {
-    Next n = {-1, 0, 0u, 0};
+    Next n = {-1, 0, 0u, 0, 0};
     while (!dead) {
       if (fi >= fit.i1) {
-        if (kBlocks || fpos >= end) break;
-        const Segment s = next_segment(pre, a.R, a.heads, a.groups, fpos, end);
+        if (kBlocks || !fwalk.more()) break;
+        const Segment s = fwalk.next(rq.pre, a.R, a.heads, a.groups);
         if (!s.live) continue;
-        fit = make_items<kBlocks>(a, s, 0);
+        fit = make_items<kBlocks>(a, rq, s, 0);
         funit = s.unit;
         fi = fit.i0 + warp;
         continue;
@@ -416,127 +416,148 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       const int i = fi;
       fi += NW;
       if (!item_tokens<kItem, kBlocks>(fit, list, i, n.tb, n.members)) continue;
-      const long long row = item_row(a, fit, n.tb);
-      if (row < 0) {
-        if (lane == 0) atomicOr(cta_flags, kErrBadPage);
-        continue;
-      }
-      n.row = (int)row;
+      n.page = __ldg(a.page_table + (size_t)fit.slot * a.max_pages + n.tb / kPage);
+      n.kv_head = fit.kv_head;
       n.unit = funit;
       break;
     }
     return n;
   };
-  const uint32_t stage = sbase + warp * L::kStage;
-  const uint32_t bar = sbase + L::kBarOff + warp * 8;
-  const float* scales = reinterpret_cast<const float*>(smem + L::kScaleOff + warp * L::kScaleBytes);
-  auto issue = [&](const Next& n) {
+  // The warp's D stages are used in turn: its k-th piece lies in stage k % D.
+  constexpr int D = L::D;
+  auto stage_of = [&](int k) { return sbase + (warp * D + k % D) * L::kStage; };
+  auto scales_of = [&](int k) { return L::kScaleOff + (warp * D + k % D) * L::kScaleBytes; };
+  auto bar_of = [&](int k) { return sbase + L::kBarOff + (warp * D + k % D) * 8; };
+  const Next none = {-1, 0, 0u, 0, 0};
+  Next fl[D], nxt = none;     // pieces in flight, oldest first; the one after them
+#pragma unroll
+  for (int d = 0; d < D; ++d) fl[d] = none;
+  int issued = 0;
+  // ask for the copies of the next piece whose page exists
+  auto fetch = [&]() -> Next {
+    Next n = nxt;
+    while (n.unit >= 0 && (n.page < 0 || n.page >= a.num_pages)) {
+      if (lane == 0) atomicOr(cta_flags, kErrBadPage);
+      n = feed();
+    }
+    if (n.unit < 0) return nxt = n;
     if (lane == 0) {
+      const int row = (n.page * a.kv_heads + n.kv_head) * kPage + n.tb % kPage;
+      const uint32_t stage = stage_of(issued), bar = bar_of(issued);
       mbar_arrive_expect_tx(bar, L::kStage + L::kScaleBytes);
       if (KF == kBf16) {
-        tma_load_2d(stage, &k_map, 0, n.row, bar);
-        tma_load_2d(stage + L::kTileBytes / 2, &k_map, 64, n.row, bar);
-        tma_load_2d(stage + L::kTileBytes, &v_map, 0, n.row, bar);
-        tma_load_2d(stage + L::kTileBytes + L::kTileBytes / 2, &v_map, 64, n.row, bar);
+        tma_load_2d(stage, &k_map, 0, row, bar);
+        tma_load_2d(stage + L::kTileBytes / 2, &k_map, 64, row, bar);
+        tma_load_2d(stage + L::kTileBytes, &v_map, 0, row, bar);
+        tma_load_2d(stage + L::kTileBytes + L::kTileBytes / 2, &v_map, 64, row, bar);
       } else {
-        const uint32_t sc = sbase + L::kScaleOff + warp * L::kScaleBytes;
-        tma_load_2d(stage, &k_map, 0, n.row, bar);
-        bulk_load(sc, a.k_scale + n.row, kItem * 4, bar);
-        tma_load_2d(stage + L::kTileBytes, &v_map, 0, n.row, bar);
-        bulk_load(sc + kItem * 4, a.v_scale + n.row, kItem * 4, bar);
+        const uint32_t sc = sbase + scales_of(issued);
+        tma_load_2d(stage, &k_map, 0, row, bar);
+        bulk_load(sc, a.k_scale + row, kItem * 4, bar);
+        tma_load_2d(stage + L::kTileBytes, &v_map, 0, row, bar);
+        bulk_load(sc + kItem * 4, a.v_scale + row, kItem * 4, bar);
       }
     }
+    ++issued;
+    nxt = feed();
+    return n;
   };
 
-  Next cur = {-1, 0, 0u, 0}, nxt = {-1, 0, 0u, 0};
   int used = 0;           // pieces this warp has waited for
   bool primed = false;
-  long long pos = begin;
-  while (pos < end) {
-    const Segment s = next_segment(pre, a.R, a.heads, a.groups, pos, end);
+  while (walk.more()) {
+    const Segment s = walk.next(rq.pre, a.R, a.heads, a.groups);
     if (!s.live) continue;
     const int row_first = s.group * kTile;
     const int nrows = min(kTile, a.P * a.nq - row_first);
     const int p0 = row_first / a.nq;
     int n_items = 0;
     if (kBlocks) {
-      n_items = join_lists(a, s, p0, (row_first + nrows - 1) / a.nq, list, bits, cta_flags + 1) *
+      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits, cta_flags + 1) *
                 (kBlock / kItem);
-      fit = make_items<kBlocks>(a, s, n_items);
+      fit = make_items<kBlocks>(a, rq, s, n_items);
       funit = s.unit;
       fi = fit.i0 + warp;
       primed = false;
     }
     if (!primed) {
       primed = true;
-      cur = feed();
-      if (cur.unit >= 0) {
-        issue(cur);
-        nxt = feed();
-      }
+      nxt = feed();
+#pragma unroll
+      for (int d = 0; d < D; ++d) fl[d] = fetch();
     }
-    const Items it = kBlocks ? fit : make_items<kBlocks>(a, s, 0);
+    const Items it = kBlocks ? fit : make_items<kBlocks>(a, rq, s, 0);
     // ---- the unit's rows ----------------------------------------------------
-    const bool pad = it.slot < 0 || it.slot >= a.n_slots;
-    auto q_index = [&](int i) {
-      const int pk = row_first + i, p = pk / a.nq;
+    auto q_index = [&](int pk, int p) {   // packed row pk of the unit head, draft row p = pk / nq
       return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
     };
-    auto len_of = [&](int i) { return i < nrows && !pad ? row_len(a, s.r, (row_first + i) / a.nq) : 0; };
-    const int L0 = len_of(g), L1 = len_of(g + 8);
-    const int d0 = (row_first + min(g, nrows - 1)) / a.nq - p0;
-    const int d1 = (row_first + min(g + 8, nrows - 1)) / a.nq - p0;
+    const int pk0 = row_first + g, pd0 = pk0 / a.nq, pk1 = pk0 + 8, pd1 = pk1 / a.nq;
+    const bool has0 = g < nrows, has1 = g + 8 < nrows;
+    const int L0 = has0 && it.glen > 0 ? row_len(a, s.r, pd0) : 0;
+    const int L1 = has1 && it.glen > 0 ? row_len(a, s.r, pd1) : 0;
     QRows<KF> q;
-    q.load(g < nrows ? a.q + q_index(g) * kDim : nullptr,
-           g + 8 < nrows ? a.q + q_index(g + 8) * kDim : nullptr, a.scale_log2, lane);
+    q.load(has0 ? a.q + q_index(pk0, pd0) * kDim : nullptr,
+           has1 ? a.q + q_index(pk1, pd1) * kDim : nullptr, a.scale_log2, lane);
     State st;
     st.reset();
     // ---- its pieces -----------------------------------------------------------
-    while (cur.unit == s.unit) {
+    while (fl[0].unit == s.unit) {
+      const Next cur = fl[0];
       const bool stall = a.stall_test && warp == 0 && used == 0;
-      if (!mbar_wait_bounded(stall ? sbase + L::kBarOff + NW * 8 : bar,
-                             stall ? 0u : (uint32_t)(used & 1), a.wait_ns)) {
+      if (!mbar_wait_bounded(stall ? sbase + L::kBarOff + NW * D * 8 : bar_of(used),
+                             stall ? 0u : (uint32_t)((used / D) & 1), a.wait_ns)) {
         if (lane == 0) atomicOr(cta_flags, kErrTimeout);
         dead = true;
-        break;
       }
-      ++used;
-      __syncwarp();
-      const int e0 = (cur.members >> d0) & 1u ? L0 : 0, e1 = (cur.members >> d1) & 1u ? L1 : 0;
-      const bool whole = __all_sync(0xffffffffu, (g >= nrows || cur.tb + kItem <= e0) &&
-                                                     (g + 8 >= nrows || cur.tb + kItem <= e1));
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      const int e0 = has0 && (cur.members >> (pd0 - p0)) & 1u ? L0 : 0;
+      const int e1 = has1 && (cur.members >> (pd1 - p0)) & 1u ? L1 : 0;
+      const bool whole = __all_sync(0xffffffffu, (!has0 || cur.tb + kItem <= e0) &&
+                                                     (!has1 || cur.tb + kItem <= e1));
+      const uint32_t stage = stage_of(used);
+      const float* scales = reinterpret_cast<const float*>(smem + scales_of(used));
       if (whole)
         piece<KF, false>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
       else
         piece<KF, true>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
+      ++used;
       // every lane's reads of the stage come before the copies that refill it
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      cur = nxt;
-      if (cur.unit >= 0) {
-        issue(cur);
-        nxt = feed();
-      }
+#pragma unroll
+      for (int d = 0; d + 1 < D; ++d) fl[d] = fl[d + 1];
+      fl[D - 1] = fetch();
     }
     if (dead) {
       // let the copies in flight land, take no more
-      if (cur.unit >= 0 && lane == 0) (void)mbar_wait_bounded(bar, (uint32_t)(used & 1), 200000000ull);
-      cur.unit = nxt.unit = -1;
-    }
-    // ---- join the warps ---------------------------------------------------------
-    {
-      float l0 = st.l0, l1 = st.l1;
+      for (; used < issued; ++used)
+        if (lane == 0) (void)mbar_wait_bounded(bar_of(used), (uint32_t)((used / D) & 1), 200000000ull);
 #pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-      }
+      for (int d = 0; d < D; ++d) fl[d] = none;
+      nxt = none;
+    }
+    // ---- join the warps: the upper half into the lower, then those by rows -----
+    constexpr int NH = NW / 2;
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
+      st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
+    }
+    if (KF == kFp8) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        st.o[j][0] *= st.mv, st.o[j][1] *= st.mv, st.o[j][2] *= st.mv, st.o[j][3] *= st.mv;
+    }
+    const int place = warp < NH ? warp : warp - NH;
+    float* w0 = merge + (size_t)(place * kTile + g) * kMergeStride;
+    float* w1 = w0 + 8 * kMergeStride;
+    float2* ml0 = ml + place * kTile + g;
+    auto put = [&]() {
       if (t == 0) {
-        ml[warp * kTile + g] = make_float2(st.m0, l0);
-        ml[warp * kTile + g + 8] = make_float2(st.m1, l1);
+        ml0[0] = make_float2(st.m0, st.l0);
+        ml0[8] = make_float2(st.m1, st.l1);
       }
-      float* w0 = merge + (size_t)(warp * kTile + g) * kMergeStride;
-      float* w1 = w0 + 8 * kMergeStride;
       if (KF == kBf16) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -544,15 +565,61 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
           *reinterpret_cast<float2*>(w1 + 8 * j + 2 * t) = make_float2(st.o[j][2], st.o[j][3]);
         }
       } else {
-        const float f = st.mv;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const float* e = st.o[2 * ch];
           const float* d = st.o[2 * ch + 1];
-          *reinterpret_cast<float4*>(w0 + 16 * ch + 4 * t) = make_float4(e[0] * f, d[0] * f, e[1] * f, d[1] * f);
-          *reinterpret_cast<float4*>(w1 + 16 * ch + 4 * t) = make_float4(e[2] * f, d[2] * f, e[3] * f, d[3] * f);
+          *reinterpret_cast<float4*>(w0 + 16 * ch + 4 * t) = make_float4(e[0], d[0], e[1], d[1]);
+          *reinterpret_cast<float4*>(w1 + 16 * ch + 4 * t) = make_float4(e[2], d[2], e[3], d[3]);
         }
       }
+    };
+    if (warp >= NH) put();
+    __syncthreads();
+    if (warp < NH) {
+      const float2 x0 = ml0[0], x1 = ml0[8];
+      const float n0 = fmaxf(st.m0, x0.x), n1 = fmaxf(st.m1, x1.x);
+      const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+      // a half with nothing visible in the row holds zeros (or 0 * NaN: dropped)
+      const bool has_a0 = st.m0 != -INFINITY, has_a1 = st.m1 != -INFINITY;
+      const bool has_b0 = x0.x != -INFINITY, has_b1 = x1.x != -INFINITY;
+      const float a0 = ex2_approx(st.m0 - r0), a1 = ex2_approx(st.m1 - r1);
+      const float b0 = ex2_approx(x0.x - r0), b1 = ex2_approx(x1.x - r1);
+      st.l0 = (has_a0 ? st.l0 * a0 : 0.f) + (has_b0 ? x0.y * b0 : 0.f);
+      st.l1 = (has_a1 ? st.l1 * a1 : 0.f) + (has_b1 ? x1.y * b1 : 0.f);
+      st.m0 = n0, st.m1 = n1;
+      auto fold = [](bool ha, float a, float fa, bool hb, float b, float fb) {
+        return (ha ? a * fa : 0.f) + (hb ? b * fb : 0.f);
+      };
+      if (KF == kBf16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 y0 = *reinterpret_cast<const float2*>(w0 + 8 * j + 2 * t);
+          const float2 y1 = *reinterpret_cast<const float2*>(w1 + 8 * j + 2 * t);
+          st.o[j][0] = fold(has_a0, st.o[j][0], a0, has_b0, y0.x, b0);
+          st.o[j][1] = fold(has_a0, st.o[j][1], a0, has_b0, y0.y, b0);
+          st.o[j][2] = fold(has_a1, st.o[j][2], a1, has_b1, y1.x, b1);
+          st.o[j][3] = fold(has_a1, st.o[j][3], a1, has_b1, y1.y, b1);
+        }
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const float4 y0 = *reinterpret_cast<const float4*>(w0 + 16 * ch + 4 * t);
+          const float4 y1 = *reinterpret_cast<const float4*>(w1 + 16 * ch + 4 * t);
+          float* e = st.o[2 * ch];
+          float* d = st.o[2 * ch + 1];
+          e[0] = fold(has_a0, e[0], a0, has_b0, y0.x, b0);
+          d[0] = fold(has_a0, d[0], a0, has_b0, y0.y, b0);
+          e[1] = fold(has_a0, e[1], a0, has_b0, y0.z, b0);
+          d[1] = fold(has_a0, d[1], a0, has_b0, y0.w, b0);
+          e[2] = fold(has_a1, e[2], a1, has_b1, y1.x, b1);
+          d[2] = fold(has_a1, d[2], a1, has_b1, y1.y, b1);
+          e[3] = fold(has_a1, e[3], a1, has_b1, y1.z, b1);
+          d[3] = fold(has_a1, d[3], a1, has_b1, y1.w, b1);
+        }
+      }
+      __syncwarp();
+      put();
     }
     __syncthreads();
     const bool complete = s.o0 == 0 && s.o1 == s.cap;
@@ -562,13 +629,14 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
     }
     for (int i = warp; i < nrows; i += NW) {
+      const int pk = row_first + i, p = pk / a.nq;
       float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) m = fmaxf(m, ml[w * kTile + i].x);
+      for (int w = 0; w < NH; ++w) m = fmaxf(m, ml[w * kTile + i].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
+        for (int w = 0; w < NH; ++w) {
           const float2 x = ml[w * kTile + i];
           const float f = ex2_approx(x.x - m);
           if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
@@ -578,10 +646,10 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
         }
       }
       if (__any_sync(0xffffffffu, !finite4(o)))
-        careful_row<KF, kItem, kBlocks>(a, it, list, a.q + q_index(i) * kDim, len_of(i),
-                                 (row_first + i) / a.nq - p0, lane, m, l, o);
+        careful_row<KF, kItem, kBlocks>(a, it, list, a.q + q_index(pk, p) * kDim,
+                                        it.glen > 0 ? row_len(a, s.r, p) : 0, p - p0, lane, m, l, o);
       if (complete) {
-        write_row(a, q_index(i), m, l, o, lane);
+        write_row(a, q_index(pk, p), m, l, o, lane);
       } else {
         const size_t at = (size_t)slot_out * kTile + i;
         if (lane == 0) a.part_ml[at] = make_float2(m, l);
@@ -600,12 +668,15 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // The join of units that several CTAs shared.  Block (c, i): row i of the unit
 // that CTA c started and did not end.  Its parts are CTA c's second slot and the
-// first slots of the CTAs behind it, added in that order in each of four warps'
-// shares, so the result does not depend on timing.
+// first slots of the CTAs behind it; their maxima and sums are read at once, one
+// a thread, then four warps add the outputs, each its share in a fixed order, so
+// the result does not depend on timing.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
-  __shared__ float2 sml[4];
-  __shared__ float so[4][kDim];
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+  __shared__ float factor[kMaxCtas];
+  __shared__ float red[2][4];
+  __shared__ float4 so[4][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = min(a.group_rows, a.P * a.nq);
   const int c = blockIdx.x / rows, i = blockIdx.x - c * rows;
@@ -616,31 +687,51 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int head = k / a.groups, pk = (k - head * a.groups) * a.group_rows + i;
   if (pk >= a.P * a.nq) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = warp; s < rec.splits; s += 4) {
-    const size_t at = (size_t)slot(s) * a.group_rows + i;
-    const float2 x = a.part_ml[at];
-    if (x.x == -INFINITY) continue;
-    const float4 v = reinterpret_cast<const float4*>(a.part_o + at * kDim)[lane];
-    const float mn = fmaxf(m, x.x), f = ex2_approx(m - mn), h = ex2_approx(x.x - mn);
-    l = fmaf(l, f, x.y * h);
-    o = make_float4(fmaf(o.x, f, v.x * h), fmaf(o.y, f, v.y * h), fmaf(o.z, f, v.z * h), fmaf(o.w, f, v.w * h));
-    m = mn;
+  auto part = [&](int s) { return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i; };
+  constexpr int kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+  float2 x[kPer];
+  float m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int s = threadIdx.x + e * kJoinThreads;
+    x[e] = s < rec.splits ? a.part_ml[part(s)] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, x[e].x);
   }
-  if (lane == 0) sml[warp] = make_float2(m, l);
-  reinterpret_cast<float4*>(so[warp])[lane] = o;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int s = threadIdx.x + e * kJoinThreads;
+    // a part with nothing visible in the row is not read: factor -1 says so
+    const float f = x[e].x == -INFINITY ? -1.f : ex2_approx(x[e].x - m);
+    if (s < rec.splits) {
+      factor[s] = f;
+      if (f >= 0.f || f != f) l = fmaf(x[e].y, f, l);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = warp; s < rec.splits; s += 4) {
+    const float f = factor[s];
+    if (f == -1.f) continue;
+    const float4 v = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[lane];
+    o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+  }
+  so[warp][lane] = o;
   __syncthreads();
   if (warp) return;
   for (int w = 1; w < 4; ++w) {
-    const float2 x = sml[w];
-    if (x.x == -INFINITY) continue;
-    const float4 v = reinterpret_cast<const float4*>(so[w])[lane];
-    const float mn = fmaxf(m, x.x), f = ex2_approx(m - mn), h = ex2_approx(x.x - mn);
-    l = fmaf(l, f, x.y * h);
-    o = make_float4(fmaf(o.x, f, v.x * h), fmaf(o.y, f, v.y * h), fmaf(o.z, f, v.z * h), fmaf(o.w, f, v.w * h));
-    m = mn;
+    const float4 v = so[w][lane];
+    o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
   }
   const int p = pk / a.nq;
   write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, lane);
@@ -690,7 +781,7 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(attn_join_kernel, ctas * (a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows), 128, 0, stream, a);
+  cudaError_t e = launch_pdl(attn_join_kernel, ctas * (a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows), kJoinThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

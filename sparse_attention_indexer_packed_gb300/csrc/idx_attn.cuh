@@ -108,29 +108,57 @@ __device__ __forceinline__ int find_request(const int* pre, int R, int x) {
   return lo;
 }
 
-// The stretch that begins at `pos`; pos moves behind it.
-__device__ __forceinline__ Segment next_segment(const int* pre, int R, int heads, int groups,
-                                                long long& pos, long long end) {
-  Segment s;
-  const int per = heads * groups;
-  s.r = find_request(pre, R, (int)(pos / per));
-  const int wt = pre[s.r + 1] - pre[s.r];
-  const long long base = (long long)pre[s.r] * per;
-  const int k = (int)((pos - base) / wt);
-  const int o = (int)(pos - base - (long long)k * wt);
-  s.head = k / groups;
-  s.group = k - s.head * groups;
-  s.unit = s.r * per + k;
-  s.start = pos - o;
-  s.cap = wt - kUnitCost;
-  const long long left = end - pos;
-  const int take = left < wt - o ? (int)left : wt - o;
-  s.o0 = o < s.cap ? o : s.cap;
-  s.o1 = o + take < s.cap ? o + take : s.cap;
-  s.live = s.o1 > s.o0 || (s.cap == 0 && o == 0);
-  pos += take;
-  return s;
-}
+// A walk over the stretches of [pos, end), unit by unit: one search at its
+// start, no division after it.
+struct Walk {
+  long long pos, end, start;   // start: the current unit's first position
+  int r, head, group, unit, wt;
+
+  __device__ __forceinline__ void begin(const int* pre, int R, int heads, int groups,
+                                        long long first, long long last) {
+    pos = first;
+    end = last;
+    if (pos >= end) return;
+    const int per = heads * groups;
+    r = find_request(pre, R, (int)(pos / per));
+    wt = pre[r + 1] - pre[r];
+    const long long base = (long long)pre[r] * per;
+    const int k = (int)((pos - base) / wt);
+    start = base + (long long)k * wt;
+    head = k / groups;
+    group = k - head * groups;
+    unit = r * per + k;
+  }
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  __device__ __forceinline__ Segment next(const int* pre, int R, int heads, int groups) {
+    Segment s;
+    s.unit = unit;
+    s.r = r;
+    s.head = head;
+    s.group = group;
+    s.start = start;
+    s.cap = wt - kUnitCost;
+    const int o = (int)(pos - start);
+    const long long left = end - pos;
+    const int take = left < wt - o ? (int)left : wt - o;
+    s.o0 = o < s.cap ? o : s.cap;
+    s.o1 = o + take < s.cap ? o + take : s.cap;
+    s.live = s.o1 > s.o0 || (s.cap == 0 && o == 0);
+    pos += take;
+    if (o + take == wt) {
+      start += wt;
+      ++unit;
+      if (++group == groups) {
+        group = 0;
+        if (++head == heads) {
+          head = 0;
+          if (++r < R) wt = pre[r + 1] - pre[r];
+        }
+      }
+    }
+    return s;
+  }
+};
 
 // The CTA that holds position x.
 __device__ __forceinline__ int owner(long long x, long long W, int C) {

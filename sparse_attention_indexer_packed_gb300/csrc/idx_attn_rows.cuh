@@ -26,39 +26,86 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Four e4m3 codes of four floats (round to nearest even, saturating), and what
+// they stand for taken off the floats.
+__device__ __forceinline__ uint32_t e4m3x4_take(float (&x)[4]) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h1, %4, %3;\n\t"
+      "mov.b32 %0, {h0, h1};\n\t}"
+      : "=r"(d)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2x2(d, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
+  return d;
+}
+
+// The exponent e that brings x * 2^e into [2^7, 2^8) (0 for zero), e in [-100, 100].
+__device__ __forceinline__ int to_2_7(float x) {
+  int e = 0;
+  if (x > 0.f) e = 7 - (((int)(__float_as_uint(x) >> 23) & 0xff) - 127);
+  return max(-100, min(100, e));
+}
+
+// The smallest power of two above x (x finite, >= 0; at least 2^-100).
+__device__ __forceinline__ float pow2_above(float x) {
+  const int e = max(27, (int)(__float_as_uint(x) >> 23));
+  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
+}
+
 // Length of draft row p of request r, inside [0, max_pages * 64].
 __device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {
   const int L = __ldg(a.row_lens + r * a.P + p), cap = a.max_pages * kPage;
   return L < 0 ? 0 : (L > cap ? cap : L);
 }
 
-// pre[r] = sum of the unit weights of the requests before r, pre[R] the total
-// (one warp).  flags gets IDX_DEVERR_LEN_CLAMPED from the first CTA.
+// The requests as the CTA needs them: pre[r] = sum of the unit weights of the
+// requests before r (pre[R]: the total), their slots and their longest rows (0
+// for a pad request).
+struct Requests {
+  int *pre, *slot, *len;
+};
+constexpr int kRequestsBytes = 3 * (kMaxGroups + 4) * 4;
+__device__ __forceinline__ Requests requests_at(uint8_t* smem) {
+  int* p = reinterpret_cast<int*>(smem);
+  return {p, p + (kMaxGroups + 4), p + 2 * (kMaxGroups + 4)};
+}
+
+// Fill the table (every thread of the CTA, one request a thread at a time; ends
+// with a barrier).  sums: one int a warp.  flags gets IDX_DEVERR_LEN_CLAMPED
+// from the first CTA.
 template <int IT, bool kBlocks>
-__device__ __forceinline__ void build_prefix(const AttnArgs& a, int* pre, unsigned int* flags,
-                                             int lane) {
+__device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests& q, int* sums,
+                                               unsigned int* flags) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nt = blockDim.x;
+  if (threadIdx.x == 0) *flags = 0u;
   int run = 0;
-  bool clamped = false;
-  for (int v0 = 0; v0 < a.R; v0 += 32) {
-    const int v = v0 + lane;
-    int wt = 0;
+  for (int v0 = 0; v0 < a.R; v0 += nt) {
+    const int v = v0 + threadIdx.x;
+    int wt = 0, n = 0;
+    bool clamped = false;
     if (v < a.R) {
-      const int slot = __ldg(a.slot_ids + v);
-      int n = 0;
-      if (slot >= 0 && slot < a.n_slots) {
-        for (int p = 0; p < a.P; ++p) {
-          n = max(n, row_len(a, v, p));
-          clamped |= __ldg(a.row_lens + v * a.P + p) > a.max_pages * kPage;
-        }
-      }
+      // every load goes out before any is used
+      const int slot = __ldg(a.slot_ids + v), cap = a.max_pages * kPage;
+      int most = 0;
+#pragma unroll 4
+      for (int p = 0; p < a.P; ++p) most = max(most, __ldg(a.row_lens + v * a.P + p));
+      const bool pad = slot < 0 || slot >= a.n_slots;
+      clamped = !pad && most > cap && blockIdx.x == 0;
+      n = pad ? 0 : min(most, cap);
+      q.slot[v] = slot;
+      q.len[v] = n;
       if (kBlocks) {
         // at most: every draft row of a group lists other blocks
         const int drafts = min(a.P, (a.group_rows + a.nq - 2) / a.nq + 1);
-        n = min((n + kBlock - 1) / kBlock, a.topk * drafts) * (kBlock / IT);
+        wt = min((n + kBlock - 1) / kBlock, a.topk * drafts) * (kBlock / IT) + kUnitCost;
       } else {
-        n = (n + IT - 1) / IT;
+        wt = (n + IT - 1) / IT + kUnitCost;
       }
-      wt = n + kUnitCost;
     }
     int incl = wt;
 #pragma unroll
@@ -66,14 +113,21 @@ __device__ __forceinline__ void build_prefix(const AttnArgs& a, int* pre, unsign
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (v < a.R) pre[v] = run + incl - wt;
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int before = run, total = run;
+    for (int w = 0; w < nt / 32; ++w) {
+      const int y = sums[w];
+      if (w < warp) before += y;
+      total += y;
+    }
+    if (v < a.R) q.pre[v] = before + incl - wt;
+    if (clamped) atomicOr(flags, kErrLenClamped);
+    run = total;
+    __syncthreads();   // sums is free again, and the table complete
   }
-  clamped = __any_sync(0xffffffffu, clamped);
-  if (lane == 0) {
-    pre[a.R] = run;
-    *flags = (clamped && blockIdx.x == 0) ? kErrLenClamped : 0u;
-  }
+  if (threadIdx.x == 0) q.pre[a.R] = run;
+  __syncthreads();
 }
 
 // The lists of draft rows p0 .. p1 (at most kMaxDrafts) of the segment's unit
@@ -81,15 +135,15 @@ __device__ __forceinline__ void build_prefix(const AttnArgs& a, int* pre, unsign
 // p - p0.  Every thread of the CTA; returns the number of blocks.  bits: 2 *
 // kMaxBlockWords words of scratch.  A set bit a block and a running count of them
 // give each entry its place, so a block listed twice takes one.
-__device__ __forceinline__ int join_lists(const AttnArgs& a, const Segment& s, int p0, int p1,
-                                          uint32_t* list, uint32_t* bits, unsigned int* count) {
+__device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq, const Segment& s,
+                                          int p0, int p1, uint32_t* list, uint32_t* bits,
+                                          unsigned int* count) {
   uint32_t* rank = bits + kMaxBlockWords;
   const int lane = threadIdx.x & 31, nt = blockDim.x;
   const int which = s.head * a.lists / a.heads;
-  const int slot = __ldg(a.slot_ids + s.r);
-  const bool pad = slot < 0 || slot >= a.n_slots;
-  const int words = (a.max_pages + 63) / 64;
-  const int entries = pad ? 0 : (p1 - p0 + 1) * a.topk;
+  const int longest = rq.len[s.r];
+  const int words = (longest + 32 * kBlock - 1) / (32 * kBlock);
+  const int entries = longest > 0 ? (p1 - p0 + 1) * a.topk : 0;
   auto entry = [&](int e, int& p) {
     p = p0 + e / a.topk;
     const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + which) * a.topk + e % a.topk);
@@ -160,15 +214,14 @@ struct Items {
 // The items of a stretch.  n: the unit's joined items (block lists), of which the
 // stretch takes the share that its positions have of the unit's.
 template <bool kBlocks>
-__device__ __forceinline__ Items make_items(const AttnArgs& a, const Segment& s, int n) {
+__device__ __forceinline__ Items make_items(const AttnArgs& a, const Requests& rq, const Segment& s,
+                                            int n) {
   Items it;
   it.r = s.r;
   it.head = s.head;
   it.kv_head = s.head * a.kv_heads / a.heads;
-  it.slot = __ldg(a.slot_ids + s.r);
-  it.glen = 0;
-  if (it.slot >= 0 && it.slot < a.n_slots)
-    for (int p = 0; p < a.P; ++p) it.glen = max(it.glen, row_len(a, s.r, p));
+  it.slot = rq.slot[s.r];
+  it.glen = rq.len[s.r];
   if (kBlocks) {
     it.i0 = s.cap ? (int)((long long)n * s.o0 / s.cap) : 0;
     it.i1 = s.cap ? (int)((long long)n * s.o1 / s.cap) : 0;

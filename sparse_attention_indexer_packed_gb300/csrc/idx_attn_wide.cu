@@ -91,8 +91,8 @@ struct AWLayout {
   static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
   static constexpr int kNumBars = 4 * NS + 9;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;       // flags, count, abort, tmem
-  static constexpr int kPreOff = (kCtlOff + 32 + 15) & ~15;
-  static constexpr int kListOff = kPreOff + (kMaxGroups + 4) * 4;
+  static constexpr int kPreOff = (kCtlOff + 16 + 48 + 15) & ~15;   // and one int a warp
+  static constexpr int kListOff = kPreOff + kRequestsBytes;
   static constexpr int kBytes = kListOff + kMaxList * 4;
   static constexpr int kSmem = kBytes + 1024;
   static constexpr int kThreads = 320;
@@ -209,30 +209,6 @@ __device__ __forceinline__ void group_sync() {   // the two softmax groups
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// Four e4m3 codes of four floats (round to nearest even, saturating), and what
-// they stand for taken off the floats.
-__device__ __forceinline__ uint32_t e4m3x4_take(float (&x)[4]) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 h0, h1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h1, %4, %3;\n\t"
-      "mov.b32 %0, {h0, h1};\n\t}"
-      : "=r"(d)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
-  uint32_t lo, hi;
-  e4m3x4_to_f16x2x2(d, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
-  return d;
-}
-
-// The smallest power of two above x (x finite, >= 0; at least 2^-100).
-__device__ __forceinline__ float pow2_above(float x) {
-  const int e = max(27, (int)(__float_as_uint(x) >> 23));
-  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
-}
-
 // F lanes a row (128 / F rows of a group, or fewer).
 template <int KF, int F, bool kBlocks>
 __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
@@ -248,7 +224,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   unsigned int* ctl = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);  // flags, count, abort, tmem
   volatile unsigned int* abort_flag = ctl + 2;
-  int* pre = reinterpret_cast<int*>(smem + L::kPreOff);
+  const Requests rq = requests_at(smem + L::kPreOff);
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kXchOff);
   float* xch = reinterpret_cast<float*>(smem + L::kXchOff);
@@ -293,14 +269,13 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 8) build_prefix<kTok, kBlocks>(a, pre, ctl, lane);
   tc_fence_before();
-  __syncthreads();
+  build_requests<kTok, kBlocks>(a, rq, reinterpret_cast<int*>(ctl + 4), ctl);
   tc_fence_after();
   const uint32_t tmem = ctl[3];
 
   const int per = a.heads * a.groups;
-  const long long W = (long long)pre[a.R] * per;
+  const long long W = (long long)rq.pre[a.R] * per;
   // no CTA takes less than about four pages
   const long long want = (W + 3) / 4;
   const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
@@ -334,9 +309,10 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   int tile0 = 0;            // pages of the CTA's earlier segments (producer, issuer, groups)
   int segs = 0;             // segments with pages so far
   int cnt0 = 0, cnt1 = 0;   // pages of group 0 / 1 so far
-  long long pos = begin;
-  while (pos < end) {
-    const Segment s = next_segment(pre, a.R, a.heads, a.groups, pos, end);
+  Walk walk;
+  walk.begin(rq.pre, a.R, a.heads, a.groups, begin, end);
+  while (walk.more()) {
+    const Segment s = walk.next(rq.pre, a.R, a.heads, a.groups);
     if (!s.live) continue;
     const int row_first = s.group * a.group_rows;
     const int nrows = min(a.group_rows, a.P * a.nq - row_first);
@@ -344,9 +320,9 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
     int n_items = 0;
     if (kBlocks) {
       __syncthreads();      // every role is done with the last unit's list
-      n_items = 2 * join_lists(a, s, p0, (row_first + nrows - 1) / a.nq, list, bits, ctl + 1);
+      n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits, ctl + 1);
     }
-    const Items it = make_items<kBlocks>(a, s, n_items);
+    const Items it = make_items<kBlocks>(a, rq, s, n_items);
     // the second page of a request's last block may not exist
     int i1 = it.i1;
     if (kBlocks && i1 == n_items && n_items > 0 &&
@@ -487,9 +463,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
           float amax = 0.f;
 #pragma unroll
           for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          int ex = 0;
-          if (amax > 0.f) ex = 7 - (((int)(__float_as_uint(amax) >> 23) & 0xff) - 127);
-          ex = max(-100, min(100, ex));
+          const int ex = to_2_7(amax);
           const float up = ldexpf(1.f, ex);
           post *= ldexpf(1.f, -ex);
           if (g == 0) {
