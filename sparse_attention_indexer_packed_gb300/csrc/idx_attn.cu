@@ -24,8 +24,12 @@
 //    against transposed-ldmatrix values.  An e4m3 piece is decoded to exact f16
 //    in registers;
 //  * warps keep softmax states of their own; they are joined through shared
-//    memory at a unit's end.  A unit inside one CTA is written at once; one
-//    that was cut leaves (m, l, out) in the workspace for the join kernel;
+//    memory at a unit's end.  A unit inside one CTA is written at once; of one
+//    that was cut each CTA leaves (m, l, out) in the workspace for a join kernel.
+//    (Joined in this kernel by the CTA that comes last, through tagged counters:
+//    measured slower on small calls, 1 x 1K 9.4 -> 10.5 us and blocks 1 x 32K
+//    11.5 -> 14.7, the fences and counter round trips costing more than the
+//    second launch);
 //  * every wait is bounded, as in the score kernels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -105,45 +109,50 @@ template <int KF>
 struct QRows {
   uint32_t a[8][4];
   float post0, post1;
-  __device__ void load(const uint16_t* r0, const uint16_t* r1, float scale_log2, int lane) {
-    const int t = lane & 3;
-    if (KF == kBf16) {
+  // the rows' words as they lie in memory: the loads go out, nothing waits
+  __device__ __forceinline__ void load(const uint16_t* r0, const uint16_t* r1) {
+    const int t = threadIdx.x & 3;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        const int o = 16 * ks + 2 * t;
-        a[ks][0] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o)) : 0u;
-        a[ks][1] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o)) : 0u;
-        a[ks][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o + 8)) : 0u;
-        a[ks][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o + 8)) : 0u;
+    for (int c = 0; c < 8; ++c) {
+      if (KF == kBf16) {
+        const int o = 16 * c + 2 * t;
+        a[c][0] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o)) : 0u;
+        a[c][1] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o)) : 0u;
+        a[c][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o + 8)) : 0u;
+        a[c][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o + 8)) : 0u;
+      } else {
+        const int o = 16 * c + 4 * t;
+        const uint2 u = r0 ? __ldg(reinterpret_cast<const uint2*>(r0 + o)) : make_uint2(0, 0);
+        const uint2 v = r1 ? __ldg(reinterpret_cast<const uint2*>(r1 + o)) : make_uint2(0, 0);
+        a[c][0] = u.x, a[c][2] = u.y, a[c][1] = v.x, a[c][3] = v.y;
       }
-      post0 = post1 = scale_log2;
-    } else {
-      uint2 u[2][8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        u[0][c] = r0 ? __ldg(reinterpret_cast<const uint2*>(r0 + 16 * c + 4 * t)) : make_uint2(0, 0);
-        u[1][c] = r1 ? __ldg(reinterpret_cast<const uint2*>(r1 + 16 * c + 4 * t)) : make_uint2(0, 0);
-      }
-      post0 = scale_log2 * to_f16(u[0], 0);
-      post1 = scale_log2 * to_f16(u[1], 1);
     }
   }
-  __device__ float to_f16(const uint2 (&u)[8], int half) {
+  // what the scores are to be multiplied by; e4m3 keys: the rows to scaled f16
+  __device__ __forceinline__ void finish(float scale_log2) {
+    post0 = post1 = scale_log2;
+    if (KF == kFp8) {
+      post0 *= to_f16(0);
+      post1 *= to_f16(1);
+    }
+  }
+  __device__ __forceinline__ float to_f16(int half) {
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(bf16_lo(u[c].x)), fabsf(bf16_hi(u[c].x)))),
-                   fmaxf(fabsf(bf16_lo(u[c].y)), fabsf(bf16_hi(u[c].y))));
+#pragma unroll
+      for (int e = half; e < 4; e += 2)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(a[c][e])), fabsf(bf16_hi(a[c][e]))));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int e = to_2_7(amax);
-    const float up = ldexpf(1.f, e);
+    const int x = to_2_7(amax);
+    const float up = ldexpf(1.f, x);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      a[c][half] = pack_f16(bf16_lo(u[c].x) * up, bf16_hi(u[c].x) * up);
-      a[c][2 + half] = pack_f16(bf16_lo(u[c].y) * up, bf16_hi(u[c].y) * up);
-    }
-    return ldexpf(1.f, -e);
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int e = half; e < 4; e += 2)
+        a[c][e] = pack_f16(bf16_lo(a[c][e]) * up, bf16_hi(a[c][e]) * up);
+    return ldexpf(1.f, -x);
   }
 };
 
@@ -344,6 +353,14 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
   }
 }
 
+// A part of a shared unit's row: (running max, sum) and the unnormalised output.
+__device__ __forceinline__ void put_part(const AttnArgs& a, int slot, int i, float m, float l,
+                                         float4 o, int lane) {
+  const size_t at = (size_t)slot * kTile + i;
+  if (lane == 0) a.part_ml[at] = make_float2(m, l);
+  reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
+}
+
 template <int KF, bool kBlocks>
 __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -383,8 +400,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   const long long want = (W + NW - 1) / NW;
   const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
   const int c = blockIdx.x;
-  const long long begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
-  SplitRecord record = {-1, 0};
+  const long long begin = c < C ? div(W * c, C) : 0, end = c < C ? div(W * (c + 1), C) : 0;
 
   // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
   // The page id is loaded here and looked at when the copy is issued, a piece
@@ -395,6 +411,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     uint32_t members;
     int page, kv_head;
   };
+  SplitRecord record = {-1, 0};
   Walk walk, fwalk;
   walk.begin(rq.pre, a.R, a.heads, a.groups, begin, end);
   fwalk = walk;
@@ -473,18 +490,18 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     const int p0 = row_first / a.nq;
     int n_items = 0;
     if (kBlocks) {
-      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits, cta_flags + 1) *
+      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits) *
                 (kBlock / kItem);
       fit = make_items<kBlocks>(a, rq, s, n_items);
       funit = s.unit;
       fi = fit.i0 + warp;
       primed = false;
     }
-    if (!primed) {
+    // the first page id, the queries and the first copies overlap
+    const bool prime = !primed;
+    if (prime) {
       primed = true;
       nxt = feed();
-#pragma unroll
-      for (int d = 0; d < D; ++d) fl[d] = fetch();
     }
     const Items it = kBlocks ? fit : make_items<kBlocks>(a, rq, s, 0);
     // ---- the unit's rows ----------------------------------------------------
@@ -497,7 +514,12 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     const int L1 = has1 && it.glen > 0 ? row_len(a, s.r, pd1) : 0;
     QRows<KF> q;
     q.load(has0 ? a.q + q_index(pk0, pd0) * kDim : nullptr,
-           has1 ? a.q + q_index(pk1, pd1) * kDim : nullptr, a.scale_log2, lane);
+           has1 ? a.q + q_index(pk1, pd1) * kDim : nullptr);
+    if (prime) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) fl[d] = fetch();
+    }
+    q.finish(a.scale_log2);
     State st;
     st.reset();
     // ---- its pieces -----------------------------------------------------------
@@ -648,13 +670,10 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       if (__any_sync(0xffffffffu, !finite4(o)))
         careful_row<KF, kItem, kBlocks>(a, it, list, a.q + q_index(pk, p) * kDim,
                                         it.glen > 0 ? row_len(a, s.r, p) : 0, p - p0, lane, m, l, o);
-      if (complete) {
+      if (complete)
         write_row(a, q_index(pk, p), m, l, o, lane);
-      } else {
-        const size_t at = (size_t)slot_out * kTile + i;
-        if (lane == 0) a.part_ml[at] = make_float2(m, l);
-        reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
-      }
+      else
+        put_part(a, slot_out, i, m, l, o, lane);
     }
     __syncthreads();
   }
@@ -777,11 +796,8 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
     e = blocks ? launch_kf<kFp8, true>(a, k_map, v_map, grid, dev, stream)
                : launch_kf<kFp8, false>(a, k_map, v_map, grid, dev, stream);
   if (e != cudaSuccess) return e;
-  return launch_attn_join(a, grid, stream);
-}
-
-cudaError_t launch_attn_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(attn_join_kernel, ctas * (a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows), kJoinThreads, 0, stream, a);
+  const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
+  e = launch_pdl(attn_join_kernel, grid * rows, kJoinThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -19,7 +19,7 @@ constexpr uint32_t kErrTimeout = 2u;
 constexpr uint32_t kErrLenClamped = 4u;
 
 // Where a unit that several CTAs share begins: written by the CTA that starts
-// it, read by the join.  unit < 0: this CTA starts no shared unit.
+// it, read by the join kernel.  unit < 0: this CTA starts no shared unit.
 struct SplitRecord {
   int unit, splits;
 };
@@ -108,6 +108,13 @@ __device__ __forceinline__ int find_request(const int* pre, int R, int x) {
   return lo;
 }
 
+// x / y of two positions (x >= 0, y > 0): in 32 bits where they fit, which is
+// several times as fast.
+__device__ __forceinline__ long long div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (unsigned int)x / (unsigned int)y;
+  return x / y;
+}
+
 // A walk over the stretches of [pos, end), unit by unit: one search at its
 // start, no division after it.
 struct Walk {
@@ -120,10 +127,10 @@ struct Walk {
     end = last;
     if (pos >= end) return;
     const int per = heads * groups;
-    r = find_request(pre, R, (int)(pos / per));
+    r = find_request(pre, R, (int)div(pos, per));
     wt = pre[r + 1] - pre[r];
     const long long base = (long long)pre[r] * per;
-    const int k = (int)((pos - base) / wt);
+    const int k = (int)div(pos - base, wt);
     start = base + (long long)k * wt;
     head = k / groups;
     group = k - head * groups;
@@ -162,7 +169,7 @@ struct Walk {
 
 // The CTA that holds position x.
 __device__ __forceinline__ int owner(long long x, long long W, int C) {
-  return (int)(((x + 1) * C + W - 1) / W) - 1;
+  return (int)div((x + 1) * C + W - 1, W) - 1;
 }
 
 }  // namespace attn
@@ -171,7 +178,6 @@ cudaError_t launch_attn(int key_format, const AttnArgs& args, const CUtensorMap&
                         const CUtensorMap& v_map, cudaStream_t stream);
 cudaError_t launch_attn_wide(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
                              const CUtensorMap& v_map, int grid, int dev, cudaStream_t stream);
-cudaError_t launch_attn_join(const AttnArgs& args, int ctas, cudaStream_t stream);
 // CTAs launch_attn uses on the current device (0: the device cannot be asked).
 int attn_ctas();
 

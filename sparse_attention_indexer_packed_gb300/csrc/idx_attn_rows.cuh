@@ -136,8 +136,8 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
 // kMaxBlockWords words of scratch.  A set bit a block and a running count of them
 // give each entry its place, so a block listed twice takes one.
 __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq, const Segment& s,
-                                          int p0, int p1, uint32_t* list, uint32_t* bits,
-                                          unsigned int* count) {
+                                          int p0, int p1, uint32_t* list, uint32_t* bits) {
+  constexpr int kKeep = 2;   // entries a thread keeps in registers between the passes
   uint32_t* rank = bits + kMaxBlockWords;
   const int lane = threadIdx.x & 31, nt = blockDim.x;
   const int which = s.head * a.lists / a.heads;
@@ -149,44 +149,49 @@ __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq,
     const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + which) * a.topk + e % a.topk);
     return id >= 0 && (long long)id * kBlock < row_len(a, s.r, p) ? id : -1;
   };
-  for (int w = threadIdx.x; w < words; w += nt) bits[w] = 0u;
-  __syncthreads();
-  for (int e = threadIdx.x; e < entries; e += nt) {
-    int p;
-    const int id = entry(e, p);
-    if (id >= 0) atomicOr(&bits[id >> 5], 1u << (id & 31));
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int w0 = 0; w0 < words; w0 += 32) {
-      const int w = w0 + lane;
-      const int cnt = w < words ? __popc(bits[w]) : 0;
-      int incl = cnt;
+  int keep[kKeep], who[kKeep];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (w < words) rank[w] = (uint32_t)(run + incl - cnt);
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) *count = (unsigned int)run;
+  for (int k = 0; k < kKeep; ++k) {
+    const int e = threadIdx.x + k * nt;
+    who[k] = 0;
+    keep[k] = e < entries ? entry(e, who[k]) : -1;
   }
+  for (int w = threadIdx.x; w < words; w += nt) bits[w] = 0u;
+  for (int w = threadIdx.x; w < entries; w += nt) list[w] = 0u;
   __syncthreads();
-  const int n = (int)*count;
-  for (int w = threadIdx.x; w < n; w += nt) list[w] = 0u;
-  __syncthreads();
-  for (int e = threadIdx.x; e < entries; e += nt) {
-    int p;
-    const int id = entry(e, p);
-    if (id >= 0) {
-      const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
-      atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (keep[k] >= 0) f(keep[k], who[k]);
+    for (int e = threadIdx.x + kKeep * nt; e < entries; e += nt) {
+      int p;
+      const int id = entry(e, p);
+      if (id >= 0) f(id, p);
     }
-  }
+  };
+  each([&](int id, int) { atomicOr(&bits[id >> 5], 1u << (id & 31)); });
   __syncthreads();
-  return n;
+  // blocks before each word: every warp for itself, and in shared memory
+  int run = 0;
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    const int w = w0 + lane;
+    const int cnt = w < words ? __popc(bits[w]) : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (w < words) rank[w] = (uint32_t)(run + incl - cnt);   // every warp writes the same
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+  each([&](int id, int p) {
+    const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
+    atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
+  });
+  __syncthreads();
+  return run;
 }
 
 // Four consecutive dims of a plane row as fp32.

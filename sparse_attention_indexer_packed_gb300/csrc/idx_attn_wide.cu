@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   const long long want = (W + 3) / 4;
   const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
   const int c = blockIdx.x;
-  const long long begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
+  const long long begin = c < C ? div(W * c, C) : 0, end = c < C ? div(W * (c + 1), C) : 0;
   SplitRecord record = {-1, 0};
 
   // A bounded wait of a whole warp; false once any role has given up.
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
     int n_items = 0;
     if (kBlocks) {
       __syncthreads();      // every role is done with the last unit's list
-      n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits, ctl + 1);
+      n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits);
     }
     const Items it = make_items<kBlocks>(a, rq, s, n_items);
     // the second page of a request's last block may not exist
