@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -66,8 +67,8 @@ _SIGNATURES = {
     "idx_topk_merge": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "idx_score_topk_noalloc": (_I, [_P, _P, _I, _P, _P, _I, _I64, _P, _I, _I, _P, _P, _I, _I,
                                     _I, _I, _I, _I, _P, _P, _P]),
-    "idx_store_kv": (_I, [_P, _P, _I64, _I64, _P, _I64, _I, ctypes.POINTER(IdxPool),
-                          ctypes.POINTER(IdxPool), _P]),
+    # (the pools are passed as the struct's bytes: see _pool_bytes)
+    "idx_store_kv": (_I, [_P, _P, _I64, _I64, _P, _I64, _I, _P, _P, _P]),
     "idx_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "idx_attn_paged": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I, _P, _I, _I, _P, _P, _I, _I, _I, _F,
                             _P, _P, _P, _SZ, _P]),
@@ -345,6 +346,7 @@ def idx_noalloc_errors(stream=None) -> int:
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ROW_BYTES = {"bf16": 256, "fp8_e4m3": 128, "nvfp4": 64}
+_SCALE_BYTES = {"bf16": 0, "fp8_e4m3": 4, "nvfp4": 8}
 
 
 def _want(t: torch.Tensor, name: str, dtype, shape) -> int:
@@ -375,13 +377,14 @@ def _plane(payload, scale, name: str, kv_dtype: str):
     want = _ROW_BYTES.get(kv_dtype)
     if want is None:
         raise IdxError(f"unknown dtype {kv_dtype!r}")
-    if payload.dim() != 2 or payload.shape[1] * payload.element_size() != want:
+    shape = payload.shape
+    if len(shape) != 2 or shape[1] * payload.element_size() != want:
         raise IdxError(f"{name}_payload must be [rows, {want} bytes] for a {kv_dtype} cache")
-    rows = payload.shape[0]
+    rows = shape[0]
     if rows % PAGE:
         raise IdxError(f"{name}_payload must hold whole pages of {PAGE} rows")
     if scale is not None or kv_dtype == "fp8_e4m3":
-        if kv_dtype == "fp8_e4m3" and (scale is None or scale.numel() * scale.element_size() != rows * 4):
+        if kv_dtype == "fp8_e4m3" and (scale is None or scale.nbytes != rows * 4):
             raise IdxError(f"{name}_scale must hold one fp32 per row")
         scale = _dev(scale, f"{name}_scale")
     return _dev(payload, f"{name}_payload"), scale, rows // PAGE
@@ -399,10 +402,15 @@ def _source(src, name: str, tokens: int, kv_heads: int):
     return src.data_ptr(), (stride if tokens > 1 else kv_heads * DIM)
 
 
-def _plane_struct(payload, scale, name: str, kv_dtype: str) -> IdxPool:
+# IdxPool's fields (checked below): packing them is a tenth of filling a ctypes struct.
+_POOL = struct.Struct("=iiiiqQQqq")
+assert _POOL.size == ctypes.sizeof(IdxPool)
+
+
+def _pool_bytes(payload, scale, name: str, kv_dtype: str) -> bytes:
     ptr, scale_ptr, pages = _plane(payload, scale, name, kv_dtype)
-    return IdxPool(DTYPES[kv_dtype], PAGE, DIM, 0, pages, ptr, scale_ptr, _ROW_BYTES[kv_dtype],
-                   {"bf16": 0, "fp8_e4m3": 4, "nvfp4": 8}[kv_dtype])
+    return _POOL.pack(DTYPES[kv_dtype], PAGE, DIM, 0, pages, ptr, scale_ptr or 0,
+                      _ROW_BYTES[kv_dtype], _SCALE_BYTES[kv_dtype])
 
 
 def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
@@ -414,14 +422,14 @@ def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_sc
         raise IdxError("a source and its payload plane come together, and the keys always")
     T = slot_mapping.numel()
     k_ptr, k_stride = _source(k_src, "k_src", T, kv_heads)
-    k_pool = _plane_struct(k_payload, k_scale, "k", kv_dtype)
+    k_pool = _pool_bytes(k_payload, k_scale, "k", kv_dtype)
     v_ptr, v_stride, v_pool = None, 0, None
     if v_src is not None:
         v_ptr, v_stride = _source(v_src, "v_src", T, kv_heads)
-        v_pool = ctypes.byref(_plane_struct(v_payload, v_scale, "v", kv_dtype))
+        v_pool = _pool_bytes(v_payload, v_scale, "v", kv_dtype)
     rc = lib().idx_store_kv(k_ptr, v_ptr, k_stride, v_stride,
                             _want(slot_mapping, "slot_mapping", torch.int64, (T,)), T, kv_heads,
-                            ctypes.byref(k_pool), v_pool, _stream_of(k_src, stream))
+                            k_pool, v_pool, _stream_of(k_src, stream))
     if rc:
         _check(rc, "idx_store_kv")
 
@@ -442,18 +450,20 @@ def alloc_attn_workspace(packed_queries: int, q_heads: int, kv_heads: int, lists
 def _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, slot_ids,
                row_lens, kv_heads):
     """The arguments the two attention calls begin with, and R, P, q_heads."""
-    if q.dim() != 4 or q.shape[3] != DIM:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != DIM:
         raise IdxError(f"q must be [requests, draft rows, q_heads, {DIM}]")
-    R, P, Hq, _ = q.shape
+    R, P, Hq, _ = shape
     kp, ks, k_pages = _plane(k_payload, k_scale, "k", kv_dtype)
     vp, vs, v_pages = _plane(v_payload, v_scale, "v", kv_dtype)
     if kv_heads < 1 or k_pages != v_pages or k_pages % kv_heads:
         raise IdxError("the planes must hold the same whole pages of kv_heads heads")
-    if page_table.dim() != 2:
+    table = page_table.shape
+    if len(table) != 2:
         raise IdxError("page_table must be [n_slots, max_pages]")
-    n_slots, max_pages = page_table.shape
-    return (_want(q, "q", _BF16, q.shape), kp, ks, vp, vs, DTYPES[kv_dtype], k_pages // kv_heads,
-            kv_heads, _want(page_table, "page_table", _I32, page_table.shape), n_slots, max_pages,
+    n_slots, max_pages = table
+    return (_want(q, "q", _BF16, shape), kp, ks, vp, vs, DTYPES[kv_dtype], k_pages // kv_heads,
+            kv_heads, _want(page_table, "page_table", _I32, table), n_slots, max_pages,
             _want(slot_ids, "slot_ids", _I32, (R,)),
             _want(row_lens, "row_lens", _I32, (R, P))), R, P, Hq
 

@@ -249,6 +249,11 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   if (num_pages < 1 || num_pages > 0x7fffffffLL / idx::kPage / kv_heads)
     return fail(IDX_ERR_INVALID, "num_pages * kv_heads must be in [1, 2^31 / 64) (got %lld x %d)",
                 (long long)num_pages, kv_heads);
+  const int group = idx::attn::group_rows(P, q_heads / heads, blocks);
+  const long long units = (long long)R * heads * (((long long)P * (q_heads / heads) + group - 1) / group);
+  if (units > idx::attn::kMaxUnits)
+    return fail(IDX_ERR_INVALID, "at most %lld (request, key head or list, row group) units a call (got %lld)",
+                idx::attn::kMaxUnits, units);
   if (!workspace) return fail(IDX_ERR_INVALID, "workspace is NULL");
   if (!aligned(workspace, 256)) return fail(IDX_ERR_INVALID, "workspace must be 256-byte aligned");
   const size_t need = idx_attn_workspace_bytes(P, q_heads, kv_heads, blocks ? lists : 0);
@@ -292,8 +297,17 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   a.topk = blocks ? topk : 0;
   a.heads = heads;
   a.nq = q_heads / heads;
-  a.group_rows = idx::attn::group_rows(P, a.nq, blocks);
+  a.group_rows = group;
   a.groups = (P * a.nq + a.group_rows - 1) / a.group_rows;
+  a.by_per = idx::attn::Divisor::of(heads * a.groups);
+  a.by_groups = idx::attn::Divisor::of(a.groups);
+  a.by_nq = idx::attn::Divisor::of(a.nq);
+  a.by_topk = idx::attn::Divisor::of(blocks ? topk : 1);
+  a.by_kv = idx::attn::Divisor::of(heads / kv_heads > 1 ? heads / kv_heads : 1);
+  a.by_list = idx::attn::Divisor::of(heads / a.lists > 1 ? heads / a.lists : 1);
+  a.unit_cost = idx::attn::unit_cost(a.group_rows, blocks);
+  a.shift = idx::attn::position_shift(R, (long long)heads * a.groups, max_pages,
+                                      blocks ? (long long)topk * P : 0, a.unit_cost);
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.wait_ns = idx::wait_limit_ns();
   a.stall_test = idx::stall_test();

@@ -183,33 +183,32 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
                                       int glen) {
   const int t = lane & 3, m = lane >> 3, rr = lane & 7;
   constexpr int TB = ALayout<KF>::kTileBytes;
+  // the four token tiles' chains side by side
   float s[4][4];
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-    const uint32_t row = stage + (uint32_t)((nt * 8 + rr) * 128);
+  for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+  const uint32_t krow = stage + (uint32_t)(rr * 128);
+#pragma unroll
+  for (int c = 0; c < (KF == kBf16 ? 4 : 2); ++c) {
+    const int ch = 4 * c + m;
+    const uint32_t at = krow + (KF == kBf16 ? (uint32_t)((ch >> 3) * (TB / 2)) : 0u) + (uint32_t)(((ch ^ rr) & 7) << 4);
+    uint32_t w[4][4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) ldmatrix_x4(at + nt * 1024, w[nt][0], w[nt][1], w[nt][2], w[nt][3]);
     if (KF == kBf16) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int ch = 4 * c + m;
-        uint32_t b0, b1, b2, b3;
-        ldmatrix_x4(row + (uint32_t)((ch >> 3) * (TB / 2)) + (uint32_t)(((ch ^ rr) & 7) << 4), b0,
-                    b1, b2, b3);
-        mma_bf16_16816(s[nt], q.a[2 * c], b0, b1);
-        mma_bf16_16816(s[nt], q.a[2 * c + 1], b2, b3);
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) mma_bf16_16816(s[nt], q.a[2 * c + e], w[nt][2 * e], w[nt][2 * e + 1]);
     } else {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[4];
-        ldmatrix_x4(row + (uint32_t)((((4 * c + m) ^ rr) & 7) << 4), w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int nt = 0; nt < 4; ++nt) {
           uint32_t lo, hi;
-          e4m3x4_to_f16x2x2(w[e], lo, hi);
+          e4m3x4_to_f16x2x2(w[nt][e], lo, hi);
           mma_f16_16816(s[nt], q.a[4 * c + e], lo, hi);
         }
-      }
     }
   }
   // scores in log2 units, their row maxima
@@ -394,13 +393,11 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 
   build_requests<kItem, kBlocks>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
 
-  const int per = a.heads * a.groups;
-  const long long W = (long long)rq.pre[a.R] * per;
+  const int W = rq.pre[a.R] * (int)a.by_per.d;
   // no CTA takes less than about one piece a warp
-  const long long want = (W + NW - 1) / NW;
-  const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
+  const int C = min((W + NW - 1) / NW, (int)gridDim.x);
   const int c = blockIdx.x;
-  const long long begin = c < C ? div(W * c, C) : 0, end = c < C ? div(W * (c + 1), C) : 0;
+  const int begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
 
   // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
   // The page id is loaded here and looked at when the copy is issued, a piece
@@ -413,7 +410,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   };
   SplitRecord record = {-1, 0};
   Walk walk, fwalk;
-  walk.begin(rq.pre, a.R, a.heads, a.groups, begin, end);
+  walk.begin(a, rq.pre, begin, end);
   fwalk = walk;
   Items fit = {};
   int funit = -1, fi = 0;
@@ -423,9 +420,9 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     while (!dead) {
       if (fi >= fit.i1) {
         if (kBlocks || !fwalk.more()) break;
-        const Segment s = fwalk.next(rq.pre, a.R, a.heads, a.groups);
+        const Segment s = fwalk.next(a, rq.pre);
         if (!s.live) continue;
-        fit = make_items<kBlocks>(a, rq, s, 0);
+        fit = make_items<kItem, kBlocks>(a, rq, s, 0);
         funit = s.unit;
         fi = fit.i0 + warp;
         continue;
@@ -483,16 +480,16 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   int used = 0;           // pieces this warp has waited for
   bool primed = false;
   while (walk.more()) {
-    const Segment s = walk.next(rq.pre, a.R, a.heads, a.groups);
+    const Segment s = walk.next(a, rq.pre);
     if (!s.live) continue;
     const int row_first = s.group * kTile;
     const int nrows = min(kTile, a.P * a.nq - row_first);
-    const int p0 = row_first / a.nq;
+    const int p0 = a.by_nq.div(row_first);
     int n_items = 0;
     if (kBlocks) {
       n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits) *
                 (kBlock / kItem);
-      fit = make_items<kBlocks>(a, rq, s, n_items);
+      fit = make_items<kItem, kBlocks>(a, rq, s, n_items);
       funit = s.unit;
       fi = fit.i0 + warp;
       primed = false;
@@ -503,15 +500,16 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       primed = true;
       nxt = feed();
     }
-    const Items it = kBlocks ? fit : make_items<kBlocks>(a, rq, s, 0);
+    const Items it = kBlocks ? fit : make_items<kItem, kBlocks>(a, rq, s, 0);
     // ---- the unit's rows ----------------------------------------------------
     auto q_index = [&](int pk, int p) {   // packed row pk of the unit head, draft row p = pk / nq
       return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
     };
-    const int pk0 = row_first + g, pd0 = pk0 / a.nq, pk1 = pk0 + 8, pd1 = pk1 / a.nq;
+    const int pk0 = row_first + g, pd0 = a.by_nq.div(pk0), pk1 = pk0 + 8, pd1 = a.by_nq.div(pk1);
     const bool has0 = g < nrows, has1 = g + 8 < nrows;
-    const int L0 = has0 && it.glen > 0 ? row_len(a, s.r, pd0) : 0;
-    const int L1 = has1 && it.glen > 0 ? row_len(a, s.r, pd1) : 0;
+    // with one draft row the request's longest row is the row
+    const int L0 = !has0 || it.glen == 0 ? 0 : a.P == 1 ? it.glen : row_len(a, s.r, pd0);
+    const int L1 = !has1 || it.glen == 0 ? 0 : a.P == 1 ? it.glen : row_len(a, s.r, pd1);
     QRows<KF> q;
     q.load(has0 ? a.q + q_index(pk0, pd0) * kDim : nullptr,
            has1 ? a.q + q_index(pk1, pd1) * kDim : nullptr);
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
     }
     for (int i = warp; i < nrows; i += NW) {
-      const int pk = row_first + i, p = pk / a.nq;
+      const int pk = row_first + i, p = a.by_nq.div(pk);
       float m = -INFINITY, l = 0.f;
 #pragma unroll
       for (int w = 0; w < NH; ++w) m = fmaxf(m, ml[w * kTile + i].x);
@@ -701,9 +699,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   const int c = blockIdx.x / rows, i = blockIdx.x - c * rows;
   const SplitRecord rec = a.records[c];
   if (rec.unit < 0) return;
-  const int per = a.heads * a.groups;
-  const int r = rec.unit / per, k = rec.unit - r * per;
-  const int head = k / a.groups, pk = (k - head * a.groups) * a.group_rows + i;
+  const int r = a.by_per.div(rec.unit), k = rec.unit - r * (int)a.by_per.d;
+  const int head = a.by_groups.div(k), pk = (k - head * a.groups) * a.group_rows + i;
   if (pk >= a.P * a.nq) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto part = [&](int s) { return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i; };
@@ -752,7 +749,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     const float4 v = so[w][lane];
     o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
   }
-  const int p = pk / a.nq;
+  const int p = a.by_nq.div(pk);
   write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, lane);
 }
 

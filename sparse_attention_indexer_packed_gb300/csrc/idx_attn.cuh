@@ -24,6 +24,24 @@ struct SplitRecord {
   int unit, splits;
 };
 
+// Division of x in [0, 2^31) by a fixed d in [1, 2^31): (x * m) >> (32 + s) with
+// m = ceil(2^(32 + s) / d), s = ceil(log2 d) - 1 (Granlund and Montgomery, "Division
+// by Invariant Integers using Multiplication", 1994): exact for 31-bit x.
+struct Divisor {
+  unsigned int d, m, s;
+  static Divisor of(int d) {
+    Divisor v;
+    v.d = (unsigned int)d;
+    v.s = 0;
+    while ((2ull << v.s) < (unsigned long long)d) ++v.s;
+    v.m = (unsigned int)((((1ull << 32) << v.s) + d - 1) / d);
+    return v;
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return d == 1 ? x : (int)(__umulhi((unsigned int)x, m) >> s);
+  }
+};
+
 }  // namespace attn
 
 // Arguments of one attention call.  A "unit" is what shares one read of the
@@ -54,6 +72,10 @@ struct AttnArgs {
   int nq;                      // query heads of a unit head
   int group_rows;              // packed rows of a group (16, or up to 128)
   int groups;                  // row groups of a unit head
+  attn::Divisor by_per, by_groups, by_nq, by_topk;  // heads * groups, groups, nq, topk
+  attn::Divisor by_kv, by_list;  // unit heads of a key head, of a list
+  int shift;                   // pieces of a position: 2^shift
+  int unit_cost;               // positions that stand for a unit's end
   float scale_log2;            // softmax scale times log2(e)
   unsigned long long wait_ns;
   int stall_test;
@@ -79,21 +101,45 @@ inline size_t part_o_bytes(int ctas, int group_rows) {
 }
 
 // ---------------------------------------------------------------------------
-// The split.  Every unit of request r has weight wt(r) = items(r) + kUnitCost,
-// items(r) = its pieces (with block lists: an upper bound of them).
-// The units' weights lie end to end on a line of W positions, in the order
-// (request, unit head, row group); CTA c of C takes [W c / C, W (c + 1) / C).
-// A CTA's part of a unit is its items inside that range; the last kUnitCost
-// positions of a unit stand for the cost of ending it and hold no item, except
-// that a unit with no items is ended by the CTA that holds its first position.
+// The split.  Every unit of request r has weight wt(r) = cap(r) + unit_cost, cap(r)
+// = its pieces (with block lists: an upper bound of them) in lots of 2^shift.  The
+// units' weights lie end to end on a line of W positions, in the order (request,
+// unit head, row group); CTA c of C takes [W c / C, W (c + 1) / C).  A CTA's part of
+// a unit is its lots inside that range; the last unit_cost positions of a unit
+// stand for the cost of ending it and hold none, except that a unit with no lot is
+// ended by the CTA that holds its first position.  The host picks the shift (0 but
+// for calls of many million pieces) so that W * (C + 1) stays below 2^31.
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 8;
+constexpr long long kMaxPositions = 0x7fffffffll / (kMaxCtas + 1);
+constexpr long long kMaxUnits = 1 << 18;
+constexpr int kMaxUnitCost = 32;
+static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit the line");
+
+// Positions that stand for a unit's end, in pieces of its kernel.  A stretch of a
+// unit costs a CTA about 2.5 us beside its pieces (queries, join, output; 5 with
+// lists, which are joined too and whose copies start anew).  Too few and a CTA ends
+// up with many small units; too many and the long ones wait.  Measured (us a call):
+// 48 ragged requests x 4 heads 36.2 / 28.3 / 24.9 / 26.9 at 4 / 8 / 12 / 24; 24
+// ragged requests with lists 25.5 / 20.6 / 17.8 / 18.1 at 4 / 8 / 24 / 48; 16 x 131K
+// with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
+inline int unit_cost(int group_rows, bool blocks) {
+  return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
+}
+
+// The shift of a call: no request has more than `pages` pages or, with lists of
+// `listed` entries in all, two pages an entry; a piece is half a page or a page.
+inline int position_shift(int R, long long per, int pages, long long listed, int unit_cost) {
+  long long most = listed > 0 && listed < (pages + 1) / 2 ? 4 * listed : 2ll * pages + 2;
+  int shift = 0;
+  while (R * per * (((most + (1ll << shift) - 1) >> shift) + unit_cost) > kMaxPositions && shift < 24) ++shift;
+  return shift;
+}
 
 struct Segment {
   int unit;          // (r * heads + unit head) * groups + group
   int r, head, group;
-  int o0, o1, cap;   // items [o0, o1) of cap
-  long long start;   // the unit's first position
+  int o0, o1, cap;   // lots [o0, o1) of cap
+  int start;         // the unit's first position
   bool live;         // false: nothing to do in this stretch
 };
 
@@ -108,58 +154,47 @@ __device__ __forceinline__ int find_request(const int* pre, int R, int x) {
   return lo;
 }
 
-// x / y of two positions (x >= 0, y > 0): in 32 bits where they fit, which is
-// several times as fast.
-__device__ __forceinline__ long long div(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return (unsigned int)x / (unsigned int)y;
-  return x / y;
-}
-
 // A walk over the stretches of [pos, end), unit by unit: one search at its
 // start, no division after it.
 struct Walk {
-  long long pos, end, start;   // start: the current unit's first position
+  int pos, end, start;   // start: the current unit's first position
   int r, head, group, unit, wt;
 
-  __device__ __forceinline__ void begin(const int* pre, int R, int heads, int groups,
-                                        long long first, long long last) {
+  __device__ __forceinline__ void begin(const AttnArgs& a, const int* pre, int first, int last) {
     pos = first;
     end = last;
     if (pos >= end) return;
-    const int per = heads * groups;
-    r = find_request(pre, R, (int)div(pos, per));
+    r = find_request(pre, a.R, a.by_per.div(pos));
     wt = pre[r + 1] - pre[r];
-    const long long base = (long long)pre[r] * per;
-    const int k = (int)div(pos - base, wt);
-    start = base + (long long)k * wt;
-    head = k / groups;
-    group = k - head * groups;
+    const int per = (int)a.by_per.d, base = pre[r] * per;
+    const int k = per == 1 ? 0 : (pos - base) / wt;
+    start = base + k * wt;
+    head = a.by_groups.div(k);
+    group = k - head * a.groups;
     unit = r * per + k;
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
-  __device__ __forceinline__ Segment next(const int* pre, int R, int heads, int groups) {
+  __device__ __forceinline__ Segment next(const AttnArgs& a, const int* pre) {
     Segment s;
     s.unit = unit;
     s.r = r;
     s.head = head;
     s.group = group;
     s.start = start;
-    s.cap = wt - kUnitCost;
-    const int o = (int)(pos - start);
-    const long long left = end - pos;
-    const int take = left < wt - o ? (int)left : wt - o;
-    s.o0 = o < s.cap ? o : s.cap;
-    s.o1 = o + take < s.cap ? o + take : s.cap;
+    s.cap = wt - a.unit_cost;
+    const int o = pos - start, take = min(end - pos, wt - o);
+    s.o0 = min(o, s.cap);
+    s.o1 = min(o + take, s.cap);
     s.live = s.o1 > s.o0 || (s.cap == 0 && o == 0);
     pos += take;
     if (o + take == wt) {
       start += wt;
       ++unit;
-      if (++group == groups) {
+      if (++group == a.groups) {
         group = 0;
-        if (++head == heads) {
+        if (++head == a.heads) {
           head = 0;
-          if (++r < R) wt = pre[r + 1] - pre[r];
+          if (++r < a.R) wt = pre[r + 1] - pre[r];
         }
       }
     }
@@ -168,8 +203,8 @@ struct Walk {
 };
 
 // The CTA that holds position x.
-__device__ __forceinline__ int owner(long long x, long long W, int C) {
-  return (int)div((x + 1) * C + W - 1, W) - 1;
+__device__ __forceinline__ int owner(int x, int W, int C) {
+  return ((x + 1) * C + W - 1) / W - 1;   // at most W (C + 1) < 2^31
 }
 
 }  // namespace attn

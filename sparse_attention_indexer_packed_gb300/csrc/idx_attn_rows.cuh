@@ -102,10 +102,11 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
       if (kBlocks) {
         // at most: every draft row of a group lists other blocks
         const int drafts = min(a.P, (a.group_rows + a.nq - 2) / a.nq + 1);
-        wt = min((n + kBlock - 1) / kBlock, a.topk * drafts) * (kBlock / IT) + kUnitCost;
+        wt = min((n + kBlock - 1) / kBlock, a.topk * drafts) * (kBlock / IT);
       } else {
-        wt = (n + IT - 1) / IT + kUnitCost;
+        wt = (n + IT - 1) / IT;
       }
+      wt = ((wt + (1 << a.shift) - 1) >> a.shift) + a.unit_cost;
     }
     int incl = wt;
 #pragma unroll
@@ -140,13 +141,14 @@ __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq,
   constexpr int kKeep = 2;   // entries a thread keeps in registers between the passes
   uint32_t* rank = bits + kMaxBlockWords;
   const int lane = threadIdx.x & 31, nt = blockDim.x;
-  const int which = s.head * a.lists / a.heads;
+  const int which = a.by_list.div(s.head);
   const int longest = rq.len[s.r];
   const int words = (longest + 32 * kBlock - 1) / (32 * kBlock);
   const int entries = longest > 0 ? (p1 - p0 + 1) * a.topk : 0;
   auto entry = [&](int e, int& p) {
-    p = p0 + e / a.topk;
-    const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + which) * a.topk + e % a.topk);
+    const int d = a.by_topk.div(e);
+    p = p0 + d;
+    const int id = __ldg(a.block_ids + (((size_t)s.r * a.P + p) * a.lists + which) * a.topk + (e - d * a.topk));
     return id >= 0 && (long long)id * kBlock < row_len(a, s.r, p) ? id : -1;
   };
   int keep[kKeep], who[kKeep];
@@ -218,22 +220,28 @@ struct Items {
 
 // The items of a stretch.  n: the unit's joined items (block lists), of which the
 // stretch takes the share that its positions have of the unit's.
-template <bool kBlocks>
+template <int IT, bool kBlocks>
 __device__ __forceinline__ Items make_items(const AttnArgs& a, const Requests& rq, const Segment& s,
                                             int n) {
   Items it;
   it.r = s.r;
   it.head = s.head;
-  it.kv_head = s.head * a.kv_heads / a.heads;
+  it.kv_head = a.by_kv.div(s.head);
   it.slot = rq.slot[s.r];
   it.glen = rq.len[s.r];
   if (kBlocks) {
-    it.i0 = s.cap ? (int)((long long)n * s.o0 / s.cap) : 0;
-    it.i1 = s.cap ? (int)((long long)n * s.o1 / s.cap) : 0;
+    // the unit has n items, at most cap lots: every CTA takes its share of them
+    const int lots = (n + (1 << a.shift) - 1) >> a.shift;
+    const bool exact = lots >= s.cap;
+    it.i0 = exact ? s.o0 : (int)((float)lots * (float)s.o0 / (float)s.cap);
+    it.i1 = exact || s.o1 == s.cap ? min(s.o1, lots) : (int)((float)lots * (float)s.o1 / (float)s.cap);
   } else {
+    n = (it.glen + IT - 1) / IT;
     it.i0 = s.o0;
     it.i1 = s.o1;
   }
+  it.i0 = min(it.i0 << a.shift, n);
+  it.i1 = min(it.i1 << a.shift, n);
   return it;
 }
 

@@ -274,13 +274,11 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl[3];
 
-  const int per = a.heads * a.groups;
-  const long long W = (long long)rq.pre[a.R] * per;
+  const int W = rq.pre[a.R] * (int)a.by_per.d;
   // no CTA takes less than about four pages
-  const long long want = (W + 3) / 4;
-  const int C = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
+  const int C = min((W + 4 - 1) / 4, (int)gridDim.x);
   const int c = blockIdx.x;
-  const long long begin = c < C ? div(W * c, C) : 0, end = c < C ? div(W * (c + 1), C) : 0;
+  const int begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
   SplitRecord record = {-1, 0};
 
   // A bounded wait of a whole warp; false once any role has given up.
@@ -310,19 +308,19 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   int segs = 0;             // segments with pages so far
   int cnt0 = 0, cnt1 = 0;   // pages of group 0 / 1 so far
   Walk walk;
-  walk.begin(rq.pre, a.R, a.heads, a.groups, begin, end);
+  walk.begin(a, rq.pre, begin, end);
   while (walk.more()) {
-    const Segment s = walk.next(rq.pre, a.R, a.heads, a.groups);
+    const Segment s = walk.next(a, rq.pre);
     if (!s.live) continue;
     const int row_first = s.group * a.group_rows;
     const int nrows = min(a.group_rows, a.P * a.nq - row_first);
-    const int p0 = row_first / a.nq;
+    const int p0 = a.by_nq.div(row_first);
     int n_items = 0;
     if (kBlocks) {
       __syncthreads();      // every role is done with the last unit's list
       n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits);
     }
-    const Items it = make_items<kBlocks>(a, rq, s, n_items);
+    const Items it = make_items<kTok, kBlocks>(a, rq, s, n_items);
     // the second page of a request's last block may not exist
     int i1 = it.i1;
     if (kBlocks && i1 == n_items && n_items > 0 &&
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
       const int row = quad * kWarpRows + lane % kWarpRows;   // of the group
       const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
       const bool live = row < nrows;
-      const int pk = row_first + (live ? row : 0), p = pk / a.nq;
+      const int pk = row_first + (live ? row : 0), p = a.by_nq.div(pk);
       const size_t q_row = ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
       const bool pad = it.slot < 0 || it.slot >= a.n_slots;
       const int len = live && !pad ? row_len(a, s.r, p) : 0;
@@ -732,7 +730,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
         const int r2 = __shfl_sync(0xffffffffu, row, src);
-        const int pk2 = row_first + r2, p2 = pk2 / a.nq;
+        const int pk2 = row_first + r2, p2 = a.by_nq.div(pk2);
         const size_t q2 = ((size_t)s.r * a.P + p2) * a.q_heads + s.head * a.nq + (pk2 - p2 * a.nq);
         float m2, l2;
         float4 o2;

@@ -8,7 +8,9 @@
 //
 // What bounds it: 256 bytes in and 256 (or 132) out a row: HBM, and for a decode
 // step's few rows the launch.  16 lanes hold a row (one 16-byte load a lane), so
-// a warp's loads cover two whole rows and the row maximum is four shuffles.
+// the row maximum is four shuffles.  A CTA takes consecutive tokens of one head
+// and one plane, whose rows and scales lie side by side in the cache: their writes
+// fill whole sectors.
 #include <stdint.h>
 
 #include "idx_internal.cuh"
@@ -18,60 +20,77 @@ namespace idx {
 
 namespace {
 
-template <int KF>
-__global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a) {
+constexpr int kRowsAtOnce = 16;   // rows of a 256-thread CTA at a time
+
+// Each 16 lanes store kTokens rows, kRowsAtOnce tokens apart; their loads all go
+// out before any is used.
+template <int KF, int kTokens>
+__global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int chunks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long rows = a.tokens * a.heads;
-  const long long item = (long long)blockIdx.x * (blockDim.x / 16) + threadIdx.x / 16;
+  const int hp = blockIdx.x / chunks, chunk = blockIdx.x - hp * chunks;
+  const int plane = hp >= a.heads, h = hp - (plane ? a.heads : 0);
   const int lane = threadIdx.x & 15;
-  const int plane = item >= rows;
-  const long long k = item - (plane ? rows : 0);
-  const bool live = k < rows && plane < a.planes;
-  long long slot = -1;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  long long tok = 0;
-  int h = 0;
-  if (live) {
-    tok = k / a.heads;
-    h = (int)(k - tok * a.heads);
-    slot = __ldg(reinterpret_cast<const long long*>(a.slots) + tok);
-    const uint16_t* src = plane ? a.src[1] + tok * a.stride[1] : a.src[0] + tok * a.stride[0];
-    u = __ldg(reinterpret_cast<const uint4*>(src + h * kDim) + lane);
-  }
-  const bool write = slot >= 0 && slot < a.num_slots;
-  const long long row = (slot / kPage * a.heads + h) * kPage + slot % kPage;
+  const uint16_t* src = (plane ? a.src[1] : a.src[0]) + h * kDim;
+  const long long stride = plane ? a.stride[1] : a.stride[0];
   uint8_t* payload = plane ? a.payload[1] : a.payload[0];
-  if (KF == kBf16) {
-    if (write) reinterpret_cast<uint4*>(payload + row * 256)[lane] = u;
-    return;
-  }
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  float x[8], m = 0.f;
+  const long long tok0 = (long long)chunk * (kRowsAtOnce * kTokens) + threadIdx.x / 16;
+  uint4 u[kTokens];
+  long long row[kTokens];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    m = fmax_nan(m, fmax_nan(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+  for (int j = 0; j < kTokens; ++j) {
+    const long long tok = tok0 + j * kRowsAtOnce;
+    u[j] = make_uint4(0, 0, 0, 0);
+    row[j] = -1;
+    if (tok < a.tokens) {
+      u[j] = __ldcs(reinterpret_cast<const uint4*>(src + tok * stride) + lane);
+      row[j] = __ldg(reinterpret_cast<const long long*>(a.slots) + tok);
+    }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float amax = fmax_nan(m, kAmaxFloor), up = e4m3_up(amax);
-  if (!write) return;
-  const uint32_t lo = e4m3x2(__fmul_rn(x[0], up), __fmul_rn(x[1], up)) |
-                      (e4m3x2(__fmul_rn(x[2], up), __fmul_rn(x[3], up)) << 16);
-  const uint32_t hi = e4m3x2(__fmul_rn(x[4], up), __fmul_rn(x[5], up)) |
-                      (e4m3x2(__fmul_rn(x[6], up), __fmul_rn(x[7], up)) << 16);
-  reinterpret_cast<uint2*>(payload + row * 128)[lane] = make_uint2(lo, hi);
-  if (lane == 0) (plane ? a.scale[1] : a.scale[0])[row] = __fdiv_rn(amax, kE4m3Max);
+  for (int j = 0; j < kTokens; ++j) {
+    const long long slot = row[j];
+    const bool write = slot >= 0 && slot < a.num_slots;
+    const long long r = (slot / kPage * a.heads + h) * kPage + slot % kPage;
+    if (KF == kBf16) {
+      if (write) reinterpret_cast<uint4*>(payload + r * 256)[lane] = u[j];
+      continue;
+    }
+    const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+    float x[8], m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      m = fmax_nan(m, fmax_nan(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float amax = fmax_nan(m, kAmaxFloor), up = e4m3_up(amax);
+    if (!write) continue;
+    const uint32_t lo = e4m3x2(__fmul_rn(x[0], up), __fmul_rn(x[1], up)) |
+                        (e4m3x2(__fmul_rn(x[2], up), __fmul_rn(x[3], up)) << 16);
+    const uint32_t hi = e4m3x2(__fmul_rn(x[4], up), __fmul_rn(x[5], up)) |
+                        (e4m3x2(__fmul_rn(x[6], up), __fmul_rn(x[7], up)) << 16);
+    reinterpret_cast<uint2*>(payload + r * 128)[lane] = make_uint2(lo, hi);
+    if (lane == 0) (plane ? a.scale[1] : a.scale[0])[r] = __fdiv_rn(amax, kE4m3Max);
+  }
+}
+
+template <int KF>
+cudaError_t launch(const StoreArgs& a, cudaStream_t stream) {
+  // four rows a thread once that still gives every SM a CTA or two
+  const bool many = a.tokens * a.heads * a.planes >= 16384;
+  const int per = kRowsAtOnce * (many ? 4 : 1);
+  const int chunks = (int)((a.tokens + per - 1) / per);
+  const int grid = chunks * a.heads * a.planes;
+  return many ? launch_pdl(store_kv_kernel<KF, 4>, grid, 256, 0, stream, a, chunks)
+              : launch_pdl(store_kv_kernel<KF, 1>, grid, 256, 0, stream, a, chunks);
 }
 
 }  // namespace
 
 cudaError_t launch_store_kv(int key_format, const StoreArgs& a, cudaStream_t stream) {
-  const long long items = a.tokens * a.heads * a.planes;
-  const int grid = (int)((items + 15) / 16);
-  cudaError_t e = key_format == kBf16 ? launch_pdl(store_kv_kernel<kBf16>, grid, 256, 0, stream, a)
-                                      : launch_pdl(store_kv_kernel<kFp8>, grid, 256, 0, stream, a);
+  const cudaError_t e = key_format == kBf16 ? launch<kBf16>(a, stream) : launch<kFp8>(a, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -40,7 +40,7 @@ BAD = [
     (dict(vp=None), -1), (dict(table=None), -1), (dict(slots=None), -1), (dict(lens=None), -1),
     (dict(out=None), -1), (dict(ws=None), -1), (dict(ws=FAKE + 64), -1), (dict(nb=1000), -1),
     (dict(q=FAKE + 8), -1), (dict(kp=FAKE + 8), -1), (dict(vp=FAKE + 8), -1),
-    (dict(dtype=1, ks=FAKE + 4, vs=FAKE), -1),
+    (dict(dtype=1, ks=FAKE + 4, vs=FAKE), -1), (dict(R=2048, P=1, Hq=1024, kv_heads=1024), -1),
 ]
 
 
