@@ -159,8 +159,7 @@ struct QRows {
 // Softmax state of the two rows a lane holds (g and g + 8), and its part of the
 // unnormalised output.  m in log2 units, the same in the four lanes of a row;
 // l is the lane's own part of the sum.  e4m3 values: o is held in units of mv, a
-// power of two at or above every value scale so far, so that weight times
-// scale / mv fits f16.
+// power of two, so that weight times scale / mv fits f16.
 struct State {
   float m0, m1, l0, l1, mv;
   float o[16][4];
@@ -211,82 +210,95 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
         }
     }
   }
-  // scores in log2 units, their row maxima
+  // y: the scores before the rows' factor, two tokens of a row at a time; their
+  // row maxima (post is positive, so it keeps the order)
+  float2 y0[4], y1[4];
   float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
   for (int nt = 0; nt < 4; ++nt) {
-    float f0 = q.post0, f1 = q.post0, f2 = q.post1, f3 = q.post1;
+    y0[nt] = make_float2(s[nt][0], s[nt][1]);
+    y1[nt] = make_float2(s[nt][2], s[nt][3]);
     if (KF == kFp8) {
       const float2 ks = *reinterpret_cast<const float2*>(scales + nt * 8 + 2 * t);
-      f0 *= ks.x, f1 *= ks.y, f2 *= ks.x, f3 *= ks.y;
+      y0[nt] = fmul2_rn(y0[nt], ks);
+      y1[nt] = fmul2_rn(y1[nt], ks);
     }
-    s[nt][0] *= f0, s[nt][1] *= f1, s[nt][2] *= f2, s[nt][3] *= f3;
     if (kMask) {
       const int t0 = tb + nt * 8 + 2 * t;
-      if (t0 >= len0) s[nt][0] = -INFINITY;
-      if (t0 + 1 >= len0) s[nt][1] = -INFINITY;
-      if (t0 >= len1) s[nt][2] = -INFINITY;
-      if (t0 + 1 >= len1) s[nt][3] = -INFINITY;
+      if (t0 >= len0) y0[nt].x = -INFINITY;
+      if (t0 + 1 >= len0) y0[nt].y = -INFINITY;
+      if (t0 >= len1) y1[nt].x = -INFINITY;
+      if (t0 + 1 >= len1) y1[nt].y = -INFINITY;
     }
-    mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
-    mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+    mx0 = fmaxf(mx0, fmaxf(y0[nt].x, y0[nt].y));
+    mx1 = fmaxf(mx1, fmaxf(y1[nt].x, y1[nt].y));
   }
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
   }
-  const float mn0 = fmaxf(st.m0, mx0), mn1 = fmaxf(st.m1, mx1);
+  const float mn0 = fmaxf(st.m0, mx0 * q.post0), mn1 = fmaxf(st.m1, mx1 * q.post1);
   const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
   float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
   st.m0 = mn0, st.m1 = mn1;
-  float l0 = 0.f, l1 = 0.f;
+  const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
+  const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
+  float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
   for (int nt = 0; nt < 4; ++nt) {
-    s[nt][0] = ex2_approx(s[nt][0] - ref0);
-    s[nt][1] = ex2_approx(s[nt][1] - ref0);
-    s[nt][2] = ex2_approx(s[nt][2] - ref1);
-    s[nt][3] = ex2_approx(s[nt][3] - ref1);
-    l0 += s[nt][0] + s[nt][1];
-    l1 += s[nt][2] + s[nt][3];
+    y0[nt] = ffma2_rn(y0[nt], p0, r0);
+    y1[nt] = ffma2_rn(y1[nt], p1, r1);
+    y0[nt].x = ex2_approx(y0[nt].x), y0[nt].y = ex2_approx(y0[nt].y);
+    y1[nt].x = ex2_approx(y1[nt].x), y1[nt].y = ex2_approx(y1[nt].y);
+    l0 = fadd2_rn(l0, y0[nt]);
+    l1 = fadd2_rn(l1, y1[nt]);
   }
-  st.l0 = fmaf(st.l0, c0, l0);
-  st.l1 = fmaf(st.l1, c1, l1);
+  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
+  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
   if (KF == kFp8) {
-    // weights times value scales, in units of mv
-    float vs[4][2], top = 0.f;
+    // weights times value scales, in units of mv: a power of two that the scales
+    // may pass by 2^6 (a weight is at most 1, so f16 holds the product)
+    float2 vs[4];
+    float top = 0.f;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const float2 v = *reinterpret_cast<const float2*>(scales + kItem + nt * 8 + 2 * t);
-      vs[nt][0] = v.x, vs[nt][1] = v.y;
+      vs[nt] = *reinterpret_cast<const float2*>(scales + kItem + nt * 8 + 2 * t);
       if (kMask) {
         const int t0 = tb + nt * 8 + 2 * t;
-        if (t0 >= glen) vs[nt][0] = 0.f;
-        if (t0 + 1 >= glen) vs[nt][1] = 0.f;
+        if (t0 >= glen) vs[nt].x = 0.f;
+        if (t0 + 1 >= glen) vs[nt].y = 0.f;
       }
+      top = fmaxf(top, fmaxf(fabsf(vs[nt].x), fabsf(vs[nt].y)));
+    }
+    if (!(top < INFINITY)) {   // only finite scales set the unit
+      top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = fabsf(vs[nt][e]);
-        if (x < INFINITY) top = fmaxf(top, x);
+      for (int nt = 0; nt < 4; ++nt) {
+        if (fabsf(vs[nt].x) < INFINITY) top = fmaxf(top, fabsf(vs[nt].x));
+        if (fabsf(vs[nt].y) < INFINITY) top = fmaxf(top, fabsf(vs[nt].y));
       }
     }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float mv = fmaxf(st.mv, pow2_above(top));
-    const float inv = 1.f / mv;   // a power of two: exact
-    const float shrink = st.mv * inv;
-    st.mv = mv;
-    c0 *= shrink, c1 *= shrink;
+    if (__any_sync(0xffffffffu, top > st.mv * 64.f || st.mv == 0.f)) {
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mv = fmaxf(st.mv, pow2_above(top));
+      const float shrink = st.mv / mv;
+      st.mv = mv;
+      c0 *= shrink, c1 *= shrink;
+    }
+    const float inv = 1.f / st.mv;   // a power of two: exact
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const float r0 = vs[nt][0] * inv, r1 = vs[nt][1] * inv;
-      s[nt][0] *= r0, s[nt][1] *= r1, s[nt][2] *= r0, s[nt][3] *= r1;
+      const float2 r = fmul2_rn(vs[nt], make_float2(inv, inv));
+      y0[nt] = fmul2_rn(y0[nt], r);
+      y1[nt] = fmul2_rn(y1[nt], r);
       if (kMask) {   // a masked token's scale may be anything
         const int t0 = tb + nt * 8 + 2 * t;
-        if (t0 >= len0) s[nt][0] = 0.f;
-        if (t0 + 1 >= len0) s[nt][1] = 0.f;
-        if (t0 >= len1) s[nt][2] = 0.f;
-        if (t0 + 1 >= len1) s[nt][3] = 0.f;
+        if (t0 >= len0) y0[nt].x = 0.f;
+        if (t0 + 1 >= len0) y0[nt].y = 0.f;
+        if (t0 >= len1) y1[nt].x = 0.f;
+        if (t0 + 1 >= len1) y1[nt].y = 0.f;
       }
     }
   }
@@ -300,20 +312,17 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     uint32_t p[4], plo[4];
-    if (KF == kBf16) {
-      // a weight as the sum of two bf16 (together 16 bits): rounded to one, the
-      // weights would cost as much precision as the result's own rounding
+    const float2 w[4] = {y0[2 * ks], y1[2 * ks], y0[2 * ks + 1], y1[2 * ks + 1]};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = s[2 * ks + (e >> 1)][2 * (e & 1)], y = s[2 * ks + (e >> 1)][2 * (e & 1) + 1];
-        p[e] = pack_bf16(x, y);
-        plo[e] = pack_bf16(x - bf16_lo(p[e]), y - bf16_hi(p[e]));
+    for (int e = 0; e < 4; ++e) {
+      if (KF == kBf16) {
+        // a weight as the sum of two bf16 (together 16 bits): rounded to one, the
+        // weights would cost as much precision as the result's own rounding
+        p[e] = pack_bf16(w[e].x, w[e].y);
+        plo[e] = pack_bf16(w[e].x - bf16_lo(p[e]), w[e].y - bf16_hi(p[e]));
+      } else {
+        p[e] = pack_f16(w[e].x, w[e].y);
       }
-    } else {
-      p[0] = pack_f16(s[2 * ks][0], s[2 * ks][1]);
-      p[1] = pack_f16(s[2 * ks][2], s[2 * ks][3]);
-      p[2] = pack_f16(s[2 * ks + 1][0], s[2 * ks + 1][1]);
-      p[3] = pack_f16(s[2 * ks + 1][2], s[2 * ks + 1][3]);
     }
     uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;   // which of the lane's tokens exist
     if (kMask) {
@@ -686,14 +695,14 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 // The join of units that several CTAs shared.  Block (c, i): row i of the unit
 // that CTA c started and did not end.  Its parts are CTA c's second slot and the
 // first slots of the CTAs behind it; their maxima and sums are read at once, one
-// a thread, then four warps add the outputs, each its share in a fixed order, so
+// a thread, then the warps add the outputs, each its share in a fixed order, so
 // the result does not depend on timing.
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = 4, kJoinThreads = 32 * kJoinWarps;
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
   __shared__ float factor[kMaxCtas];
-  __shared__ float red[2][4];
-  __shared__ float4 so[4][32];
+  __shared__ float red[2][kJoinWarps];
+  __shared__ float4 so[kJoinWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = min(a.group_rows, a.P * a.nq);
   const int c = blockIdx.x / rows, i = blockIdx.x - c * rows;
@@ -704,11 +713,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   if (pk >= a.P * a.nq) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto part = [&](int s) { return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i; };
-  constexpr int kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
-  float2 x[kPer];
+  static_assert(kMaxCtas <= 2 * kJoinThreads, "two parts a thread");
+  float2 x[2];
   float m = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
+  for (int e = 0; e < 2; ++e) {
     const int s = threadIdx.x + e * kJoinThreads;
     x[e] = s < rec.splits ? a.part_ml[part(s)] : make_float2(-INFINITY, 0.f);
     m = fmaxf(m, x[e].x);
@@ -717,35 +726,47 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) red[0][warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[0][w]);
   float l = 0.f;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int s = threadIdx.x + e * kJoinThreads;
+  for (int e = 0; e < 2; ++e) {
     // a part with nothing visible in the row is not read: factor -1 says so
+    const int s = threadIdx.x + e * kJoinThreads;
     const float f = x[e].x == -INFINITY ? -1.f : ex2_approx(x[e].x - m);
-    if (s < rec.splits) {
-      factor[s] = f;
-      if (f >= 0.f || f != f) l = fmaf(x[e].y, f, l);
-    }
+    if (s < rec.splits) factor[s] = f;
+    if (x[e].x != -INFINITY) l = fmaf(x[e].y, f, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l += red[1][w];
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = warp; s < rec.splits; s += 4) {
-    const float f = factor[s];
-    if (f == -1.f) continue;
-    const float4 v = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[lane];
-    o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+  // eight parts' loads at a time
+  for (int s0 = warp; s0 < rec.splits; s0 += 8 * kJoinWarps) {
+    float4 v[8];
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int s = s0 + e * kJoinWarps;
+      f[e] = s < rec.splits ? factor[s] : -1.f;
+      v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (f[e] != -1.f) v[e] = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[lane];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (f[e] != -1.f)
+        o = make_float4(fmaf(v[e].x, f[e], o.x), fmaf(v[e].y, f[e], o.y), fmaf(v[e].z, f[e], o.z),
+                        fmaf(v[e].w, f[e], o.w));
   }
   so[warp][lane] = o;
   __syncthreads();
   if (warp) return;
-  for (int w = 1; w < 4; ++w) {
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
     const float4 v = so[w][lane];
     o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
   }

@@ -55,8 +55,9 @@ using namespace attn;
 constexpr int kTok = kPage;          // tokens of a tile
 constexpr int kLanes = 128;          // tensor-memory lanes, product rows
 constexpr float kSlack = 8.f;        // log2 units a score may pass the running maximum by
-// Tensor-memory columns: the queries; S then P of each group; O of each group.
-constexpr int kColQ = 0, kColS = 64, kColO = 256, kCols = 512;
+// Tensor-memory columns: the queries; S of each group, and in its place P (bf16
+// caches), or P of its own, 32 columns a group (e4m3); O of each group.
+constexpr int kColQ = 0, kColS = 64, kColP = 192, kColO = 256, kCols = 512;
 
 template <int KF>
 struct AWCfg;
@@ -71,7 +72,7 @@ struct AWCfg<kBf16> {
 template <>
 struct AWCfg<kFp8> {
   static constexpr int kRowBytes = 128;
-  static constexpr int kStages = 8;
+  static constexpr int kStages = 6;
   static constexpr uint32_t kIdQK = instr_desc(0u, kLanes, kTok);                // e4m3
   static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);   // f16
 };
@@ -80,16 +81,16 @@ template <int KF>
 struct AWLayout {
   static constexpr int NS = AWCfg<KF>::kStages;
   static constexpr int kTile = kTok * AWCfg<KF>::kRowBytes;  // keys or values of a page
-  static constexpr int kV16 = KF == kFp8 ? kTok * 256 : 0;   // decoded values, one a group
+  static constexpr int kV16 = KF == kFp8 ? kTok * 256 : 0;   // decoded values, two a group
   static constexpr int kScale = KF == kFp8 ? kTok * 4 : 0;
   static constexpr int kV16Off = NS * 2 * kTile;
-  static constexpr int kScaleOff = kV16Off + 2 * kV16;
+  static constexpr int kScaleOff = kV16Off + 4 * kV16;
   static constexpr int kXchOff = kScaleOff + NS * 2 * kScale;  // [32 dims][128 rows] floats
   static constexpr int kMlOff = kXchOff + 32 * kLanes * 4;
   static constexpr int kInfoOff = kMlOff + 2 * kLanes * 8;     // valid tokens of each stage
-  // full_k full_v empty_k empty_v [NS], s_full p_full pv_done [2], q_full, stall, drain
+  // full_k full_v empty_k empty_v [NS], s_full p_full pv_done s_free [2], q_full, stall, drain
   static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
-  static constexpr int kNumBars = 4 * NS + 9;
+  static constexpr int kNumBars = 4 * NS + 11;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;       // flags, count, abort, tmem
   static constexpr int kPreOff = (kCtlOff + 16 + 48 + 15) & ~15;   // and one int a warp
   static constexpr int kListOff = kPreOff + kRequestsBytes;
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   auto s_full = [&](int g) { return bars + 8 * (4 * NS + g); };
   auto p_full = [&](int g) { return bars + 8 * (4 * NS + 2 + g); };
   auto pv_done = [&](int g) { return bars + 8 * (4 * NS + 4 + g); };
-  const uint32_t q_full = bars + 8 * (4 * NS + 6), stall_bar = q_full + 8, drain = q_full + 16;
+  auto s_free = [&](int g) { return bars + 8 * (4 * NS + 6 + g); };
+  const uint32_t q_full = bars + 8 * (4 * NS + 8), stall_bar = q_full + 8, drain = q_full + 16;
   auto k_tile = [&](int s) { return sbase + s * 2 * L::kTile; };
   auto v_tile = [&](int s) { return sbase + s * 2 * L::kTile + L::kTile; };
 
@@ -254,6 +256,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
       mbar_init(s_full(g), 1);
       mbar_init(p_full(g), kLanes);
       mbar_init(pv_done(g), 1);
+      mbar_init(s_free(g), 4);
     }
     mbar_init(q_full, kLanes);
     mbar_init(stall_bar, 1);
@@ -417,12 +420,16 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
       int k0 = cnt0, k1 = cnt1;
       for (int b = 0; b < n && ok; ++b) {
         const int tile = tile0 + b, st = tile % NS, g = b & 1;
-        const uint32_t ph = (uint32_t)((g ? k1++ : k0++) & 1);
-        ok = wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
+        const int cnt = g ? k1++ : k0++;
+        const uint32_t ph = (uint32_t)(cnt & 1);
+        // e4m3: the group's next scores as soon as it has read these
+        if (KF == kFp8 && b + 2 < n) ok = wait(s_free(g), ph) && qk(b + 2);
+        ok = ok && wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + kColO + kDim * g, p = tmem + kColS + 64 * g;
-        const uint32_t v = KF == kBf16 ? v_tile(st) : sbase + L::kV16Off + g * L::kV16;
+        const uint32_t d = tmem + kColO + kDim * g;
+        const uint32_t p = tmem + (KF == kBf16 ? kColS + 64 * g : kColP + 32 * g);
+        const uint32_t v = KF == kBf16 ? v_tile(st) : sbase + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16;
 #pragma unroll
         for (int ks = 0; ks < kTok / 16; ++ks) {
           const uint64_t vd = desc_mnmajor_sw128(v + ks * 2048, kTok * 128);
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
         }
         if (KF == kBf16) tc_commit_warp(empty_v(st));
         tc_commit_warp(pv_done(g));
-        if (b + 2 < n) ok = qk(b + 2);
+        if (KF == kBf16 && b + 2 < n) ok = qk(b + 2);
       }
     } else {
       // ---- softmax group g: pages g, g + 2, ... ------------------------------
@@ -489,6 +496,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
       float m = -INFINITY, l = 0.f, mv = 0.f;
       int cnt = g ? cnt1 : cnt0;
       const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
+      const uint32_t pp = KF == kBf16 ? sp : tl + kColP + 32 * g;
       for (int b = g; b < n; b += 2, ++cnt) {
         const int tile = tile0 + b, st = tile % NS;
         int tb;
@@ -497,9 +505,9 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
         if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
         const int valid = info[st];
         if (KF == kFp8) {
-          // this page's values as f16, rows past the request's tokens as zeros;
-          // the buffer is free once the group's last product has ended
-          if (cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
+          // this page's values as f16, rows past the request's tokens as zeros, in
+          // the buffer of the group's page before the last (whose product has
+          // ended: that was waited for before the last page's weights)
           const int t = threadIdx.x & 127;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
             e4m3x4_to_f16x2x2(u.z, y.x, y.y);
             e4m3x4_to_f16x2x2(u.w, y.z, y.w);
             // dims 16 ch .. +7 and +8 .. +15: two 16-byte chunks of a 64-dim half
-            uint8_t* base = smem + L::kV16Off + g * L::kV16 + (ch >> 2) * (kTok * 128) + tok * 128;
+            uint8_t* base = smem + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16 + (ch >> 2) * (kTok * 128) + tok * 128;
             const int c0 = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = x;
             *reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (tok & 7)) << 4)) = y;
@@ -546,30 +554,42 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
             for (int f = 1; f < F; ++f) raw[j] = part == f ? all[f][j] : raw[j];
           }
         }
-        float x[kPart];
+        if (KF == kFp8) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free(g));
+        }
+        // y: the scores before the row's factor, two tokens at a time
+        constexpr int kHalf = kPart / 2;
+        float2 y[kHalf];
         const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * 2 * L::kScale) + part * kPart;
 #pragma unroll
-        for (int j = 0; j < kPart; j += 4) {
-          float4 f = make_float4(post, post, post, post);
-          if (KF == kFp8) {
-            const float4 k4 = *reinterpret_cast<const float4*>(ks + j);
-            f = make_float4(post * k4.x, post * k4.y, post * k4.z, post * k4.w);
+        for (int j = 0; j < kHalf; ++j)
+          y[j] = make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
+        if (KF == kFp8) {
+#pragma unroll
+          for (int j = 0; j < kHalf; j += 2) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ks + 2 * j);
+            y[j] = fmul2_rn(y[j], make_float2(k4.x, k4.y));
+            y[j + 1] = fmul2_rn(y[j + 1], make_float2(k4.z, k4.w));
           }
-          x[j] = __uint_as_float(raw[j]) * f.x;
-          x[j + 1] = __uint_as_float(raw[j + 1]) * f.y;
-          x[j + 2] = __uint_as_float(raw[j + 2]) * f.z;
-          x[j + 3] = __uint_as_float(raw[j + 3]) * f.w;
         }
         const int visible = min(min(len, tb + valid) - tb, (members >> bit) & 1u ? kTok : 0) - part * kPart;
         const bool masked = __any_sync(0xffffffffu, visible < kPart);
         if (masked) {
 #pragma unroll
-          for (int j = 0; j < kPart; ++j)
-            if (j >= visible) x[j] = -INFINITY;
+          for (int j = 0; j < kHalf; ++j) {
+            if (2 * j >= visible) y[j].x = -INFINITY;
+            if (2 * j + 1 >= visible) y[j].y = -INFINITY;
+          }
         }
-        float top = x[0];
+        float t0 = fmaxf(y[0].x, y[0].y), t1 = fmaxf(y[1].x, y[1].y);
 #pragma unroll
-        for (int j = 1; j < kPart; ++j) top = fmaxf(top, x[j]);
+        for (int j = 2; j < kHalf; j += 2) {
+          t0 = fmaxf(t0, fmaxf(y[j].x, y[j].y));
+          t1 = fmaxf(t1, fmaxf(y[j + 1].x, y[j + 1].y));
+        }
+        const float top = fmaxf(t0, t1) * post;   // post is positive: the order is kept
         float shrink = 1.f;     // what the output gathered so far is to be multiplied by
         if (top > m + (m == -INFINITY ? 0.f : kSlack)) {
           shrink = ex2_approx(m - top);
@@ -577,27 +597,44 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
           m = top;
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum = 0.f;
+        const float2 pp2 = make_float2(post, post), rr2 = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-        for (int j = 0; j < kPart; ++j) {
-          x[j] = ex2_approx(x[j] - ref);
-          sum += x[j];
+        for (int j = 0; j < kHalf; ++j) {
+          y[j] = ffma2_rn(y[j], pp2, rr2);
+          y[j].x = ex2_approx(y[j].x), y[j].y = ex2_approx(y[j].y);
+          if (j & 1) sum1 = fadd2_rn(sum1, y[j]);
+          else sum0 = fadd2_rn(sum0, y[j]);
         }
-        l += sum;
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         if (KF == kFp8) {
           // times the value scales, in units of mv: a power of two that the
           // scales may pass by 2^6 (weights up to 2^8 stay inside f16)
           const float* vs = ks + kTok;
-          float r[kPart], most = 0.f;
+          float2 r[kHalf];
+          float most = 0.f;
 #pragma unroll
-          for (int j = 0; j < kPart; j += 4) {
-            const float4 v4 = *reinterpret_cast<const float4*>(vs + j);
-            r[j] = v4.x, r[j + 1] = v4.y, r[j + 2] = v4.z, r[j + 3] = v4.w;
+          for (int j = 0; j < kHalf; j += 2) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vs + 2 * j);
+            r[j] = make_float2(v4.x, v4.y);
+            r[j + 1] = make_float2(v4.z, v4.w);
+          }
+          if (masked) {   // a masked token's scale may be anything
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) {
+              if (2 * j >= visible) r[j].x = 0.f;
+              if (2 * j + 1 >= visible) r[j].y = 0.f;
+            }
           }
 #pragma unroll
-          for (int j = 0; j < kPart; ++j) {
-            const float y = fabsf(r[j]);
-            if (y < INFINITY && (!masked || j < visible)) most = fmaxf(most, y);
+          for (int j = 0; j < kHalf; ++j) most = fmaxf(most, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
+          if (!(most < INFINITY)) {   // only finite scales set the unit
+            most = 0.f;
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) {
+              if (fabsf(r[j].x) < INFINITY) most = fmaxf(most, fabsf(r[j].x));
+              if (fabsf(r[j].y) < INFINITY) most = fmaxf(most, fabsf(r[j].y));
+            }
           }
           if (most > mv * 64.f || mv == 0.f) {
             const float up = pow2_above(most);
@@ -606,11 +643,12 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
           }
           const float inv = 1.f / mv;
 #pragma unroll
-          for (int j = 0; j < kPart; ++j) {
-            x[j] *= r[j] * inv;
-            if (masked && j >= visible) x[j] = 0.f;   // its scale may be anything
-          }
+          for (int j = 0; j < kHalf; ++j) y[j] = fmul2_rn(y[j], fmul2_rn(r[j], make_float2(inv, inv)));
         }
+        // e4m3: the output is still, and P's columns free, once the last product
+        // has ended (bf16: its scores came after that)
+        if (KF == kFp8 && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
+        if (KF == kFp8) tc_fence_after();
         if (b >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll
           for (int ch = 0; ch < kDim; ch += 32) {
@@ -623,14 +661,14 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
           }
         }
         // the weights as operand rows: the lane's own tokens, zeros for the others
-        uint32_t hi[kPart / 2], lo[kPart / 2];
+        uint32_t hi[kHalf], lo[kHalf];
 #pragma unroll
-        for (int j = 0; j < kPart / 2; ++j) {
+        for (int j = 0; j < kHalf; ++j) {
           if (KF == kBf16) {
-            hi[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-            lo[j] = pack_bf16(x[2 * j] - bf16_lo(hi[j]), x[2 * j + 1] - bf16_hi(hi[j]));
+            hi[j] = pack_bf16(y[j].x, y[j].y);
+            lo[j] = pack_bf16(y[j].x - bf16_lo(hi[j]), y[j].y - bf16_hi(hi[j]));
           } else {
-            hi[j] = pack_f16(x[2 * j], x[2 * j + 1]);
+            hi[j] = pack_f16(y[j].x, y[j].y);
           }
         }
 #pragma unroll
@@ -638,11 +676,11 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
           uint32_t z[kPart / 2];
 #pragma unroll
           for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
-          tm_st<kPart / 2>(sp + f * (kPart / 2), z);
+          tm_st<kPart / 2>(pp + f * (kPart / 2), z);
           if (KF == kBf16) {
 #pragma unroll
             for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
-            tm_st<kPart / 2>(sp + 32 + f * (kPart / 2), z);
+            tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
           }
         }
         tm_wait_st();
