@@ -40,6 +40,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "idx_attn.cuh"
 #include "idx_attn_rows.cuh"
@@ -77,9 +78,15 @@ struct AWCfg<kFp8> {
   static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);   // f16
 };
 
-template <int KF>
+template <int KF, int F>
 struct AWLayout {
   static constexpr int NS = AWCfg<KF>::kStages;
+  // Whether the softmax groups take registers from the other warps: 200 and more
+  // instead of 168.  128 rows (64 scores a lane) 76 -> 67 us on 8 x 64K bf16, e4m3
+  // 169 -> 162 on 16 x 131K; without it 64 rows of bf16 are 1% faster.
+  static constexpr bool kSplitRegs = KF == kFp8 || F == 1;
+  // two softmax groups; producer, issuer (and two idle warps: whole warpgroups)
+  static constexpr int kThreads = kSplitRegs ? 384 : 320;
   static constexpr int kTile = kTok * AWCfg<KF>::kRowBytes;  // keys or values of a page
   static constexpr int kV16 = KF == kFp8 ? kTok * 256 : 0;   // decoded values, two a group
   static constexpr int kScale = KF == kFp8 ? kTok * 4 : 0;
@@ -92,11 +99,10 @@ struct AWLayout {
   static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
   static constexpr int kNumBars = 4 * NS + 11;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;       // flags, count, abort, tmem
-  static constexpr int kPreOff = (kCtlOff + 16 + 48 + 15) & ~15;   // and one int a warp
+  static constexpr int kPreOff = (kCtlOff + 16 + kThreads / 32 * 4 + 15) & ~15;   // and one int a warp
   static constexpr int kListOff = kPreOff + kRequestsBytes;
   static constexpr int kBytes = kListOff + kMaxList * 4;
   static constexpr int kSmem = kBytes + 1024;
-  static constexpr int kThreads = 320;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // a list's bits are held in the exchange area, free between two units
   static_assert(2 * kMaxBlockWords * 4 <= 32 * kLanes * 4, "block bits");
@@ -212,10 +218,10 @@ __device__ __forceinline__ void group_sync() {   // the two softmax groups
 
 // F lanes a row (128 / F rows of a group, or fewer).
 template <int KF, int F, bool kBlocks>
-__global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
+__global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
     attn_wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
-  using L = AWLayout<KF>;
+  using L = AWLayout<KF, F>;
   constexpr int NS = L::NS;
   constexpr int kPart = kTok / F;      // tokens of a lane
   constexpr int kWarpRows = 32 / F;    // rows of a softmax warp
@@ -312,485 +318,500 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
   int cnt0 = 0, cnt1 = 0;   // pages of group 0 / 1 so far
   Walk walk;
   walk.begin(a, rq.pre, begin, end);
-  while (walk.more()) {
-    const Segment s = walk.next(a, rq.pre);
-    if (!s.live) continue;
-    const int row_first = s.group * a.group_rows;
-    const int nrows = min(a.group_rows, a.P * a.nq - row_first);
-    const int p0 = a.by_nq.div(row_first);
-    int n_items = 0;
-    if (kBlocks) {
-      __syncthreads();      // every role is done with the last unit's list
-      n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits);
-    }
-    const Items it = make_items<kTok, kBlocks>(a, rq, s, n_items);
-    // the second page of a request's last block may not exist
-    int i1 = it.i1;
-    if (kBlocks && i1 == n_items && n_items > 0 &&
-        (int)(list[n_items / 2 - 1] & 0xffffu) * kBlock + kPage >= it.glen)
-      --i1;
-    const int n = max(0, i1 - it.i0);
+  // The walk over the CTA's stretches, once for the softmax groups and once for the
+  // others: two copies of the code, each within its warps' registers.
+  auto work = [&](auto softmax) {
+    while (walk.more()) {
+      const Segment s = walk.next(a, rq.pre);
+      if (!s.live) continue;
+      const int row_first = s.group * a.group_rows;
+      const int nrows = min(a.group_rows, a.P * a.nq - row_first);
+      const int p0 = a.by_nq.div(row_first);
+      int n_items = 0;
+      if (kBlocks) {
+        __syncthreads();      // every role is done with the last unit's list
+        n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits);
+      }
+      const Items it = make_items<kTok, kBlocks>(a, rq, s, n_items);
+      // the second page of a request's last block may not exist
+      int i1 = it.i1;
+      if (kBlocks && i1 == n_items && n_items > 0 &&
+          (int)(list[n_items / 2 - 1] & 0xffffu) * kBlock + kPage >= it.glen)
+        --i1;
+      const int n = max(0, i1 - it.i0);
 
-    if (warp == 8) {
-      // ---- producer ---------------------------------------------------------
-      // page ids 32 items at a time, one a lane
-      auto page_of = [&](int i) {
-        int tb = 0, pg = -1;
-        uint32_t m;
-        if (i < i1 && item_tokens<kTok, kBlocks>(it, list, i, tb, m))
-          pg = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
-        if (i < i1 && (pg < 0 || pg >= a.num_pages)) {
-          atomicOr(ctl, kErrBadPage);
-          pg = -1;
-        }
-        return pg;
-      };
-      int next_ids = dead ? -1 : page_of(it.i0 + lane), ids = -1;
-      for (int b = 0; b < n && !dead; ++b) {
-        if ((b & 31) == 0) {
-          ids = next_ids;
-          next_ids = page_of(it.i0 + b + 32 + lane);
-        }
-        const int pg = __shfl_sync(0xffffffffu, ids, b & 31);
-        const int tile = tile0 + b, st = tile % NS;
-        const uint32_t ph = (uint32_t)((tile / NS) & 1) ^ 1u;
-        int tb = 0;
-        uint32_t m;
-        item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, m);
-        const int row = (pg * a.kv_heads + it.kv_head) * kPage;
-        if (!wait(empty_k(st), ph)) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile);
-          if (pg >= 0) {
-            tma_load_2d(k_tile(st), &k_map, 0, row, full_k(st));
-            if (KF == kBf16) tma_load_2d(k_tile(st) + L::kTile / 2, &k_map, 64, row, full_k(st));
+      if constexpr (!softmax.value) {
+      if (warp == 8) {
+        // ---- producer ---------------------------------------------------------
+        // page ids 32 items at a time, one a lane
+        auto page_of = [&](int i) {
+          int tb = 0, pg = -1;
+          uint32_t m;
+          if (i < i1 && item_tokens<kTok, kBlocks>(it, list, i, tb, m))
+            pg = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
+          if (i < i1 && (pg < 0 || pg >= a.num_pages)) {
+            atomicOr(ctl, kErrBadPage);
+            pg = -1;
           }
-        }
-        ++sent_k;
-        if (!wait(empty_v(st), ph)) break;
-        if (lane == 0) {
-          info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
-          // both planes' scales come with the values: the group reads them, and
-          // it gives the values' stage back itself
-          mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + 2 * L::kScale);
-          if (pg >= 0) {
-            tma_load_2d(v_tile(st), &v_map, 0, row, full_v(st));
-            if (KF == kBf16) {
-              tma_load_2d(v_tile(st) + L::kTile / 2, &v_map, 64, row, full_v(st));
-            } else {
-              const uint32_t sc = sbase + L::kScaleOff + st * 2 * L::kScale;
-              bulk_load(sc, a.k_scale + row, L::kScale, full_v(st));
-              bulk_load(sc + L::kScale, a.v_scale + row, L::kScale, full_v(st));
+          return pg;
+        };
+        int next_ids = dead ? -1 : page_of(it.i0 + lane), ids = -1;
+        for (int b = 0; b < n && !dead; ++b) {
+          if ((b & 31) == 0) {
+            ids = next_ids;
+            next_ids = page_of(it.i0 + b + 32 + lane);
+          }
+          const int pg = __shfl_sync(0xffffffffu, ids, b & 31);
+          const int tile = tile0 + b, st = tile % NS;
+          const uint32_t ph = (uint32_t)((tile / NS) & 1) ^ 1u;
+          int tb = 0;
+          uint32_t m;
+          item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, m);
+          const int row = (pg * a.kv_heads + it.kv_head) * kPage;
+          if (!wait(empty_k(st), ph)) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile);
+            if (pg >= 0) {
+              tma_load_2d(k_tile(st), &k_map, 0, row, full_k(st));
+              if (KF == kBf16) tma_load_2d(k_tile(st) + L::kTile / 2, &k_map, 64, row, full_k(st));
             }
           }
-        }
-        ++sent_v;
-        __syncwarp();
-      }
-    } else if (warp == 9) {
-      // ---- product issuer -----------------------------------------------------
-      constexpr uint32_t kIdQK = AWCfg<KF>::kIdQK, kIdPV = AWCfg<KF>::kIdPV;
-      auto qk = [&](int b) -> bool {
-        const int tile = tile0 + b, st = tile % NS, g = b & 1;
-        if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + kColS + 64 * g;
-        if (KF == kBf16) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts_f16(d, tmem + kColQ + ks * 8,
-                       desc_kmajor_sw128(k_tile(st) + (ks >> 2) * (L::kTile / 2) + (ks & 3) * 32),
-                       kIdQK, ks > 0);
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)   // the query's two terms, four steps of 32 each
-            mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32), kIdQK,
-                      ks > 0);
-        }
-        tc_commit_warp(empty_k(st));
-        tc_commit_warp(s_full(g));
-        return true;
-      };
-      bool ok = n > 0 && !dead;
-      if (ok && a.stall_test && segs == 0) ok = wait(stall_bar, 0);
-      ok = ok && wait(q_full, (uint32_t)(segs & 1));
-      tc_fence_after();
-      ok = ok && qk(0);
-      if (n > 1) ok = ok && qk(1);
-      int k0 = cnt0, k1 = cnt1;
-      for (int b = 0; b < n && ok; ++b) {
-        const int tile = tile0 + b, st = tile % NS, g = b & 1;
-        const int cnt = g ? k1++ : k0++;
-        const uint32_t ph = (uint32_t)(cnt & 1);
-        // e4m3: the group's next scores as soon as it has read these
-        if (KF == kFp8 && b + 2 < n) ok = wait(s_free(g), ph) && qk(b + 2);
-        ok = ok && wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + kColO + kDim * g;
-        const uint32_t p = tmem + (KF == kBf16 ? kColS + 64 * g : kColP + 32 * g);
-        const uint32_t v = KF == kBf16 ? v_tile(st) : sbase + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16;
-#pragma unroll
-        for (int ks = 0; ks < kTok / 16; ++ks) {
-          const uint64_t vd = desc_mnmajor_sw128(v + ks * 2048, kTok * 128);
-          mma_ts_f16(d, p + ks * 8, vd, kIdPV, b >= 2 || ks > 0);
-          if (KF == kBf16) mma_ts_f16(d, p + 32 + ks * 8, vd, kIdPV, 1);
-        }
-        if (KF == kBf16) tc_commit_warp(empty_v(st));
-        tc_commit_warp(pv_done(g));
-        if (KF == kBf16 && b + 2 < n) ok = qk(b + 2);
-      }
-    } else {
-      // ---- softmax group g: pages g, g + 2, ... ------------------------------
-      const int g = warp >> 2, quad = warp & 3;
-      const int part = lane / kWarpRows;
-      const int row = quad * kWarpRows + lane % kWarpRows;   // of the group
-      const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-      const bool live = row < nrows;
-      const int pk = row_first + (live ? row : 0), p = a.by_nq.div(pk);
-      const size_t q_row = ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
-      const bool pad = it.slot < 0 || it.slot >= a.n_slots;
-      const int len = live && !pad ? row_len(a, s.r, p) : 0;
-      const int bit = p - p0;
-      float post = a.scale_log2;
-      if (n > 0 && (g == 0 || KF == kFp8)) {
-        // the lane's query row; group 0 puts it into tensor memory
-        const uint4* qp = reinterpret_cast<const uint4*>(a.q + q_row * kDim);
-        uint32_t w[64];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint4 u = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
-          w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
-        }
-        if (KF == kFp8) {
-          // scaled by a power of two that brings the row's largest magnitude into
-          // [2^7, 2^8), then two e4m3 terms
-          float amax = 0.f;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          const int ex = to_2_7(amax);
-          const float up = ldexpf(1.f, ex);
-          post *= ldexpf(1.f, -ex);
-          if (g == 0) {
-            uint32_t lo[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
-                            bf16_hi(w[2 * e + 1]) * up};
-              w[e] = e4m3x4_take(x);
-              lo[e] = e4m3x4_take(x);
+          ++sent_k;
+          if (!wait(empty_v(st), ph)) break;
+          if (lane == 0) {
+            info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
+            // both planes' scales come with the values: the group reads them, and
+            // it gives the values' stage back itself
+            mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + 2 * L::kScale);
+            if (pg >= 0) {
+              tma_load_2d(v_tile(st), &v_map, 0, row, full_v(st));
+              if (KF == kBf16) {
+                tma_load_2d(v_tile(st) + L::kTile / 2, &v_map, 64, row, full_v(st));
+              } else {
+                const uint32_t sc = sbase + L::kScaleOff + st * 2 * L::kScale;
+                bulk_load(sc, a.k_scale + row, L::kScale, full_v(st));
+                bulk_load(sc + L::kScale, a.v_scale + row, L::kScale, full_v(st));
+              }
             }
-            tm_st<32>(tl + kColQ, w);
-            tm_st<32>(tl + kColQ + 32, lo);
           }
-        } else {
-          tm_st<32>(tl + kColQ, w);
-          tm_st<32>(tl + kColQ + 32, w + 32);
-        }
-        if (g == 0) {
-          tm_wait_st();
-          tc_fence_before();
-          mbar_arrive(q_full);
-        }
-      }
-      float m = -INFINITY, l = 0.f, mv = 0.f;
-      int cnt = g ? cnt1 : cnt0;
-      const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
-      const uint32_t pp = KF == kBf16 ? sp : tl + kColP + 32 * g;
-      for (int b = g; b < n; b += 2, ++cnt) {
-        const int tile = tile0 + b, st = tile % NS;
-        int tb;
-        uint32_t members;
-        item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, members);
-        if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
-        const int valid = info[st];
-        if (KF == kFp8) {
-          // this page's values as f16, rows past the request's tokens as zeros, in
-          // the buffer of the group's page before the last (whose product has
-          // ended: that was waited for before the last page's weights)
-          const int t = threadIdx.x & 127;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = t + 128 * e, tok = k >> 3, ch = k & 7;   // 16 codes
-            uint4 u = *reinterpret_cast<const uint4*>(smem + (v_tile(st) - sbase) + tok * 128 + ((ch ^ (tok & 7)) << 4));
-            if (tok >= valid) u = make_uint4(0, 0, 0, 0);
-            uint4 x, y;
-            e4m3x4_to_f16x2x2(u.x, x.x, x.y);
-            e4m3x4_to_f16x2x2(u.y, x.z, x.w);
-            e4m3x4_to_f16x2x2(u.z, y.x, y.y);
-            e4m3x4_to_f16x2x2(u.w, y.z, y.w);
-            // dims 16 ch .. +7 and +8 .. +15: two 16-byte chunks of a 64-dim half
-            uint8_t* base = smem + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16 + (ch >> 2) * (kTok * 128) + tok * 128;
-            const int c0 = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = x;
-            *reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (tok & 7)) << 4)) = y;
-          }
-        } else if (valid < kTok) {
-          // whatever lies past the request's tokens must not meet a weight of zero
-          const int t = threadIdx.x & 127;
-          for (int k = valid * 16 + t; k < kTok * 16; k += 128) {
-            const int tok = k >> 4, ch = k & 15;
-            *reinterpret_cast<uint4*>(smem + (v_tile(st) - sbase) + (ch >> 3) * (kTok * 128) + tok * 128 + ((ch & 7) << 4)) =
-                make_uint4(0, 0, 0, 0);
-          }
-        }
-        if (!wait(s_full(g), (uint32_t)(cnt & 1))) break;
-        tc_fence_after();
-        // the lane's scores
-        uint32_t raw[kPart];
-        if constexpr (F == 1) {
-          tm_ld<32>(sp, raw);
-          tm_ld<32>(sp + 32, raw + 32);
-          tc_wait_ld();
-        } else {
-          uint32_t all[F][kPart];
-#pragma unroll
-          for (int f = 0; f < F; ++f) tm_ld<kPart>(sp + f * kPart, all[f]);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < kPart; ++j) {
-            raw[j] = all[0][j];
-#pragma unroll
-            for (int f = 1; f < F; ++f) raw[j] = part == f ? all[f][j] : raw[j];
-          }
-        }
-        if (KF == kFp8) {
-          tc_fence_before();
+          ++sent_v;
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free(g));
         }
-        // y: the scores before the row's factor, two tokens at a time
-        constexpr int kHalf = kPart / 2;
-        float2 y[kHalf];
-        const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * 2 * L::kScale) + part * kPart;
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j)
-          y[j] = make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
-        if (KF == kFp8) {
-#pragma unroll
-          for (int j = 0; j < kHalf; j += 2) {
-            const float4 k4 = *reinterpret_cast<const float4*>(ks + 2 * j);
-            y[j] = fmul2_rn(y[j], make_float2(k4.x, k4.y));
-            y[j + 1] = fmul2_rn(y[j + 1], make_float2(k4.z, k4.w));
-          }
-        }
-        const int visible = min(min(len, tb + valid) - tb, (members >> bit) & 1u ? kTok : 0) - part * kPart;
-        const bool masked = __any_sync(0xffffffffu, visible < kPart);
-        if (masked) {
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) {
-            if (2 * j >= visible) y[j].x = -INFINITY;
-            if (2 * j + 1 >= visible) y[j].y = -INFINITY;
-          }
-        }
-        float t0 = fmaxf(y[0].x, y[0].y), t1 = fmaxf(y[1].x, y[1].y);
-#pragma unroll
-        for (int j = 2; j < kHalf; j += 2) {
-          t0 = fmaxf(t0, fmaxf(y[j].x, y[j].y));
-          t1 = fmaxf(t1, fmaxf(y[j + 1].x, y[j + 1].y));
-        }
-        const float top = fmaxf(t0, t1) * post;   // post is positive: the order is kept
-        float shrink = 1.f;     // what the output gathered so far is to be multiplied by
-        if (top > m + (m == -INFINITY ? 0.f : kSlack)) {
-          shrink = ex2_approx(m - top);
-          l *= shrink;
-          m = top;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 pp2 = make_float2(post, post), rr2 = make_float2(-ref, -ref);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          y[j] = ffma2_rn(y[j], pp2, rr2);
-          y[j].x = ex2_approx(y[j].x), y[j].y = ex2_approx(y[j].y);
-          if (j & 1) sum1 = fadd2_rn(sum1, y[j]);
-          else sum0 = fadd2_rn(sum0, y[j]);
-        }
-        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        if (KF == kFp8) {
-          // times the value scales, in units of mv: a power of two that the
-          // scales may pass by 2^6 (weights up to 2^8 stay inside f16)
-          const float* vs = ks + kTok;
-          float2 r[kHalf];
-          float most = 0.f;
-#pragma unroll
-          for (int j = 0; j < kHalf; j += 2) {
-            const float4 v4 = *reinterpret_cast<const float4*>(vs + 2 * j);
-            r[j] = make_float2(v4.x, v4.y);
-            r[j + 1] = make_float2(v4.z, v4.w);
-          }
-          if (masked) {   // a masked token's scale may be anything
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) {
-              if (2 * j >= visible) r[j].x = 0.f;
-              if (2 * j + 1 >= visible) r[j].y = 0.f;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) most = fmaxf(most, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
-          if (!(most < INFINITY)) {   // only finite scales set the unit
-            most = 0.f;
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) {
-              if (fabsf(r[j].x) < INFINITY) most = fmaxf(most, fabsf(r[j].x));
-              if (fabsf(r[j].y) < INFINITY) most = fmaxf(most, fabsf(r[j].y));
-            }
-          }
-          if (most > mv * 64.f || mv == 0.f) {
-            const float up = pow2_above(most);
-            shrink *= mv / up;      // mv = 0: nothing gathered yet
-            mv = up;
-          }
-          const float inv = 1.f / mv;
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j) y[j] = fmul2_rn(y[j], fmul2_rn(r[j], make_float2(inv, inv)));
-        }
-        // e4m3: the output is still, and P's columns free, once the last product
-        // has ended (bf16: its scores came after that)
-        if (KF == kFp8 && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
-        if (KF == kFp8) tc_fence_after();
-        if (b >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
-#pragma unroll
-          for (int ch = 0; ch < kDim; ch += 32) {
-            uint32_t o[32];
-            tm_ld<32>(oc + ch, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-            tm_st<32>(oc + ch, o);
-          }
-        }
-        // the weights as operand rows: the lane's own tokens, zeros for the others
-        uint32_t hi[kHalf], lo[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
+      } else if (warp == 9) {
+        // ---- product issuer -----------------------------------------------------
+        constexpr uint32_t kIdQK = AWCfg<KF>::kIdQK, kIdPV = AWCfg<KF>::kIdPV;
+        auto qk = [&](int b) -> bool {
+          const int tile = tile0 + b, st = tile % NS, g = b & 1;
+          if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
+          tc_fence_after();
+          const uint32_t d = tmem + kColS + 64 * g;
           if (KF == kBf16) {
-            hi[j] = pack_bf16(y[j].x, y[j].y);
-            lo[j] = pack_bf16(y[j].x - bf16_lo(hi[j]), y[j].y - bf16_hi(hi[j]));
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ts_f16(d, tmem + kColQ + ks * 8,
+                         desc_kmajor_sw128(k_tile(st) + (ks >> 2) * (L::kTile / 2) + (ks & 3) * 32),
+                         kIdQK, ks > 0);
           } else {
-            hi[j] = pack_f16(y[j].x, y[j].y);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)   // the query's two terms, four steps of 32 each
+              mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32), kIdQK,
+                        ks > 0);
           }
-        }
+          tc_commit_warp(empty_k(st));
+          tc_commit_warp(s_full(g));
+          return true;
+        };
+        bool ok = n > 0 && !dead;
+        if (ok && a.stall_test && segs == 0) ok = wait(stall_bar, 0);
+        ok = ok && wait(q_full, (uint32_t)(segs & 1));
+        tc_fence_after();
+        ok = ok && qk(0);
+        if (n > 1) ok = ok && qk(1);
+        int k0 = cnt0, k1 = cnt1;
+        for (int b = 0; b < n && ok; ++b) {
+          const int tile = tile0 + b, st = tile % NS, g = b & 1;
+          const int cnt = g ? k1++ : k0++;
+          const uint32_t ph = (uint32_t)(cnt & 1);
+          // e4m3: the group's next scores as soon as it has read these
+          if (KF == kFp8 && b + 2 < n) ok = wait(s_free(g), ph) && qk(b + 2);
+          ok = ok && wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + kColO + kDim * g;
+          const uint32_t p = tmem + (KF == kBf16 ? kColS + 64 * g : kColP + 32 * g);
+          const uint32_t v = KF == kBf16 ? v_tile(st) : sbase + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16;
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          uint32_t z[kPart / 2];
-#pragma unroll
-          for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
-          tm_st<kPart / 2>(pp + f * (kPart / 2), z);
-          if (KF == kBf16) {
-#pragma unroll
-            for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
-            tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
+          for (int ks = 0; ks < kTok / 16; ++ks) {
+            const uint64_t vd = desc_mnmajor_sw128(v + ks * 2048, kTok * 128);
+            mma_ts_f16(d, p + ks * 8, vd, kIdPV, b >= 2 || ks > 0);
+            if (KF == kBf16) mma_ts_f16(d, p + 32 + ks * 8, vd, kIdPV, 1);
           }
-        }
-        tm_wait_st();
-        tc_fence_before();
-        if (KF == kFp8 || valid < kTok) fence_async();
-        mbar_arrive(p_full(g));
-        if (KF == kFp8) {
-          // codes and scales of the page have been read
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty_v(st));
+          if (KF == kBf16) tc_commit_warp(empty_v(st));
+          tc_commit_warp(pv_done(g));
+          if (KF == kBf16 && b + 2 < n) ok = qk(b + 2);
         }
       }
-      // ---- the unit's end: the parts and the groups meet ------------------------
-      if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
-      tc_fence_after();
-      ml[g * kLanes + quad * 32 + lane] = make_float2(m, l);
-      group_sync();
-      float M = -INFINITY, sum = 0.f;
+      } else {
+        // ---- softmax group g: pages g, g + 2, ... ------------------------------
+        const int g = warp >> 2, quad = warp & 3;
+        const int part = lane / kWarpRows;
+        const int row = quad * kWarpRows + lane % kWarpRows;   // of the group
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
+        const bool live = row < nrows;
+        const int pk = row_first + (live ? row : 0), p = a.by_nq.div(pk);
+        const size_t q_row = ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
+        const bool pad = it.slot < 0 || it.slot >= a.n_slots;
+        const int len = live && !pad ? row_len(a, s.r, p) : 0;
+        const int bit = p - p0;
+        float post = a.scale_log2;
+        if (n > 0 && (g == 0 || KF == kFp8)) {
+          // the lane's query row; group 0 puts it into tensor memory
+          const uint4* qp = reinterpret_cast<const uint4*>(a.q + q_row * kDim);
+          uint32_t w[64];
 #pragma unroll
-      for (int f = 0; f < 2 * F; ++f)
-        M = fmaxf(M, ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int f = 0; f < 2 * F; ++f) {
-        const float2 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
-        if (e.x != -INFINITY) sum = fmaf(e.y, ex2_approx(e.x - ref), sum);
-      }
-      const float mine = ex2_approx(m - ref) * (KF == kFp8 ? mv : 1.f);
-      const bool complete = s.o0 == 0 && s.o1 == s.cap;
-      const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
-      const float inv = M == -INFINITY ? 0.f : 1.f / sum;
-      bool odd = false;
-      for (int ch = 0; ch < kDim; ch += 32) {
-        uint32_t o[32];
-        float v[32];
-        tm_ld<32>(oc + ch, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = m == -INFINITY ? 0.f : __uint_as_float(o[e]) * mine;   // no page: nothing gathered
-#pragma unroll
-          for (int d = kWarpRows; d < 32; d <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
-        }
-        if (g == 1 && part == 0) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) xch[e * kLanes + row] = v[e];
-        }
-        group_sync();
-        if (g == 0 && part == 0 && live) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[e] += xch[e * kLanes + row];
-            odd |= !isfinite(v[e]);
+          for (int e = 0; e < 16; ++e) {
+            const uint4 u = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
+            w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
           }
-          if (complete) {
-            uint4* out = reinterpret_cast<uint4*>(a.out + q_row * kDim + ch);
+          if (KF == kFp8) {
+            // scaled by a power of two that brings the row's largest magnitude into
+            // [2^7, 2^8), then two e4m3 terms
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+            const int ex = to_2_7(amax);
+            const float up = ldexpf(1.f, ex);
+            post *= ldexpf(1.f, -ex);
+            if (g == 0) {
+              uint32_t lo[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
+                              bf16_hi(w[2 * e + 1]) * up};
+                w[e] = e4m3x4_take(x);
+                lo[e] = e4m3x4_take(x);
+              }
+              tm_st<32>(tl + kColQ, w);
+              tm_st<32>(tl + kColQ + 32, lo);
+            }
+          } else {
+            tm_st<32>(tl + kColQ, w);
+            tm_st<32>(tl + kColQ + 32, w + 32);
+          }
+          if (g == 0) {
+            tm_wait_st();
+            tc_fence_before();
+            mbar_arrive(q_full);
+          }
+        }
+        float m = -INFINITY, l = 0.f, mv = 0.f;
+        int cnt = g ? cnt1 : cnt0;
+        const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
+        const uint32_t pp = KF == kBf16 ? sp : tl + kColP + 32 * g;
+        for (int b = g; b < n; b += 2, ++cnt) {
+          const int tile = tile0 + b, st = tile % NS;
+          int tb;
+          uint32_t members;
+          item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, members);
+          if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
+          const int valid = info[st];
+          if (KF == kFp8) {
+            // this page's values as f16, rows past the request's tokens as zeros, in
+            // the buffer of the group's page before the last (whose product has
+            // ended: that was waited for before the last page's weights)
+            const int t = threadIdx.x & 127;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint4 u;
-              u.x = pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv);
-              u.y = pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
-              u.z = pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv);
-              u.w = pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
-              out[e] = u;
+              const int k = t + 128 * e, tok = k >> 3, ch = k & 7;   // 16 codes
+              uint4 u = *reinterpret_cast<const uint4*>(smem + (v_tile(st) - sbase) + tok * 128 + ((ch ^ (tok & 7)) << 4));
+              if (tok >= valid) u = make_uint4(0, 0, 0, 0);
+              uint4 x, y;
+              e4m3x4_to_f16x2x2(u.x, x.x, x.y);
+              e4m3x4_to_f16x2x2(u.y, x.z, x.w);
+              e4m3x4_to_f16x2x2(u.z, y.x, y.y);
+              e4m3x4_to_f16x2x2(u.w, y.z, y.w);
+              // dims 16 ch .. +7 and +8 .. +15: two 16-byte chunks of a 64-dim half
+              uint8_t* base = smem + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16 + (ch >> 2) * (kTok * 128) + tok * 128;
+              const int c0 = (ch & 3) * 2;
+              *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = x;
+              *reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (tok & 7)) << 4)) = y;
             }
+          } else if (valid < kTok) {
+            // whatever lies past the request's tokens must not meet a weight of zero
+            const int t = threadIdx.x & 127;
+            for (int k = valid * 16 + t; k < kTok * 16; k += 128) {
+              const int tok = k >> 4, ch = k & 15;
+              *reinterpret_cast<uint4*>(smem + (v_tile(st) - sbase) + (ch >> 3) * (kTok * 128) + tok * 128 + ((ch & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (!wait(s_full(g), (uint32_t)(cnt & 1))) break;
+          tc_fence_after();
+          // the lane's scores
+          uint32_t raw[kPart];
+          if constexpr (F == 1) {
+            tm_ld<32>(sp, raw);
+            tm_ld<32>(sp + 32, raw + 32);
+            tc_wait_ld();
           } else {
-            float4* out = reinterpret_cast<float4*>(a.part_o + at * kDim + ch);
+            uint32_t all[F][kPart];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) out[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int f = 0; f < F; ++f) tm_ld<kPart>(sp + f * kPart, all[f]);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kPart; ++j) {
+              raw[j] = all[0][j];
+#pragma unroll
+              for (int f = 1; f < F; ++f) raw[j] = part == f ? all[f][j] : raw[j];
+            }
+          }
+          if (KF == kFp8) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free(g));
+          }
+          // y: the scores before the row's factor, two tokens at a time
+          constexpr int kHalf = kPart / 2;
+          float2 y[kHalf];
+          const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * 2 * L::kScale) + part * kPart;
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j)
+            y[j] = make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
+          if (KF == kFp8) {
+#pragma unroll
+            for (int j = 0; j < kHalf; j += 2) {
+              const float4 k4 = *reinterpret_cast<const float4*>(ks + 2 * j);
+              y[j] = fmul2_rn(y[j], make_float2(k4.x, k4.y));
+              y[j + 1] = fmul2_rn(y[j + 1], make_float2(k4.z, k4.w));
+            }
+          }
+          const int visible = min(min(len, tb + valid) - tb, (members >> bit) & 1u ? kTok : 0) - part * kPart;
+          const bool masked = __any_sync(0xffffffffu, visible < kPart);
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) {
+              if (2 * j >= visible) y[j].x = -INFINITY;
+              if (2 * j + 1 >= visible) y[j].y = -INFINITY;
+            }
+          }
+          float t0 = fmaxf(y[0].x, y[0].y), t1 = fmaxf(y[1].x, y[1].y);
+#pragma unroll
+          for (int j = 2; j < kHalf; j += 2) {
+            t0 = fmaxf(t0, fmaxf(y[j].x, y[j].y));
+            t1 = fmaxf(t1, fmaxf(y[j + 1].x, y[j + 1].y));
+          }
+          const float top = fmaxf(t0, t1) * post;   // post is positive: the order is kept
+          float shrink = 1.f;     // what the output gathered so far is to be multiplied by
+          if (top > m + (m == -INFINITY ? 0.f : kSlack)) {
+            shrink = ex2_approx(m - top);
+            l *= shrink;
+            m = top;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 pp2 = make_float2(post, post), rr2 = make_float2(-ref, -ref);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) {
+            y[j] = ffma2_rn(y[j], pp2, rr2);
+            y[j].x = ex2_approx(y[j].x), y[j].y = ex2_approx(y[j].y);
+            if (j & 1) sum1 = fadd2_rn(sum1, y[j]);
+            else sum0 = fadd2_rn(sum0, y[j]);
+          }
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          if (KF == kFp8) {
+            // times the value scales, in units of mv: a power of two that the
+            // scales may pass by 2^6 (weights up to 2^8 stay inside f16)
+            const float* vs = ks + kTok;
+            float2 r[kHalf];
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < kHalf; j += 2) {
+              const float4 v4 = *reinterpret_cast<const float4*>(vs + 2 * j);
+              r[j] = make_float2(v4.x, v4.y);
+              r[j + 1] = make_float2(v4.z, v4.w);
+            }
+            if (masked) {   // a masked token's scale may be anything
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j) {
+                if (2 * j >= visible) r[j].x = 0.f;
+                if (2 * j + 1 >= visible) r[j].y = 0.f;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) most = fmaxf(most, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
+            if (!(most < INFINITY)) {   // only finite scales set the unit
+              most = 0.f;
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j) {
+                if (fabsf(r[j].x) < INFINITY) most = fmaxf(most, fabsf(r[j].x));
+                if (fabsf(r[j].y) < INFINITY) most = fmaxf(most, fabsf(r[j].y));
+              }
+            }
+            if (most > mv * 64.f || mv == 0.f) {
+              const float up = pow2_above(most);
+              shrink *= mv / up;      // mv = 0: nothing gathered yet
+              mv = up;
+            }
+            const float inv = 1.f / mv;
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) y[j] = fmul2_rn(y[j], fmul2_rn(r[j], make_float2(inv, inv)));
+          }
+          // e4m3: the output is still, and P's columns free, once the last product
+          // has ended (bf16: its scores came after that)
+          if (KF == kFp8 && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
+          if (KF == kFp8) tc_fence_after();
+          if (b >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll
+            for (int ch = 0; ch < kDim; ch += 32) {
+              uint32_t o[32];
+              tm_ld<32>(oc + ch, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+              tm_st<32>(oc + ch, o);
+            }
+          }
+          // the weights as operand rows: the lane's own tokens, zeros for the others
+          uint32_t hi[kHalf], lo[kHalf];
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) {
+            if (KF == kBf16) {
+              hi[j] = pack_bf16(y[j].x, y[j].y);
+              lo[j] = pack_bf16(y[j].x - bf16_lo(hi[j]), y[j].y - bf16_hi(hi[j]));
+            } else {
+              hi[j] = pack_f16(y[j].x, y[j].y);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            uint32_t z[kPart / 2];
+#pragma unroll
+            for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
+            tm_st<kPart / 2>(pp + f * (kPart / 2), z);
+            if (KF == kBf16) {
+#pragma unroll
+              for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
+              tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
+            }
+          }
+          tm_wait_st();
+          tc_fence_before();
+          if (KF == kFp8 || valid < kTok) fence_async();
+          mbar_arrive(p_full(g));
+          if (KF == kFp8) {
+            // codes and scales of the page have been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_v(st));
           }
         }
+        // ---- the unit's end: the parts and the groups meet ------------------------
+        if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
+        tc_fence_after();
+        ml[g * kLanes + quad * 32 + lane] = make_float2(m, l);
         group_sync();
-      }
-      if (g == 0 && part == 0 && live) {
-        if (complete) {
-          if (a.lse) a.lse[q_row] = M == -INFINITY ? M : (M + log2f(sum)) * kLn2;
-        } else {
-          a.part_ml[at] = make_float2(M, sum);
+        float M = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int f = 0; f < 2 * F; ++f)
+          M = fmaxf(M, ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int f = 0; f < 2 * F; ++f) {
+          const float2 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
+          if (e.x != -INFINITY) sum = fmaf(e.y, ex2_approx(e.x - ref), sum);
+        }
+        const float mine = ex2_approx(m - ref) * (KF == kFp8 ? mv : 1.f);
+        const bool complete = s.o0 == 0 && s.o1 == s.cap;
+        const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
+        const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+        bool odd = false;
+        for (int ch = 0; ch < kDim; ch += 32) {
+          uint32_t o[32];
+          float v[32];
+          tm_ld<32>(oc + ch, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[e] = m == -INFINITY ? 0.f : __uint_as_float(o[e]) * mine;   // no page: nothing gathered
+#pragma unroll
+            for (int d = kWarpRows; d < 32; d <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
+          }
+          if (g == 1 && part == 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) xch[e * kLanes + row] = v[e];
+          }
+          group_sync();
+          if (g == 0 && part == 0 && live) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              v[e] += xch[e * kLanes + row];
+              odd |= !isfinite(v[e]);
+            }
+            if (complete) {
+              uint4* out = reinterpret_cast<uint4*>(a.out + q_row * kDim + ch);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 u;
+                u.x = pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv);
+                u.y = pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv);
+                u.z = pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv);
+                u.w = pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv);
+                out[e] = u;
+              }
+            } else {
+              float4* out = reinterpret_cast<float4*>(a.part_o + at * kDim + ch);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) out[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+          }
+          group_sync();
+        }
+        if (g == 0 && part == 0 && live) {
+          if (complete) {
+            if (a.lse) a.lse[q_row] = M == -INFINITY ? M : (M + log2f(sum)) * kLn2;
+          } else {
+            a.part_ml[at] = make_float2(M, sum);
+          }
+        }
+        // rows that met something not finite: token by token, so that only the
+        // rows that see it keep it
+        uint32_t todo = g == 0 ? __ballot_sync(0xffffffffu, odd) : 0u;
+        while (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int r2 = __shfl_sync(0xffffffffu, row, src);
+          const int pk2 = row_first + r2, p2 = a.by_nq.div(pk2);
+          const size_t q2 = ((size_t)s.r * a.P + p2) * a.q_heads + s.head * a.nq + (pk2 - p2 * a.nq);
+          float m2, l2;
+          float4 o2;
+          careful_row<KF, kTok, kBlocks>(a, it, list, a.q + q2 * kDim, __shfl_sync(0xffffffffu, len, src),
+                                         p2 - p0, lane, m2, l2, o2);
+          if (complete) {
+            write_row(a, q2, m2, l2, o2, lane);
+          } else {
+            const size_t at2 = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + r2;
+            if (lane == 0) a.part_ml[at2] = make_float2(m2, l2);
+            reinterpret_cast<float4*>(a.part_o + at2 * kDim)[lane] = o2;
+          }
         }
       }
-      // rows that met something not finite: token by token, so that only the
-      // rows that see it keep it
-      uint32_t todo = g == 0 ? __ballot_sync(0xffffffffu, odd) : 0u;
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int r2 = __shfl_sync(0xffffffffu, row, src);
-        const int pk2 = row_first + r2, p2 = a.by_nq.div(pk2);
-        const size_t q2 = ((size_t)s.r * a.P + p2) * a.q_heads + s.head * a.nq + (pk2 - p2 * a.nq);
-        float m2, l2;
-        float4 o2;
-        careful_row<KF, kTok, kBlocks>(a, it, list, a.q + q2 * kDim, __shfl_sync(0xffffffffu, len, src),
-                                       p2 - p0, lane, m2, l2, o2);
-        if (complete) {
-          write_row(a, q2, m2, l2, o2, lane);
-        } else {
-          const size_t at2 = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + r2;
-          if (lane == 0) a.part_ml[at2] = make_float2(m2, l2);
-          reinterpret_cast<float4*>(a.part_o + at2 * kDim)[lane] = o2;
-        }
+      if (s.o0 == 0 && s.o1 != s.cap) {
+        record.unit = s.unit;
+        record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
       }
+      tile0 += n;
+      segs += n > 0;
+      cnt0 += (n + 1) / 2;
+      cnt1 += n / 2;
     }
-    if (s.o0 == 0 && s.o1 != s.cap) {
-      record.unit = s.unit;
-      record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
-    }
-    tile0 += n;
-    segs += n > 0;
-    cnt0 += (n + 1) / 2;
-    cnt1 += n / 2;
+  };
+  // 384 threads start with 168 registers each (64,512): the last warpgroup needs
+  // few, the softmax groups take what it leaves (256 x 208 + 128 x 88 = 64,512)
+  if (warp >= 8) {
+    if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    work(std::integral_constant<bool, false>());
+  } else {
+    if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    work(std::integral_constant<bool, true>());
   }
 
   // after a timeout: the copies and products in flight end before the block does
@@ -820,7 +841,7 @@ __global__ void __launch_bounds__(AWLayout<KF>::kThreads, 1)
 template <int KF, int F, bool kBlocks>
 cudaError_t launch_kfb(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
                        int grid, int dev, cudaStream_t stream) {
-  using L = AWLayout<KF>;
+  using L = AWLayout<KF, F>;
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_limit_once(attn_wide_kernel<KF, F, kBlocks>, L::kSmem, dev, attr_done);
   if (e != cudaSuccess) return e;
