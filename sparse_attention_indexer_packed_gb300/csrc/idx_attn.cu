@@ -692,26 +692,48 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The join of units that several CTAs shared.  Block (c, i): row i of the unit
+// The join of units that several CTAs shared: block (c, i) has row i of the unit
 // that CTA c started and did not end.  Its parts are CTA c's second slot and the
 // first slots of the CTAs behind it; their maxima and sums are read at once, one
 // a thread, then the warps add the outputs, each its share in a fixed order, so
 // the result does not depend on timing.
+// A call of few units may have 100 parts a row.  kFew: four blocks a row, 32 dims
+// each, and a block for every unit, which looks its CTA up (1 x 131K: 30.2 -> 23.7
+// us a call, four draft rows 36.0 -> 27.4; but 1 x 1K 8.9 -> 9.3, so only where a
+// unit may have over 32 parts).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 4, kJoinThreads = 32 * kJoinWarps;
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+constexpr int kFewSplit = 4;
+template <bool kFew>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int ctas) {
   __shared__ float factor[kMaxCtas];
   __shared__ float red[2][kJoinWarps];
   __shared__ float4 so[kJoinWarps][32];
+  __shared__ int found;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(a.group_rows, a.P * a.nq);
-  const int c = blockIdx.x / rows, i = blockIdx.x - c * rows;
-  const SplitRecord rec = a.records[c];
+  int c, i;
+  SplitRecord rec;
+  if (kFew) {
+    const int unit = blockIdx.x / (rows * kFewSplit);
+    i = blockIdx.x / kFewSplit - unit * rows;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    for (int k = threadIdx.x; k < ctas; k += kJoinThreads)
+      if (a.records[k].unit == unit) found = k;
+    __syncthreads();
+    c = found;
+    if (c < 0) return;
+  } else {
+    c = blockIdx.x / rows;
+    i = blockIdx.x - c * rows;
+  }
+  rec = a.records[c];
   if (rec.unit < 0) return;
   const int r = a.by_per.div(rec.unit), k = rec.unit - r * (int)a.by_per.d;
   const int head = a.by_groups.div(k), pk = (k - head * a.groups) * a.group_rows + i;
   if (pk >= a.P * a.nq) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto part = [&](int s) { return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i; };
   static_assert(kMaxCtas <= 2 * kJoinThreads, "two parts a thread");
   float2 x[2];
@@ -744,17 +766,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) l += red[1][w];
+  // a warp takes kAt parts at a time (a lane: four dims of one), eight such loads
+  // in flight
+  constexpr int kAt = kFew ? kFewSplit : 1, kLanes = 32 / kAt;
+  const int dim4 = (kFew ? (int)(blockIdx.x % kFewSplit) * kLanes : 0) + lane % kLanes;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // eight parts' loads at a time
-  for (int s0 = warp; s0 < rec.splits; s0 += 8 * kJoinWarps) {
+  for (int s0 = warp * kAt + lane / kLanes; s0 < rec.splits; s0 += 8 * kJoinWarps * kAt) {
     float4 v[8];
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int s = s0 + e * kJoinWarps;
+      const int s = s0 + e * kJoinWarps * kAt;
       f[e] = s < rec.splits ? factor[s] : -1.f;
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (f[e] != -1.f) v[e] = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[lane];
+      if (f[e] != -1.f) v[e] = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[dim4];
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -764,14 +789,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   }
   so[warp][lane] = o;
   __syncthreads();
-  if (warp) return;
+  if (threadIdx.x >= kLanes) return;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 v = so[w][lane];
-    o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-  }
+  for (int w = 0; w < kJoinWarps; ++w)
+#pragma unroll
+    for (int e = 0; e < kAt; ++e) {
+      const float4 v = so[w][e * kLanes + lane];
+      o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    }
   const int p = a.by_nq.div(pk);
-  write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, lane);
+  write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, dim4);
 }
 
 template <int KF, bool kBlocks>
@@ -815,7 +843,10 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
                : launch_kf<kFp8, false>(a, k_map, v_map, grid, dev, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
-  e = launch_pdl(attn_join_kernel, grid * rows, kJoinThreads, 0, stream, a);
+  const int units = a.R * (int)a.by_per.d;
+  const bool few = units * 16 <= grid && a.most > 32 * 8;
+  e = few ? launch_pdl(attn_join_kernel<true>, units * rows * kFewSplit, kJoinThreads, 0, stream, a, grid)
+          : launch_pdl(attn_join_kernel<false>, grid * rows, kJoinThreads, 0, stream, a, grid);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -74,6 +74,7 @@ struct AttnArgs {
   int groups;                  // row groups of a unit head
   attn::Divisor by_per, by_groups, by_nq, by_topk;  // heads * groups, groups, nq, topk
   attn::Divisor by_kv, by_list;  // unit heads of a key head, of a list
+  long long most;              // pieces a unit may have at most, as the host knows it
   int shift;                   // pieces of a position: 2^shift
   int unit_cost;               // positions that stand for a unit's end
   float scale_log2;            // softmax scale times log2(e)
@@ -126,10 +127,14 @@ inline int unit_cost(int group_rows, bool blocks) {
   return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
 }
 
-// The shift of a call: no request has more than `pages` pages or, with lists of
-// `listed` entries in all, two pages an entry; a piece is half a page or a page.
-inline int position_shift(int R, long long per, int pages, long long listed, int unit_cost) {
-  long long most = listed > 0 && listed < (pages + 1) / 2 ? 4 * listed : 2ll * pages + 2;
+// The most half-page pieces a unit of the call may have, from what the host knows:
+// the page table's width, and with block lists the entries of all draft rows.
+inline long long most_pieces(int pages, long long listed) {
+  return listed > 0 && listed < (pages + 1) / 2 ? 4 * listed : 2ll * pages + 2;
+}
+
+// The shift of a call of R requests with `per` units each.
+inline int position_shift(int R, long long per, long long most, int unit_cost) {
   int shift = 0;
   while (R * per * (((most + (1ll << shift) - 1) >> shift) + unit_cost) > kMaxPositions && shift < 24) ++shift;
   return shift;
