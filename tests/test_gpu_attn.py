@@ -337,3 +337,94 @@ def test_shards_join_by_lse():
     assert (z - wl).abs().max() <= 2e-5
     # each side: a bf16 rounding of the weights and of the result
     assert (out - whole.float()).abs().max() <= 2 * 2.0 ** -8 * whole.float().abs().max() + 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,Hq", [(1, 16), (4, 16), (4, 32)])
+def test_one_long_request_over_many_parts(dtype, P, Hq):
+    """One unit over every CTA: the join of a hundred parts a row."""
+    c = _attn.make(dtype, [drafts(20011, P)], 1, 101)
+    q = draws(1, P, Hq, 24)
+    out, l, flags = run(c, q)
+    again, l2, _ = run(c, q)
+    assert flags == 0 and torch.equal(out, again) and torch.equal(l, l2)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,Hq,Hkv", [(1, 4, 2), (6, 4, 1)])
+def test_many_short_requests(dtype, P, Hq, Hkv):
+    """More requests than the threads that read them, several units a CTA."""
+    g = torch.Generator().manual_seed(3)
+    lens = [drafts(int(L), P) for L in torch.randint(0, 90, (700,), generator=g)]
+    c = _attn.make(dtype, lens, Hkv, 103, pads=(0, 255, 256, 699))
+    q = draws(700, P, Hq, 25)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("blocks", [False, True])
+def test_page_tables_so_wide_that_pieces_are_counted_in_lots(blocks):
+    """The line of positions is kept short by counting pieces two at a time."""
+    R, P = (64, 1) if not blocks else (150, 16)
+    lens = [drafts(L, P) for L in ([900, 65, 0, 31] * 64)[:R]]
+    c = _attn.make("bf16", lens, 2, 105, max_pages=65536 if not blocks else 20000)
+    q = draws(R, P, 4, 26)
+    ids = lists_for(lens, 2, 256, 27, P) if blocks else None
+    out, l, flags = run(c, q, block_ids=ids, lists=2 if blocks else 0)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ctas", [3, 0])
+def test_blocks_of_wide_units(dtype, ctas):
+    """Block lists with more than 16 rows a unit, several units a CTA."""
+    P = 4
+    lens = [drafts(L, P) for L in (3000, 0, 129, 4096, 64, 2049)]
+    c = _attn.make(dtype, lens, 2, 107, pads=(4,))
+    q = draws(len(lens), P, 16, 28)
+    ids = lists_for(lens, 2, 7, 29, P)
+    idx.idx_set_grid_limit(ctas)
+    try:
+        out, l, flags = run(c, q, block_ids=ids, lists=2)
+    finally:
+        idx.idx_set_grid_limit(0)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, 2))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scores_far_apart_with_many_rows(dtype):
+    """The wide kernel's late raises of the running maximum, and values over many scales."""
+    c = _attn.make(dtype, [drafts(1500, 4)], 1, 109, spread=True)
+    q = draws(1, 4, 16, 30, scale=40.0)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_one_draft_rows_token_among_many_rows(dtype, bad):
+    """As the narrow test: the newest token is not finite, only the last draft row sees it."""
+    lens = [drafts(200, 4), drafts(65, 4)]
+    c = _attn.make(dtype, lens, 1, 111)
+    q = draws(2, 4, 16, 31)
+    clean = _attn.reference(c, q, 128 ** -0.5)
+    page = c.page_table[int(c.slot_ids[0])]
+    row = int(page[199 // 64]) * 64 + 199 % 64
+    for p in (c.k, c.v):
+        if dtype == "bf16":
+            p[0][row] = bad
+        else:
+            p[1][row] = bad
+    out, l, flags = run(c, q)
+    assert flags == 0
+    keep = torch.ones((2, 4, 16), dtype=torch.bool)
+    keep[0, 3] = False
+    d = (out.cpu().double() - clean[0]).abs()
+    assert (d[keep] <= clean[2][keep]).all()
+    assert ((l.cpu().double() - clean[1]).abs()[keep] <= clean[3][keep]).all()
+    assert not torch.isfinite(out[0, 3].float()).all()
