@@ -3,7 +3,8 @@
 The translation units compile in parallel into ``_build/`` and link into
 ``sparse_attention_indexer_packed_gb300/libidx.so`` with the CUDA runtime
 linked statically, so the library loads without a driver (its symbols can be
-inspected on a machine with no GPU).
+inspected on a machine with no GPU).  ``_binding.so`` beside it is the CPython
+module of the small-call operators (csrc/idx_binding.c).
 """
 from __future__ import annotations
 
@@ -11,11 +12,13 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libidx.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["idx_api.cu", "idx_score.cu", "idx_wide.cu", "idx_topk.cu", "idx_store.cu", "idx_noalloc.cu",
            "idx_attn.cu", "idx_attn_wide.cu", "idx_kv.cu", "idx_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -73,6 +76,12 @@ def build_library(verbose: bool = False, force: bool = False) -> str:
         tmp = LIB + tag
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "idx_binding.c")
+    if force or _stale(BINDING, [src, headers[-1]]):
+        tmp = BINDING + tag
+        run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"],
+             src, "-o", tmp, "-L" + HERE, "-l:libidx.so", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, BINDING)
     return LIB
 
 

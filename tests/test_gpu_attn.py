@@ -428,3 +428,37 @@ def test_one_draft_rows_token_among_many_rows(dtype, bad):
     assert (d[keep] <= clean[2][keep]).all()
     assert ((l.cpu().double() - clean[1]).abs()[keep] <= clean[3][keep]).all()
     assert not torch.isfinite(out[0, 3].float()).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_native_call_and_the_python_one_agree(dtype):
+    from sparse_attention_indexer_packed_gb300 import _lib
+    assert idx.idx_attn_paged is not _lib.idx_attn_paged, "the CPython module has not been built"
+    lens = [drafts(L, 2) for L in (300, 77)]
+    c = _attn.to_device(_attn.make(dtype, lens, 1, 113))
+    q = draws(2, 2, 4, 32).cuda()
+    ids = torch.tensor([[[0, 2], [1, 2]] * 2] * 2, dtype=torch.int32, device="cuda")
+    ws = idx.alloc_attn_workspace(2, 4, 1, 2)
+    scale = 128 ** -0.5
+    got = []
+    for paged, blocks in ((idx.idx_attn_paged, idx.idx_attn_blocks), (_lib.idx_attn_paged, _lib.idx_attn_blocks)):
+        out, l = torch.empty_like(q), torch.empty((2, 2, 4), device="cuda")
+        paged(q, *c.args(), 1, scale, out, l, ws)
+        got.append((out.clone(), l.clone()))
+        paged(q, *c.args(), kv_heads=1, sm_scale=scale, out=out, out_lse=None, workspace=ws)
+        assert torch.equal(out, got[-1][0])
+        blocks(q, *c.args(), ids, 2, 1, scale, out, l, ws)
+        got.append((out.clone(), l.clone()))
+        good = (q, *c.args(), 1, scale, out, l, ws)
+        for at, bad in ((0, q.float()), (0, q[..., :64]), (0, q.transpose(1, 2)), (1, c.k[0][:65]),
+                        (6, c.page_table.long()), (7, c.slot_ids[:1]), (8, c.row_lens.t()), (9, 3),
+                        (10, -1.0), (11, out[:1]), (12, l.double()), (13, ws[:1024]), (13, ws.cpu()),
+                        (5, "int8")):
+            with pytest.raises(idx.IdxError):
+                paged(*good[:at], bad, *good[at + 1:])
+        good = (q, *c.args(), ids, 2, 1, scale, out, l, ws)
+        for at, bad in ((9, ids[:, :3]), (9, ids.long()), (9, None), (10, 3), (10, 0)):
+            with pytest.raises(idx.IdxError):
+                blocks(*good[:at], bad, *good[at + 1:])
+    for a, b in ((0, 2), (1, 3)):
+        assert torch.equal(got[a][0], got[b][0]) and torch.equal(got[a][1], got[b][1])

@@ -173,3 +173,33 @@ def test_norm_makes_the_index_steps_e4m3_queries():
     y = x.double() / torch.sqrt((x.double() ** 2).mean(1, keepdim=True) + 1e-6)
     back = out.float().double() * sc.double()
     assert ((back - y).abs() <= y.abs() * 2.0 ** -4 + sc.double() * 2.0 ** -10 + 1e-6).all()
+
+
+def test_the_native_calls_and_the_python_ones_agree():
+    """The CPython module's functions, the Python functions of the same names, keywords and a
+    given stream (which the module hands on), and what both refuse."""
+    from sparse_attention_indexer_packed_gb300 import _lib
+    assert idx.idx_store_kv is not _lib.idx_store_kv, "the CPython module has not been built"
+    src = tokens(70, 2, 21).cuda()
+    slots = torch.randperm(128, generator=torch.Generator().manual_seed(1))[:70].cuda()
+    for dtype in ("bf16", "fp8_e4m3"):
+        got = []
+        for call in (lambda *a: idx.idx_store_kv(*a), lambda *a: _lib.idx_store_kv(*a),
+                     lambda *a: idx.idx_store_kv(*a, stream=torch.cuda.current_stream())):
+            planes = [tuple(None if t is None else t.cuda() for t in _attn.plane(256, dtype, 7)) for _ in range(2)]
+            call(src[:, :2], src[:, 2:4], slots, *planes[0], *planes[1], dtype, 2)
+            got.append([t.cpu() for p in planes for t in p if t is not None])
+        for other in got[1:]:
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(got[0], other))
+    x = torch.randn((5, 256), device="cuda").to(torch.bfloat16)
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    out, sc = torch.empty((5, 256), dtype=torch.uint8, device="cuda"), torch.empty((5, 2), device="cuda")
+    for call in (idx.idx_add_rmsnorm_fp8, _lib.idx_add_rmsnorm_fp8):
+        out.zero_()
+        call(x, None, w, 1e-6, 128, out, sc)
+        check_norm(x, None, w, 1e-6, 128, (out.view(torch.float8_e4m3fn), sc, None))
+        for bad in ((x.float(), None, w, 1e-6, 128, out, sc), (x, None, w[:7], 1e-6, 128, out, sc),
+                    (x, None, w, 1e-6, 64, out, sc), (x, x.t(), w, 1e-6, 128, out, sc),
+                    (x, None, w, 1e-6, 128, out, sc[:, :1]), (x.cpu(), None, w, 1e-6, 128, out, sc)):
+            with pytest.raises(idx.IdxError):
+                call(*bad)
