@@ -92,9 +92,9 @@ struct AWLayout {
   static constexpr int kScale = KF == kFp8 ? kTok * 4 : 0;
   static constexpr int kV16Off = NS * 2 * kTile;
   static constexpr int kScaleOff = kV16Off + 4 * kV16;
-  static constexpr int kXchOff = kScaleOff + NS * 2 * kScale;  // [32 dims][128 rows] floats
-  static constexpr int kMlOff = kXchOff + 32 * kLanes * 4;
-  static constexpr int kInfoOff = kMlOff + 2 * kLanes * 8;     // valid tokens of each stage
+  static constexpr int kBitsOff = kScaleOff + NS * 2 * kScale;     // block bits while lists are joined
+  static constexpr int kMlOff = kBitsOff + 2 * kMaxBlockWords * 4;  // (max, sum, value unit) of each lane
+  static constexpr int kInfoOff = kMlOff + 2 * kLanes * 16;         // valid tokens of each stage
   // full_k full_v empty_k empty_v [NS], s_full p_full pv_done s_free [2], q_full, stall, drain
   static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
   static constexpr int kNumBars = 4 * NS + 11;
@@ -104,8 +104,6 @@ struct AWLayout {
   static constexpr int kBytes = kListOff + kMaxList * 4;
   static constexpr int kSmem = kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  // a list's bits are held in the exchange area, free between two units
-  static_assert(2 * kMaxBlockWords * 4 <= 32 * kLanes * 4, "block bits");
   static_assert(kV16Off % 1024 == 0, "operand tiles on 1024 bytes");
 };
 
@@ -233,9 +231,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
   volatile unsigned int* abort_flag = ctl + 2;
   const Requests rq = requests_at(smem + L::kPreOff);
   uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kXchOff);
-  float* xch = reinterpret_cast<float*>(smem + L::kXchOff);
-  float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
+  float4* ml = reinterpret_cast<float4*>(smem + L::kMlOff);
   volatile int* info = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
   const uint32_t bars = sbase + L::kBarOff;
   auto full_k = [&](int s) { return bars + 8 * s; };
@@ -707,7 +704,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         // ---- the unit's end: the parts and the groups meet ------------------------
         if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
         tc_fence_after();
-        ml[g * kLanes + quad * 32 + lane] = make_float2(m, l);
+        ml[g * kLanes + quad * 32 + lane] = make_float4(m, l, mv, 0.f);
         group_sync();
         float M = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -716,36 +713,34 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int f = 0; f < 2 * F; ++f) {
-          const float2 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
+          const float4 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
           if (e.x != -INFINITY) sum = fmaf(e.y, ex2_approx(e.x - ref), sum);
         }
-        const float mine = ex2_approx(m - ref) * (KF == kFp8 ? mv : 1.f);
+        // Either group finishes half the dims: its warps see the tensor-memory lanes
+        // of both groups' outputs.  A lane without a page has gathered nothing.
+        const float4 e0 = ml[quad * 32 + lane], e1 = ml[kLanes + quad * 32 + lane];
+        const bool has0 = e0.x != -INFINITY, has1 = e1.x != -INFINITY;
+        const float f0 = ex2_approx(e0.x - ref) * (KF == kFp8 ? e0.z : 1.f);
+        const float f1 = ex2_approx(e1.x - ref) * (KF == kFp8 ? e1.z : 1.f);
         const bool complete = s.o0 == 0 && s.o1 == s.cap;
         const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
         const float inv = M == -INFINITY ? 0.f : 1.f / sum;
         bool odd = false;
-        for (int ch = 0; ch < kDim; ch += 32) {
-          uint32_t o[32];
-          float v[32];
-          tm_ld<32>(oc + ch, o);
+#pragma unroll 1
+        for (int ch = g * (kDim / 2); ch < (g + 1) * (kDim / 2); ch += 32) {
+          uint32_t o0[32], o1[32];
+          tm_ld<32>(tl + kColO + ch, o0);
+          tm_ld<32>(tl + kColO + kDim + ch, o1);
           tc_wait_ld();
+          float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            v[e] = m == -INFINITY ? 0.f : __uint_as_float(o[e]) * mine;   // no page: nothing gathered
+            v[e] = (has0 ? __uint_as_float(o0[e]) * f0 : 0.f) + (has1 ? __uint_as_float(o1[e]) * f1 : 0.f);
 #pragma unroll
             for (int d = kWarpRows; d < 32; d <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
+            odd |= !isfinite(v[e]);
           }
-          if (g == 1 && part == 0) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) xch[e * kLanes + row] = v[e];
-          }
-          group_sync();
-          if (g == 0 && part == 0 && live) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              v[e] += xch[e * kLanes + row];
-              odd |= !isfinite(v[e]);
-            }
+          if (part == 0 && live) {
             if (complete) {
               uint4* out = reinterpret_cast<uint4*>(a.out + q_row * kDim + ch);
 #pragma unroll
@@ -763,7 +758,6 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               for (int e = 0; e < 8; ++e) out[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
           }
-          group_sync();
         }
         if (g == 0 && part == 0 && live) {
           if (complete) {
@@ -772,9 +766,14 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             a.part_ml[at] = make_float2(M, sum);
           }
         }
+        volatile unsigned int* odd_rows = ctl + 4;   // [group][quad], one bit a lane
+        const uint32_t seen = __ballot_sync(0xffffffffu, odd && part == 0 && live);
+        if (lane == 0) odd_rows[g * 4 + quad] = seen;
+        tc_fence_before();
+        group_sync();      // the outputs have been read, the next unit may write them
         // rows that met something not finite: token by token, so that only the
         // rows that see it keep it
-        uint32_t todo = g == 0 ? __ballot_sync(0xffffffffu, odd) : 0u;
+        uint32_t todo = g == 0 ? odd_rows[quad] | odd_rows[4 + quad] : 0u;
         while (todo) {
           const int src = __ffs(todo) - 1;
           todo &= todo - 1;
