@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 
   const int W = rq.pre[a.R] * (int)a.by_per.d;
   // no CTA takes less than about one piece a warp
-  const int C = min((W + NW - 1) / NW, (int)gridDim.x);
+  static_assert(NW == kLeast, "positions a CTA takes at least");
+  const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
   const int c = blockIdx.x;
   const int begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
 
@@ -692,20 +693,89 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The join of units that several CTAs shared: block (c, i) has row i of the unit
-// that CTA c started and did not end.  Its parts are CTA c's second slot and the
-// first slots of the CTAs behind it; their maxima and sums are read at once, one
-// a thread, then the warps add the outputs, each its share in a fixed order, so
-// the result does not depend on timing.
-// A call of few units may have 100 parts a row.  kFew: four blocks a row, 32 dims
-// each, and a block for every unit, which looks its CTA up (1 x 131K: 30.2 -> 23.7
-// us a call, four draft rows 36.0 -> 27.4; but 1 x 1K 8.9 -> 9.3, so only where a
-// unit may have over 32 parts).
+// The join of units that several CTAs shared.  The parts of the unit that CTA c
+// started and did not end are CTA c's second slot and the first slots of the CTAs
+// behind it; a row's maxima and sums are read at once, one a lane, then its
+// outputs are added in a fixed order, so the result does not depend on timing.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 4, kJoinThreads = 32 * kJoinWarps;
+
+__device__ __forceinline__ size_t part_at(const AttnArgs& a, int c, int s, int i) {
+  return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i;
+}
+
+// Output row and packed row of row i of the unit; false past the unit's rows.
+__device__ __forceinline__ bool joined_row(const AttnArgs& a, int unit, int i, size_t& row) {
+  const int r = a.by_per.div(unit), k = unit - r * (int)a.by_per.d;
+  const int head = a.by_groups.div(k), pk = (k - head * a.groups) * a.group_rows + i;
+  if (pk >= a.P * a.nq) return false;
+  const int p = a.by_nq.div(pk);
+  row = ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq);
+  return true;
+}
+
+__device__ __forceinline__ void add_scaled(float4& o, const float4& v, float f) {
+  o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+}
+
+// One warp a row, block (c, rows / 4).
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = (min(a.group_rows, a.P * a.nq) + kJoinWarps - 1) / kJoinWarps;
+  const int c = blockIdx.x / quads, i = (blockIdx.x - c * quads) * kJoinWarps + warp;
+  const SplitRecord rec = a.records[c];
+  size_t row;
+  if (rec.unit < 0 || !joined_row(a, rec.unit, i, row)) return;
+  constexpr int kPer = (kMaxCtas + 31) / 32;
+  float2 x[kPer];
+  float m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int s = lane + 32 * e;
+    x[e] = make_float2(-INFINITY, 0.f);
+    if (s < rec.splits) x[e] = a.part_ml[part_at(a, c, s, i)];
+    m = fmaxf(m, x[e].x);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    // a part with nothing visible in the row is not read: factor -1 says so
+    const float f = x[e].x == -INFINITY ? -1.f : ex2_approx(x[e].x - m);
+    if (x[e].x != -INFINITY) l = fmaf(x[e].y, f, l);
+    x[e].x = f;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    for (int s0 = 32 * e; s0 < min(rec.splits, 32 * e + 32); s0 += 8) {
+      float4 v[8];
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {   // eight parts' loads in flight
+        f[k] = __shfl_sync(0xffffffffu, x[e].x, (s0 + k) & 31);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f[k] != -1.f)
+          v[k] = reinterpret_cast<const float4*>(a.part_o + part_at(a, c, s0 + k, i) * kDim)[lane];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (f[k] != -1.f) add_scaled(o, v[k], f[k]);
+    }
+  }
+  write_row(a, row, m, l, o, lane);
+}
+
+// A call of few units may have 100 parts a row: four blocks a row, 32 dims each,
+// and a block for every unit, which looks its CTA up (1 x 131K: 30.2 -> 23.7 us a
+// call, four draft rows 36.0 -> 27.4; but 1 x 1K 8.9 -> 9.3, so only where a unit
+// may have over 32 parts).
 constexpr int kFewSplit = 4;
-template <bool kFew>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_few_kernel(const AttnArgs a, int ctas) {
   __shared__ float factor[kMaxCtas];
   __shared__ float red[2][kJoinWarps];
   __shared__ float4 so[kJoinWarps][32];
@@ -713,39 +783,28 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(a.group_rows, a.P * a.nq);
-  int c, i;
-  SplitRecord rec;
-  if (kFew) {
-    const int unit = blockIdx.x / (rows * kFewSplit);
-    i = blockIdx.x / kFewSplit - unit * rows;
-    if (threadIdx.x == 0) found = -1;
-    __syncthreads();
-    for (int k = threadIdx.x; k < ctas; k += kJoinThreads)
-      if (a.records[k].unit == unit) found = k;
-    __syncthreads();
-    c = found;
-    if (c < 0) return;
-  } else {
-    c = blockIdx.x / rows;
-    i = blockIdx.x - c * rows;
-  }
-  rec = a.records[c];
-  if (rec.unit < 0) return;
-  const int r = a.by_per.div(rec.unit), k = rec.unit - r * (int)a.by_per.d;
-  const int head = a.by_groups.div(k), pk = (k - head * a.groups) * a.group_rows + i;
-  if (pk >= a.P * a.nq) return;
-  auto part = [&](int s) { return (size_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.group_rows + i; };
+  const int unit = blockIdx.x / (rows * kFewSplit), i = blockIdx.x / kFewSplit - unit * rows;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  for (int k = threadIdx.x; k < ctas; k += kJoinThreads)
+    if (a.records[k].unit == unit) found = k;
+  __syncthreads();
+  const int c = found;
+  size_t row;
+  if (c < 0 || !joined_row(a, unit, i, row)) return;
+  const int splits = a.records[c].splits;
   static_assert(kMaxCtas <= 2 * kJoinThreads, "two parts a thread");
   float2 x[2];
   float m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int s = threadIdx.x + e * kJoinThreads;
-    x[e] = s < rec.splits ? a.part_ml[part(s)] : make_float2(-INFINITY, 0.f);
+    x[e] = make_float2(-INFINITY, 0.f);
+    if (s < splits) x[e] = a.part_ml[part_at(a, c, s, i)];
     m = fmaxf(m, x[e].x);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (lane == 0) red[0][warp] = m;
   __syncthreads();
 #pragma unroll
@@ -753,39 +812,35 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   float l = 0.f;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    // a part with nothing visible in the row is not read: factor -1 says so
     const int s = threadIdx.x + e * kJoinThreads;
     const float f = x[e].x == -INFINITY ? -1.f : ex2_approx(x[e].x - m);
-    if (s < rec.splits) factor[s] = f;
+    if (s < splits) factor[s] = f;
     if (x[e].x != -INFINITY) l = fmaf(x[e].y, f, l);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) l += red[1][w];
-  // a warp takes kAt parts at a time (a lane: four dims of one), eight such loads
-  // in flight
-  constexpr int kAt = kFew ? kFewSplit : 1, kLanes = 32 / kAt;
-  const int dim4 = (kFew ? (int)(blockIdx.x % kFewSplit) * kLanes : 0) + lane % kLanes;
+  // a warp takes four parts at a time, eight lanes each, eight such loads in flight
+  constexpr int kLanes = 32 / kFewSplit, kStep = kJoinWarps * kFewSplit;
+  const int dim4 = (int)(blockIdx.x % kFewSplit) * kLanes + lane % kLanes;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = warp * kAt + lane / kLanes; s0 < rec.splits; s0 += 8 * kJoinWarps * kAt) {
+  for (int s0 = warp * kFewSplit + lane / kLanes; s0 < splits; s0 += 8 * kStep) {
     float4 v[8];
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int s = s0 + e * kJoinWarps * kAt;
-      f[e] = s < rec.splits ? factor[s] : -1.f;
+      const int s = s0 + e * kStep;
+      f[e] = s < splits ? factor[s] : -1.f;
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (f[e] != -1.f) v[e] = reinterpret_cast<const float4*>(a.part_o + part(s) * kDim)[dim4];
+      if (f[e] != -1.f) v[e] = reinterpret_cast<const float4*>(a.part_o + part_at(a, c, s, i) * kDim)[dim4];
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (f[e] != -1.f)
-        o = make_float4(fmaf(v[e].x, f[e], o.x), fmaf(v[e].y, f[e], o.y), fmaf(v[e].z, f[e], o.z),
-                        fmaf(v[e].w, f[e], o.w));
+      if (f[e] != -1.f) add_scaled(o, v[e], f[e]);
   }
   so[warp][lane] = o;
   __syncthreads();
@@ -794,12 +849,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w)
 #pragma unroll
-    for (int e = 0; e < kAt; ++e) {
-      const float4 v = so[w][e * kLanes + lane];
-      o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-    }
-  const int p = a.by_nq.div(pk);
-  write_row(a, ((size_t)r * a.P + p) * a.q_heads + head * a.nq + (pk - p * a.nq), m, l, o, dim4);
+    for (int e = 0; e < kFewSplit; ++e) add_scaled(o, so[w][e * kLanes + lane], 1.f);
+  write_row(a, row, m, l, o, dim4);
 }
 
 template <int KF, bool kBlocks>
@@ -830,10 +881,16 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int grid = attn_ctas();
-  if (grid <= 0) return cudaErrorInvalidDevice;
-  const bool blocks = a.block_ids != nullptr;
-  if (a.group_rows > kTile)
+  const int sms = attn_ctas();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // no more CTAs than the longest contexts the page table can hold give work to
+  const bool wide = a.group_rows > kTile, blocks = a.block_ids != nullptr;
+  const long long units = (long long)a.R * (int)a.by_per.d;
+  const long long pieces = wide ? (a.most + 1) / 2 : a.most;
+  const long long line = units * (((pieces + (1ll << a.shift) - 1) >> a.shift) + a.unit_cost);
+  const long long least = wide ? kLeastWide : kLeast;
+  const int grid = (int)((line + least - 1) / least < sms ? (line + least - 1) / least : sms);
+  if (wide)
     e = launch_attn_wide(key_format, a, k_map, v_map, grid, dev, stream);
   else if (key_format == kBf16)
     e = blocks ? launch_kf<kBf16, true>(a, k_map, v_map, grid, dev, stream)
@@ -843,10 +900,10 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
                : launch_kf<kFp8, false>(a, k_map, v_map, grid, dev, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
-  const int units = a.R * (int)a.by_per.d;
-  const bool few = units * 16 <= grid && a.most > 32 * 8;
-  e = few ? launch_pdl(attn_join_kernel<true>, units * rows * kFewSplit, kJoinThreads, 0, stream, a, grid)
-          : launch_pdl(attn_join_kernel<false>, grid * rows, kJoinThreads, 0, stream, a, grid);
+  e = units * 16 <= grid && a.most > 32 * 8
+          ? launch_pdl(attn_join_few_kernel, (int)units * rows * kFewSplit, kJoinThreads, 0, stream, a, grid)
+          : launch_pdl(attn_join_kernel, grid * ((rows + kJoinWarps - 1) / kJoinWarps), kJoinThreads, 0,
+                       stream, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -111,6 +111,7 @@ inline size_t part_o_bytes(int ctas, int group_rows) {
 // ended by the CTA that holds its first position.  The host picks the shift (0 but
 // for calls of many million pieces) so that W * (C + 1) stays below 2^31.
 // ---------------------------------------------------------------------------
+constexpr int kLeast = 8, kLeastWide = 4;   // positions a CTA takes at least
 constexpr long long kMaxPositions = 0x7fffffffll / (kMaxCtas + 1);
 constexpr long long kMaxUnits = 1 << 18;
 constexpr int kMaxUnitCost = 32;

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
 
   const int W = rq.pre[a.R] * (int)a.by_per.d;
   // no CTA takes less than about four pages
-  const int C = min((W + 4 - 1) / 4, (int)gridDim.x);
+  const int C = min((W + kLeastWide - 1) / kLeastWide, (int)gridDim.x);
   const int c = blockIdx.x;
   const int begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
   SplitRecord record = {-1, 0};
