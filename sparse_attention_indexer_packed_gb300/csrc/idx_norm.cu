@@ -10,10 +10,11 @@
 // What bounds it: 7 bytes an element (x, residual in; residual, codes out)
 // against ~6 flop, so HBM; a few rows are a matter of latency.
 //
-// How: one CTA a row; the row stays in registers between the two passes over it
-// (sum of squares, then maximum and codes), so every byte crosses HBM once.
-// Rows of a multiple of 8 elements on 16-byte boundaries take 16-byte accesses;
-// any other row goes element by element through shared memory.
+// How: a row stays in registers between the two passes over it (sum of squares,
+// then maximum and codes), so every byte crosses HBM once.  Rows of a multiple of 8
+// elements on 16-byte boundaries take 16-byte accesses: a row of up to 128 elements
+// belongs to 16 lanes, up to 512 to a warp (neither needs a barrier), a longer one
+// to a CTA.  Any other row goes element by element through shared memory.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -61,13 +62,33 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// kVec 16-byte pieces a thread: a row has at most kVec * 8 * blockDim elements.
-template <int kVec>
-__global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
+// Sum (or maximum) over the threads of a row: kLanes of a warp, or (0) the block.
+template <bool kMax, int kLanes>
+__device__ __forceinline__ float row_reduce(float x, float* buf) {
+  if constexpr (kLanes == 0) {
+    return block_reduce<kMax>(x, buf);
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = kMax ? fmax_nan(x, y) : x + y;
+    }
+    return x;
+  }
+}
+
+// kVec 16-byte pieces a thread.  kLanes: threads of a row (16 or 32, 256 threads of
+// them a CTA), or 0: a CTA a row.
+template <int kVec, int kLanes>
+__global__ void __launch_bounds__(kLanes ? 256 : 1024) norm_vec_kernel(const NormArgs a) {
   __shared__ float buf[2][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long row = blockIdx.x;
-  const int nv = a.dim / 8, nt = blockDim.x;
+  const int nt = kLanes ? kLanes : blockDim.x, t = kLanes ? threadIdx.x % kLanes : threadIdx.x;
+  constexpr int kRows = kLanes ? 256 / (kLanes ? kLanes : 1) : 1;   // of a CTA
+  const long long want = (long long)blockIdx.x * kRows + (kLanes ? threadIdx.x / (256 / kRows) : 0);
+  const bool live = want < a.rows;       // lanes past the last row only take part in the shuffles
+  const long long row = live ? want : 0;
+  const int nv = live ? a.dim / 8 : 0;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.x_stride);
   const uint4* res = a.residual ? reinterpret_cast<const uint4*>(a.residual + row * a.residual_stride) : nullptr;
   const uint4* w = reinterpret_cast<const uint4*>(a.weight);
@@ -75,7 +96,7 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
   uint4 ux[kVec], ur[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int v = threadIdx.x + j * nt;
+    const int v = t + j * nt;
     ux[j] = ur[j] = make_uint4(0, 0, 0, 0);
     if (v < nv) {
       ux[j] = __ldcs(x + v);
@@ -85,7 +106,7 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int v = threadIdx.x + j * nt;
+    const int v = t + j * nt;
     const uint32_t wx[4] = {ux[j].x, ux[j].y, ux[j].z, ux[j].w};
     const uint32_t wr[4] = {ur[j].x, ur[j].y, ur[j].z, ur[j].w};
     uint32_t o[4];
@@ -101,11 +122,11 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
     if (a.out_residual && v < nv)
       __stcs(reinterpret_cast<uint4*>(a.out_residual + row * a.dim) + v, make_uint4(o[0], o[1], o[2], o[3]));
   }
-  const float rstd = rsqrtf(block_reduce<false>(sum, buf[0]) / (float)a.dim + a.eps);
+  const float rstd = rsqrtf(row_reduce<false, kLanes>(sum, buf[0]) / (float)a.dim + a.eps);
   float top = 0.f, group_top[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int v = threadIdx.x + j * nt;
+    const int v = t + j * nt;
     float m = 0.f;
     if (v < nv) {
       const uint4 u = __ldg(w + v);
@@ -121,11 +142,11 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a) {
     group_top[j] = m;
     top = fmax_nan(top, m);
   }
-  if (!a.group) top = block_reduce<true>(top, buf[1]);
+  if (!a.group) top = row_reduce<true, kLanes>(top, buf[1]);
   const int groups = a.group ? (a.dim + kGroup - 1) / kGroup : 1;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int v = threadIdx.x + j * nt;
+    const int v = t + j * nt;
     // a group of 128 is 16 lanes' pieces
     const float m = a.group ? lanes_max<16>(group_top[j]) : top;
     const float amax = fmax_nan(m, kAmaxFloor), up = e4m3_up(amax);
@@ -192,21 +213,28 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t stream) {
                    on16(a.x) && on16(a.residual) && on16(a.weight) && on16(a.out_residual) &&
                    (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
   cudaError_t e;
-  const int grid = (int)a.rows;
-  if (vec) {
-    const int nv = a.dim / 8;
-    // about two pieces a thread, 64 to 1024 threads
-    int threads = ((nv + 1) / 2 + 31) / 32 * 32;
-    threads = threads < 64 ? 64 : (threads > 1024 ? 1024 : threads);
-    if (nv <= 2 * threads) e = launch_pdl(norm_vec_kernel<2>, grid, threads, 0, stream, a);
-    else e = launch_pdl(norm_vec_kernel<4>, grid, threads, 0, stream, a);
+  const int nv = a.dim / 8;
+  auto grid_of = [&](int rows) { return (int)((a.rows + rows - 1) / rows); };
+  if (vec && nv <= 16) {
+    e = launch_pdl(norm_vec_kernel<1, 16>, grid_of(16), 256, 0, stream, a);
+  } else if (vec && nv <= 64) {
+    e = nv <= 32 ? launch_pdl(norm_vec_kernel<1, 32>, grid_of(8), 256, 0, stream, a)
+                 : launch_pdl(norm_vec_kernel<2, 32>, grid_of(8), 256, 0, stream, a);
+  } else if (vec) {
+    // two pieces a thread; four for many long rows: more CTAs an SM then overlap
+    // one row's passes with another's loads (9000 x 8192: 91 -> 79 us, 6000 x 12288:
+    // 112 -> 81; but 64 x 6144 2.6 -> 3.4)
+    const int per = (nv > 640 && a.rows >= 1024) || nv > 2048 ? 4 : 2;
+    int threads = ((nv + per - 1) / per + 31) / 32 * 32;
+    threads = threads < 64 ? 64 : threads;
+    e = per == 2 ? launch_pdl(norm_vec_kernel<2, 0>, grid_of(1), threads, 0, stream, a)
+                 : launch_pdl(norm_vec_kernel<4, 0>, grid_of(1), threads, 0, stream, a);
   } else {
-    const int bytes = a.dim * (int)sizeof(float);
     static std::atomic<unsigned long long> attr_done{0};
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = smem_limit_once(norm_any_kernel, kMaxNormDim * (int)sizeof(float), dev, attr_done);
-    if (e == cudaSuccess) e = launch_pdl(norm_any_kernel, grid, 256, (size_t)bytes, stream, a);
+    if (e == cudaSuccess) e = launch_pdl(norm_any_kernel, grid_of(1), 256, (size_t)a.dim * sizeof(float), stream, a);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
