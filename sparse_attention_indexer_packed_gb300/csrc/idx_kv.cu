@@ -11,6 +11,7 @@
 // the row maximum is four shuffles.  A CTA takes consecutive tokens of one head
 // and one plane, whose rows and scales lie side by side in the cache: their writes
 // fill whole sectors.
+#include <cuda_bf16.h>
 #include <stdint.h>
 
 #include "idx_internal.cuh"
@@ -21,6 +22,11 @@ namespace idx {
 namespace {
 
 constexpr int kRowsAtOnce = 16;   // rows of a 256-thread CTA at a time
+
+__device__ __forceinline__ __nv_bfloat162 magnitudes(uint32_t w) {
+  w &= 0x7fff7fffu;
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
 
 // Each 16 lanes store kTokens rows, kRowsAtOnce tokens apart; their loads all go
 // out before any is used.
@@ -48,30 +54,28 @@ __global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int ch
   }
 #pragma unroll
   for (int j = 0; j < kTokens; ++j) {
-    const long long slot = row[j];
-    const bool write = slot >= 0 && slot < a.num_slots;
-    const long long r = (slot / kPage * a.heads + h) * kPage + slot % kPage;
+    const unsigned long long slot = (unsigned long long)row[j];   // negative: past every slot
+    const bool write = slot < (unsigned long long)a.num_slots;
+    const unsigned long long r = ((slot >> 6) * a.heads + h) * kPage + (slot & (kPage - 1));
     if (KF == kBf16) {
       if (write) reinterpret_cast<uint4*>(payload + r * 256)[lane] = u[j];
       continue;
     }
     const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-    float x[8], m = 0.f;
+    // the row's largest magnitude on bf16 pairs, a NaN kept
+    __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(magnitudes(w[0]), magnitudes(w[1])),
+                                    __hmax2_nan(magnitudes(w[2]), magnitudes(w[3])));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-      m = fmax_nan(m, fmax_nan(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 8; o > 0; o >>= 1) m2 = __hmax2_nan(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    const float m = fmax_nan(__low2float(m2), __high2float(m2));
     const float amax = fmax_nan(m, kAmaxFloor), up = e4m3_up(amax);
     if (!write) continue;
-    const uint32_t lo = e4m3x2(__fmul_rn(x[0], up), __fmul_rn(x[1], up)) |
-                        (e4m3x2(__fmul_rn(x[2], up), __fmul_rn(x[3], up)) << 16);
-    const uint32_t hi = e4m3x2(__fmul_rn(x[4], up), __fmul_rn(x[5], up)) |
-                        (e4m3x2(__fmul_rn(x[6], up), __fmul_rn(x[7], up)) << 16);
-    reinterpret_cast<uint2*>(payload + r * 128)[lane] = make_uint2(lo, hi);
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c[e] = e4m3x2(__fmul_rn(__uint_as_float(w[e] << 16), up),
+                    __fmul_rn(__uint_as_float(w[e] & 0xffff0000u), up));
+    reinterpret_cast<uint2*>(payload + r * 128)[lane] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     if (lane == 0) (plane ? a.scale[1] : a.scale[0])[r] = __fdiv_rn(amax, kE4m3Max);
   }
 }
