@@ -1,5 +1,7 @@
 /*
- * libidx — packed sparse-attention index scoring + block top-k for GB300 (sm_103a).
+ * libidx — packed sparse-attention index scoring + block top-k for GB300 (sm_103a), and the
+ * operators of the layer around it: the key-value store, attention over the paged cache or over
+ * the chosen blocks, and the residual + RMS norm with an e4m3 result.
  *
  * C ABI.  Every pointer named "device" must point to device memory of the current
  * CUDA device; "host" pointers are read before the call returns.  Streams are
@@ -476,8 +478,8 @@ IDX_API int idx_set_wait_limit_ns(uint64_t ns);
 /* idx_set_stall_test — diagnostic (process-wide, off by default): with on != 0, in
  * every score CTA one role's first pipeline wait goes to a barrier that nothing
  * completes (the 16-row kernel: warp 0, after issuing its first copies; the
- * tensor-core kernel: the MMA issuer), so it runs out after the wait limit and the
- * call ends through the timeout path described above, with IDX_DEVERR_TIMEOUT set.
+ * tensor-core kernel: the MMA issuer; the attention kernels: warp 0's first piece, and
+ * the product issuer), so it runs out after the wait limit and the call ends through the timeout path described above, with IDX_DEVERR_TIMEOUT set.
  * Outputs of such a call are meaningless.  Lets a test exercise failure handling
  * on the GPU without a fault.  Always returns IDX_OK. */
 IDX_API int idx_set_stall_test(int on);

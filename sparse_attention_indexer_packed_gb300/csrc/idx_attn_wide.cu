@@ -9,8 +9,8 @@
 // the products: no key or value passes through registers.
 //
 // What bounds it: the cache's bytes.  A bf16 page is 32 KB, 1400 cycles of an
-// SM's share of the HBM rate; the products take ~400 of them and the weights'
-// arithmetic ~600 of each of the two softmax groups.
+// SM's share of the HBM rate; the products take ~400 of them, and of each softmax
+// group's ~2800 cycles a page (two groups alternate) half is waiting for scores.
 //
 // How a row is laid out.  A lane of a softmax warp owns one tensor-memory lane,
 // so the softmax needs no shuffle.  With 64 rows or fewer each row is given F =
@@ -33,6 +33,16 @@
 // 8 significant bits are 4 + 4; exact for elements within 2^10 of the row's
 // largest); the values are decoded to f16, exactly, by the group that uses them,
 // and the weights times the value's scale are one f16 (11 bits).
+//
+// Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 164 us, 6.0
+// TB/s of cache, 0.89 of the copy peak (the warp-level kernel, four groups of 16 rows:
+// 548); 32 rows 157 us, 0.93.  128 rows, 8 x 64K: 68 to 71 us, 0.54: a lane's 64
+// weights.  e4m3, 64 rows 161 us, 0.47; 32 rows 147: a group needs ~2700 cycles a page
+// (waits 600, decoding the values 540, weights 930, two thirds of it the scales), and
+// two groups alternate.  Up to 16 rows this kernel is the slower one (e4m3 16 x 131K
+// 152 us against 122 at the time, 1 x 1K 12.8 against 9.3).
+// Tried and slower: the values decoded by four warps of their own (161 -> 189); each
+// group finishing a slice through shared memory at a unit's end (166 -> 183).
 //
 // Every wait is bounded, as in the score kernels.
 #include <cuda_bf16.h>
