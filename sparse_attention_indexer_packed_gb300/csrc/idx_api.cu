@@ -273,6 +273,9 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_payload, 16) || !aligned(v_payload, 16) ||
       !aligned(k_scale, 16) || !aligned(v_scale, 16))
     return fail(IDX_ERR_INVALID, "q, out and the cache planes must be 16-byte aligned");
+  if (!aligned(page_table, 4) || !aligned(slot_ids, 4) || !aligned(row_lens, 4) ||
+      !aligned(block_ids, 4) || !aligned(out_lse, 4))
+    return fail(IDX_ERR_INVALID, "tables, lists and out_lse must be 4-byte aligned");
 
   idx::AttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -798,8 +801,8 @@ int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t
       (v_src && (v_stride < (int64_t)kv_heads * IDX_DIM || v_stride % 8 != 0)))
     return fail(IDX_ERR_INVALID,
                 "token strides must be multiples of 8 elements and at least kv_heads * 128");
-  if (!aligned(k_src, 16) || !aligned(v_src, 16))
-    return fail(IDX_ERR_INVALID, "k_src and v_src must be 16-byte aligned");
+  if (!aligned(k_src, 16) || !aligned(v_src, 16) || !aligned(slot_mapping, 8))
+    return fail(IDX_ERR_INVALID, "k_src and v_src must be 16-byte, slot_mapping 8-byte aligned");
   for (const idx_pool* p : pools) {
     if (!p) continue;
     if (!p->payload || (dtype == IDX_FP8_E4M3 && !p->scale))
@@ -876,6 +879,8 @@ int idx_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual,
   if (!x || !weight || !out || !out_scale) return fail(IDX_ERR_INVALID, "a required pointer is NULL");
   if (x_stride < dim || (residual && residual_stride < dim))
     return fail(IDX_ERR_INVALID, "row strides must be at least dim");
+  if (num_rows > 1 && residual && out_residual == residual && residual_stride != dim)
+    return fail(IDX_ERR_INVALID, "out_residual may be residual itself only when its stride is dim");
   if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(out_residual, 2) ||
       !aligned(out_scale, 4))
     return fail(IDX_ERR_INVALID, "bf16 pointers must be 2-byte, out_scale 4-byte aligned");

@@ -41,6 +41,7 @@ BAD = [
     (dict(out=None), -1), (dict(ws=None), -1), (dict(ws=FAKE + 64), -1), (dict(nb=1000), -1),
     (dict(q=FAKE + 8), -1), (dict(kp=FAKE + 8), -1), (dict(vp=FAKE + 8), -1),
     (dict(dtype=1, ks=FAKE + 4, vs=FAKE), -1), (dict(R=2048, P=1, Hq=1024, kv_heads=1024), -1),
+    (dict(table=FAKE + 2), -1), (dict(slots=FAKE + 1), -1), (dict(lens=FAKE + 2), -1), (dict(lse=FAKE + 2), -1),
 ]
 
 
@@ -97,7 +98,7 @@ def store(L, k=FAKE, v=FAKE, ks=256, vs=256, slots=FAKE, T=4, H=2, kp=None, vp=N
     (dict(vp=pool(1)), -1), (dict(vp=pool(pages=12)), -1), (dict(kp=pool(payload=None)), -1),
     (dict(kp=pool(1, scale=None), vp=pool(1)), -1), (dict(kp=pool(page_size=32)), -1),
     (dict(kp=pool(dim=64)), -1), (dict(kp=pool(payload_row_bytes=128)), -1),
-    (dict(kp=pool(payload=FAKE + 8)), -1), (dict(kp=pool(1, scale=FAKE + 2), vp=pool(1)), -1),
+    (dict(slots=FAKE + 4), -1), (dict(kp=pool(payload=FAKE + 8)), -1), (dict(kp=pool(1, scale=FAKE + 2), vp=pool(1)), -1),
 ])
 def test_store_refusals(L, over, status):
     assert store(L, **over) == status
@@ -120,7 +121,7 @@ def norm(L, **over):
     dict(T=-1), dict(T=1 << 31), dict(n=0), dict(n=32769), dict(g=64), dict(g=-128), dict(eps=-1.0),
     dict(eps=float("nan")), dict(x=None), dict(w=None), dict(out=None), dict(sc=None), dict(xs=255),
     dict(rs=255), dict(x=FAKE + 1), dict(r=FAKE + 1), dict(w=FAKE + 1), dict(sc=FAKE + 2),
-    dict(res=FAKE + 1)])
+    dict(res=FAKE + 1), dict(rs=512)])
 def test_norm_refusals(L, over):
     assert norm(L, **over) == -1
     assert L.idx_last_error() != b""
