@@ -588,6 +588,8 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
       st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
     }
+    st.m0 = not_empty(st.m0, st.l0);
+    st.m1 = not_empty(st.m1, st.l1);
     if (KF == kFp8) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)

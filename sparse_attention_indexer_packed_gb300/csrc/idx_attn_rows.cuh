@@ -290,6 +290,13 @@ __device__ __forceinline__ long long item_row(const AttnArgs& a, const Items& it
   return ((long long)page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
 }
 
+// The running maximum of a row's part for the join.  -inf means "no visible token"
+// there, and the part is not read; a row that saw nothing but NaN scores has that
+// maximum too, but its sum is NaN, and any finite value keeps it in.
+__device__ __forceinline__ float not_empty(float m, float l) {
+  return m == -INFINITY && l != l ? 0.f : m;
+}
+
 // One row of a stretch token by token (one warp, lane = four dims), for rows
 // whose joined output is not finite: the tiled products put 0 * NaN into a row
 // that does not see the NaN, this does not.
@@ -322,6 +329,7 @@ __device__ __noinline__ void careful_row(const AttnArgs& a, const Items& it, con
       m = mn;
     }
   }
+  m = not_empty(m, l);
 }
 
 __device__ __forceinline__ bool finite4(float4 o) {

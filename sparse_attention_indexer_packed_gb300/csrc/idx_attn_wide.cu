@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         // ---- the unit's end: the parts and the groups meet ------------------------
         if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
         tc_fence_after();
+        m = not_empty(m, l);
         ml[g * kLanes + quad * 32 + lane] = make_float4(m, l, mv, 0.f);
         group_sync();
         float M = -INFINITY, sum = 0.f;

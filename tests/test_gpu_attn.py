@@ -462,3 +462,26 @@ def test_the_native_call_and_the_python_one_agree(dtype):
                 blocks(*good[:at], bad, *good[at + 1:])
     for a, b in ((0, 2), (1, 3)):
         assert torch.equal(got[a][0], got[b][0]) and torch.equal(got[a][1], got[b][1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("Hq", [4, 16])
+def test_rows_that_see_nothing_but_nan_are_nan(dtype, Hq):
+    """Not mistaken for rows that see nothing: a request of one token, one of 200, all NaN."""
+    lens = [drafts(1, 4), drafts(200, 4), drafts(90, 4)]
+    c = _attn.make(dtype, lens, 1, 115)
+    q = draws(3, 4, Hq, 33)
+    clean = _attn.reference(c, q, 128 ** -0.5)
+    for r, n in ((0, 1), (1, 200)):
+        rows = _attn.token_rows(c.page_table[int(c.slot_ids[r])].tolist(), n, 0, 1)
+        (c.k[0] if dtype == "bf16" else c.k[1])[rows] = float("nan")
+    out, l, flags = run(c, q)
+    assert flags == 0
+    out, l = out.cpu().float(), l.cpu()
+    for r in range(2):
+        for p in range(4):
+            if lens[r][p] > 0:
+                assert torch.isnan(out[r, p]).all() and torch.isnan(l[r, p]).all()
+            else:
+                assert (out[r, p] == 0).all() and torch.isinf(l[r, p]).all()
+    assert ((out[2].double() - clean[0][2]).abs() <= clean[2][2]).all()
