@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  build_requests<kItem, kBlocks>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
+  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
 
   const int W = rq.pre[a.R] * (int)a.by_per.d;
   // no CTA takes less than about one piece a warp

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
-  build_requests<kTok, kBlocks>(a, rq, reinterpret_cast<int*>(ctl + 4), ctl);
+  build_requests<kTok, kBlocks, true>(a, rq, reinterpret_cast<int*>(ctl + 4), ctl);
   tc_fence_after();
   const uint32_t tmem = ctl[3];
 

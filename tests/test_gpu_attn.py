@@ -485,3 +485,17 @@ def test_rows_that_see_nothing_but_nan_are_nan(dtype, Hq):
             else:
                 assert (out[r, p] == 0).all() and torch.isinf(l[r, p]).all()
     assert ((out[2].double() - clean[0][2]).abs() <= clean[2][2]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("blocks,Hq,more", [(False, 4, 0), (True, 4, 0), (True, 2, 0), (False, 1, 40)])
+def test_many_draft_rows(dtype, blocks, Hq, more):
+    """A chunk of 70 tokens a request, each with its own length; few requests, and many."""
+    P = 70
+    lens = [drafts(L, P) for L in [300, 40, 0, 129] + list(range(more))]
+    c = _attn.make(dtype, lens, 1, 117)
+    q = draws(len(lens), P, Hq, 34)
+    ids = lists_for(lens, 2, 3, 35, P) if blocks else None
+    out, l, flags = run(c, q, block_ids=ids, lists=2 if blocks else 0)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, 2))
