@@ -16,6 +16,15 @@
 //  * a persistent grid, one CTA per SM; every CTA takes an equal stretch of the
 //    units' 32-token pieces (idx_attn.cuh), so one long request is split over
 //    many CTAs and many short ones share a CTA;
+//  * where the units are many and of like lengths they are not cut: teams of 1, 2, 4
+//    or 8 warps take whole units in turn, so that the cost of a unit's end (3 us for
+//    a CTA) is paid by several at a time.  The host picks the team from the units'
+//    number, every CTA finds from the lengths whether to deal or to cut (Cost).
+//    Cut / dealt, us: bf16 64 x 8 heads x 256 tokens 26.1 / 18.1, x 1K 53.4 / 46.2,
+//    x 8K 300 / 297; 256 x 8 x 100 61.7 / 26.8; 1 x 200 8.7 / 7.5; e4m3 64 x 8 x 256
+//    27.1 / 13.9, x 1K 47.0 / 32.1, 256 x 8 x 100 75.5 / 22.9.  The second way in
+//    the kernel costs calls that cut 1 to 4% (1 x 1K 9.1 -> 9.4), those of e4m3 with
+//    more units than SMs 9%;
 //  * a warp owns one shared-memory stage of one piece (keys and values, by TMA
 //    through the page table) and refills it as soon as it has been used; no
 //    stage is shared between warps, so there is no "empty" barrier;
@@ -33,11 +42,11 @@
 //  * every wait is bounded, as in the score kernels.
 //
 // Measured (one GB300, calls back to back): bf16 16 x 131K, 16 rows: 152 us, 6.49
-// TB/s of cache, 0.96 of the copy peak.  e4m3 16 x 131K: 96 us, 5.30 TB/s, 0.78: the
+// TB/s of cache, 0.96 of the copy peak.  e4m3 16 x 131K: 97 us, 5.24 TB/s, 0.77: the
 // products' operands are decoded in registers, 8 warps of 255 registers leave the
 // issue slots 36% used and the warps waiting on their own chains (12 warps of 168
 // registers spill: 117 us).  Lists, 16 x 131K, 4 x 4 rows, 64 blocks: 65 us for 369 MB
-// of joined blocks, 5.7 TB/s.  Short calls are latency: 1 x 1K 9.1 us (request table
+// of joined blocks, 5.7 TB/s.  Short calls are latency: 1 x 1K 9.4 us (request table
 // 0.9, first page id 2, first tile 4.3, output 5.7, join 8.7), 48 ragged requests
 // 25 us (first tiles 5 to 8, last output 21, join 25).
 // Tried and slower: two e4m3 query terms on m16n8k32 (113 -> 134 us, one stage a
@@ -91,7 +100,7 @@ struct ALayout {
   static constexpr int kMergeOff = kScaleOff + NW * D * kScaleBytes;
   static constexpr int kMlOff = kMergeOff + NW / 2 * kTile * kMergeStride * 4;
   static constexpr int kBarOff = kMlOff + NW / 2 * kTile * 8;
-  static constexpr int kCtlOff = kBarOff + (NW * D + 1) * 8;       // flags, count, one int a warp
+  static constexpr int kCtlOff = kBarOff + (NW * D + 1) * 8;       // flags, longest unit, one int a warp
   static constexpr int kPreOff = (kCtlOff + 8 + NW * 4 + 15) & ~15;
   static constexpr int kListOff = kPreOff + kRequestsBytes;
   static constexpr int kBytes = kListOff + kMaxList * 4;
@@ -383,15 +392,106 @@ __device__ __forceinline__ void put_part(const AttnArgs& a, int slot, int i, flo
   reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
 }
 
+// What the estimates below count in: the time in which an SM at its full rate takes a
+// piece (bf16 0.38 us, HBM's share; e4m3 0.23, the warps' own).  A warp alone needs
+// kAlone of it for a piece; kEnd and kEndAlone are a team's and a warp's cost of a unit
+// beside its pieces, kStretch that of another stretch of the line, kCut of the first
+// one and the join.
+template <int KF>
+struct Cost {
+  static constexpr float kAlone = 5.f;
+  static constexpr float kEnd = KF == kBf16 ? 6.f : 12.f, kEndAlone = KF == kBf16 ? 3.f : 6.f;
+  static constexpr float kStretch = KF == kBf16 ? 7.f : 14.f, kCut = KF == kBf16 ? 9.6f : 13.f;
+};
+
+// Whether the units of the call are dealt whole to teams of TW warps rather than cut
+// along the line: the estimate of both, the first from what the host knows (Dealt).
+// Every CTA comes to the same answer.
+template <int KF, int TW>
+__device__ __forceinline__ bool whole_units(const AttnArgs& a, const Requests& rq, int longest, int C) {
+  if (a.shift > 0) return false;
+  const int per = (int)a.by_per.d;
+  const float units = (float)(a.R * per), each = __fdividef(1.f, (float)C);
+  const float total = (float)((rq.pre[a.R] - a.R * a.unit_cost) * per), mean = __fdividef(total, units);
+  const float whole = a.dealt_ends + fmaxf(mean, (float)TW) * a.dealt_piece +
+                      ((float)longest - mean) * (Cost<KF>::kAlone / TW);
+  const float cut = fmaxf(total * each, Cost<KF>::kAlone) + Cost<KF>::kStretch * units * each + Cost<KF>::kCut;
+  return whole <= cut;
+}
+
+// The rows of a unit that one warp has (g and g + 8 of every lane, i0 and i1 their
+// places in out).
 template <int KF, bool kBlocks>
-__global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
-    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
-                const __grid_constant__ CUtensorMap v_map) {
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const Items& it, const uint32_t* list,
+                                           const State& st, int r, int row_first, int nrows, int p0,
+                                           bool has0, bool has1, size_t i0, size_t i1, int lane) {
+  const int t = lane & 3;
+  const bool see0 = st.m0 != -INFINITY, see1 = st.m1 != -INFINITY;
+  const float f0 = see0 ? 1.f / st.l0 : 0.f, f1 = see1 ? 1.f / st.l1 : 0.f;
+  bool odd0 = false, odd1 = false;   // something not finite: nothing visible is 0, not 0 * NaN
+  uint16_t* o0 = a.out + i0 * kDim;
+  uint16_t* o1 = a.out + i1 * kDim;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      odd0 |= see0 && !(fabsf(st.o[j][e]) < INFINITY);
+      odd1 |= see1 && !(fabsf(st.o[j][e + 2]) < INFINITY);
+    }
+  auto two = [](bool see, float x, float y, float f) { return see ? pack_bf16(x * f, y * f) : 0u; };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float* x = st.o[2 * j];
+    const float* y = st.o[2 * j + 1];
+    if (KF == kBf16) {
+      if (has0) {
+        *reinterpret_cast<uint32_t*>(o0 + 16 * j + 2 * t) = two(see0, x[0], x[1], f0);
+        *reinterpret_cast<uint32_t*>(o0 + 16 * j + 8 + 2 * t) = two(see0, y[0], y[1], f0);
+      }
+      if (has1) {
+        *reinterpret_cast<uint32_t*>(o1 + 16 * j + 2 * t) = two(see1, x[2], x[3], f1);
+        *reinterpret_cast<uint32_t*>(o1 + 16 * j + 8 + 2 * t) = two(see1, y[2], y[3], f1);
+      }
+    } else {
+      if (has0)
+        *reinterpret_cast<uint2*>(o0 + 16 * j + 4 * t) =
+            make_uint2(two(see0, x[0], y[0], f0), two(see0, x[1], y[1], f0));
+      if (has1)
+        *reinterpret_cast<uint2*>(o1 + 16 * j + 4 * t) =
+            make_uint2(two(see1, x[2], y[2], f1), two(see1, x[3], y[3], f1));
+    }
+  }
+  if (a.lse && t == 0) {
+    if (has0) a.lse[i0] = see0 ? (st.m0 + log2f(st.l0)) * kLn2 : st.m0;
+    if (has1) a.lse[i1] = see1 ? (st.m1 + log2f(st.l1)) * kLn2 : st.m1;
+  }
+  const uint32_t odds = __ballot_sync(0xffffffffu, odd0), more = __ballot_sync(0xffffffffu, odd1);
+  for (int i = 0; (odds | more) != 0u && i < nrows; ++i) {
+    if (((i < 8 ? odds : more) >> (4 * (i & 7)) & 0xfu) == 0u) continue;
+    const int pk = row_first + i, p = a.by_nq.div(pk);
+    const size_t at = ((size_t)r * a.P + p) * a.q_heads + it.head * a.nq + (pk - p * a.nq);
+    float m, l;
+    float4 o;
+    __syncwarp();
+    careful_row<KF, kItem, kBlocks>(a, it, list, a.q + at * kDim, it.glen > 0 ? row_len(a, r, p) : 0,
+                                    p - p0, lane, m, l, o);
+    write_row(a, at, m, l, o, lane);
+  }
+}
+
+// The CTA's units, TW warps a unit: its stretch of the line (kCut, TW = NW), or whole
+// units dealt in turn to the teams of all CTAs (kWhole), or the one that `whole` says.
+// record: the unit the CTA started and did not end.
+// (One body for either needs less code but a branch and a register here and there.
+// bf16, teams of 8: two bodies 1 x 400 8.74, 8 x 1000 13.66; one 8.92, 14.3.  e4m3: the
+// second body of a kernel comes out 8 to 20% slower, one body 1 to 5%.)
+enum class Deal { kCut, kWhole, kEither };
+template <int KF, bool kBlocks, int TW, Deal kDeal>
+__device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& k_map,
+                                          const CUtensorMap& v_map, uint8_t* smem, int W, int C,
+                                          bool whole, SplitRecord& record) {
   using L = ALayout<KF>;
   constexpr int NW = L::NW;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
   const Requests rq = requests_at(smem + L::kPreOff);
@@ -399,31 +499,19 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
   float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  if (lane == 0) {
-    for (int d = 0; d < L::D; ++d) mbar_init(sbase + L::kBarOff + (warp * L::D + d) * 8, 1);
-    if (warp == 0) mbar_init(sbase + L::kBarOff + NW * L::D * 8, 1);  // the stall test's barrier
-    fence_barrier_init();
-  }
-  if (threadIdx.x == 0) {
-    prefetch_tensormap(&k_map);
-    prefetch_tensormap(&v_map);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
-
-  const int W = rq.pre[a.R] * (int)a.by_per.d;
-  // no CTA takes less than about one piece a warp
-  static_assert(NW == kLeast, "positions a CTA takes at least");
-  const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
   const int c = blockIdx.x;
-  const int begin = c < C ? W * c / C : 0, end = c < C ? W * (c + 1) / C : 0;
+  const bool cut = kDeal == Deal::kCut || (kDeal == Deal::kEither && !whole);
+  const int team = warp / TW, member = warp % TW;
+  auto team_sync = [&]() {
+    if (TW == NW)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TW * 32) : "memory");
+  };
 
-  // ---- this warp's feed: items warp, warp + NW, ... of each stretch ---------
+  // ---- this warp's feed: items member, member + TW, ... of each stretch ---------
   // The page id is loaded here and looked at when the copy is issued, a piece
   // later, so nothing waits for it.
   struct Next {
@@ -432,9 +520,11 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     uint32_t members;
     int page, kv_head;
   };
-  SplitRecord record = {-1, 0};
   Walk walk, fwalk;
-  walk.begin(a, rq.pre, begin, end);
+  if (cut)
+    walk.begin(a, rq.pre, c < C ? W * c / C : 0, c < C ? W * (c + 1) / C : 0);
+  else
+    walk.begin_units(a, team * (int)gridDim.x + c, (NW / TW) * (int)gridDim.x);
   fwalk = walk;
   Items fit = {};
   int funit = -1, fi = 0;
@@ -444,15 +534,15 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     while (!dead) {
       if (fi >= fit.i1) {
         if (kBlocks || !fwalk.more()) break;
-        const Segment s = fwalk.next(a, rq.pre);
+        const Segment s = cut ? fwalk.next(a, rq.pre) : fwalk.next_unit(a, rq.pre);
         if (!s.live) continue;
         fit = make_items<kItem, kBlocks>(a, rq, s, 0);
         funit = s.unit;
-        fi = fit.i0 + warp;
+        fi = fit.i0 + member;
         continue;
       }
       const int i = fi;
-      fi += NW;
+      fi += TW;
       if (!item_tokens<kItem, kBlocks>(fit, list, i, n.tb, n.members)) continue;
       n.page = __ldg(a.page_table + (size_t)fit.slot * a.max_pages + n.tb / kPage);
       n.kv_head = fit.kv_head;
@@ -504,7 +594,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   int used = 0;           // pieces this warp has waited for
   bool primed = false;
   while (walk.more()) {
-    const Segment s = walk.next(a, rq.pre);
+    const Segment s = cut ? walk.next(a, rq.pre) : walk.next_unit(a, rq.pre);
     if (!s.live) continue;
     const int row_first = s.group * kTile;
     const int nrows = min(kTile, a.P * a.nq - row_first);
@@ -515,7 +605,7 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
                 (kBlock / kItem);
       fit = make_items<kItem, kBlocks>(a, rq, s, n_items);
       funit = s.unit;
-      fi = fit.i0 + warp;
+      fi = fit.i0 + member;
       primed = false;
     }
     // the first page id, the queries and the first copies overlap
@@ -582,7 +672,6 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       nxt = none;
     }
     // ---- join the warps: the upper half into the lower, then those by rows -----
-    constexpr int NH = NW / 2;
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
       st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
@@ -595,7 +684,14 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       for (int j = 0; j < 16; ++j)
         st.o[j][0] *= st.mv, st.o[j][1] *= st.mv, st.o[j][2] *= st.mv, st.o[j][3] *= st.mv;
     }
-    const int place = warp < NH ? warp : warp - NH;
+    if constexpr (TW == 1) {
+      // one warp has the whole unit: its rows are written from the registers
+      write_rows<KF, kBlocks>(a, it, list, st, s.r, row_first, nrows, p0, has0, has1,
+                              q_index(pk0, pd0), q_index(pk1, pd1), lane);
+      continue;
+    }
+    constexpr int nh = TW > 1 ? TW / 2 : 1;
+    const int first = team * nh, place = first + (member < nh ? member : member - nh);
     float* w0 = merge + (size_t)(place * kTile + g) * kMergeStride;
     float* w1 = w0 + 8 * kMergeStride;
     float2* ml0 = ml + place * kTile + g;
@@ -620,9 +716,9 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
         }
       }
     };
-    if (warp >= NH) put();
-    __syncthreads();
-    if (warp < NH) {
+    if (member >= nh) put();
+    team_sync();
+    if (member < nh) {
       const float2 x0 = ml0[0], x1 = ml0[8];
       const float n0 = fmaxf(st.m0, x0.x), n1 = fmaxf(st.m1, x1.x);
       const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
@@ -667,26 +763,28 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       __syncwarp();
       put();
     }
-    __syncthreads();
-    const bool complete = s.o0 == 0 && s.o1 == s.cap;
+    team_sync();
+    const bool complete = !cut || (s.o0 == 0 && s.o1 == s.cap);
     const int slot_out = 2 * c + (s.o0 == 0 ? 1 : 0);
     if (s.o0 == 0 && !complete) {
       record.unit = s.unit;
       record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
     }
-    for (int i = warp; i < nrows; i += NW) {
+    for (int i = member; i < nrows; i += TW) {
       const int pk = row_first + i, p = a.by_nq.div(pk);
       float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < NH; ++w) m = fmaxf(m, ml[w * kTile + i].x);
+      for (int w = 0; w < NW / 2; ++w)
+        if (w < nh) m = fmaxf(m, ml[(first + w) * kTile + i].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < NH; ++w) {
-          const float2 x = ml[w * kTile + i];
+        for (int w = 0; w < NW / 2; ++w) {
+          if (w >= nh) break;
+          const float2 x = ml[(first + w) * kTile + i];
           const float f = ex2_approx(x.x - m);
           if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
-          const float4 v = *reinterpret_cast<const float4*>(merge + (size_t)(w * kTile + i) * kMergeStride + 4 * lane);
+          const float4 v = *reinterpret_cast<const float4*>(merge + (size_t)((first + w) * kTile + i) * kMergeStride + 4 * lane);
           l = fmaf(x.y, f, l);
           o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
         }
@@ -699,12 +797,57 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
       else
         put_part(a, slot_out, i, m, l, o, lane);
     }
-    __syncthreads();
+    team_sync();
+  }
+  if (!cut) __syncthreads();
+}
+
+template <int KF, bool kBlocks, int TW>
+__global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map) {
+  using L = ALayout<KF>;
+  constexpr int NW = L::NW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
+  const Requests rq = requests_at(smem + L::kPreOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    for (int d = 0; d < L::D; ++d) mbar_init(sbase + L::kBarOff + (warp * L::D + d) * 8, 1);
+    if (warp == 0) mbar_init(sbase + L::kBarOff + NW * L::D * 8, 1);  // the stall test's barrier
+    fence_barrier_init();
   }
   if (threadIdx.x == 0) {
-    a.records[c] = record;
-    a.err_bytes[c] = (uint8_t)*cta_flags;
-    if (c == 0) *a.err_count = gridDim.x;
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
+
+  const int W = rq.pre[a.R] * (int)a.by_per.d;
+  // no CTA takes less than about one piece a warp
+  static_assert(NW == kLeast, "positions a CTA takes at least");
+  const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
+  SplitRecord record = {-1, 0};
+  const bool whole = !kBlocks && whole_units<KF, TW>(a, rq, (int)cta_flags[1], C);
+  if constexpr (kBlocks)
+    run_units<KF, true, NW, Deal::kCut>(a, k_map, v_map, smem, W, C, false, record);
+  else if constexpr (KF == kFp8 && TW == NW)
+    run_units<KF, false, NW, Deal::kEither>(a, k_map, v_map, smem, W, C, whole, record);
+  else if (whole)
+    run_units<KF, false, TW, Deal::kWhole>(a, k_map, v_map, smem, W, C, true, record);
+  else
+    run_units<KF, false, NW, Deal::kCut>(a, k_map, v_map, smem, W, C, false, record);
+  if (threadIdx.x == 0) {
+    a.records[blockIdx.x] = record;
+    a.err_bytes[blockIdx.x] = (uint8_t)*cta_flags;
+    if (blockIdx.x == 0) *a.err_count = gridDim.x;
   }
 }
 
@@ -869,16 +1012,56 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_few_kernel(const AttnA
   write_row(a, row, m, l, o, dim4);
 }
 
-template <int KF, bool kBlocks>
+template <int KF, bool kBlocks, int TW>
 cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
                       int grid, int dev, cudaStream_t stream) {
   using L = ALayout<KF>;
   static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = smem_limit_once(attn_kernel<KF, kBlocks>, L::kSmem, dev, attr_done);
+  cudaError_t e = smem_limit_once(attn_kernel<KF, kBlocks, TW>, L::kSmem, dev, attr_done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_kernel<KF, kBlocks>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
+  e = launch_pdl(attn_kernel<KF, kBlocks, TW>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+// What it costs to deal `units` units whole to teams of tw warps on `grid` SMs: `ends`
+// and, for each piece of their mean length, `piece`.  Full turns keep every warp busy,
+// the last one those that it has.
+struct Dealt {
+  float ends, piece;
+};
+template <int KF>
+Dealt dealt(int units, int grid, int tw) {
+  const int teams = grid * (kLeast / tw), full = units / teams, rest = units - full * teams;
+  const float busy = (float)(rest * tw) / (float)grid;
+  const float last = rest == 0 ? 0.f : busy > Cost<KF>::kAlone ? busy : Cost<KF>::kAlone;
+  return {(float)(full + (rest > 0)) * (tw == 1 ? Cost<KF>::kEndAlone : Cost<KF>::kEnd),
+          ((float)kLeast * (float)full + last) / (float)tw};
+}
+
+// The team size, where units are dealt whole, is the one with which units of 16 pieces
+// would take least: how long they are is known on the device only.
+template <int KF>
+cudaError_t launch_team(AttnArgs a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid,
+                        int dev, cudaStream_t stream) {
+  const int units = a.R * (int)a.by_per.d;
+  int team = 0;
+  float least = 0.f;
+  for (int tw = kLeast; tw >= 1; tw /= 2) {
+    const Dealt d = dealt<KF>(units, grid, tw);
+    const float cost = d.ends + 16.f * d.piece;
+    if (team > 0 && cost >= least) continue;
+    team = tw;
+    least = cost;
+    a.dealt_ends = d.ends;
+    a.dealt_piece = d.piece;
+  }
+  switch (team) {
+    case 1: return launch_kf<KF, false, 1>(a, k_map, v_map, grid, dev, stream);
+    case 2: return launch_kf<KF, false, 2>(a, k_map, v_map, grid, dev, stream);
+    case 4: return launch_kf<KF, false, 4>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_kf<KF, false, 8>(a, k_map, v_map, grid, dev, stream);
+  }
 }
 
 }  // namespace
@@ -909,11 +1092,11 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
   if (wide)
     e = launch_attn_wide(key_format, a, k_map, v_map, grid, dev, stream);
   else if (key_format == kBf16)
-    e = blocks ? launch_kf<kBf16, true>(a, k_map, v_map, grid, dev, stream)
-               : launch_kf<kBf16, false>(a, k_map, v_map, grid, dev, stream);
+    e = blocks ? launch_kf<kBf16, true, 8>(a, k_map, v_map, grid, dev, stream)
+               : launch_team<kBf16>(a, k_map, v_map, grid, dev, stream);
   else
-    e = blocks ? launch_kf<kFp8, true>(a, k_map, v_map, grid, dev, stream)
-               : launch_kf<kFp8, false>(a, k_map, v_map, grid, dev, stream);
+    e = blocks ? launch_kf<kFp8, true, 8>(a, k_map, v_map, grid, dev, stream)
+               : launch_team<kFp8>(a, k_map, v_map, grid, dev, stream);
   if (e != cudaSuccess) return e;
   const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
   e = units * 16 <= grid && a.most > 32 * 8

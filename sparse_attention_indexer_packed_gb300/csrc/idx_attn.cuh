@@ -77,6 +77,7 @@ struct AttnArgs {
   long long most;              // pieces a unit may have at most, as the host knows it
   int shift;                   // pieces of a position: 2^shift
   int unit_cost;               // positions that stand for a unit's end
+  float dealt_ends, dealt_piece;  // estimate of units dealt whole (up to 16 rows, no lists)
   float scale_log2;            // softmax scale times log2(e)
   unsigned long long wait_ns;
   int stall_test;
@@ -161,14 +162,22 @@ __device__ __forceinline__ int find_request(const int* pre, int R, int x) {
 }
 
 // A walk over the stretches of [pos, end), unit by unit: one search at its
-// start, no division after it.
+// start, no division after it.  Or (begin_units) over whole units, every step-th.
 struct Walk {
   int pos, end, start;   // start: the current unit's first position
   int r, head, group, unit, wt;
+  int step;              // 0: stretches
+
+  __device__ __forceinline__ void begin_units(const AttnArgs& a, int first, int stride) {
+    pos = first;
+    end = a.R * (int)a.by_per.d;
+    step = stride;
+  }
 
   __device__ __forceinline__ void begin(const AttnArgs& a, const int* pre, int first, int last) {
     pos = first;
     end = last;
+    step = 0;
     if (pos >= end) return;
     r = find_request(pre, a.R, a.by_per.div(pos));
     wt = pre[r + 1] - pre[r];
@@ -180,6 +189,21 @@ struct Walk {
     unit = r * per + k;
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
+  __device__ __forceinline__ Segment next_unit(const AttnArgs& a, const int* pre) {
+    Segment s;
+    s.unit = pos;
+    s.r = a.by_per.div(pos);
+    const int k = pos - s.r * (int)a.by_per.d;
+    s.head = a.by_groups.div(k);
+    s.group = k - s.head * a.groups;
+    s.start = 0;
+    s.cap = pre[s.r + 1] - pre[s.r] - a.unit_cost;
+    s.o0 = 0;
+    s.o1 = s.cap;
+    s.live = true;
+    pos += step;
+    return s;
+  }
   __device__ __forceinline__ Segment next(const AttnArgs& a, const int* pre) {
     Segment s;
     s.unit = unit;

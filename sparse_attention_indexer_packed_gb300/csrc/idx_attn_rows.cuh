@@ -98,17 +98,19 @@ __device__ __forceinline__ Requests requests_at(uint8_t* smem) {
 
 // Fill the table (every thread of the CTA, one request a thread at a time; ends
 // with a barrier).  sums: one int a warp.  flags gets IDX_DEVERR_LEN_CLAMPED
-// from the first CTA.  kMany (the wide kernel): where a request has 32 draft rows
+// from the first CTA.  kWide (the wide kernel): where a request has 32 draft rows
 // or more and the requests are two a warp at most, a warp takes a request first,
 // its lanes over the rows: 4 requests of 256 rows 27.1 -> 20.2 us, 8 of 64
 // 19.5 -> 18.1, 16 of 32 20.9 -> 20.5; but 128 of 64 24.6 -> 27.6 and 512 of 17
 // 25.9 -> 41.0, so more requests stay one a thread.
-template <int IT, bool kBlocks, bool kMany>
+template <int IT, bool kBlocks, bool kWide>
 __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests& q, int* sums,
                                                unsigned int* flags) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nt = blockDim.x;
+  int* longest = reinterpret_cast<int*>(flags + 1);   // pieces of the longest unit (not kWide)
   if (threadIdx.x == 0) *flags = 0u;
-  const bool many = kMany && a.P >= 32 && a.R <= 2 * (nt / 32);
+  if (!kWide && threadIdx.x == 0) *longest = 0;
+  const bool many = kWide && a.P >= 32 && a.R <= 2 * (nt / 32);
   if (many) {
     for (int v = warp; v < a.R; v += nt / 32) {
       int most = 0;
@@ -122,7 +124,7 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
   int run = 0;
   for (int v0 = 0; v0 < a.R; v0 += nt) {
     const int v = v0 + threadIdx.x;
-    int wt = 0, n = 0;
+    int wt = 0, n = 0, lots = 0;
     bool clamped = false;
     if (v < a.R) {
       // every load goes out before any is used
@@ -146,7 +148,8 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
       } else {
         wt = (n + IT - 1) / IT;
       }
-      wt = ((wt + (1 << a.shift) - 1) >> a.shift) + a.unit_cost;
+      lots = (wt + (1 << a.shift) - 1) >> a.shift;
+      wt = lots + a.unit_cost;
     }
     int incl = wt;
 #pragma unroll
@@ -163,6 +166,10 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
       total += y;
     }
     if (v < a.R) q.pre[v] = before + incl - wt;
+    if (!kWide && !kBlocks) {
+      lots = __reduce_max_sync(0xffffffffu, lots);
+      if (lane == 0) atomicMax(longest, lots);
+    }
     if (clamped) atomicOr(flags, kErrLenClamped);
     run = total;
     __syncthreads();   // sums is free again, and the table complete

@@ -499,3 +499,28 @@ def test_many_draft_rows(dtype, blocks, Hq, more):
     out, l, flags = run(c, q, block_ids=ids, lists=2 if blocks else 0)
     assert flags == 0
     _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, 2))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,Hkv", [(2, 1), (5, 1), (3, 4), (23, 1), (10, 4), (67, 2)])
+def test_many_short_requests_on_few_ctas(dtype, R, Hkv):
+    """Units that warps, pairs, fours and whole CTAs take, in one turn and in several; the last
+    row of request 1 sees a NaN that its other rows do not."""
+    lens = [drafts(L % 190, 3) for L in range(1, 37 * R, 37)]
+    lens[1] = drafts(40, 3)
+    c = _attn.make(dtype, lens, Hkv, 121, pads=(4,) if R > 4 else ())
+    q = draws(R, 3, 2 * Hkv, 36)
+    ref = _attn.reference(c, q, 128 ** -0.5)
+    rows = _attn.token_rows(c.page_table[int(c.slot_ids[1])].tolist(), 40, 0, Hkv)
+    (c.v[0] if dtype == "bf16" else c.v[1])[rows[-1]] = float("nan")
+    idx.idx_set_grid_limit(4)
+    try:
+        out, l, flags = run(c, q)
+        again, l2, _ = run(c, q)
+    finally:
+        idx.idx_set_grid_limit(0)
+    assert flags == 0
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(l, l2)
+    assert torch.isnan(out[1, 2, :2].float()).all()
+    out[1, 2, :2] = ref[0][1, 2, :2].to(out)
+    _attn.check(out, l, ref)
