@@ -22,7 +22,9 @@
 //    number, every CTA finds from the lengths whether to deal or to cut (Cost).
 //    Cut / dealt, us: bf16 64 x 8 heads x 256 tokens 26.1 / 18.1, x 1K 53.4 / 46.2,
 //    x 8K 300 / 297; 256 x 8 x 100 61.7 / 26.8; 1 x 200 8.7 / 7.5; e4m3 64 x 8 x 256
-//    27.1 / 13.9, x 1K 47.0 / 32.1, 256 x 8 x 100 75.5 / 22.9.  The second way in
+//    27.1 / 13.9, x 1K 47.0 / 32.1, 256 x 8 x 100 75.5 / 22.9.  Lists: bf16 128 x 4
+//    lists of 16 blocks 92.1 / 71.9, 60 x 4 of 12 38.9 / 31.7, e4m3 74.3 / 56.7 and
+//    36.3 / 27.5 (the host decides; no join kernel runs).  The second way in
 //    the kernel costs calls that cut 1 to 4% (1 x 1K 9.1 -> 9.4), those of e4m3 with
 //    more units than SMs 9%;
 //  * a warp owns one shared-memory stage of one piece (keys and values, by TMA
@@ -107,7 +109,6 @@ struct ALayout {
   // the block bits are only held while a list is joined: in the merge area,
   // which is free between two units
   static constexpr int kBitsOff = kMergeOff;
-  static_assert(2 * kMaxBlockWords * 4 <= kMlOff - kMergeOff, "block bits");
   static constexpr int kSmem = kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -397,25 +398,31 @@ __device__ __forceinline__ void put_part(const AttnArgs& a, int slot, int i, flo
 // kAlone of it for a piece; kEnd and kEndAlone are a team's and a warp's cost of a unit
 // beside its pieces, kStretch that of another stretch of the line, kCut of the first
 // one and the join.
-template <int KF>
+template <int KF, bool kBlocks>
 struct Cost {
-  static constexpr float kAlone = 5.f;
-  static constexpr float kEnd = KF == kBf16 ? 6.f : 12.f, kEndAlone = KF == kBf16 ? 3.f : 6.f;
-  static constexpr float kStretch = KF == kBf16 ? 7.f : 14.f, kCut = KF == kBf16 ? 9.6f : 13.f;
+  static constexpr float kAlone = 5.f, kList = !kBlocks ? 0.f : KF == kBf16 ? 6.f : 9.f;
+  static constexpr float kEnd = (KF == kBf16 ? 6.f : 12.f) + kList;
+  static constexpr float kEndAlone = KF == kBf16 ? 3.f : 6.f;
+  static constexpr float kStretch = (KF == kBf16 ? 7.f : 14.f) + kList;
+  static constexpr float kCut = (KF == kBf16 ? 9.6f : 13.f) + kList;
 };
+
+// Words of a team's joined list.
+__host__ __device__ constexpr int team_list_words(int tw) { return kMaxList / (kLeast / tw); }
 
 // Whether the units of the call are dealt whole to teams of TW warps rather than cut
 // along the line: the estimate of both, the first from what the host knows (Dealt).
 // Every CTA comes to the same answer.
 template <int KF, int TW>
 __device__ __forceinline__ bool whole_units(const AttnArgs& a, const Requests& rq, int longest, int C) {
+  using K = Cost<KF, false>;
   if (a.shift > 0) return false;
   const int per = (int)a.by_per.d;
   const float units = (float)(a.R * per), each = __fdividef(1.f, (float)C);
   const float total = (float)((rq.pre[a.R] - a.R * a.unit_cost) * per), mean = __fdividef(total, units);
   const float whole = a.dealt_ends + fmaxf(mean, (float)TW) * a.dealt_piece +
-                      ((float)longest - mean) * (Cost<KF>::kAlone / TW);
-  const float cut = fmaxf(total * each, Cost<KF>::kAlone) + Cost<KF>::kStretch * units * each + Cost<KF>::kCut;
+                      ((float)longest - mean) * (K::kAlone / TW);
+  const float cut = fmaxf(total * each, K::kAlone) + K::kStretch * units * each + K::kCut;
   return whole <= cut;
 }
 
@@ -495,8 +502,12 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
   const uint32_t sbase = smem_u32(smem);
   unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
   const Requests rq = requests_at(smem + L::kPreOff);
-  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff);
+  constexpr int kTeams = NW / TW;
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff) + team_list_words(TW) * (threadIdx.x / (32 * TW));
+  // a team's block bits lie where its parts will
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + L::kBitsOff) +
+                   (L::kMlOff - L::kMergeOff) / 4 / kTeams * (threadIdx.x / (32 * TW));
+  static_assert(!kBlocks || 2 * kMaxBlockWords * 4 * kTeams <= L::kMlOff - L::kMergeOff, "block bits");
   float* merge = reinterpret_cast<float*>(smem + L::kMergeOff);
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -601,7 +612,8 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
     const int p0 = a.by_nq.div(row_first);
     int n_items = 0;
     if (kBlocks) {
-      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits) *
+      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits,
+                           threadIdx.x % (32 * TW), 32 * TW, team_sync) *
                 (kBlock / kItem);
       fit = make_items<kItem, kBlocks>(a, rq, s, n_items);
       funit = s.unit;
@@ -802,7 +814,7 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
   if (!cut) __syncthreads();
 }
 
-template <int KF, bool kBlocks, int TW>
+template <int KF, bool kBlocks, int TW, Deal kDeal>
 __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map) {
@@ -835,15 +847,17 @@ __global__ void __launch_bounds__(ALayout<KF>::kThreads, 1)
   static_assert(NW == kLeast, "positions a CTA takes at least");
   const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
   SplitRecord record = {-1, 0};
-  const bool whole = !kBlocks && whole_units<KF, TW>(a, rq, (int)cta_flags[1], C);
-  if constexpr (kBlocks)
-    run_units<KF, true, NW, Deal::kCut>(a, k_map, v_map, smem, W, C, false, record);
-  else if constexpr (KF == kFp8 && TW == NW)
-    run_units<KF, false, NW, Deal::kEither>(a, k_map, v_map, smem, W, C, whole, record);
-  else if (whole)
-    run_units<KF, false, TW, Deal::kWhole>(a, k_map, v_map, smem, W, C, true, record);
-  else
-    run_units<KF, false, NW, Deal::kCut>(a, k_map, v_map, smem, W, C, false, record);
+  if constexpr (kDeal != Deal::kEither) {
+    run_units<KF, kBlocks, TW, kDeal>(a, k_map, v_map, smem, W, C, false, record);
+  } else {
+    const bool whole = whole_units<KF, TW>(a, rq, (int)cta_flags[1], C);
+    if constexpr (KF == kFp8 && TW == NW)
+      run_units<KF, kBlocks, NW, Deal::kEither>(a, k_map, v_map, smem, W, C, whole, record);
+    else if (whole)
+      run_units<KF, kBlocks, TW, Deal::kWhole>(a, k_map, v_map, smem, W, C, true, record);
+    else
+      run_units<KF, kBlocks, NW, Deal::kCut>(a, k_map, v_map, smem, W, C, false, record);
+  }
   if (threadIdx.x == 0) {
     a.records[blockIdx.x] = record;
     a.err_bytes[blockIdx.x] = (uint8_t)*cta_flags;
@@ -1012,14 +1026,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_few_kernel(const AttnA
   write_row(a, row, m, l, o, dim4);
 }
 
-template <int KF, bool kBlocks, int TW>
+template <int KF, bool kBlocks, int TW, Deal kDeal>
 cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
                       int grid, int dev, cudaStream_t stream) {
   using L = ALayout<KF>;
   static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = smem_limit_once(attn_kernel<KF, kBlocks, TW>, L::kSmem, dev, attr_done);
+  cudaError_t e = smem_limit_once(attn_kernel<KF, kBlocks, TW, kDeal>, L::kSmem, dev, attr_done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_kernel<KF, kBlocks, TW>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
+  e = launch_pdl(attn_kernel<KF, kBlocks, TW, kDeal>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1030,37 +1044,70 @@ cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtenso
 struct Dealt {
   float ends, piece;
 };
-template <int KF>
+template <int KF, bool kBlocks>
 Dealt dealt(int units, int grid, int tw) {
+  using K = Cost<KF, kBlocks>;
   const int teams = grid * (kLeast / tw), full = units / teams, rest = units - full * teams;
   const float busy = (float)(rest * tw) / (float)grid;
-  const float last = rest == 0 ? 0.f : busy > Cost<KF>::kAlone ? busy : Cost<KF>::kAlone;
-  return {(float)(full + (rest > 0)) * (tw == 1 ? Cost<KF>::kEndAlone : Cost<KF>::kEnd),
+  const float last = rest == 0 ? 0.f : busy > K::kAlone ? busy : K::kAlone;
+  return {(float)(full + (rest > 0)) * (tw == 1 ? K::kEndAlone : K::kEnd),
           ((float)kLeast * (float)full + last) / (float)tw};
 }
 
-// The team size, where units are dealt whole, is the one with which units of 16 pieces
-// would take least: how long they are is known on the device only.
-template <int KF>
-cudaError_t launch_team(AttnArgs a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid,
-                        int dev, cudaStream_t stream) {
+// The team size for units dealt whole: the one with which `units` of so many pieces
+// would take least, and what they would.
+template <int KF, bool kBlocks>
+int team_for(AttnArgs& a, int grid, float pieces, float& least) {
   const int units = a.R * (int)a.by_per.d;
   int team = 0;
-  float least = 0.f;
-  for (int tw = kLeast; tw >= 1; tw /= 2) {
-    const Dealt d = dealt<KF>(units, grid, tw);
-    const float cost = d.ends + 16.f * d.piece;
+  for (int tw = kLeast; tw >= (kBlocks ? 2 : 1); tw /= 2) {
+    // a team holds its joined list, and the parts of two warps the bits it is made with
+    if (kBlocks && min(a.P, kMaxDrafts) * a.topk > team_list_words(tw)) break;
+    const Dealt d = dealt<KF, kBlocks>(units, grid, tw);
+    const float cost = d.ends + pieces * d.piece;
     if (team > 0 && cost >= least) continue;
     team = tw;
     least = cost;
     a.dealt_ends = d.ends;
     a.dealt_piece = d.piece;
   }
+  return team;
+}
+
+// The whole cache: units of 16 pieces are assumed for the team; how long they are is
+// known on the device only, which decides whether they are dealt whole at all.
+template <int KF>
+cudaError_t launch_paged(AttnArgs a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid,
+                         int dev, cudaStream_t stream) {
+  float least;
+  switch (team_for<KF, false>(a, grid, 16.f, least)) {
+    case 1: return launch_kf<KF, false, 1, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+    case 2: return launch_kf<KF, false, 2, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+    case 4: return launch_kf<KF, false, 4, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_kf<KF, false, 8, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+  }
+}
+
+// Lists: their length bounds the units', so the host decides, for full lists (each
+// further draft row's taken to add an eighth of its own), and a call that deals needs no
+// join.  Only where the estimates lie apart: they are equally good for one of 368 units
+// of 32 blocks (122.8 us cut, 131 dealt), and a batch of contexts shorter than their
+// lists is better cut (96 units of 1 to 16 blocks 15.6, 18.7 dealt; all of 16 25.0, 22.2).
+template <int KF>
+cudaError_t launch_lists(AttnArgs a, const CUtensorMap& k_map, const CUtensorMap& v_map, int grid,
+                         int dev, cudaStream_t stream, bool& whole) {
+  using K = Cost<KF, true>;
+  const float full = (float)(a.topk * (kBlock / kItem)) * (1.f + (float)(a.P - 1) / 8.f);
+  const float pieces = fminf(full, (float)a.most);
+  const float share = (float)(a.R * (int)a.by_per.d) / (float)grid;
+  float least;
+  const int team = team_for<KF, true>(a, grid, pieces, least);
+  whole = least <= 0.83f * (fmaxf(share * pieces, K::kAlone) + K::kStretch * share + K::kCut);
+  if (!whole) return launch_kf<KF, true, 8, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
   switch (team) {
-    case 1: return launch_kf<KF, false, 1>(a, k_map, v_map, grid, dev, stream);
-    case 2: return launch_kf<KF, false, 2>(a, k_map, v_map, grid, dev, stream);
-    case 4: return launch_kf<KF, false, 4>(a, k_map, v_map, grid, dev, stream);
-    default: return launch_kf<KF, false, 8>(a, k_map, v_map, grid, dev, stream);
+    case 2: return launch_kf<KF, true, 2, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 4: return launch_kf<KF, true, 4, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_kf<KF, true, 8, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
   }
 }
 
@@ -1089,15 +1136,16 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
   const long long line = units * (((pieces + (1ll << a.shift) - 1) >> a.shift) + a.unit_cost);
   const long long least = wide ? kLeastWide : kLeast;
   const int grid = (int)((line + least - 1) / least < sms ? (line + least - 1) / least : sms);
+  bool whole = false;
   if (wide)
     e = launch_attn_wide(key_format, a, k_map, v_map, grid, dev, stream);
-  else if (key_format == kBf16)
-    e = blocks ? launch_kf<kBf16, true, 8>(a, k_map, v_map, grid, dev, stream)
-               : launch_team<kBf16>(a, k_map, v_map, grid, dev, stream);
+  else if (blocks)
+    e = key_format == kBf16 ? launch_lists<kBf16>(a, k_map, v_map, grid, dev, stream, whole)
+                            : launch_lists<kFp8>(a, k_map, v_map, grid, dev, stream, whole);
   else
-    e = blocks ? launch_kf<kFp8, true, 8>(a, k_map, v_map, grid, dev, stream)
-               : launch_team<kFp8>(a, k_map, v_map, grid, dev, stream);
-  if (e != cudaSuccess) return e;
+    e = key_format == kBf16 ? launch_paged<kBf16>(a, k_map, v_map, grid, dev, stream)
+                            : launch_paged<kFp8>(a, k_map, v_map, grid, dev, stream);
+  if (e != cudaSuccess || whole) return e;
   const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
   e = units * 16 <= grid && a.most > 32 * 8
           ? launch_pdl(attn_join_few_kernel, (int)units * rows * kFewSplit, kJoinThreads, 0, stream, a, grid)

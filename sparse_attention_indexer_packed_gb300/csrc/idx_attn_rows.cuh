@@ -166,7 +166,7 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
       total += y;
     }
     if (v < a.R) q.pre[v] = before + incl - wt;
-    if (!kWide && !kBlocks) {
+    if (!kWide) {
       lots = __reduce_max_sync(0xffffffffu, lots);
       if (lane == 0) atomicMax(longest, lots);
     }
@@ -180,14 +180,16 @@ __device__ __forceinline__ void build_requests(const AttnArgs& a, const Requests
 
 // The lists of draft rows p0 .. p1 (at most kMaxDrafts) of the segment's unit
 // joined in ascending order: list[i] = block id | drafts that list it << 16, bit
-// p - p0.  Every thread of the CTA; returns the number of blocks.  bits: 2 *
-// kMaxBlockWords words of scratch.  A set bit a block and a running count of them
+// p - p0.  All nt threads that share the unit, tid of them this one, with their
+// barrier; returns the number of blocks.  bits: 2 * kMaxBlockWords words of scratch.  A set bit a block and a running count of them
 // give each entry its place, so a block listed twice takes one.
+template <class Sync>
 __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq, const Segment& s,
-                                          int p0, int p1, uint32_t* list, uint32_t* bits) {
+                                          int p0, int p1, uint32_t* list, uint32_t* bits, int tid,
+                                          int nt, const Sync& sync) {
   constexpr int kKeep = 2;   // entries a thread keeps in registers between the passes
   uint32_t* rank = bits + kMaxBlockWords;
-  const int lane = threadIdx.x & 31, nt = blockDim.x;
+  const int lane = tid & 31;
   const int which = a.by_list.div(s.head);
   const int longest = rq.len[s.r];
   const int words = (longest + 32 * kBlock - 1) / (32 * kBlock);
@@ -201,25 +203,25 @@ __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq,
   int keep[kKeep], who[kKeep];
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
-    const int e = threadIdx.x + k * nt;
+    const int e = tid + k * nt;
     who[k] = 0;
     keep[k] = e < entries ? entry(e, who[k]) : -1;
   }
-  for (int w = threadIdx.x; w < words; w += nt) bits[w] = 0u;
-  for (int w = threadIdx.x; w < entries; w += nt) list[w] = 0u;
-  __syncthreads();
+  for (int w = tid; w < words; w += nt) bits[w] = 0u;
+  for (int w = tid; w < entries; w += nt) list[w] = 0u;
+  sync();
   auto each = [&](auto&& f) {
 #pragma unroll
     for (int k = 0; k < kKeep; ++k)
       if (keep[k] >= 0) f(keep[k], who[k]);
-    for (int e = threadIdx.x + kKeep * nt; e < entries; e += nt) {
+    for (int e = tid + kKeep * nt; e < entries; e += nt) {
       int p;
       const int id = entry(e, p);
       if (id >= 0) f(id, p);
     }
   };
   each([&](int id, int) { atomicOr(&bits[id >> 5], 1u << (id & 31)); });
-  __syncthreads();
+  sync();
   // blocks before each word: every warp for itself, and in shared memory
   int run = 0;
   for (int w0 = 0; w0 < words; w0 += 32) {
@@ -239,7 +241,7 @@ __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq,
     const uint32_t at = rank[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1u));
     atomicOr(&list[at], (uint32_t)id | (1u << (16 + p - p0)));
   });
-  __syncthreads();
+  sync();
   return run;
 }
 

@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
       int n_items = 0;
       if (kBlocks) {
         __syncthreads();      // every role is done with the last unit's list
-        n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits);
+        n_items = 2 * join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits, threadIdx.x,
+                                 blockDim.x, []() { __syncthreads(); });
       }
       const Items it = make_items<kTok, kBlocks>(a, rq, s, n_items);
       // the second page of a request's last block may not exist

@@ -524,3 +524,22 @@ def test_many_short_requests_on_few_ctas(dtype, R, Hkv):
     assert torch.isnan(out[1, 2, :2].float()).all()
     out[1, 2, :2] = ref[0][1, 2, :2].to(out)
     _attn.check(out, l, ref)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,lists,topk", [(5, 1, 3), (3, 2, 9), (7, 2, 5), (20, 2, 4), (9, 1, 256)])
+def test_many_short_lists_on_few_ctas(dtype, R, lists, topk):
+    """The same with block lists, each team joining its own."""
+    lens = [drafts(97 * k % 2900, 4) for k in range(R)]
+    c = _attn.make(dtype, lens, 1, 123, pads=(1,))
+    q = draws(R, 4, 2 * lists, 37)
+    ids = lists_for(lens, lists, topk, 38, 4)
+    idx.idx_set_grid_limit(4)
+    try:
+        out, l, flags = run(c, q, block_ids=ids, lists=lists)
+        again, l2, _ = run(c, q, block_ids=ids, lists=lists)
+    finally:
+        idx.idx_set_grid_limit(0)
+    assert flags == 0
+    assert torch.equal(out, again) and torch.equal(l, l2)
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, lists))
