@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
       mbar_init(pv_done(g), 1);
       mbar_init(s_free(g), 4);
     }
-    mbar_init(q_full, kLanes);
+    mbar_init(q_full, 2 * kLanes);
     mbar_init(stall_bar, 1);
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -472,45 +472,63 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         const int len = live && !pad ? row_len(a, s.r, p) : 0;
         const int bit = p - p0;
         float post = a.scale_log2;
-        if (n > 0 && (g == 0 || KF == kFp8)) {
-          // the lane's query row; group 0 puts it into tensor memory
+        if (n > 0) {
+          // the lane's query row into tensor memory, either group half of it
           const uint4* qp = reinterpret_cast<const uint4*>(a.q + q_row * kDim);
-          uint32_t w[64];
+          auto words = [&](int first, int e) {
+            return live ? __ldg(qp + first + e) : make_uint4(0, 0, 0, 0);
+          };
+          if constexpr (KF == kBf16) {
+            uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint4 u = live ? __ldg(qp + e) : make_uint4(0, 0, 0, 0);
-            w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
-          }
-          if (KF == kFp8) {
+            for (int e = 0; e < 8; ++e) {
+              const uint4 u = words(8 * g, e);
+              w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
+            }
+            tm_st<32>(tl + kColQ + 32 * g, w);
+          } else {
             // scaled by a power of two that brings the row's largest magnitude into
-            // [2^7, 2^8), then two e4m3 terms
+            // [2^7, 2^8), then two e4m3 terms: the group's half first, then the other,
+            // of which it needs the magnitude only
+            uint32_t w[32];
             float amax = 0.f;
+            {
+              float top[4] = {0.f, 0.f, 0.f, 0.f};
+              uint4 other[8];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+              for (int e = 0; e < 8; ++e) {
+                const uint4 u = words(8 * g, e);
+                w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) other[e] = words(8 - 8 * g, e);
+              auto largest = [&](float t, uint32_t x) { return fmaxf(t, fmaxf(fabsf(bf16_lo(x)), fabsf(bf16_hi(x)))); };
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top[k] = largest(top[k], w[4 * e + k]);
+                top[0] = largest(top[0], other[e].x), top[1] = largest(top[1], other[e].y);
+                top[2] = largest(top[2], other[e].z), top[3] = largest(top[3], other[e].w);
+              }
+              amax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            }
             const int ex = to_2_7(amax);
             const float up = ldexpf(1.f, ex);
             post *= ldexpf(1.f, -ex);
-            if (g == 0) {
-              uint32_t lo[32];
+            uint32_t lo[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
-                              bf16_hi(w[2 * e + 1]) * up};
-                w[e] = e4m3x4_take(x);
-                lo[e] = e4m3x4_take(x);
-              }
-              tm_st<32>(tl + kColQ, w);
-              tm_st<32>(tl + kColQ + 32, lo);
+            for (int e = 0; e < 16; ++e) {
+              float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
+                            bf16_hi(w[2 * e + 1]) * up};
+              w[e] = e4m3x4_take(x);
+              lo[e] = e4m3x4_take(x);
             }
-          } else {
-            tm_st<32>(tl + kColQ, w);
-            tm_st<32>(tl + kColQ + 32, w + 32);
+            tm_st<16>(tl + kColQ + 16 * g, w);
+            tm_st<16>(tl + kColQ + 32 + 16 * g, lo);
           }
-          if (g == 0) {
-            tm_wait_st();
-            tc_fence_before();
-            mbar_arrive(q_full);
-          }
+          tm_wait_st();
+          tc_fence_before();
+          mbar_arrive(q_full);
         }
         float m = -INFINITY, l = 0.f, mv = 0.f;
         int cnt = g ? cnt1 : cnt0;
