@@ -25,7 +25,7 @@
 //    27.1 / 13.9, x 1K 47.0 / 32.1, 256 x 8 x 100 75.5 / 22.9.  Lists: bf16 128 x 4
 //    lists of 16 blocks 92.1 / 71.9, 60 x 4 of 12 38.9 / 31.7, e4m3 74.3 / 56.7 and
 //    36.3 / 27.5 (the host decides; no join kernel runs).  The second way in
-//    the kernel costs calls that cut 1 to 4% (1 x 1K 9.1 -> 9.4), those of e4m3 with
+//    the kernel costs calls that cut 1 to 6% (1 x 1K 9.1 -> 9.5), those of e4m3 with
 //    more units than SMs 9%;
 //  * a warp owns one shared-memory stage of one piece (keys and values, by TMA
 //    through the page table) and refills it as soon as it has been used; no
@@ -48,7 +48,7 @@
 // products' operands are decoded in registers, 8 warps of 255 registers leave the
 // issue slots 36% used and the warps waiting on their own chains (12 warps of 168
 // registers spill: 117 us).  Lists, 16 x 131K, 4 x 4 rows, 64 blocks: 65 us for 369 MB
-// of joined blocks, 5.7 TB/s.  Short calls are latency: 1 x 1K 9.4 us (request table
+// of joined blocks, 5.7 TB/s.  Short calls are latency: 1 x 1K 9.5 us (request table
 // 0.9, first page id 2, first tile 4.3, output 5.7, join 8.7), 48 ragged requests
 // 25 us (first tiles 5 to 8, last output 21, join 25).
 // Tried and slower: two e4m3 query terms on m16n8k32 (113 -> 134 us, one stage a
