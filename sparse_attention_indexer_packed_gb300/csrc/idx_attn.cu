@@ -182,15 +182,16 @@ struct QRows {
 
 // Softmax state of the two rows a lane holds (g and g + 8), and its part of the
 // unnormalised output.  m in log2 units, the same in the four lanes of a row;
-// l is the lane's own part of the sum.  e4m3 values: o is held in units of mv, a
-// power of two, so that weight times scale / mv fits f16.
+// l is the lane's own part of the sum.  e4m3 values: l and o are held in units of
+// 2^e0 and 2^e1, so that weight times scale fits f16; a scale above lim = 2^(e + 6)
+// raises them.
 struct State {
-  float m0, m1, l0, l1, mv;
+  float m0, m1, l0, l1, e0, e1, lim0, lim1;
   float o[16][4];
   __device__ __forceinline__ void reset() {
     m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
-    mv = 0.f;
+    l0 = l1 = e0 = e1 = 0.f;
+    lim0 = lim1 = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
@@ -263,9 +264,41 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
   }
   const float mn0 = fmaxf(st.m0, mx0 * q.post0), mn1 = fmaxf(st.m1, mx1 * q.post1);
-  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
-  float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
+  float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
+  float old0 = st.m0, old1 = st.m1;
   st.m0 = mn0, st.m1 = mn1;
+  float2 vs[4];
+  if (KF == kFp8) {
+    // The rows' units: what a row holds depends on the tokens that it sees alone.  A
+    // unit is part of the exponent that the weights come from and costs nothing there.
+    float top0 = 0.f, top1 = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      vs[nt] = *reinterpret_cast<const float2*>(scales + kItem + nt * 8 + 2 * t);
+      const float x = fabsf(vs[nt].x), y = fabsf(vs[nt].y);
+      if (kMask) {
+        const int t0 = tb + nt * 8 + 2 * t;
+        top0 = fmaxf(top0, fmaxf(t0 < len0 ? x : 0.f, t0 + 1 < len0 ? y : 0.f));
+        top1 = fmaxf(top1, fmaxf(t0 < len1 ? x : 0.f, t0 + 1 < len1 ? y : 0.f));
+      } else {
+        top0 = fmaxf(top0, fmaxf(x, y));
+      }
+    }
+    if (!kMask) top1 = top0;
+    old0 += st.e0, old1 += st.e1;
+    if (__any_sync(0xffffffffu, top0 > st.lim0 || top1 > st.lim1 || st.lim0 == 0.f)) {
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+      }
+      const int u0 = unit_above(top0), u1 = unit_above(top1);
+      if (top0 > st.lim0 || st.lim0 == 0.f) st.e0 = (float)u0, st.lim0 = pow2(u0 + 6);
+      if (top1 > st.lim1 || st.lim1 == 0.f) st.e1 = (float)u1, st.lim1 = pow2(u1 + 6);
+    }
+    ref0 += st.e0, ref1 += st.e1;
+  }
+  const float c0 = ex2_approx(old0 - ref0), c1 = ex2_approx(old1 - ref1);
   const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
   const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -277,46 +310,9 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
     y1[nt].x = ex2_approx(y1[nt].x), y1[nt].y = ex2_approx(y1[nt].y);
     l0 = fadd2_rn(l0, y0[nt]);
     l1 = fadd2_rn(l1, y1[nt]);
-  }
-  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
-  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
-  if (KF == kFp8) {
-    // weights times value scales, in units of mv: a power of two that the scales
-    // may pass by 2^6 (a weight is at most 1, so f16 holds the product)
-    float2 vs[4];
-    float top = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      vs[nt] = *reinterpret_cast<const float2*>(scales + kItem + nt * 8 + 2 * t);
-      if (kMask) {
-        const int t0 = tb + nt * 8 + 2 * t;
-        if (t0 >= glen) vs[nt].x = 0.f;
-        if (t0 + 1 >= glen) vs[nt].y = 0.f;
-      }
-      top = fmaxf(top, fmaxf(fabsf(vs[nt].x), fabsf(vs[nt].y)));
-    }
-    if (!(top < INFINITY)) {   // only finite scales set the unit
-      top = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        if (fabsf(vs[nt].x) < INFINITY) top = fmaxf(top, fabsf(vs[nt].x));
-        if (fabsf(vs[nt].y) < INFINITY) top = fmaxf(top, fabsf(vs[nt].y));
-      }
-    }
-    if (__any_sync(0xffffffffu, top > st.mv * 64.f || st.mv == 0.f)) {
-#pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mv = fmaxf(st.mv, pow2_above(top));
-      const float shrink = st.mv / mv;
-      st.mv = mv;
-      c0 *= shrink, c1 *= shrink;
-    }
-    const float inv = 1.f / st.mv;   // a power of two: exact
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const float2 r = fmul2_rn(vs[nt], make_float2(inv, inv));
-      y0[nt] = fmul2_rn(y0[nt], r);
-      y1[nt] = fmul2_rn(y1[nt], r);
+    if (KF == kFp8) {
+      y0[nt] = fmul2_rn(y0[nt], vs[nt]);
+      y1[nt] = fmul2_rn(y1[nt], vs[nt]);
       if (kMask) {   // a masked token's scale may be anything
         const int t0 = tb + nt * 8 + 2 * t;
         if (t0 >= len0) y0[nt].x = 0.f;
@@ -326,6 +322,8 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       }
     }
   }
+  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
+  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
   if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -692,9 +690,10 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
     st.m0 = not_empty(st.m0, st.l0);
     st.m1 = not_empty(st.m1, st.l1);
     if (KF == kFp8) {
+      const float u0 = st.lim0 * 0x1p-6f, u1 = st.lim1 * 0x1p-6f;   // the units
+      st.l0 *= u0, st.l1 *= u1;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        st.o[j][0] *= st.mv, st.o[j][1] *= st.mv, st.o[j][2] *= st.mv, st.o[j][3] *= st.mv;
+      for (int j = 0; j < 16; ++j) st.o[j][0] *= u0, st.o[j][1] *= u0, st.o[j][2] *= u1, st.o[j][3] *= u1;
     }
     if constexpr (TW == 1) {
       // one warp has the whole unit: its rows are written from the registers

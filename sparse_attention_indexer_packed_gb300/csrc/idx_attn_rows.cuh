@@ -78,6 +78,14 @@ __device__ __forceinline__ float pow2_above(float x) {
   return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
 }
 
+// The unit that weights times value scales up to x are held in, as a power of two
+// between 2^-99 and 2^60: the smallest above x.  (Past 2^60 the products are not
+// finite in f16, and the row is computed token by token.)
+__device__ __forceinline__ int unit_above(float x) {
+  return min(max((int)(__float_as_uint(x) >> 23) - 126, -99), 60);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // Length of draft row p of request r, inside [0, max_pages * 64].
 __device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {
   const int L = __ldg(a.row_lens + r * a.P + p), cap = a.max_pages * kPage;

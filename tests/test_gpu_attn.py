@@ -543,3 +543,30 @@ def test_many_short_lists_on_few_ctas(dtype, R, lists, topk):
     assert flags == 0
     assert torch.equal(out, again) and torch.equal(l, l2)
     _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, lists))
+
+
+@pytest.mark.parametrize("Hq", [1, 4, 12])
+@pytest.mark.parametrize("blocks", [False, True])
+def test_value_scales_of_tokens_a_row_does_not_see(Hq, blocks):
+    """A row's precision does not depend on the tokens of the other rows: the last token, or
+    the other list's blocks, have values 2^24 times larger."""
+    P = 3
+    lens = [drafts(L, P) for L in (4, 40, 300, 257)]
+    c = _attn.make("fp8_e4m3", lens, 1, 125)
+    for r, row in enumerate(lens):
+        rows = _attn.token_rows(c.page_table[int(c.slot_ids[r])].tolist(), max(row), 0, 1)
+        c.v[1][rows[-1]] *= 2.0 ** 24
+        if blocks and max(row) > 128:
+            c.v[1][rows[:128]] *= 2.0 ** 24
+    q = draws(4, P, Hq, 39)
+    ids = None
+    if blocks:
+        ids = torch.full((4, P, 2), -1, dtype=torch.int32)
+        for r, row in enumerate(lens):
+            last = (max(row) - 1) // 128
+            ids[r, 0, 0] = ids[r, 1, 1] = 0 if last == 0 else 1     # not block 0, where there is another
+            ids[r, 2, 0] = last
+            ids[r, 2, 1] = 0
+    out, l, flags = run(c, q, block_ids=ids, lists=1 if blocks else 0)
+    assert flags == 0
+    _attn.check(out, l, _attn.reference(c, q, 128 ** -0.5, ids, 1))
