@@ -182,9 +182,9 @@ struct QRows {
 
 // Softmax state of the two rows a lane holds (g and g + 8), and its part of the
 // unnormalised output.  m in log2 units, the same in the four lanes of a row;
-// l is the lane's own part of the sum.  e4m3 values: l and o are held in units of
-// 2^e0 and 2^e1, so that weight times scale fits f16; a scale above lim = 2^(e + 6)
-// raises them.
+// l is the lane's own part of the sum.  e4m3 values: o is held in units of 2^e0 and
+// 2^e1, so that weight times scale fits f16; a scale above lim = 2^(e + 6) raises
+// them.  (l is not: a unit that rises by 2^127 would flush what was summed before.)
 struct State {
   float m0, m1, l0, l1, e0, e1, lim0, lim1;
   float o[16][4];
@@ -264,13 +264,15 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
   }
   const float mn0 = fmaxf(st.m0, mx0 * q.post0), mn1 = fmaxf(st.m1, mx1 * q.post1);
-  float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
-  float old0 = st.m0, old1 = st.m1;
+  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
+  const float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
+  float co0 = c0, co1 = c1;   // what the output gathered so far is multiplied by
+  float f0 = 1.f, f1 = 1.f;   // the values' unit
+  const float old0 = st.m0, old1 = st.m1;
   st.m0 = mn0, st.m1 = mn1;
   float2 vs[4];
   if (KF == kFp8) {
-    // The rows' units: what a row holds depends on the tokens that it sees alone.  A
-    // unit is part of the exponent that the weights come from and costs nothing there.
+    // The rows' units: what a row holds depends on the tokens that it sees alone.
     float top0 = 0.f, top1 = 0.f;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
@@ -285,7 +287,7 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       }
     }
     if (!kMask) top1 = top0;
-    old0 += st.e0, old1 += st.e1;
+    const float was0 = st.e0, was1 = st.e1;
     if (__any_sync(0xffffffffu, top0 > st.lim0 || top1 > st.lim1 || st.lim0 == 0.f)) {
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) {
@@ -296,9 +298,10 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       if (top0 > st.lim0 || st.lim0 == 0.f) st.e0 = (float)u0, st.lim0 = pow2(u0 + 6);
       if (top1 > st.lim1 || st.lim1 == 0.f) st.e1 = (float)u1, st.lim1 = pow2(u1 + 6);
     }
-    ref0 += st.e0, ref1 += st.e1;
+    co0 = ex2_approx(old0 - ref0 + (was0 - st.e0));
+    co1 = ex2_approx(old1 - ref1 + (was1 - st.e1));
+    f0 = pow2(-(int)st.e0), f1 = pow2(-(int)st.e1);
   }
-  const float c0 = ex2_approx(old0 - ref0), c1 = ex2_approx(old1 - ref1);
   const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
   const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -311,8 +314,8 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
     l0 = fadd2_rn(l0, y0[nt]);
     l1 = fadd2_rn(l1, y1[nt]);
     if (KF == kFp8) {
-      y0[nt] = fmul2_rn(y0[nt], vs[nt]);
-      y1[nt] = fmul2_rn(y1[nt], vs[nt]);
+      y0[nt] = fmul2_rn(fmul2_rn(y0[nt], make_float2(f0, f0)), vs[nt]);
+      y1[nt] = fmul2_rn(fmul2_rn(y1[nt], make_float2(f1, f1)), vs[nt]);
       if (kMask) {   // a masked token's scale may be anything
         const int t0 = tb + nt * 8 + 2 * t;
         if (t0 >= len0) y0[nt].x = 0.f;
@@ -324,11 +327,11 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
   }
   st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
   st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
-  if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
+  if (__any_sync(0xffffffffu, co0 != 1.f || co1 != 1.f)) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      st.o[j][0] *= c0, st.o[j][1] *= c0;
-      st.o[j][2] *= c1, st.o[j][3] *= c1;
+      st.o[j][0] *= co0, st.o[j][1] *= co0;
+      st.o[j][2] *= co1, st.o[j][3] *= co1;
     }
   }
 #pragma unroll
@@ -691,7 +694,6 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
     st.m1 = not_empty(st.m1, st.l1);
     if (KF == kFp8) {
       const float u0 = st.lim0 * 0x1p-6f, u1 = st.lim1 * 0x1p-6f;   // the units
-      st.l0 *= u0, st.l1 *= u1;
 #pragma unroll
       for (int j = 0; j < 16; ++j) st.o[j][0] *= u0, st.o[j][1] *= u0, st.o[j][2] *= u1, st.o[j][3] *= u1;
     }

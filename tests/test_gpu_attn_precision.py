@@ -1,0 +1,66 @@
+"""How exact the attention is (needs a GPU): bounds that follow from the stated roundings, and
+caches and queries of far apart magnitudes, where a unit that is held in few bits shows."""
+import pytest
+import torch
+
+import _attn
+import _attn_bounds
+import sparse_attention_indexer_packed_gb300 as idx
+from test_gpu_attn import draws, drafts, lists_for, run
+
+pytestmark = pytest.mark.gpu
+DTYPES = ["bf16", "fp8_e4m3"]
+SM = 128 ** -0.5
+WIDE = [False, True]          # 4 draft rows of 4 heads, or of 16: the tcgen05 kernel
+
+
+def heads(wide):
+    return 16 if wide else 4
+
+
+def rows_of(c, r, n):
+    return _attn.token_rows(c.page_table[int(c.slot_ids[r])].tolist(), n, 0, c.kv_heads)
+
+
+def set_keys(c, rows, keys):
+    """Key rows of an e4m3 cache, quantized as the store does."""
+    c.k[0][rows], c.k[1][rows] = _attn.quantize(keys)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("blocks", [False, True])
+def test_no_less_exact_than_stated(dtype, wide, blocks):
+    Hq = heads(wide)
+    lens = [drafts(L, 4) for L in (700, 65, 33, 1500)]
+    c = _attn.make(dtype, lens, 1, 201)
+    q = draws(4, 4, Hq, 202)
+    ids = lists_for(lens, 1, 5, 203, 4) if blocks else None
+    out, l, flags = run(c, q, block_ids=ids, lists=1 if blocks else 0)
+    assert flags == 0
+    ref = _attn_bounds.reference(c, q, SM, ids, 1, split_query=wide and dtype != "bf16")
+    _attn_bounds.check(out, l, ref, rows=torch.isfinite(ref[1]))
+
+
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("ctas", [1, 0])
+def test_zero_values_before_large_ones_stay_in_the_sum(wide, ctas):
+    """Tokens of value zero weigh as much as the others, whatever the others' values are."""
+    lens = [drafts(L, 4) for L in (1100, 90)]
+    q = draws(2, 4, heads(wide), 204)
+    c = _attn.make("fp8_e4m3", lens, 1, 205)
+    for r, n, zeros in ((0, 1100, 560), (1, 90, 64)):
+        at = rows_of(c, r, n)
+        c.v[0][at[:zeros]] = 0
+        c.v[1][at[:zeros]] = 2.0 ** -96 / 448
+        c.v[1][at[zeros:]] = 6e10 / 448
+    idx.idx_set_grid_limit(ctas)
+    try:
+        out, l, flags = run(c, q)
+        c2 = _attn.make("fp8_e4m3", lens, 1, 205)
+        _, l2, _ = run(c2, q)
+    finally:
+        idx.idx_set_grid_limit(0)
+    assert flags == 0
+    assert torch.equal(l, l2)           # the values have no part in the weights' sum
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
