@@ -182,16 +182,16 @@ struct QRows {
 
 // Softmax state of the two rows a lane holds (g and g + 8), and its part of the
 // unnormalised output.  m in log2 units, the same in the four lanes of a row;
-// l is the lane's own part of the sum.  e4m3 values: o is held in units of 2^e0 and
-// 2^e1, so that weight times scale fits f16; a scale above lim = 2^(e + 6) raises
-// them.  (l is not: a unit that rises by 2^127 would flush what was summed before.)
+// l is the lane's own part of the sum.  e4m3 values: o is held in units of 2^n0 and
+// 2^n1 (n absolute, as m), so that weight times value scale fits f16; see raise_unit.
+// (l is not: a unit far from the weights would flush what was summed before.)
 struct State {
-  float m0, m1, l0, l1, e0, e1, lim0, lim1;
+  float m0, m1, l0, l1, n0, n1;
   float o[16][4];
   __device__ __forceinline__ void reset() {
     m0 = m1 = -INFINITY;
-    l0 = l1 = e0 = e1 = 0.f;
-    lim0 = lim1 = 0.f;
+    l0 = l1 = 0.f;
+    n0 = n1 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   }
@@ -267,12 +267,13 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
   const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
   const float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
   float co0 = c0, co1 = c1;   // what the output gathered so far is multiplied by
-  float f0 = 1.f, f1 = 1.f;   // the values' unit
-  const float old0 = st.m0, old1 = st.m1;
   st.m0 = mn0, st.m1 = mn1;
+  const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
+  const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
+  float f0 = 1.f, f1 = 1.f;   // weights to the output's unit
   float2 vs[4];
   if (KF == kFp8) {
-    // The rows' units: what a row holds depends on the tokens that it sees alone.
+    // what the weights times scales of the tokens that a row sees are at most
     float top0 = 0.f, top1 = 0.f;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
@@ -287,23 +288,26 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       }
     }
     if (!kMask) top1 = top0;
-    const float was0 = st.e0, was1 = st.e1;
-    if (__any_sync(0xffffffffu, top0 > st.lim0 || top1 > st.lim1 || st.lim0 == 0.f)) {
+    const float x0 = mx0 * q.post0, x1 = mx1 * q.post1;
+    co0 = co1 = 1.f;          // the unit does not move with the maximum
+    if (__any_sync(0xffffffffu, past_unit(top0, x0, st.n0) || past_unit(top1, x1, st.n1))) {
+      top0 = top1 = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const float2 u = ffma2_rn(y0[nt], p0, r0), w = ffma2_rn(y1[nt], p1, r1);
+        top0 = fmaxf(top0, fmaxf(fabsf(ex2_approx(u.x) * vs[nt].x), fabsf(ex2_approx(u.y) * vs[nt].y)));
+        top1 = fmaxf(top1, fmaxf(fabsf(ex2_approx(w.x) * vs[nt].x), fabsf(ex2_approx(w.y) * vs[nt].y)));
+      }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) {
         top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
         top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
       }
-      const int u0 = unit_above(top0), u1 = unit_above(top1);
-      if (top0 > st.lim0 || st.lim0 == 0.f) st.e0 = (float)u0, st.lim0 = pow2(u0 + 6);
-      if (top1 > st.lim1 || st.lim1 == 0.f) st.e1 = (float)u1, st.lim1 = pow2(u1 + 6);
+      co0 = raise_unit(top0, mn0, st.n0);
+      co1 = raise_unit(top1, mn1, st.n1);
     }
-    co0 = ex2_approx(old0 - ref0 + (was0 - st.e0));
-    co1 = ex2_approx(old1 - ref1 + (was1 - st.e1));
-    f0 = pow2(-(int)st.e0), f1 = pow2(-(int)st.e1);
+    f0 = to_unit(mn0, st.n0), f1 = to_unit(mn1, st.n1);
   }
-  const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
-  const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
   for (int nt = 0; nt < 4; ++nt) {
@@ -693,7 +697,8 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
     st.m0 = not_empty(st.m0, st.l0);
     st.m1 = not_empty(st.m1, st.l1);
     if (KF == kFp8) {
-      const float u0 = st.lim0 * 0x1p-6f, u1 = st.lim1 * 0x1p-6f;   // the units
+      // the output in the maximum's unit, as the sum
+      const float u0 = ex2_approx(st.n0 - st.m0), u1 = ex2_approx(st.n1 - st.m1);
 #pragma unroll
       for (int j = 0; j < 16; ++j) st.o[j][0] *= u0, st.o[j][1] *= u0, st.o[j][2] *= u1, st.o[j][3] *= u1;
     }

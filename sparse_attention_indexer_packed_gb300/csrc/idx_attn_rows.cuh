@@ -78,13 +78,32 @@ __device__ __forceinline__ float pow2_above(float x) {
   return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
 }
 
-// The unit that weights times value scales up to x are held in, as a power of two
-// between 2^-99 and 2^60: the smallest above x.  (Past 2^60 the products are not
-// finite in f16, and the row is computed token by token.)
-__device__ __forceinline__ int unit_above(float x) {
-  return min(max((int)(__float_as_uint(x) >> 23) - 126, -99), 60);
+// e4m3 values.  A token enters the product with the values as weight times value
+// scale, 2^(x - m) vs for a score of x (log2 units), in one f16: 11 bits, and 2^-25 of
+// the output's unit.  So the unit 2^n follows the largest such product that the row
+// has seen, which is then held as [2^3, 2^14]: what a token counts for sets it, neither
+// its scale nor its weight alone, and the smallest products lose bits, never the
+// largest.  2^n is absolute: a maximum that rises takes no part in it.
+constexpr float kMostHeld = 16384.f;
+// Whether a product may be past the unit: scales up to `top`, scores up to x.
+__device__ __forceinline__ bool past_unit(float top, float x, float n) {
+  return x != -INFINITY && !(top * ex2_approx(x - n) <= kMostHeld);
 }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// Raise n where the largest product, top 2^m, is past it: its exponent less 3.  (Where
+// every product is zero n is 2^113 below the weights.)  Returns what the output
+// gathered so far is to be multiplied by.
+__device__ __forceinline__ float raise_unit(float top, float m, float& n) {
+  if (!past_unit(top, m, n)) return 1.f;
+  const int e = max((int)((__float_as_uint(top) >> 23) & 0xffu) - 127, -110);
+  const float up = m + (float)(e - 3), factor = ex2_approx(n - up);
+  n = up;
+  return factor;
+}
+// The factor from weights, in units of 2^m, to the output's unit.  A row that has not
+// seen a score above -inf has neither.
+__device__ __forceinline__ float to_unit(float m, float n) {
+  return m == -INFINITY ? 0.f : ex2_approx(m - n);
+}
 
 // Length of draft row p of request r, inside [0, max_pages * 64].
 __device__ __forceinline__ int row_len(const AttnArgs& a, int r, int p) {

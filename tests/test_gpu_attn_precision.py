@@ -64,3 +64,48 @@ def test_zero_values_before_large_ones_stay_in_the_sum(wide, ctas):
     assert flags == 0
     assert torch.equal(l, l2)           # the values have no part in the weights' sum
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
+
+
+@pytest.mark.parametrize("wide", WIDE[:1])
+@pytest.mark.parametrize("blocks", [False, True])
+@pytest.mark.parametrize("below", [40, 60])
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 26, 2.0 ** 37])
+def test_a_large_value_of_little_weight(wide, blocks, below, factor):
+    """A visible token whose values are far above the others' but whose weight is 2^-below."""
+    lens = [drafts(L, 4) for L in (40, 300, 257, 610)]
+    c = _attn.make("fp8_e4m3", lens, 1, 206)
+    q = draws(4, 4, heads(wide), 207)
+    q[..., 0] = 8.0
+    for r, at in ((0, 0), (1, 150), (2, 253), (3, 300)):       # first, middle, last token that all see
+        rows = rows_of(c, r, max(lens[r]))
+        k = _attn.values64(c.k, rows).float()
+        k[:, 0] = 0
+        k[at] = 0
+        k[at, 0] = -below * 0.6931472 / (8 * SM)
+        set_keys(c, rows, k)
+        c.v[1][rows[at]] *= factor
+    ids = torch.arange(5, dtype=torch.int32).expand(4, 4, 5).contiguous() if blocks else None
+    out, l, flags = run(c, q, block_ids=ids, lists=1 if blocks else 0)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, ids, 1, split_query=wide))
+
+
+@pytest.mark.parametrize("wide", WIDE[:1])
+@pytest.mark.parametrize("up", [True, False])
+def test_scores_and_value_scales_that_run_against_each_other(wide, up):
+    """The maximum rises by 2^7 log2 units (or falls) along the cache while the values shrink (or
+    grow) by as much: every token counts the same, none of them in another's unit."""
+    n = 900
+    lens = [drafts(n, 4)]
+    c = _attn.make("fp8_e4m3", lens, 1, 208)
+    q = draws(1, 4, heads(wide), 209)
+    q[..., 0] = 16.0
+    rows = rows_of(c, 0, n)
+    ramp = torch.linspace(-64, 64, n) * (1 if up else -1)          # log2 units
+    k = _attn.values64(c.k, rows).float() * 0.25
+    k[:, 0] = ramp * 0.6931472 / (16 * SM)
+    set_keys(c, rows, k)
+    c.v[1][rows] = c.v[1][rows] * torch.exp2(-ramp)[:, None]
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
