@@ -343,7 +343,8 @@ IDX_API size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_
  *                        idx_workspace_errors reads its flags.
  * What lies in the cache past a row's length (uninitialised pages, NaN) does not reach the row.
  * Sums and softmax statistics are fp32; for the product with the values the weights are
- * held as two bf16 (bf16 cache, 16 bits) or one f16 (e4m3 cache).  Asynchronous on stream; allocates nothing;
+ * held as two bf16 (bf16 cache, 2^-17 of the weight), or weight times value scale as one f16
+ * (e4m3 cache): 2^-11 of it, or 2^-28 of the row's largest such product.  Asynchronous on stream; allocates nothing;
  * capturable.  R <= IDX_MAX_REQUESTS, P * q_heads <= IDX_MAX_ROWS_PER_REQUEST, num_pages *
  * kv_heads < 2^31 / 64; q_heads a multiple of kv_heads; requests times key heads (or lists)
  * times groups of 128 rows at most 2^18.

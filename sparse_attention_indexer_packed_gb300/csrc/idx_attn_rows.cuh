@@ -72,12 +72,6 @@ __device__ __forceinline__ int to_2_7(float x) {
   return max(-100, min(100, e));
 }
 
-// The smallest power of two above x (x finite, >= 0; at least 2^-100).
-__device__ __forceinline__ float pow2_above(float x) {
-  const int e = max(27, (int)(__float_as_uint(x) >> 23));
-  return __uint_as_float((uint32_t)min(e + 1, 254) << 23);
-}
-
 // e4m3 values.  A token enters the product with the values as weight times value
 // scale, 2^(x - m) vs for a score of x (log2 units), in one f16: 11 bits, and 2^-25 of
 // the output's unit.  So the unit 2^n follows the largest such product that the row

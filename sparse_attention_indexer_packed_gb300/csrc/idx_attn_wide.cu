@@ -103,7 +103,7 @@ struct AWLayout {
   static constexpr int kV16Off = NS * 2 * kTile;
   static constexpr int kScaleOff = kV16Off + 4 * kV16;
   static constexpr int kBitsOff = kScaleOff + NS * 2 * kScale;     // block bits while lists are joined
-  static constexpr int kMlOff = kBitsOff + 2 * kMaxBlockWords * 4;  // (max, sum, value unit) of each lane
+  static constexpr int kMlOff = kBitsOff + 2 * kMaxBlockWords * 4;  // (max, sum, output unit) of each lane
   static constexpr int kInfoOff = kMlOff + 2 * kLanes * 16;         // valid tokens of each stage
   // full_k full_v empty_k empty_v [NS], s_full p_full pv_done s_free [2], q_full, stall, drain
   static constexpr int kBarOff = (kInfoOff + NS * 4 + 7) & ~7;
@@ -530,7 +530,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(q_full);
         }
-        float m = -INFINITY, l = 0.f, mv = 0.f;
+        float m = -INFINITY, l = 0.f;
+        float unit = -INFINITY;   // e4m3: the output is held in units of 2^unit
         int cnt = g ? cnt1 : cnt0;
         const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
         const uint32_t pp = KF == kBf16 ? sp : tl + kColP + 32 * g;
@@ -645,8 +646,9 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
           if (KF == kFp8) {
-            // times the value scales, in units of mv: a power of two that the
-            // scales may pass by 2^6 (weights up to 2^8 stay inside f16)
+            // times the value scales, in the output's unit, which does not move with
+            // the maximum (raise_unit; weights are up to 2^8 here)
+            shrink = 1.f;
             const float* vs = ks + kTok;
             float2 r[kHalf];
             float most = 0.f;
@@ -665,22 +667,16 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) most = fmaxf(most, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
-            if (!(most < INFINITY)) {   // only finite scales set the unit
+            if (past_unit(most, top, unit)) {
               most = 0.f;
 #pragma unroll
-              for (int j = 0; j < kHalf; ++j) {
-                if (fabsf(r[j].x) < INFINITY) most = fmaxf(most, fabsf(r[j].x));
-                if (fabsf(r[j].y) < INFINITY) most = fmaxf(most, fabsf(r[j].y));
-              }
+              for (int j = 0; j < kHalf; ++j)
+                most = fmaxf(most, fmaxf(fabsf(y[j].x * r[j].x), fabsf(y[j].y * r[j].y)));
+              shrink = raise_unit(most, m, unit);
             }
-            if (most > mv * 64.f || mv == 0.f) {
-              const float up = pow2_above(most);
-              shrink *= mv / up;      // mv = 0: nothing gathered yet
-              mv = up;
-            }
-            const float inv = 1.f / mv;
+            const float f = to_unit(m, unit);
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) y[j] = fmul2_rn(y[j], fmul2_rn(r[j], make_float2(inv, inv)));
+            for (int j = 0; j < kHalf; ++j) y[j] = fmul2_rn(fmul2_rn(y[j], make_float2(f, f)), r[j]);
           }
           // e4m3: the output is still, and P's columns free, once the last product
           // has ended (bf16: its scores came after that)
@@ -734,7 +730,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         if (!dead && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) m = -INFINITY;
         tc_fence_after();
         m = not_empty(m, l);
-        ml[g * kLanes + quad * 32 + lane] = make_float4(m, l, mv, 0.f);
+        ml[g * kLanes + quad * 32 + lane] = make_float4(m, l, unit, 0.f);
         group_sync();
         float M = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -750,8 +746,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         // of both groups' outputs.  A lane without a page has gathered nothing.
         const float4 e0 = ml[quad * 32 + lane], e1 = ml[kLanes + quad * 32 + lane];
         const bool has0 = e0.x != -INFINITY, has1 = e1.x != -INFINITY;
-        const float f0 = ex2_approx(e0.x - ref) * (KF == kFp8 ? e0.z : 1.f);
-        const float f1 = ex2_approx(e1.x - ref) * (KF == kFp8 ? e1.z : 1.f);
+        const float f0 = ex2_approx((KF == kFp8 ? e0.z : e0.x) - ref);
+        const float f1 = ex2_approx((KF == kFp8 ? e1.z : e1.x) - ref);
         const bool complete = s.o0 == 0 && s.o1 == s.cap;
         const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
         const float inv = M == -INFINITY ? 0.f : 1.f / sum;

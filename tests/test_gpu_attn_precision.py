@@ -66,7 +66,7 @@ def test_zero_values_before_large_ones_stay_in_the_sum(wide, ctas):
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
 
 
-@pytest.mark.parametrize("wide", WIDE[:1])
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("blocks", [False, True])
 @pytest.mark.parametrize("below", [40, 60])
 @pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 26, 2.0 ** 37])
@@ -90,7 +90,7 @@ def test_a_large_value_of_little_weight(wide, blocks, below, factor):
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, ids, 1, split_query=wide))
 
 
-@pytest.mark.parametrize("wide", WIDE[:1])
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("up", [True, False])
 def test_scores_and_value_scales_that_run_against_each_other(wide, up):
     """The maximum rises by 2^7 log2 units (or falls) along the cache while the values shrink (or
