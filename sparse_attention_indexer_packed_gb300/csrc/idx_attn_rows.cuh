@@ -65,6 +65,18 @@ __device__ __forceinline__ uint32_t e4m3x4_take(float (&x)[4]) {
   return d;
 }
 
+// Four e5m2 codes of four floats (round to nearest even).
+__device__ __forceinline__ uint32_t e5m2x4(const float (&x)[4]) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 h0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 h1, %4, %3;\n\t"
+      "mov.b32 %0, {h0, h1};\n\t}"
+      : "=r"(d)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  return d;
+}
+
 // The exponent e that brings x * 2^e into [2^7, 2^8) (0 for zero), e in [-100, 100].
 __device__ __forceinline__ int to_2_7(float x) {
   int e = 0;

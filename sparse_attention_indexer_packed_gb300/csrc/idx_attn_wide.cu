@@ -29,10 +29,13 @@
 // to 2^8 are as exact as any): the output is rescaled then, which is rare.
 //
 // Precision.  bf16 cache: the weights are two bf16 (16 bits).  e4m3 cache: the
-// keys meet the queries as e4m3 codes, the query split into two e4m3 terms (its
-// 8 significant bits are 4 + 4; exact for elements within 2^10 of the row's
-// largest); the values are decoded to f16, exactly, by the group that uses them,
-// and the weights times the value's scale are one f16 (11 bits).
+// keys meet the queries as e4m3 codes, the query split into an e4m3 term (4 of its 8
+// significant bits) and an e5m2 term: what is left is a whole number up to 8 of the
+// query's own last place, which 3 bits hold.  Exact for elements within 2^13 of the
+// row's largest, and off by 2^-21 of the largest below (checked over every bf16
+// value; with e4m3 as the second term 2^10 and 2^-17, e5m2 reaches 2^7 lower); the
+// values are decoded to f16, exactly, by the group that uses them, and the weights
+// times the value's scale are one f16 (11 bits; raise_unit).
 //
 // Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 164 us, 6.0
 // TB/s of cache, 0.89 of the copy peak (the warp-level kernel, four groups of 16 rows:
@@ -85,6 +88,7 @@ struct AWCfg<kFp8> {
   static constexpr int kRowBytes = 128;
   static constexpr int kStages = 6;
   static constexpr uint32_t kIdQK = instr_desc(0u, kLanes, kTok);                // e4m3
+  static constexpr uint32_t kIdQKLow = kIdQK | (1u << 7);                        // e5m2 by e4m3
   static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);   // f16
 };
 
@@ -422,8 +426,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           } else {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)   // the query's two terms, four steps of 32 each
-              mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32), kIdQK,
-                        ks > 0);
+              mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32),
+                        ks < 4 ? kIdQK : AWCfg<kFp8>::kIdQKLow, ks > 0);
           }
           tc_commit_warp(empty_k(st));
           tc_commit_warp(s_full(g));
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             tm_st<32>(tl + kColQ + 32 * g, w);
           } else {
             // scaled by a power of two that brings the row's largest magnitude into
-            // [2^7, 2^8), then two e4m3 terms: the group's half first, then the other,
+            // [2^7, 2^8), then an e4m3 and an e5m2 term: the group's half first, then the other,
             // of which it needs the magnitude only
             uint32_t w[32];
             float amax = 0.f;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
                             bf16_hi(w[2 * e + 1]) * up};
               w[e] = e4m3x4_take(x);
-              lo[e] = e4m3x4_take(x);
+              lo[e] = e5m2x4(x);
             }
             tm_st<16>(tl + kColQ + 16 * g, w);
             tm_st<16>(tl + kColQ + 32 + 16 * g, lo);

@@ -42,6 +42,19 @@ def test_no_less_exact_than_stated(dtype, wide, blocks):
     _attn_bounds.check(out, l, ref, rows=torch.isfinite(ref[1]))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+def test_few_tokens_of_like_weights(dtype, wide):
+    """Where the weights' own rounding does not average out: bf16 weights of one term instead of
+    two would be past the bound several times over (test_attn_bounds_cpu.py)."""
+    lens = [drafts(L, 4) for L in range(5, 29)]
+    c = _attn.make(dtype, lens, 1, 218)
+    q = draws(len(lens), 4, heads(wide), 219, scale=0.3)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide and dtype != "bf16"))
+
+
 @pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("ctas", [1, 0])
 def test_zero_values_before_large_ones_stay_in_the_sum(wide, ctas):
@@ -109,3 +122,25 @@ def test_scores_and_value_scales_that_run_against_each_other(wide, up):
     out, l, flags = run(c, q)
     assert flags == 0
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+def test_a_query_with_an_outlier_channel(dtype, wide):
+    """One channel 2^12 above the others, which no key goes by: the scores are the others'."""
+    lens = [drafts(300, 4), drafts(70, 4)]
+    c = _attn.make(dtype, lens, 1, 210)
+    g = torch.Generator().manual_seed(211)
+    q = (1 + torch.rand((2, 4, heads(wide), 128), generator=g)) * (
+        2.0 * torch.randint(0, 2, (2, 4, heads(wide), 128), generator=g) - 1)
+    q[..., 5] = 4096.0
+    q = q.to(torch.bfloat16)
+    if dtype == "bf16":
+        c.k[0][:, 5] = 0
+    else:
+        c.k[0][:, 5] &= 0x80        # a zero
+    for r in range(2):              # (what no row sees is NaN again)
+        assert torch.isfinite(_attn.values64(c.k, rows_of(c, r, max(lens[r])))).all()
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide and dtype != "bf16"))
