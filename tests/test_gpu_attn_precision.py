@@ -144,3 +144,38 @@ def test_a_query_with_an_outlier_channel(dtype, wide):
     out, l, flags = run(c, q)
     assert flags == 0
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide and dtype != "bf16"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_query_that_is_not_finite(dtype, wide, bad):
+    """Its row is NaN (keys of either sign meet it); the others do not notice."""
+    lens = [drafts(200, 4)]
+    c = _attn.make(dtype, lens, 1, 212)
+    q = draws(1, 4, heads(wide), 213)
+    ref = _attn_bounds.reference(c, q, SM, split_query=wide and dtype != "bf16")
+    q[0, 1, 3, 7] = bad
+    out, l, flags = run(c, q)
+    assert flags == 0
+    rows = torch.ones((1, 4, heads(wide)), dtype=torch.bool)
+    rows[0, 1, 3] = False
+    _attn_bounds.check(out, l, ref, rows=rows)
+    assert torch.isnan(out[0, 1, 3].float()).all() and torch.isnan(l[0, 1, 3])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+def test_queries_near_the_largest_number(dtype, wide):
+    """Queries of 2^118 on keys of 2^-118: ordinary scores."""
+    lens = [drafts(150, 4)]
+    c = _attn.make(dtype, lens, 1, 214)
+    q = draws(1, 4, heads(wide), 215)
+    clean = _attn_bounds.reference(c, q, SM, split_query=wide and dtype != "bf16")
+    if dtype == "bf16":
+        c.k[0].mul_(2.0 ** -118)
+    else:
+        c.k[1].mul_(2.0 ** -118)
+    out, l, flags = run(c, q * 2.0 ** 118)
+    assert flags == 0
+    _attn_bounds.check(out, l, clean)
