@@ -156,8 +156,8 @@ struct QRows {
   __device__ __forceinline__ void finish(float scale_log2) {
     post0 = post1 = scale_log2;
     if (KF == kFp8) {
-      post0 *= to_f16(0);
-      post1 *= to_f16(1);
+      post0 = fmaxf(post0 * to_f16(0), kLeastPost);
+      post1 = fmaxf(post1 * to_f16(1), kLeastPost);
     }
   }
   __device__ __forceinline__ float to_f16(int half) {

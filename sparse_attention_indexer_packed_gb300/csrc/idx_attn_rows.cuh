@@ -279,6 +279,10 @@ __device__ __forceinline__ int join_lists(const AttnArgs& a, const Requests& rq,
   return run;
 }
 
+// What scores are multiplied by is never 0: a masked score's -inf would turn NaN.
+// (Scores that small are 0 next to anything.)
+constexpr float kLeastPost = 0x1p-126f;
+
 // Four consecutive dims of a plane row as fp32.
 template <int KF>
 __device__ __forceinline__ float4 plane_f32(const uint8_t* payload, const float* scale,

@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             }
             const int ex = to_2_7(amax);
             const float up = ldexpf(1.f, ex);
-            post *= ldexpf(1.f, -ex);
+            post = fmaxf(post * ldexpf(1.f, -ex), kLeastPost);
             uint32_t lo[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {

@@ -179,3 +179,15 @@ def test_queries_near_the_largest_number(dtype, wide):
     out, l, flags = run(c, q * 2.0 ** 118)
     assert flags == 0
     _attn_bounds.check(out, l, clean)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", WIDE)
+def test_scores_that_are_next_to_nothing(dtype, wide):
+    """Queries of 2^-110 under a scale of 1e-20: every visible token counts the same."""
+    lens = [drafts(150, 4), drafts(20, 4)]
+    c = _attn.make(dtype, lens, 1, 220)
+    q = draws(2, 4, heads(wide), 221) * 2.0 ** -110
+    out, l, flags = run(c, q, sm_scale=1e-20)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, 1e-20))
