@@ -662,8 +662,8 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       }
       dead = __any_sync(0xffffffffu, dead);
       if (dead) break;
-      const int e0 = has0 && (cur.members >> (pd0 - p0)) & 1u ? L0 : 0;
-      const int e1 = has1 && (cur.members >> (pd1 - p0)) & 1u ? L1 : 0;
+      const int e0 = has0 && (!kBlocks || (cur.members >> (pd0 - p0)) & 1u) ? L0 : 0;
+      const int e1 = has1 && (!kBlocks || (cur.members >> (pd1 - p0)) & 1u) ? L1 : 0;
       const bool whole = __all_sync(0xffffffffu, (!has0 || cur.tb + kItem <= e0) &&
                                                      (!has1 || cur.tb + kItem <= e1));
       const uint32_t stage = stage_of(used);

@@ -333,7 +333,8 @@ __device__ __forceinline__ Items make_items(const AttnArgs& a, const Requests& r
 }
 
 // Item i of the stretch: its first token, and for block lists the drafts that
-// list its block (bit p - p0).  False: nothing there.
+// list its block (bit p - p0, below kMaxDrafts; a group of the whole cache may have
+// more draft rows than the word has bits, and they all see it).  False: nothing there.
 template <int IT, bool kBlocks>
 __device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
                                             uint32_t& members) {
@@ -378,7 +379,8 @@ __device__ __noinline__ void careful_row(const AttnArgs& a, const Items& it, con
   for (int i = it.i0; i < it.i1; ++i) {
     int tb;
     uint32_t members;
-    if (!item_tokens<IT, kBlocks>(it, list, i, tb, members) || !((members >> draft_bit) & 1u)) continue;
+    if (!item_tokens<IT, kBlocks>(it, list, i, tb, members)) continue;
+    if (kBlocks && !((members >> draft_bit) & 1u)) continue;
     const long long row = item_row(a, it, tb);
     if (row < 0) continue;
     for (int e = 0; e < IT && tb + e < len; ++e) {

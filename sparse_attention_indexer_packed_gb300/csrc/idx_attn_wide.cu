@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               y[j + 1] = fmul2_rn(y[j + 1], make_float2(k4.z, k4.w));
             }
           }
-          const int visible = min(min(len, tb + valid) - tb, (members >> bit) & 1u ? kTok : 0) - part * kPart;
+          const bool listed = !kBlocks || ((members >> bit) & 1u);
+          const int visible = min(min(len, tb + valid) - tb, listed ? kTok : 0) - part * kPart;
           const bool masked = __any_sync(0xffffffffu, visible < kPart);
           if (masked) {
 #pragma unroll

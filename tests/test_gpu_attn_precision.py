@@ -191,3 +191,22 @@ def test_scores_that_are_next_to_nothing(dtype, wide):
     out, l, flags = run(c, q, sm_scale=1e-20)
     assert flags == 0
     _attn_bounds.check(out, l, _attn_bounds.reference(c, q, 1e-20))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_token_that_the_last_of_many_draft_rows_sees(dtype, bad):
+    """70 draft rows in one unit, the newest token not finite: the rows past the 32nd are
+    recomputed token by token and come out as if it were not there."""
+    P, n = 70, 150
+    c = _attn.make(dtype, [drafts(n, P)], 1, 216)
+    q = draws(1, P, 1, 217)
+    ref = _attn_bounds.reference(c, q, SM, split_query=dtype != "bf16")
+    last = rows_of(c, 0, n)[-1]
+    (c.v[0] if dtype == "bf16" else c.v[1])[last] = bad
+    out, l, flags = run(c, q)
+    assert flags == 0
+    rows = torch.ones((1, P, 1), dtype=torch.bool)
+    rows[0, P - 1] = False
+    _attn_bounds.check(out, l, ref, rows=rows)
+    assert not torch.isfinite(out[0, P - 1].float()).all()
