@@ -163,21 +163,14 @@ __device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t* v) {
   if constexpr (N == 32) {
     uint32_t(&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(v);
     tc_ld_32cols(taddr, r);
-  } else if constexpr (N == 16) {
+  } else {
+    static_assert(N == 16, "16 or 32 columns");
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
           "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
           "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr)
-        : "memory");
-  } else {
-    static_assert(N == 8, "8, 16 or 32 columns");
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7])
         : "r"(taddr)
         : "memory");
   }
@@ -204,17 +197,13 @@ __device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t* v) {
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15])
         : "memory");
-  } else if constexpr (N == 8) {
+  } else {
+    static_assert(N == 8, "8, 16 or 32 columns");
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
             taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
-  } else {
-    static_assert(N == 4, "4, 8, 16 or 32 columns");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
   }
 }
 __device__ __forceinline__ void tm_wait_st() {
@@ -888,7 +877,7 @@ cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtenso
 #define IDX_LAUNCH(F)                                                              \
   (blocks ? launch_kfb<KF, F, true>(a, k_map, v_map, grid, dev, stream)            \
           : launch_kfb<KF, F, false>(a, k_map, v_map, grid, dev, stream))
-  if (rows <= 16) return IDX_LAUNCH(8);
+  // (17 rows at least: launch_attn sends units of up to 16 to the other kernel)
   if (rows <= 32) return IDX_LAUNCH(4);
   if (rows <= 64) return IDX_LAUNCH(2);
   return IDX_LAUNCH(1);
