@@ -302,8 +302,9 @@ IDX_API int idx_score_topk_perrow(const void* q, const float* q_scale, int q_dty
  *                          of 8, 16-byte aligned.  v_src NULL with v_pool NULL: keys only
  *                          (an index pool's bf16 or e4m3 keys, with kv_heads = 1).
  *   slot_mapping (device): int64 [num_tokens], page * 64 + offset of each token; negative or
- *                          >= num_pages * 64 skips the token.  Slots must differ: of two
- *                          tokens with one slot either may stay.
+ *                          >= num_pages * 64 skips the token.  Slots must differ: the row
+ *                          of two tokens with one slot may hold parts of both, such as the
+ *                          codes of one under the scale of the other.
  *   k_pool, v_pool (host): planes of num_pages * kv_heads head pages, the same dtype.
  * Asynchronous on stream; allocates nothing; capturable.  IDX_ERR_INVALID for arguments out of range;
  * IDX_ERR_UNSUPPORTED for an NVFP4 pool (idx_store_nvfp4 writes those).  num_tokens == 0 is

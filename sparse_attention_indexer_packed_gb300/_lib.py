@@ -416,8 +416,9 @@ def _pool_bytes(payload, scale, name: str, kv_dtype: str) -> bytes:
 def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
                  kv_dtype: str, kv_heads: int, stream=None) -> None:
     """k_src, v_src: bf16 [tokens, kv_heads, 128], tokens any stride apart (a slice of a
-    fused projection); v_src, v_payload, v_scale None: keys only.  Planes as for
-    idx_attn_paged, or an index pool's (kv_heads 1)."""
+    fused projection); v_src, v_payload, v_scale None: keys only.  slot_mapping: int64, page *
+    64 + offset, every token's its own (negative: skipped).  Planes as for idx_attn_paged, or
+    an index pool's (kv_heads 1)."""
     if k_src is None or k_payload is None or (v_src is None) != (v_payload is None):
         raise IdxError("a source and its payload plane come together, and the keys always")
     T = slot_mapping.numel()
