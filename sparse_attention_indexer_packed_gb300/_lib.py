@@ -528,18 +528,20 @@ def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_sc
         _check(rc, "idx_add_rmsnorm_fp8")
 
 
+NATIVE_CALLS = ("idx_attn_paged", "idx_attn_blocks", "idx_store_kv", "idx_add_rmsnorm_fp8")
+
+
 def _native_calls():
     """The four small-call operators of the CPython module, or these functions themselves
     where it has not been built (or torch lacks the bare stream call): the same checks and
     the same library calls, slower on the host."""
-    here = (idx_attn_paged, idx_attn_blocks, idx_store_kv, idx_add_rmsnorm_fp8)
+    here = tuple(globals()[name] for name in NATIVE_CALLS)
     if _raw_stream is None or not os.path.exists(LIB_PATH):
         return here
     try:
         from . import _binding
-    except ImportError:    # not built, or built for another interpreter
-        return here
-    _binding.bind((torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-                   torch.float8_e4m3fn), _raw_stream, _check, here)
-    return (_binding.idx_attn_paged, _binding.idx_attn_blocks, _binding.idx_store_kv,
-            _binding.idx_add_rmsnorm_fp8)
+        _binding.bind((torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+                       torch.float8_e4m3fn), _raw_stream, _check, here)
+        return tuple(getattr(_binding, name) for name in NATIVE_CALLS)
+    except (ImportError, TypeError, AttributeError):
+        return here    # not built, built for another interpreter or from another state of the sources

@@ -4,7 +4,8 @@ The translation units compile in parallel into ``_build/`` and link into
 ``sparse_attention_indexer_packed_gb300/libidx.so`` with the CUDA runtime
 linked statically, so the library loads without a driver (its symbols can be
 inspected on a machine with no GPU).  ``_binding.so`` beside it is the CPython
-module of the small-call operators (csrc/idx_binding.c).
+module of the small-call operators (csrc/idx_binding.c); it needs gcc and Python's
+headers, and where one is missing those operators go through ctypes.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,7 +61,7 @@ def build_library(verbose: bool = False, force: bool = False) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose:
             print(r.stdout + r.stderr)
         return r
@@ -72,17 +74,43 @@ def build_library(verbose: bool = False, force: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         list(ex.map(compile_one, jobs))
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
-    if force or jobs or _stale(LIB, objs):
+    relinked = force or jobs or _stale(LIB, objs)
+    if relinked:
         tmp = LIB + tag
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "idx_binding.c")
-    if force or _stale(BINDING, [src, headers[-1]]):
-        tmp = BINDING + tag
-        run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"],
-             src, "-o", tmp, "-L" + HERE, "-l:libidx.so", "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, BINDING)
+    if _build_binding([os.path.join(CSRC, "idx_binding.c"), headers[-1]], tag, run, force) or relinked:
+        _drop_native_calls()
     return LIB
+
+
+def _build_binding(deps: list, tag: str, run, force: bool) -> bool:
+    """Build the CPython module from deps[0] where that is due and can be done.  True: the file
+    changed."""
+    if not force and not _stale(BINDING, deps):
+        return False
+    include = sysconfig.get_paths()["include"]
+    missing = "gcc" if shutil.which("gcc") is None else (
+        "" if os.path.exists(os.path.join(include, "Python.h")) else "Python.h")
+    if missing:
+        print(f"{missing} not found: the layer operators are called through ctypes", file=sys.stderr)
+        if os.path.exists(BINDING):      # built from another state of the sources
+            os.remove(BINDING)
+            return True
+        return False
+    run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I" + include, deps[0], "-o", BINDING + tag,
+         "-L" + HERE, "-l:libidx.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(BINDING + tag, BINDING)
+    return True
+
+
+def _drop_native_calls() -> None:
+    """A process that has loaded the CPython module holds the library from before this build with
+    it; its calls go through ctypes, to the library that lib() loads."""
+    package = sys.modules.get("sparse_attention_indexer_packed_gb300")
+    if package is not None and hasattr(package, "_lib"):
+        for name in package._lib.NATIVE_CALLS:
+            setattr(package, name, getattr(package._lib, name))
 
 
 if __name__ == "__main__":
