@@ -64,6 +64,8 @@ def build_library(verbose: bool = False, force: bool = False) -> str:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose:
             print(r.stdout + r.stderr)
+        elif r.stderr.strip():
+            print(r.stderr.strip(), file=sys.stderr)     # warnings: registers that are spilled
         return r
 
     def compile_one(job):

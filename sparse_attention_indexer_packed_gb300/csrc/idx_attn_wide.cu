@@ -44,6 +44,10 @@
 // (waits 600, decoding the values 540, weights 930, two thirds of it the scales), and
 // two groups alternate.  Up to 16 rows this kernel is the slower one (e4m3 16 x 131K
 // 152 us against 122 at the time, 1 x 1K 12.8 against 9.3).
+// Registers: 168 a thread at launch, and every instantiation spills; bytes of stores /
+// loads (-Xptxas -v) for 17 to 32, 33 to 64, 65 to 128 rows: bf16 4 / 4, 92 / 48, 148 /
+// 552, with lists 72 / 24, 216 / 224, 164 / 324; e4m3 156 / 224, 152 / 232, 128 / 232,
+// with lists 124 / 236, 160 / 280, 160 / 276.
 // Tried and slower: the values decoded by four warps of their own (161 -> 189); each
 // group finishing a slice through shared memory at a unit's end (166 -> 183).
 //

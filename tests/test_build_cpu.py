@@ -77,3 +77,16 @@ def test_a_build_in_a_process_with_the_old_module_goes_on_through_ctypes(monkeyp
     build._drop_native_calls()
     for name in _lib.NATIVE_CALLS:
         assert getattr(idx, name) is getattr(_lib, name)
+
+
+def test_warnings_of_the_compilers_are_shown(monkeypatch, tmp_path, capsys):
+    monkeypatch.setattr(build, "SOURCES", ["idx_kv.cu"])
+    monkeypatch.setattr(build, "_nvcc", lambda: "/x/bin/nvcc")
+    monkeypatch.setattr(build, "_drop_native_calls", lambda: None)
+    monkeypatch.setattr(build.os, "replace", lambda a, b: None)
+    monkeypatch.setattr(build, "_stale", lambda out, deps: False)
+    monkeypatch.setattr(build, "_build_binding", lambda *a: False)
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **k: types.SimpleNamespace(
+        returncode=0, stdout="", stderr="ptxas warning : Registers are spilled\n" if "-c" in cmd else ""))
+    build.build_library(force=True)
+    assert capsys.readouterr().err == "ptxas warning : Registers are spilled\n"
