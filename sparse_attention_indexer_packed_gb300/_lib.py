@@ -127,6 +127,7 @@ def _stream_ptr(stream) -> Optional[int]:
 # torch.cuda.current_stream() builds a Stream object (~3 us); a decode step's small
 # calls ask torch for the bare handle where it has that call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(t: torch.Tensor, stream) -> Optional[int]:
@@ -136,6 +137,18 @@ def _stream_of(t: torch.Tensor, stream) -> Optional[int]:
     if _raw_stream is None:
         return torch.cuda.current_stream(t.device).cuda_stream
     return _raw_stream(t.get_device())
+
+
+def _one_device(stream, *tensors) -> None:
+    """The library launches on the current device: everything has to be there (CUDA tensors,
+    None where an argument is left out)."""
+    here = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise IdxError(f"a tensor is on cuda:{t.get_device()} and the current device is cuda:{here}: "
+                           "all of a call's tensors must be on the current device (torch.cuda.device)")
+    if stream is not None and stream.device.index != here:
+        raise IdxError(f"the stream is of {stream.device} and the current device is cuda:{here}")
 
 
 def pool_struct(dtype: str, payload: torch.Tensor, scale: Optional[torch.Tensor]) -> IdxPool:
@@ -428,9 +441,10 @@ def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_sc
     if v_src is not None:
         v_ptr, v_stride = _source(v_src, "v_src", T, kv_heads)
         v_pool = _pool_bytes(v_payload, v_scale, "v", kv_dtype)
-    rc = lib().idx_store_kv(k_ptr, v_ptr, k_stride, v_stride,
-                            _want(slot_mapping, "slot_mapping", torch.int64, (T,)), T, kv_heads,
-                            k_pool, v_pool, _stream_of(k_src, stream))
+    slots = _want(slot_mapping, "slot_mapping", torch.int64, (T,))
+    _one_device(stream, k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale)
+    rc = lib().idx_store_kv(k_ptr, v_ptr, k_stride, v_stride, slots, T, kv_heads, k_pool, v_pool,
+                            _stream_of(k_src, stream))
     if rc:
         _check(rc, "idx_store_kv")
 
@@ -469,6 +483,13 @@ def _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, 
             _want(row_lens, "row_lens", _I32, (R, P))), R, P, Hq
 
 
+def _attn_out(q, out, out_lse, workspace):
+    """The arguments the two attention calls end with, before the stream."""
+    return (_want(out, "out", _BF16, q.shape),
+            None if out_lse is None else _want(out_lse, "out_lse", _F32, q.shape[:3]),
+            _dev(workspace, "workspace"), workspace.nbytes)
+
+
 def idx_attn_paged(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, page_table, slot_ids,
                    row_lens, kv_heads: int, sm_scale: float, out, out_lse, workspace,
                    stream=None) -> None:
@@ -477,10 +498,10 @@ def idx_attn_paged(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, pag
     128] rows with head page p * kv_heads + h; scales (fp8_e4m3 only) fp32 [rows]."""
     head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table,
                                 slot_ids, row_lens, kv_heads)
-    rc = lib().idx_attn_paged(*head, R, P, Hq, sm_scale, _want(out, "out", _BF16, q.shape),
-                              None if out_lse is None else _want(out_lse, "out_lse", _F32, (R, P, Hq)),
-                              _dev(workspace, "workspace"), workspace.nbytes,
-                              _stream_of(q, stream))
+    tail = _attn_out(q, out, out_lse, workspace)
+    _one_device(stream, q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens, out,
+                out_lse, workspace)
+    rc = lib().idx_attn_paged(*head, R, P, Hq, sm_scale, *tail, _stream_of(q, stream))
     if rc:
         _check(rc, "idx_attn_paged")
 
@@ -495,11 +516,11 @@ def idx_attn_blocks(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, pa
     head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table,
                                 slot_ids, row_lens, kv_heads)
     topk = block_ids.shape[2]
-    rc = lib().idx_attn_blocks(*head, _want(block_ids, "block_ids", _I32, (R, P * lists, topk)), lists,
-                               topk, R, P, Hq, sm_scale, _want(out, "out", _BF16, q.shape),
-                               None if out_lse is None else _want(out_lse, "out_lse", _F32, (R, P, Hq)),
-                               _dev(workspace, "workspace"), workspace.nbytes,
-                               _stream_of(q, stream))
+    ids = _want(block_ids, "block_ids", _I32, (R, P * lists, topk))
+    tail = _attn_out(q, out, out_lse, workspace)
+    _one_device(stream, q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens,
+                block_ids, out, out_lse, workspace)
+    rc = lib().idx_attn_blocks(*head, ids, lists, topk, R, P, Hq, sm_scale, *tail, _stream_of(q, stream))
     if rc:
         _check(rc, "idx_attn_blocks")
 
@@ -519,11 +540,12 @@ def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_sc
     groups = -(-n // group) if group > 0 else 1
     if out_scale.dtype is not _F32 or out_scale.numel() != T * groups:
         raise IdxError(f"out_scale must be float32 [{T}, {groups}]")
-    rc = lib().idx_add_rmsnorm_fp8(
-        xp, xs, rp, rs, _want(weight, "weight", _BF16, (n,)), T, n, group, eps, _dev(out, "out"),
-        _dev(out_scale, "out_scale"),
-        None if out_residual is None else _want(out_residual, "out_residual", _BF16, (T, n)),
-        _stream_of(x, stream))
+    outs = (_dev(out, "out"), _dev(out_scale, "out_scale"),
+            None if out_residual is None else _want(out_residual, "out_residual", _BF16, (T, n)))
+    weight_ptr = _want(weight, "weight", _BF16, (n,))
+    _one_device(stream, x, residual, weight, out, out_scale, out_residual)
+    rc = lib().idx_add_rmsnorm_fp8(xp, xs, rp, rs, weight_ptr, T, n, group, eps, *outs,
+                                   _stream_of(x, stream))
     if rc:
         _check(rc, "idx_add_rmsnorm_fp8")
 
@@ -541,7 +563,7 @@ def _native_calls():
     try:
         from . import _binding
         _binding.bind((torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-                       torch.float8_e4m3fn), _raw_stream, _check, here)
+                       torch.float8_e4m3fn), _raw_stream, _current_device, _check, here)
         return tuple(getattr(_binding, name) for name in NATIVE_CALLS)
     except (ImportError, TypeError, AttributeError):
         return here    # not built, built for another interpreter or from another state of the sources
