@@ -99,3 +99,50 @@ def test_a_stream_of_another_device_is_refused(bindings, name, args):
     for fns in bindings:
         with pytest.raises(idx.IdxError, match="current device"):
             fns[name](*args, stream=Stream())
+
+
+def mutants(a):
+    """Arguments like `a` and unlike it."""
+    if isinstance(a, Stand):
+        yield None
+        yield 3
+        for dtype in (BF, torch.float16, F32, I32, I64, U8):
+            yield Stand(dtype, *a.shape)
+        for d in range(len(a.shape)):
+            yield Stand(a.dtype, *a.shape[:d], a.shape[d] + 1, *a.shape[d + 1:])
+            yield Stand(a.dtype, *a.shape[:d], 0, *a.shape[d + 1:])
+        yield Stand(a.dtype, *a.shape, 1)
+        yield Stand(a.dtype, *a.shape[1:])
+        apart = Stand(a.dtype, *a.shape)
+        apart.real = torch.empty((2 * a.shape[0], *a.shape[1:]), dtype=a.dtype, device="meta")[::2]
+        yield apart
+        inner = Stand(a.dtype, *a.shape)
+        inner.real = torch.empty((*a.shape, 2), dtype=a.dtype, device="meta")[..., 0]
+        yield inner
+        on_cpu = Stand(a.dtype, *a.shape, device=-1)
+        on_cpu.is_cuda = False
+        yield on_cpu
+    else:
+        yield from (None, 0, 1, 3, -1, 128, 0.5, -2.0, float("nan"), True, 1 << 40, "bf16", "fp8_e4m3", "nvfp4",
+                    Stand(F32, 256))
+
+
+@pytest.mark.parametrize("name,args", CASES)
+def test_both_bindings_answer_alike(bindings, name, args):
+    """What one accepts or refuses, and in which words, the other does too."""
+    def answer(fn, a):
+        try:
+            return fn(*a)
+        except Exception as e:  # noqa: BLE001 (any refusal)
+            return type(e), str(e)
+
+    python, module = bindings
+    n = 0
+    for at in range(len(args)):
+        for m in mutants(args[at]):
+            a = [*args[:at], m, *args[at + 1:]]
+            assert answer(module[name], a) == answer(python[name], a), (at, m)
+            n += 1
+    assert n > 100
+    for a in (args[:-1], args[:3], [], [*args, None]):
+        assert answer(module[name], a) == answer(python[name], a)
