@@ -20,6 +20,8 @@ def reference(c, q, sm_scale, block_ids=None, lists=0, split_query=False, keep=N
     lse = torch.full((R, P, Hq), -float("inf"), dtype=torch.float64)
     tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
     for r in range(R):
+        if not 0 <= int(c.slot_ids[r]) < c.page_table.shape[0]:
+            continue
         pages = c.page_table[int(c.slot_ids[r])].tolist()
         for p in range(P):
             n = int(c.row_lens[r, p])
