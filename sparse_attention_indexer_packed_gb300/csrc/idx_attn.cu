@@ -288,9 +288,9 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       }
     }
     if (!kMask) top1 = top0;
-    const float x0 = mx0 * q.post0, x1 = mx1 * q.post1;
     co0 = co1 = 1.f;          // the unit does not move with the maximum
-    if (__any_sync(0xffffffffu, past_unit(top0, x0, st.n0) || past_unit(top1, x1, st.n1))) {
+    f0 = to_unit(mn0, st.n0), f1 = to_unit(mn1, st.n1);
+    if (__any_sync(0xffffffffu, past_unit(top0, f0) || past_unit(top1, f1))) {
       top0 = top1 = 0.f;
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
@@ -305,8 +305,8 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
       }
       co0 = raise_unit(top0, mn0, st.n0);
       co1 = raise_unit(top1, mn1, st.n1);
+      f0 = to_unit(mn0, st.n0), f1 = to_unit(mn1, st.n1);
     }
-    f0 = to_unit(mn0, st.n0), f1 = to_unit(mn1, st.n1);
   }
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
@@ -318,8 +318,10 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
     l0 = fadd2_rn(l0, y0[nt]);
     l1 = fadd2_rn(l1, y1[nt]);
     if (KF == kFp8) {
-      y0[nt] = fmul2_rn(fmul2_rn(y0[nt], make_float2(f0, f0)), vs[nt]);
-      y1[nt] = fmul2_rn(fmul2_rn(y1[nt], make_float2(f1, f1)), vs[nt]);
+      // (scale times factor is infinite where the weight is next to nothing and the unit
+      // far below the scale; the row is then recomputed token by token)
+      y0[nt] = fmul2_rn(y0[nt], fmul2_rn(vs[nt], make_float2(f0, f0)));
+      y1[nt] = fmul2_rn(y1[nt], fmul2_rn(vs[nt], make_float2(f1, f1)));
       if (kMask) {   // a masked token's scale may be anything
         const int t0 = tb + nt * 8 + 2 * t;
         if (t0 >= len0) y0[nt].x = 0.f;

@@ -92,24 +92,22 @@ __device__ __forceinline__ int to_2_7(float x) {
 // its scale nor its weight alone, and the smallest products lose bits, never the
 // largest.  2^n is absolute: a maximum that rises takes no part in it.
 constexpr float kMostHeld = 16384.f;
-// Whether a product may be past the unit: scales up to `top`, scores up to x.
-__device__ __forceinline__ bool past_unit(float top, float x, float n) {
-  return x != -INFINITY && !(top * ex2_approx(x - n) <= kMostHeld);
+// The factor from weights in units of 2^m to the output's unit.  A row that has not
+// seen a score above -inf has neither.
+__device__ __forceinline__ float to_unit(float m, float n) {
+  return m == -INFINITY ? 0.f : ex2_approx(m - n);
 }
+// Whether products of up to `top`, with the factor f to the unit, may be past it.
+__device__ __forceinline__ bool past_unit(float top, float f) { return !(top * f <= kMostHeld); }
 // Raise n where the largest product, top 2^m, is past it: its exponent less 3.  (Where
 // every product is zero n is 2^113 below the weights.)  Returns what the output
 // gathered so far is to be multiplied by.
 __device__ __forceinline__ float raise_unit(float top, float m, float& n) {
-  if (!past_unit(top, m, n)) return 1.f;
+  if (m == -INFINITY || !past_unit(top, to_unit(m, n))) return 1.f;
   const int e = max((int)((__float_as_uint(top) >> 23) & 0xffu) - 127, -110);
   const float up = m + (float)(e - 3), factor = ex2_approx(n - up);
   n = up;
   return factor;
-}
-// The factor from weights, in units of 2^m, to the output's unit.  A row that has not
-// seen a score above -inf has neither.
-__device__ __forceinline__ float to_unit(float m, float n) {
-  return m == -INFINITY ? 0.f : ex2_approx(m - n);
 }
 
 // Length of draft row p of request r, inside [0, max_pages * 64].

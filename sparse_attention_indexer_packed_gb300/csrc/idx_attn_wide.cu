@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) most = fmaxf(most, fmaxf(fabsf(r[j].x), fabsf(r[j].y)));
-            if (past_unit(most, top, unit)) {
+            if (past_unit(most, to_unit(top, unit))) {
               most = 0.f;
 #pragma unroll
               for (int j = 0; j < kHalf; ++j)

@@ -104,6 +104,28 @@ def test_a_large_value_of_little_weight(wide, blocks, below, factor):
 
 
 @pytest.mark.parametrize("wide", WIDE)
+def test_a_value_past_the_reach_of_the_others_unit(wide):
+    """Values of 2^-60 and one token's of 2^75 with a weight of 2^-160: no unit holds both."""
+    lens = [drafts(L, 4) for L in (40, 300)]
+    c = _attn.make("fp8_e4m3", lens, 1, 222)
+    q = draws(2, 4, heads(wide), 223)
+    q[..., 0] = 8.0
+    c.v[1].mul_(2.0 ** -60)
+    for r, at in ((0, 17), (1, 200)):
+        rows = rows_of(c, r, max(lens[r]))
+        k = _attn.values64(c.k, rows).float()
+        k[:, 0] = 0
+        k[at] = 0
+        k[at, 0] = -160 * 0.6931472 / (8 * SM)
+        set_keys(c, rows, k)
+        c.v[1][rows[at]] *= 2.0 ** 68
+        c.v[1][rows[at]] *= 2.0 ** 67      # (2^135 is no fp32)
+    out, l, flags = run(c, q)
+    assert flags == 0
+    _attn_bounds.check(out, l, _attn_bounds.reference(c, q, SM, split_query=wide))
+
+
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("up", [True, False])
 def test_scores_and_value_scales_that_run_against_each_other(wide, up):
     """The maximum rises by 2^7 log2 units (or falls) along the cache while the values shrink (or
