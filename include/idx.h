@@ -365,7 +365,9 @@ IDX_API int idx_attn_paged(const void* q, const void* k_payload, const void* k_s
  *   block_ids (device):  int32 [R][P][lists][topk], idx_score_topk's out_ids with gqa = lists.
  *                        Query head j goes by list j / (q_heads / lists).  A list is a set: its
  *                        order does not matter, a block listed twice counts once, and ids < 0
- *                        or at or past the row's own blocks are left out.
+ *                        or at or past the row's own blocks are left out.  Ids count from the
+ *                        page table's first page: of merged lists a context shard subtracts its
+ *                        first block, as it does from the lengths.
  *   lists:               q_heads must be a multiple of it, and lists and kv_heads one a multiple
  *                        of the other;  topk: 1 .. IDX_MAX_TOPK
  * The draft rows of a request that share a list position are packed: their lists are joined,

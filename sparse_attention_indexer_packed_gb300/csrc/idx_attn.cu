@@ -22,9 +22,9 @@
 //    number, every CTA finds from the lengths whether to deal or to cut (Cost).
 //    Cut / dealt, us: bf16 64 x 8 heads x 256 tokens 26.1 / 18.1, x 1K 53.4 / 46.2,
 //    x 8K 300 / 297; 256 x 8 x 100 61.7 / 26.8; 1 x 200 8.7 / 7.5; e4m3 64 x 8 x 256
-//    27.1 / 13.5, x 1K 47.0 / 32.1, 256 x 8 x 100 75.5 / 22.0.  Lists: bf16 128 x 4
-//    lists of 16 blocks 92.1 / 71.9, 60 x 4 of 12 38.9 / 31.7, e4m3 74.3 / 54.2 and
-//    36.3 / 26.5 (the host decides; no join kernel runs).  The second way in
+//    30.3 / 13.8, x 1K 54.2 / 31.7, 256 x 8 x 100 78.7 / 22.2.  Lists: bf16 128 x 4
+//    lists of 16 blocks 92.1 / 71.9, 60 x 4 of 12 38.9 / 31.7, e4m3 72.3 / 54.4 and
+//    35.4 / 26.2 (the host decides; no join kernel runs).  The second way in
 //    the kernel costs calls that cut 1 to 6% (1 x 1K 9.1 -> 9.4), those of e4m3 with
 //    more units than SMs 9%;
 //  * a warp owns one shared-memory stage of one piece (keys and values, by TMA
@@ -44,13 +44,13 @@
 //  * every wait is bounded, as in the score kernels.
 //
 // Measured (one GB300, calls back to back): bf16 16 x 131K, 16 rows: 152 us, 6.49
-// TB/s of cache, 0.96 of the copy peak.  e4m3 16 x 131K: 95 us, 5.35 TB/s, 0.79: the
+// TB/s of cache, 0.96 of the copy peak.  e4m3 16 x 131K: 96 us, 5.3 TB/s, 0.78: the
 // products' operands are decoded in registers, 8 warps of 255 registers leave the
-// issue slots 36% used and the warps waiting on their own chains (12 warps of 168
+// issue slots 34% used and the warps waiting on their own chains (12 warps of 168
 // registers spill: 117 us).  Lists, 16 x 131K, 4 x 4 rows, 64 blocks: 65 us for 369 MB
 // of joined blocks, 5.7 TB/s.  Short calls are latency: 1 x 1K 9.4 us (request table
 // 0.9, first page id 2, first tile 4.3, output 5.7, join 8.7), 48 ragged requests
-// 25 us (first tiles 5 to 8, last output 21, join 25).
+// 25 us (first tiles 5 to 8, last output 21, join 25; e4m3 29).
 // Tried and slower: two e4m3 query terms on m16n8k32 (113 -> 134 us, one stage a
 // warp); the next piece's scores under this one's weights with stages of their own
 // for keys and values (96 -> 108); 4 warps of 2 stages for bf16 (1 x 1K 8.9 -> 8.4,

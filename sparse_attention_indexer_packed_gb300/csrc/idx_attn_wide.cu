@@ -37,10 +37,10 @@
 // values are decoded to f16, exactly, by the group that uses them, and the weights
 // times the value's scale are one f16 (11 bits; raise_unit).
 //
-// Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 164 us, 6.0
-// TB/s of cache, 0.89 of the copy peak (the warp-level kernel, four groups of 16 rows:
-// 548); 32 rows 157 us, 0.93.  128 rows, 8 x 64K: 68 to 71 us, 0.54: a lane's 64
-// weights.  e4m3, 64 rows 161 us, 0.47; 32 rows 147: a group needs ~2700 cycles a page
+// Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 162 to
+// 167 us, 0.87 to 0.90 of the copy peak from one GPU to another (the warp-level kernel, four groups of 16 rows:
+// 548); 32 rows 157 us, 0.93.  128 rows, 8 x 64K: 72 to 74 us, 0.51: a lane's 64
+// weights.  e4m3, 64 rows 160 us, 0.47; 32 rows 147: a group needs ~2700 cycles a page
 // (waits 600, decoding the values 540, weights 930, two thirds of it the scales), and
 // two groups alternate.  Up to 16 rows this kernel is the slower one (e4m3 16 x 131K
 // 152 us against 122 at the time, 1 x 1K 12.8 against 9.3).

@@ -16,8 +16,8 @@
 // belongs to 16 lanes, up to 512 to a warp (neither needs a barrier), a longer one
 // to a CTA.  Any other row goes element by element through shared memory.
 //
-// Measured: 16000 x 5120 with one scale a row 87.4 us, 6.56 TB/s, 0.97 of the copy
-// peak; 9000 x 8192 in groups 79 us, 0.97; 16000 x 1024 19.3 us, 0.88; 16000 x 128 3.1
+// Measured: 16000 x 5120 with one scale a row 87.4 to 88.1 us, 6.5 TB/s, 0.96 of the copy
+// peak (89.7 a call, back to back); 9000 x 8192 in groups 79 us, 0.97; 16000 x 1024 19.3 us, 0.88; 16000 x 128 3.1
 // us (from L2); 64 x 6144 2.6 us, latency.  Element by element 16000 x 1001 takes 64
 // us, 0.26 (a warp a row with the elements in registers: 89).
 #include <cuda_bf16.h>
