@@ -346,8 +346,9 @@ IDX_API size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_
  * Sums and softmax statistics are fp32; for the product with the values the weights are
  * held as two bf16 (bf16 cache, 2^-17 of the weight), or weight times value scale as one f16
  * (e4m3 cache): 2^-11 of it, or 2^-28 of the row's largest such product.  With an e4m3 cache a
- * query element more than 2^13 below its row's largest may be off by 2^-21 of the largest.  Asynchronous on stream; allocates nothing;
- * capturable.  R <= IDX_MAX_REQUESTS, P * q_heads <= IDX_MAX_ROWS_PER_REQUEST, num_pages *
+ * query element more than 2^13 below its row's largest may be off by 2^-21 of the largest.
+ * Asynchronous on stream, on the current device, where every pointer has to be; allocates
+ * nothing; capturable.  R <= IDX_MAX_REQUESTS, P * q_heads <= IDX_MAX_ROWS_PER_REQUEST, num_pages *
  * kv_heads < 2^31 / 64; q_heads a multiple of kv_heads; requests times key heads (or lists)
  * times groups of 128 rows at most 2^18.
  */
