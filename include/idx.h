@@ -1,7 +1,8 @@
 /*
  * libidx — packed sparse-attention index scoring + block top-k for GB300 (sm_103a), and the
  * operators of the layer around it: the key-value store, attention over the paged cache or over
- * the chosen blocks, and the residual + RMS norm with an e4m3 result.
+ * the chosen blocks (bf16, e4m3 and NVFP4 caches), the residual + RMS norm with an e4m3 result,
+ * and the norm, rotation and store of a projection's queries, keys and values.
  *
  * C ABI.  Every pointer named "device" must point to device memory of the current
  * CUDA device; "host" pointers are read before the call returns.  Streams are
@@ -51,7 +52,7 @@ extern "C" {
 typedef enum {
   IDX_BF16 = 0,      /* bfloat16 */
   IDX_FP8_E4M3 = 1,  /* OCP E4M3 ("fn": no infinities, max 448) with fp32 scales */
-  IDX_NVFP4 = 2      /* e2m1 payload + E4M3 per-16 scales (keys only) */
+  IDX_NVFP4 = 2      /* e2m1 payload + E4M3 per-16 scales (keys and values) */
 } idx_dtype;
 
 typedef enum {
@@ -289,8 +290,17 @@ IDX_API int idx_score_topk_perrow(const void* q, const float* q_scale, int q_dty
  * above with kv_heads heads.  Page p of head h is head page p * kv_heads + h, so token
  * t of head h of a page lies in plane row (page * kv_heads + h) * 64 + t % 64 and each
  * head page is one contiguous tile; an idx_pool of num_pages * kv_heads pages holds one
- * plane, and with one head the layout is an index pool's.  bf16 and e4m3 planes.
+ * plane, and with one head the layout is an index pool's.  bf16, e4m3 and NVFP4 planes.
+ *
+ * An NVFP4 plane's values are code * scale * outer, with one outer scale for the plane: a power
+ * of two in [IDX_MIN_OUTER, IDX_MAX_OUTER] that the caller keeps and hands to every call.  With 1
+ * the plane is an NVFP4 index pool's.  A group's scale has E4M3's range, 2^-9 to 448 with three
+ * bits from 2^-6 on, so an outer scale is well chosen if the groups' largest magnitudes lie in
+ * [2^-3, 2688] times it.
  */
+#define IDX_MIN_OUTER 5.42101086242752217e-20f /* 2^-64 */
+#define IDX_MAX_OUTER 1.8446744073709551616e19f /* 2^64 */
+
 
 /*
  * idx_store_kv — write new keys (and values) into the cache.  bf16 planes take the bits;
@@ -307,7 +317,7 @@ IDX_API int idx_score_topk_perrow(const void* q, const float* q_scale, int q_dty
  *                          codes of one under the scale of the other.
  *   k_pool, v_pool (host): planes of num_pages * kv_heads head pages, the same dtype.
  * Asynchronous on stream; allocates nothing; capturable.  IDX_ERR_INVALID for arguments out of range;
- * IDX_ERR_UNSUPPORTED for an NVFP4 pool (idx_store_nvfp4 writes those).  num_tokens == 0 is
+ * IDX_ERR_UNSUPPORTED for an NVFP4 pool (idx_store_kv_nvfp4 writes those).  num_tokens == 0 is
  * a no-op.
  */
 IDX_API int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
@@ -315,7 +325,72 @@ IDX_API int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride,
                          const idx_pool* k_pool, const idx_pool* v_pool, void* stream);
 
 /*
- * idx_attn_workspace_bytes — device scratch of idx_attn_paged (lists 0) and idx_attn_blocks:
+ * idx_store_kv_nvfp4 — idx_store_kv into NVFP4 planes.  Per group of 16 elements y = x / outer:
+ * scale = E4M3(max |y| / 6), half to even, at most 448; codes e2m1(y / scale), half to even,
+ * saturating at 6, the sign kept; a scale of 0 gives codes of 0.  With an outer scale of 1 the
+ * bytes are idx_store_nvfp4's.  A NaN makes its group's scale NaN (0x7f, codes 0); an infinity is
+ * held as the largest value, 6 * 448 * outer, of its sign.
+ *   k_pool, v_pool (host): NVFP4 planes (IDX_ERR_UNSUPPORTED for others), the scale planes 8-byte
+ *                          aligned
+ *   k_outer, v_outer:      the planes' outer scales (v_outer is checked without values too)
+ * Everything else as for idx_store_kv.
+ */
+IDX_API int idx_store_kv_nvfp4(const void* k_src, const void* v_src, int64_t k_stride,
+                               int64_t v_stride, const int64_t* slot_mapping, int64_t num_tokens,
+                               int kv_heads, const idx_pool* k_pool, const idx_pool* v_pool,
+                               float k_outer, float v_outer, void* stream);
+
+/* The rotation of idx_norm_rope_store. */
+#define IDX_MAX_ROPE_AXES 4
+typedef struct idx_rope {
+  const float* table;         /* device, fp32 [num_positions][rotary_dim], 16-byte aligned: the
+                                 cosines of a position's rotary_dim / 2 pairs, then their sines */
+  int64_t num_positions;      /* 1 .. 2^31 - 1 */
+  const int32_t* positions;   /* device, int32 [axes][num_tokens]: a token's position on each axis */
+  int32_t axes;               /* 1 .. IDX_MAX_ROPE_AXES: 1 for text; time, height, width for video */
+  int32_t rotary_dim;         /* elements of a head that are rotated, the first ones: a multiple
+                                 of 16 up to 128 */
+  int32_t interleaved;        /* 0: pair i is elements (i, i + rotary_dim / 2); else (2i, 2i + 1) */
+  int32_t reserved;
+  uint8_t pair_axis[64];      /* the axis that pair i goes by, below axes (not read with one axis) */
+} idx_rope;
+
+/*
+ * idx_norm_rope_store — from a layer's projection to where its attention takes its operands from,
+ * in one pass: the root-mean-square norm of the queries and keys, head by head, their rotation by
+ * position, and the store of the keys and values.  In fp32, per token and head of 128 elements:
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (queries, keys; a NULL weight: y = x)
+ *   pair (a, b) = pair i of y's first rotary_dim elements, p = the token's position on the pair's
+ *   axis: (a cos - b sin, b cos + a sin) with cos = table[p][i], sin = table[p][rotary_dim/2 + i]
+ * The queries go to out_q, the keys to k_pool as idx_store_kv or idx_store_kv_nvfp4 would
+ * write them if they took fp32 (one rounding; an NVFP4 code may be that of the neighbour where
+ * y / scale lies within two fp32 steps of the border), the values, unchanged, to v_pool, in the
+ * bytes of those calls.
+ *   q, k, v (device):    bf16 [num_tokens][heads][128], q_stride, k_stride, v_stride elements
+ *                        between tokens: multiples of 8, 16-byte aligned.  q NULL with out_q NULL
+ *                        and q_heads 0: keys only.  v NULL with v_pool NULL: no values (index keys)
+ *   q_weight, k_weight (device): bf16 [128], 16-byte aligned, or NULL: no norm of that part
+ *   rope (host):         the rotation; NULL: none.  A position outside [0, num_positions) turns the
+ *                        elements that go by it into NaN (and with them an e4m3 row, an NVFP4 group)
+ *   slot_mapping:        as for idx_store_kv: a token that is skipped has its queries computed
+ *   out_q (device):      bf16 [num_tokens][q_heads][128]; with out_q_scale (device, fp32
+ *                        [num_tokens][q_heads]) e4m3 codes by idx_store_kv's rule, a query of
+ *                        idx_score_topk
+ *   k_pool, v_pool (host), k_outer, v_outer: bf16, e4m3 (outer scales 1) or NVFP4 planes
+ * out_q must not overlap the projection.  Asynchronous on stream; allocates nothing; capturable.
+ * num_tokens == 0 is a no-op.
+ */
+IDX_API int idx_norm_rope_store(const void* q, int64_t q_stride, int q_heads, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, int kv_heads,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const idx_rope* rope, const int64_t* slot_mapping,
+                                int64_t num_tokens, void* out_q, float* out_q_scale,
+                                const idx_pool* k_pool, const idx_pool* v_pool, float k_outer,
+                                float v_outer, void* stream);
+
+/*
+ * idx_attn_workspace_bytes — device scratch of idx_attn_paged (lists 0) and idx_attn_blocks, and
+ * of the same over NVFP4 caches:
  * the header, and the partial results of the units that several CTAs share.  It does not
  * depend on the number of requests or the context.  0 for arguments that do not fit together.
  */
@@ -383,6 +458,30 @@ IDX_API int idx_attn_blocks(const void* q, const void* k_payload, const void* k_
                             int num_requests, int packed_queries, int q_heads, float sm_scale,
                             void* out, float* out_lse, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/*
+ * idx_attn_paged_nvfp4, idx_attn_blocks_nvfp4 — the same over NVFP4 planes: k_scale, v_scale
+ * (device, 16-byte aligned) are E4M3 bytes [rows][8], k_outer, v_outer the planes' outer scales;
+ * sm_scale * k_outer must be a normal fp32 number.  Codes times scales are exact in f16, where the
+ * products are taken; a query element is exact within 2^21 of its row's largest; the weights
+ * enter the product with the values as one f16: 2^-11 of the weight, or 2^-39 of the row's
+ * largest weight.
+ */
+IDX_API int idx_attn_paged_nvfp4(const void* q, const void* k_payload, const void* k_scale,
+                                 const void* v_payload, const void* v_scale, int64_t num_pages,
+                                 int kv_heads, const int32_t* page_table, int n_slots,
+                                 int max_pages, const int32_t* slot_ids, const int32_t* row_lens,
+                                 int num_requests, int packed_queries, int q_heads, float sm_scale,
+                                 float k_outer, float v_outer, void* out, float* out_lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+IDX_API int idx_attn_blocks_nvfp4(const void* q, const void* k_payload, const void* k_scale,
+                                  const void* v_payload, const void* v_scale, int64_t num_pages,
+                                  int kv_heads, const int32_t* page_table, int n_slots,
+                                  int max_pages, const int32_t* slot_ids, const int32_t* row_lens,
+                                  const int32_t* block_ids, int lists, int topk, int num_requests,
+                                  int packed_queries, int q_heads, float sm_scale, float k_outer,
+                                  float v_outer, void* out, float* out_lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * idx_add_rmsnorm_fp8 — residual addition, root-mean-square norm, e4m3 result.  Per row, in

@@ -74,6 +74,14 @@ _SIGNATURES = {
                             _P, _P, _P, _SZ, _P]),
     "idx_attn_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I64, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I,
                              _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "idx_store_kv_nvfp4": (_I, [_P, _P, _I64, _I64, _P, _I64, _I, _P, _P, _F, _F, _P]),
+    "idx_attn_paged_nvfp4": (_I, [_P, _P, _P, _P, _P, _I64, _I, _P, _I, _I, _P, _P, _I, _I, _I, _F, _F,
+                                  _F, _P, _P, _P, _SZ, _P]),
+    "idx_attn_blocks_nvfp4": (_I, [_P, _P, _P, _P, _P, _I64, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I,
+                                   _I, _I, _F, _F, _F, _P, _P, _P, _SZ, _P]),
+    # (the rotation is passed as the struct's bytes: see _rope_bytes)
+    "idx_norm_rope_store": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _P, _F, _P, _P, _I64, _P, _P,
+                                 _P, _P, _F, _F, _P]),
     "idx_add_rmsnorm_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _F, _P, _P, _P, _P]),
     "idx_set_kernel_events": (_I, [_P, _P, _P]),
     "idx_set_kernel_waits": (_I, [_P, _P]),
@@ -403,6 +411,15 @@ def _plane(payload, scale, name: str, kv_dtype: str):
     return _dev(payload, f"{name}_payload"), scale, rows // PAGE
 
 
+def _plane4(payload, scale, name: str):
+    """_plane of an NVFP4 cache, whose scales are required."""
+    ptr, _, pages = _plane(payload, None, name, "nvfp4")
+    if (scale is None or scale.dtype not in (torch.uint8, torch.float8_e4m3fn)
+            or scale.shape != (pages * PAGE, DIM // 16)):
+        raise IdxError(f"{name}_scale must be uint8 or float8_e4m3fn [{pages * PAGE}, {DIM // 16}]")
+    return ptr, _dev(scale, f"{name}_scale"), pages
+
+
 def _source(src, name: str, tokens: int, kv_heads: int):
     """Pointer and token stride of new keys or values [tokens, kv_heads, 128]."""
     if src.dtype is not _BF16 or src.shape != (tokens, kv_heads, DIM):
@@ -421,17 +438,14 @@ assert _POOL.size == ctypes.sizeof(IdxPool)
 
 
 def _pool_bytes(payload, scale, name: str, kv_dtype: str) -> bytes:
-    ptr, scale_ptr, pages = _plane(payload, scale, name, kv_dtype)
+    ptr, scale_ptr, pages = (_plane4(payload, scale, name) if kv_dtype == "nvfp4" else
+                             _plane(payload, scale, name, kv_dtype))
     return _POOL.pack(DTYPES[kv_dtype], PAGE, DIM, 0, pages, ptr, scale_ptr or 0,
                       _ROW_BYTES[kv_dtype], _SCALE_BYTES[kv_dtype])
 
 
-def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
-                 kv_dtype: str, kv_heads: int, stream=None) -> None:
-    """k_src, v_src: bf16 [tokens, kv_heads, 128], tokens any stride apart (a slice of a
-    fused projection); v_src, v_payload, v_scale None: keys only.  slot_mapping: int64, page *
-    64 + offset, every token's its own (negative: skipped).  Planes as for idx_attn_paged, or
-    an index pool's (kv_heads 1)."""
+def _store_args(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale, kv_dtype, kv_heads, stream):
+    """The arguments the two store calls begin with."""
     if k_src is None or k_payload is None or (v_src is None) != (v_payload is None):
         raise IdxError("a source and its payload plane come together, and the keys always")
     T = slot_mapping.numel()
@@ -443,10 +457,108 @@ def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_sc
         v_pool = _pool_bytes(v_payload, v_scale, "v", kv_dtype)
     slots = _want(slot_mapping, "slot_mapping", torch.int64, (T,))
     _one_device(stream, k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale)
-    rc = lib().idx_store_kv(k_ptr, v_ptr, k_stride, v_stride, slots, T, kv_heads, k_pool, v_pool,
-                            _stream_of(k_src, stream))
+    return k_ptr, v_ptr, k_stride, v_stride, slots, T, kv_heads, k_pool, v_pool
+
+
+def idx_store_kv(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
+                 kv_dtype: str, kv_heads: int, stream=None) -> None:
+    """k_src, v_src: bf16 [tokens, kv_heads, 128], tokens any stride apart (a slice of a
+    fused projection); v_src, v_payload, v_scale None: keys only.  slot_mapping: int64, page *
+    64 + offset, every token's its own (negative: skipped).  Planes as for idx_attn_paged, or
+    an index pool's (kv_heads 1)."""
+    args = _store_args(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale, kv_dtype,
+                       kv_heads, stream)
+    rc = lib().idx_store_kv(*args, _stream_of(k_src, stream))
     if rc:
         _check(rc, "idx_store_kv")
+
+
+def idx_store_kv_nvfp4(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale,
+                       kv_heads: int, k_outer: float = 1.0, v_outer: float = 1.0, stream=None) -> None:
+    """idx_store_kv into NVFP4 planes: payload [rows, 64] bytes, scale uint8 (or float8_e4m3fn)
+    [rows, 8]; value = code * scale * outer, outer a power of two for each plane."""
+    args = _store_args(k_src, v_src, slot_mapping, k_payload, k_scale, v_payload, v_scale, "nvfp4",
+                       kv_heads, stream)
+    rc = lib().idx_store_kv_nvfp4(*args, k_outer, v_outer, _stream_of(k_src, stream))
+    if rc:
+        _check(rc, "idx_store_kv_nvfp4")
+
+
+class IdxRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("num_positions", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("axes", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("pair_axis", ctypes.c_uint8 * 64)]
+
+
+_ROPE = struct.Struct("=QqQiiii64s")
+assert _ROPE.size == ctypes.sizeof(IdxRope)
+
+
+def _rope_bytes(table, positions, pair_axis, interleaved, tokens: int):
+    """The rotation as the struct's bytes; None without a table."""
+    if table is None:
+        if positions is not None or pair_axis is not None:
+            raise IdxError("positions and pair_axis come with a table")
+        return None
+    if table.dim() != 2 or positions is None:
+        raise IdxError("table must be [num_positions, rotary_dim], and positions go with it")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    shape = (axes, tokens) if positions.dim() == 2 else (tokens,)
+    by = b"" if pair_axis is None else bytes(pair_axis)
+    if (axes > 1 or by) and len(by) != table.shape[1] // 2:
+        raise IdxError(f"pair_axis must name an axis for each of the {table.shape[1] // 2} pairs (got {len(by)})")
+    if len(by) > 64:
+        raise IdxError("rotary_dim must be at most 128")
+    return _ROPE.pack(_want(table, "table", _F32, table.shape), table.shape[0],
+                      _want(positions, "positions", _I32, shape), axes, table.shape[1],
+                      bool(interleaved), 0, by)
+
+
+def idx_norm_rope_store(q, k, v, q_weight, k_weight, eps: float, table, positions, pair_axis, interleaved: bool,
+                        slot_mapping, out_q, out_q_scale, k_payload, k_scale, v_payload, v_scale,
+                        kv_dtype: str, kv_heads: int, k_outer: float = 1.0, v_outer: float = 1.0,
+                        stream=None) -> None:
+    """Norm, rotation and store of a projection's parts.  q [tokens, q_heads, 128] (or None), k and
+    v (or None) [tokens, kv_heads, 128]: bf16, tokens any stride apart.  q_weight, k_weight: bf16
+    [128], or None: no norm.  table: fp32 [num_positions, rotary_dim], cosines then sines, or None: no
+    rotation; positions: int32 [tokens] or [axes, tokens]; pair_axis: the axis of each pair (bytes,
+    rotary_dim / 2 of them; None with one axis).  out_q [tokens, q_heads, 128]: bf16, or e4m3 codes with
+    out_q_scale fp32 [tokens, q_heads].  Planes as for the store calls."""
+    if k is None or k_payload is None or (v is None) != (v_payload is None) or (q is None) != (out_q is None):
+        raise IdxError("k and its plane are required, v and its plane, q and out_q come together")
+    T = slot_mapping.numel()
+    qp, qs, Hq, outq, outs = None, 0, 0, None, None
+    if q is not None:
+        if q.dim() != 3:
+            raise IdxError(f"q must be [tokens, q_heads, {DIM}]")
+        Hq = q.shape[1]
+        qp, qs = _source(q, "q", T, Hq)
+        if out_q_scale is None:
+            outq = _want(out_q, "out_q", _BF16, q.shape)
+        else:
+            if out_q.dtype is not torch.float8_e4m3fn and out_q.dtype is not torch.uint8:
+                raise IdxError("out_q must be float8_e4m3fn or uint8 with out_q_scale")
+            outq = _want(out_q, "out_q", out_q.dtype, q.shape)
+            outs = _want(out_q_scale, "out_q_scale", _F32, (T, Hq))
+    elif out_q_scale is not None:
+        raise IdxError("out_q_scale comes with q")
+    kp, ks = _source(k, "k", T, kv_heads)
+    k_pool = _pool_bytes(k_payload, k_scale, "k", kv_dtype)
+    vp, vs, v_pool = None, 0, None
+    if v is not None:
+        vp, vs = _source(v, "v", T, kv_heads)
+        v_pool = _pool_bytes(v_payload, v_scale, "v", kv_dtype)
+    weights = [None if w is None else _want(w, n, _BF16, (DIM,))
+               for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    rope = _rope_bytes(table, positions, pair_axis, interleaved, T)
+    slots = _want(slot_mapping, "slot_mapping", torch.int64, (T,))
+    _one_device(stream, q, k, v, q_weight, k_weight, table, positions, slot_mapping, out_q, out_q_scale,
+                k_payload, k_scale, v_payload, v_scale)
+    rc = lib().idx_norm_rope_store(qp, qs, Hq, kp, ks, vp, vs, kv_heads, *weights, eps, rope, slots, T, outq,
+                                   outs, k_pool, v_pool, k_outer, v_outer, _stream_of(k, stream))
+    if rc:
+        _check(rc, "idx_norm_rope_store")
 
 
 def idx_attn_workspace_bytes(packed_queries: int, q_heads: int, kv_heads: int, lists: int = 0) -> int:
@@ -469,16 +581,19 @@ def _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, 
     if len(shape) != 4 or shape[3] != DIM:
         raise IdxError(f"q must be [requests, draft rows, q_heads, {DIM}]")
     R, P, Hq, _ = shape
-    kp, ks, k_pages = _plane(k_payload, k_scale, "k", kv_dtype)
-    vp, vs, v_pages = _plane(v_payload, v_scale, "v", kv_dtype)
+    if kv_dtype is None:   # NVFP4: the call's name says so
+        (kp, ks, k_pages), (vp, vs, v_pages) = _plane4(k_payload, k_scale, "k"), _plane4(v_payload, v_scale, "v")
+    else:
+        kp, ks, k_pages = _plane(k_payload, k_scale, "k", kv_dtype)
+        vp, vs, v_pages = _plane(v_payload, v_scale, "v", kv_dtype)
     if kv_heads < 1 or k_pages != v_pages or k_pages % kv_heads:
         raise IdxError("the planes must hold the same whole pages of kv_heads heads")
     table = page_table.shape
     if len(table) != 2:
         raise IdxError("page_table must be [n_slots, max_pages]")
     n_slots, max_pages = table
-    return (_want(q, "q", _BF16, shape), kp, ks, vp, vs, DTYPES[kv_dtype], k_pages // kv_heads,
-            kv_heads, _want(page_table, "page_table", _I32, table), n_slots, max_pages,
+    return (_want(q, "q", _BF16, shape), kp, ks, vp, vs,
+            *(() if kv_dtype is None else (DTYPES[kv_dtype],)), k_pages // kv_heads, kv_heads, _want(page_table, "page_table", _I32, table), n_slots, max_pages,
             _want(slot_ids, "slot_ids", _I32, (R,)),
             _want(row_lens, "row_lens", _I32, (R, P))), R, P, Hq
 
@@ -523,6 +638,39 @@ def idx_attn_blocks(q, k_payload, k_scale, v_payload, v_scale, kv_dtype: str, pa
     rc = lib().idx_attn_blocks(*head, ids, lists, topk, R, P, Hq, sm_scale, *tail, _stream_of(q, stream))
     if rc:
         _check(rc, "idx_attn_blocks")
+
+
+def idx_attn_paged_nvfp4(q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens,
+                         kv_heads: int, sm_scale: float, out, out_lse, workspace, k_outer: float = 1.0,
+                         v_outer: float = 1.0, stream=None) -> None:
+    """idx_attn_paged over NVFP4 planes (as for idx_store_kv_nvfp4)."""
+    head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, None, page_table, slot_ids,
+                                row_lens, kv_heads)
+    tail = _attn_out(q, out, out_lse, workspace)
+    _one_device(stream, q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens, out,
+                out_lse, workspace)
+    rc = lib().idx_attn_paged_nvfp4(*head, R, P, Hq, sm_scale, k_outer, v_outer, *tail, _stream_of(q, stream))
+    if rc:
+        _check(rc, "idx_attn_paged_nvfp4")
+
+
+def idx_attn_blocks_nvfp4(q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens,
+                          block_ids, lists: int, kv_heads: int, sm_scale: float, out, out_lse, workspace,
+                          k_outer: float = 1.0, v_outer: float = 1.0, stream=None) -> None:
+    """idx_attn_blocks over NVFP4 planes (as for idx_store_kv_nvfp4)."""
+    if block_ids is None or block_ids.dim() != 3 or lists < 1:
+        raise IdxError("block_ids must be [requests, draft rows * lists, topk] and lists >= 1")
+    head, R, P, Hq = _attn_args(q, k_payload, k_scale, v_payload, v_scale, None, page_table, slot_ids,
+                                row_lens, kv_heads)
+    topk = block_ids.shape[2]
+    ids = _want(block_ids, "block_ids", _I32, (R, P * lists, topk))
+    tail = _attn_out(q, out, out_lse, workspace)
+    _one_device(stream, q, k_payload, k_scale, v_payload, v_scale, page_table, slot_ids, row_lens,
+                block_ids, out, out_lse, workspace)
+    rc = lib().idx_attn_blocks_nvfp4(*head, ids, lists, topk, R, P, Hq, sm_scale, k_outer, v_outer, *tail,
+                                     _stream_of(q, stream))
+    if rc:
+        _check(rc, "idx_attn_blocks_nvfp4")
 
 
 def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_scale,

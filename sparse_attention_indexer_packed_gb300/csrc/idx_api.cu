@@ -4,10 +4,12 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <float.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 #include <string>
 
@@ -192,18 +194,21 @@ int make_q_map(int q_dtype, const void* q, int64_t rows, CUtensorMap* map) {
 }
 
 // Tensor map over one plane of a key-value cache: bf16 rows as two 64-column
-// boxes, e4m3 rows as one 128-byte box, `box_rows` high, 128-byte swizzle.  Encoded at each call: it is a fraction of a launch's host time.
+// boxes, e4m3 rows as one 128-byte box, `box_rows` high, 128-byte swizzle; NVFP4 rows as
+// one 64-byte box with the 64-byte swizzle.  Encoded at each call: it is a fraction of a
+// launch's host time.
 int make_plane_map(int dtype, const void* payload, int64_t rows, int box_rows, CUtensorMap* map) {
   auto fn = encode_fn();
   if (!fn) return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const bool bf16 = dtype == IDX_BF16;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 256 : 128)};
-  const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : 128), (cuuint32_t)box_rows};
+  const bool bf16 = dtype == IDX_BF16, fp4 = dtype == IDX_NVFP4;
+  const cuuint64_t dims[2] = {(cuuint64_t)(fp4 ? 64 : 128), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(bf16 ? 256 : fp4 ? 64 : 128)};
+  const cuuint32_t box[2] = {(cuuint32_t)(bf16 || fp4 ? 64 : 128), (cuuint32_t)box_rows};
   const cuuint32_t estride[2] = {1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                   const_cast<void*>(payload), dims, strides, box, estride,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  fp4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(IDX_ERR_CUDA, "cuTensorMapEncodeTiled (cache plane) failed (%d)", (int)r);
@@ -218,13 +223,20 @@ int unit_heads(int q_heads, int kv_heads, int lists) {
   return hi;
 }
 
-// Whole-cache attention (block_ids NULL, lists 0) or over block lists.
+// An outer scale is a power of two, so that dividing by it is exact.
+bool outer_ok(float x) {
+  int e;
+  return x >= IDX_MIN_OUTER && x <= IDX_MAX_OUTER && std::frexp(x, &e) == 0.5f;
+}
+
+// Whole-cache attention (block_ids NULL, lists 0) or over block lists.  The outer scales
+// are 1 but for NVFP4, which the entry points of that name alone pass on.
 int attn_impl(const void* q, const void* k_payload, const void* k_scale, const void* v_payload,
               const void* v_scale, int kv_dtype, int64_t num_pages, int kv_heads,
               const int32_t* page_table, int n_slots, int max_pages, const int32_t* slot_ids,
               const int32_t* row_lens, bool blocks, const int32_t* block_ids, int lists, int topk,
-              int R, int P, int q_heads, float sm_scale, void* out, float* out_lse,
-              void* workspace, size_t workspace_bytes, void* stream) {
+              int R, int P, int q_heads, float sm_scale, float k_outer, float v_outer, bool nvfp4,
+              void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (R < 0 || R > IDX_MAX_REQUESTS)
     return fail(IDX_ERR_INVALID, "num_requests must be in [0, %d] (got %d)", IDX_MAX_REQUESTS, R);
   if (P < 1 || q_heads < 1 || (long long)P * q_heads > IDX_MAX_ROWS_PER_REQUEST)
@@ -238,18 +250,27 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
                 q_heads, kv_heads, blocks ? lists : 1);
   if (blocks && (topk < 1 || topk > IDX_MAX_TOPK))
     return fail(IDX_ERR_INVALID, "topk must be in [1, %d] (got %d)", IDX_MAX_TOPK, topk);
-  if (kv_dtype != IDX_BF16 && kv_dtype != IDX_FP8_E4M3)
-    return fail(IDX_ERR_UNSUPPORTED, "the attention reads bf16 and e4m3 caches (got dtype %d)",
+  if (!nvfp4 && kv_dtype != IDX_BF16 && kv_dtype != IDX_FP8_E4M3)
+    return fail(IDX_ERR_UNSUPPORTED,
+                "this call reads bf16 and e4m3 caches (got dtype %d; idx_attn_paged_nvfp4 and "
+                "idx_attn_blocks_nvfp4 read NVFP4)",
                 kv_dtype);
   if (!(sm_scale > 0.f) || !(sm_scale < 1e30f))
     return fail(IDX_ERR_INVALID, "sm_scale must be positive and finite (got %g)", (double)sm_scale);
+  if (!outer_ok(k_outer) || !outer_ok(v_outer))
+    return fail(IDX_ERR_INVALID, "outer scales must be powers of two in [2^-64, 2^64] (got %g, %g)",
+                (double)k_outer, (double)v_outer);
+  const float scale_log2 = sm_scale * k_outer * 1.4426950408889634f;
+  if (nvfp4 && !(scale_log2 >= FLT_MIN && scale_log2 <= FLT_MAX))
+    return fail(IDX_ERR_INVALID, "sm_scale * k_outer is out of range (got %g x %g)", (double)sm_scale,
+                (double)k_outer);
   if (n_slots < 1 || max_pages < 1 || max_pages > 65536)
     return fail(IDX_ERR_INVALID, "need n_slots >= 1 and 1 <= max_pages <= 65536 (got %d, %d)",
                 n_slots, max_pages);
   if (num_pages < 1 || num_pages > 0x7fffffffLL / idx::kPage / kv_heads)
     return fail(IDX_ERR_INVALID, "num_pages * kv_heads must be in [1, 2^31 / 64) (got %lld x %d)",
                 (long long)num_pages, kv_heads);
-  const int group = idx::attn::group_rows(P, q_heads / heads, blocks);
+  const int group = nvfp4 ? 16 : idx::attn::group_rows(P, q_heads / heads, blocks);
   const long long units = (long long)R * heads * (((long long)P * (q_heads / heads) + group - 1) / group);
   if (units > idx::attn::kMaxUnits)
     return fail(IDX_ERR_INVALID, "at most %lld (request, key head or list, row group) units a call (got %lld)",
@@ -268,8 +289,8 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   if (!q || !k_payload || !v_payload || !page_table || !slot_ids || !row_lens || !out ||
       (blocks && !block_ids))
     return fail(IDX_ERR_INVALID, "a required pointer is NULL");
-  if (kv_dtype == IDX_FP8_E4M3 && (!k_scale || !v_scale))
-    return fail(IDX_ERR_INVALID, "an e4m3 cache needs k_scale and v_scale");
+  if (kv_dtype != IDX_BF16 && (!k_scale || !v_scale))
+    return fail(IDX_ERR_INVALID, "an %s cache needs k_scale and v_scale", nvfp4 ? "NVFP4" : "e4m3");
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_payload, 16) || !aligned(v_payload, 16) ||
       !aligned(k_scale, 16) || !aligned(v_scale, 16))
     return fail(IDX_ERR_INVALID, "q, out and the cache planes must be 16-byte aligned");
@@ -311,7 +332,8 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   a.unit_cost = idx::attn::unit_cost(a.group_rows, blocks);
   a.most = idx::attn::most_pieces(max_pages, blocks ? (long long)topk * P : 0);
   a.shift = idx::attn::position_shift(R, (long long)heads * a.groups, a.most, a.unit_cost);
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
+  a.out_scale = v_outer;
   a.wait_ns = idx::wait_limit_ns();
   a.stall_test = idx::stall_test();
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -522,6 +544,94 @@ int score_topk_impl(bool perrow, int block_score, int block_begin, const void* q
     return cuda_fail(e, "launching the top-k kernel");
   }
   if (ev[2] && (e = record_event(ev[2], st)) != cudaSuccess) return cuda_fail(e, "event");
+  return IDX_OK;
+}
+
+// The planes of a cache that is written, checked: their dtype (`nvfp4`: that one, else bf16
+// or e4m3), shape and heads, the outer scales.
+int check_pools(const idx_pool* k_pool, const idx_pool* v_pool, int kv_heads, bool nvfp4,
+                float k_outer, float v_outer) {
+  if (kv_heads < 1) return fail(IDX_ERR_INVALID, "kv_heads must be >= 1 (got %d)", kv_heads);
+  const int dtype = k_pool->dtype;
+  if (nvfp4 ? dtype != IDX_NVFP4 : dtype != IDX_BF16 && dtype != IDX_FP8_E4M3)
+    return fail(IDX_ERR_UNSUPPORTED, "this call writes %s pools (got dtype %d)",
+                nvfp4 ? "NVFP4" : "bf16 and e4m3", dtype);
+  if (!outer_ok(k_outer) || !outer_ok(v_outer))
+    return fail(IDX_ERR_INVALID, "outer scales must be powers of two in [2^-64, 2^64] (got %g, %g)",
+                (double)k_outer, (double)v_outer);
+  const idx_pool* pools[2] = {k_pool, v_pool};
+  for (const idx_pool* p : pools) {
+    if (!p) continue;
+    if (p->dtype != dtype || p->page_size != IDX_PAGE_SIZE || p->dim != IDX_DIM ||
+        p->payload_row_bytes != payload_row_bytes(dtype) ||
+        p->scale_row_bytes != scale_row_bytes(dtype) || p->num_pages != k_pool->num_pages)
+      return fail(IDX_ERR_INVALID,
+                  "the pools must have the same dtype and pages, 64-token pages and dim 128");
+    if (p->num_pages < 1 || p->num_pages % kv_heads != 0)
+      return fail(IDX_ERR_INVALID,
+                  "a pool of kv_heads heads holds a multiple of kv_heads head pages (got %lld, %d)",
+                  (long long)p->num_pages, kv_heads);
+  }
+  return IDX_OK;
+}
+
+// Their pointers, checked.
+int check_planes(const idx_pool* k_pool, const idx_pool* v_pool) {
+  for (const idx_pool* p : {k_pool, v_pool}) {
+    if (!p) continue;
+    if (!p->payload || (p->dtype != IDX_BF16 && !p->scale))
+      return fail(IDX_ERR_INVALID, "a pool's plane is NULL");
+    // (an NVFP4 row's eight scales are written at once)
+    if (!aligned(p->payload, 16) || !aligned(p->scale, p->dtype == IDX_NVFP4 ? 8 : 4))
+      return fail(IDX_ERR_INVALID, "payload planes must be 16-byte, scale planes %d-byte aligned",
+                  p->dtype == IDX_NVFP4 ? 8 : 4);
+  }
+  return IDX_OK;
+}
+
+// New keys (and values) into the cache: idx_store_kv and idx_store_kv_nvfp4.
+int store_impl(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
+               const int64_t* slot_mapping, int64_t num_tokens, int kv_heads,
+               const idx_pool* k_pool, const idx_pool* v_pool, float k_outer, float v_outer,
+               bool nvfp4, void* stream) {
+  if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
+  // (no tokens: an empty source's pointer may be NULL)
+  if (num_tokens != 0 && (v_src != nullptr) != (v_pool != nullptr))
+    return fail(IDX_ERR_INVALID, "v_src and v_pool come together or not at all");
+  int rc = check_pools(k_pool, v_pool, kv_heads, nvfp4, k_outer, v_outer);
+  if (rc != IDX_OK) return rc;
+  const int dtype = k_pool->dtype;
+  if (num_tokens < 0) return fail(IDX_ERR_INVALID, "num_tokens must be >= 0");
+  if (num_tokens == 0) return IDX_OK;
+  if (num_tokens > ((int64_t)1 << 34) / kv_heads / 2)
+    return fail(IDX_ERR_INVALID, "num_tokens too large");
+  if (!k_src || !slot_mapping) return fail(IDX_ERR_INVALID, "a required pointer is NULL");
+  if (k_stride < (int64_t)kv_heads * IDX_DIM || k_stride % 8 != 0 ||
+      (v_src && (v_stride < (int64_t)kv_heads * IDX_DIM || v_stride % 8 != 0)))
+    return fail(IDX_ERR_INVALID,
+                "token strides must be multiples of 8 elements and at least kv_heads * 128");
+  if (!aligned(k_src, 16) || !aligned(v_src, 16) || !aligned(slot_mapping, 8))
+    return fail(IDX_ERR_INVALID, "k_src and v_src must be 16-byte, slot_mapping 8-byte aligned");
+  rc = check_planes(k_pool, v_pool);
+  if (rc != IDX_OK) return rc;
+  idx::StoreArgs s;
+  s.src[0] = static_cast<const uint16_t*>(k_src);
+  s.src[1] = static_cast<const uint16_t*>(v_src);
+  s.stride[0] = k_stride;
+  s.stride[1] = v_stride;
+  s.payload[0] = static_cast<uint8_t*>(k_pool->payload);
+  s.payload[1] = v_pool ? static_cast<uint8_t*>(v_pool->payload) : nullptr;
+  s.scale[0] = k_pool->scale;
+  s.scale[1] = v_pool ? v_pool->scale : nullptr;
+  s.slots = slot_mapping;
+  s.tokens = num_tokens;
+  s.num_slots = k_pool->num_pages / kv_heads * IDX_PAGE_SIZE;
+  s.heads = kv_heads;
+  s.planes = v_pool ? 2 : 1;
+  s.up[0] = 1.f / k_outer;
+  s.up[1] = 1.f / v_outer;
+  const cudaError_t e = idx::launch_store_kv(dtype, s, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "launching the key-value store kernel");
   return IDX_OK;
 }
 
@@ -772,61 +882,16 @@ int idx_topk_merge(const int32_t* cand_ids, const float* cand_scores, int world,
 int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
                  const int64_t* slot_mapping, int64_t num_tokens, int kv_heads,
                  const idx_pool* k_pool, const idx_pool* v_pool, void* stream) {
-  if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
-  if ((v_src != nullptr) != (v_pool != nullptr))
-    return fail(IDX_ERR_INVALID, "v_src and v_pool come together or not at all");
-  if (kv_heads < 1) return fail(IDX_ERR_INVALID, "kv_heads must be >= 1 (got %d)", kv_heads);
-  const int dtype = k_pool->dtype;
-  if (dtype != IDX_BF16 && dtype != IDX_FP8_E4M3)
-    return fail(IDX_ERR_UNSUPPORTED, "the store writes bf16 and e4m3 pools (got dtype %d)", dtype);
-  const idx_pool* pools[2] = {k_pool, v_pool};
-  for (const idx_pool* p : pools) {
-    if (!p) continue;
-    if (p->dtype != dtype || p->page_size != IDX_PAGE_SIZE || p->dim != IDX_DIM ||
-        p->payload_row_bytes != payload_row_bytes(dtype) ||
-        p->scale_row_bytes != scale_row_bytes(dtype) || p->num_pages != k_pool->num_pages)
-      return fail(IDX_ERR_INVALID,
-                  "the pools must have the same dtype and pages, 64-token pages and dim 128");
-    if (p->num_pages < 1 || p->num_pages % kv_heads != 0)
-      return fail(IDX_ERR_INVALID,
-                  "a pool of kv_heads heads holds a multiple of kv_heads head pages (got %lld, %d)",
-                  (long long)p->num_pages, kv_heads);
-  }
-  if (num_tokens < 0) return fail(IDX_ERR_INVALID, "num_tokens must be >= 0");
-  if (num_tokens == 0) return IDX_OK;
-  if (num_tokens > ((int64_t)1 << 34) / kv_heads / 2)
-    return fail(IDX_ERR_INVALID, "num_tokens too large");
-  if (!k_src || !slot_mapping) return fail(IDX_ERR_INVALID, "a required pointer is NULL");
-  if (k_stride < (int64_t)kv_heads * IDX_DIM || k_stride % 8 != 0 ||
-      (v_src && (v_stride < (int64_t)kv_heads * IDX_DIM || v_stride % 8 != 0)))
-    return fail(IDX_ERR_INVALID,
-                "token strides must be multiples of 8 elements and at least kv_heads * 128");
-  if (!aligned(k_src, 16) || !aligned(v_src, 16) || !aligned(slot_mapping, 8))
-    return fail(IDX_ERR_INVALID, "k_src and v_src must be 16-byte, slot_mapping 8-byte aligned");
-  for (const idx_pool* p : pools) {
-    if (!p) continue;
-    if (!p->payload || (dtype == IDX_FP8_E4M3 && !p->scale))
-      return fail(IDX_ERR_INVALID, "a pool's plane is NULL");
-    if (!aligned(p->payload, 16) || !aligned(p->scale, 4))
-      return fail(IDX_ERR_INVALID, "payload planes must be 16-byte, scale planes 4-byte aligned");
-  }
-  idx::StoreArgs s;
-  s.src[0] = static_cast<const uint16_t*>(k_src);
-  s.src[1] = static_cast<const uint16_t*>(v_src);
-  s.stride[0] = k_stride;
-  s.stride[1] = v_stride;
-  s.payload[0] = static_cast<uint8_t*>(k_pool->payload);
-  s.payload[1] = v_pool ? static_cast<uint8_t*>(v_pool->payload) : nullptr;
-  s.scale[0] = static_cast<float*>(k_pool->scale);
-  s.scale[1] = v_pool ? static_cast<float*>(v_pool->scale) : nullptr;
-  s.slots = slot_mapping;
-  s.tokens = num_tokens;
-  s.num_slots = k_pool->num_pages / kv_heads * IDX_PAGE_SIZE;
-  s.heads = kv_heads;
-  s.planes = v_pool ? 2 : 1;
-  const cudaError_t e = idx::launch_store_kv(dtype, s, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "launching the key-value store kernel");
-  return IDX_OK;
+  return store_impl(k_src, v_src, k_stride, v_stride, slot_mapping, num_tokens, kv_heads, k_pool,
+                    v_pool, 1.f, 1.f, false, stream);
+}
+
+int idx_store_kv_nvfp4(const void* k_src, const void* v_src, int64_t k_stride, int64_t v_stride,
+                       const int64_t* slot_mapping, int64_t num_tokens, int kv_heads,
+                       const idx_pool* k_pool, const idx_pool* v_pool, float k_outer, float v_outer,
+                       void* stream) {
+  return store_impl(k_src, v_src, k_stride, v_stride, slot_mapping, num_tokens, kv_heads, k_pool,
+                    v_pool, k_outer, v_outer, true, stream);
 }
 
 size_t idx_attn_workspace_bytes(int packed_queries, int q_heads, int kv_heads, int lists) {
@@ -846,8 +911,8 @@ int idx_attn_paged(const void* q, const void* k_payload, const void* k_scale,
                    void* workspace, size_t workspace_bytes, void* stream) {
   return attn_impl(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, num_pages, kv_heads,
                    page_table, n_slots, max_pages, slot_ids, row_lens, false, nullptr, 0, 0,
-                   num_requests, packed_queries, q_heads, sm_scale, out, out_lse, workspace,
-                   workspace_bytes, stream);
+                   num_requests, packed_queries, q_heads, sm_scale, 1.f, 1.f, false, out, out_lse,
+                   workspace, workspace_bytes, stream);
 }
 
 int idx_attn_blocks(const void* q, const void* k_payload, const void* k_scale,
@@ -859,8 +924,130 @@ int idx_attn_blocks(const void* q, const void* k_payload, const void* k_scale,
                     size_t workspace_bytes, void* stream) {
   return attn_impl(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, num_pages, kv_heads,
                    page_table, n_slots, max_pages, slot_ids, row_lens, true, block_ids, lists, topk,
-                   num_requests, packed_queries, q_heads, sm_scale, out, out_lse, workspace,
-                   workspace_bytes, stream);
+                   num_requests, packed_queries, q_heads, sm_scale, 1.f, 1.f, false, out, out_lse,
+                   workspace, workspace_bytes, stream);
+}
+
+int idx_attn_paged_nvfp4(const void* q, const void* k_payload, const void* k_scale,
+                         const void* v_payload, const void* v_scale, int64_t num_pages,
+                         int kv_heads, const int32_t* page_table, int n_slots, int max_pages,
+                         const int32_t* slot_ids, const int32_t* row_lens, int num_requests,
+                         int packed_queries, int q_heads, float sm_scale, float k_outer,
+                         float v_outer, void* out, float* out_lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return attn_impl(q, k_payload, k_scale, v_payload, v_scale, IDX_NVFP4, num_pages, kv_heads,
+                   page_table, n_slots, max_pages, slot_ids, row_lens, false, nullptr, 0, 0,
+                   num_requests, packed_queries, q_heads, sm_scale, k_outer, v_outer, true, out,
+                   out_lse, workspace, workspace_bytes, stream);
+}
+
+int idx_attn_blocks_nvfp4(const void* q, const void* k_payload, const void* k_scale,
+                          const void* v_payload, const void* v_scale, int64_t num_pages,
+                          int kv_heads, const int32_t* page_table, int n_slots, int max_pages,
+                          const int32_t* slot_ids, const int32_t* row_lens,
+                          const int32_t* block_ids, int lists, int topk, int num_requests,
+                          int packed_queries, int q_heads, float sm_scale, float k_outer,
+                          float v_outer, void* out, float* out_lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return attn_impl(q, k_payload, k_scale, v_payload, v_scale, IDX_NVFP4, num_pages, kv_heads,
+                   page_table, n_slots, max_pages, slot_ids, row_lens, true, block_ids, lists, topk,
+                   num_requests, packed_queries, q_heads, sm_scale, k_outer, v_outer, true, out,
+                   out_lse, workspace, workspace_bytes, stream);
+}
+
+int idx_norm_rope_store(const void* q, int64_t q_stride, int q_heads, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, int kv_heads,
+                        const void* q_weight, const void* k_weight, float eps,
+                        const idx_rope* rope, const int64_t* slot_mapping, int64_t num_tokens,
+                        void* out_q, float* out_q_scale, const idx_pool* k_pool,
+                        const idx_pool* v_pool, float k_outer, float v_outer, void* stream) {
+  if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
+  // (no tokens: an empty tensor's pointer may be NULL)
+  if (num_tokens != 0 && (v != nullptr) != (v_pool != nullptr))
+    return fail(IDX_ERR_INVALID, "v and v_pool come together or not at all");
+  if (num_tokens != 0 && ((q != nullptr) != (out_q != nullptr) || (q != nullptr) != (q_heads > 0) ||
+                          (!q && out_q_scale)))
+    return fail(IDX_ERR_INVALID, "q, q_heads and out_q come together or not at all");
+  if (q_heads < 0 || q_heads > IDX_MAX_ROWS_PER_REQUEST || kv_heads > IDX_MAX_ROWS_PER_REQUEST)
+    return fail(IDX_ERR_INVALID, "head counts must be at most %d (got %d, %d)",
+                IDX_MAX_ROWS_PER_REQUEST, q_heads, kv_heads);
+  int rc = check_pools(k_pool, v_pool, kv_heads, k_pool->dtype == IDX_NVFP4, k_outer, v_outer);
+  if (rc != IDX_OK) return rc;
+  const int dtype = k_pool->dtype;
+  if (dtype != IDX_NVFP4 && (k_outer != 1.f || v_outer != 1.f))
+    return fail(IDX_ERR_INVALID, "outer scales other than 1 are for NVFP4 pools");
+  if (!(eps >= 0.f)) return fail(IDX_ERR_INVALID, "eps must be >= 0 (got %g)", (double)eps);
+  if (rope) {
+    if (rope->rotary_dim < 16 || rope->rotary_dim > IDX_DIM || rope->rotary_dim % 16 != 0)
+      return fail(IDX_ERR_INVALID, "rotary_dim must be a multiple of 16 in [16, %d] (got %d)", IDX_DIM,
+                  rope->rotary_dim);
+    if (rope->axes < 1 || rope->axes > IDX_MAX_ROPE_AXES)
+      return fail(IDX_ERR_INVALID, "axes must be in [1, %d] (got %d)", IDX_MAX_ROPE_AXES, rope->axes);
+    if (rope->num_positions < 1 || rope->num_positions > 0x7fffffffLL)
+      return fail(IDX_ERR_INVALID, "num_positions must be in [1, 2^31) (got %lld)",
+                  (long long)rope->num_positions);
+    for (int i = 0; rope->axes > 1 && i < rope->rotary_dim / 2; ++i)
+      if (rope->pair_axis[i] >= rope->axes)
+        return fail(IDX_ERR_INVALID, "pair %d goes by axis %d of %d", i, rope->pair_axis[i], rope->axes);
+  }
+  if (num_tokens < 0) return fail(IDX_ERR_INVALID, "num_tokens must be >= 0");
+  if (num_tokens == 0) return IDX_OK;
+  const int rows = q_heads + kv_heads * (v ? 2 : 1);
+  if (num_tokens > ((int64_t)1 << 34) / rows) return fail(IDX_ERR_INVALID, "num_tokens too large");
+  if (!k || !slot_mapping || (rope && (!rope->table || !rope->positions)))
+    return fail(IDX_ERR_INVALID, "a required pointer is NULL");
+  auto stride_ok = [](const void* p, int64_t stride, int heads) {
+    return !p || (stride >= (int64_t)heads * IDX_DIM && stride % 8 == 0);
+  };
+  if (!stride_ok(q, q_stride, q_heads) || !stride_ok(k, k_stride, kv_heads) ||
+      !stride_ok(v, v_stride, kv_heads))
+    return fail(IDX_ERR_INVALID,
+                "token strides must be multiples of 8 elements and at least heads * 128");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out_q, 16) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(out_q_scale, 4) || (rope && (!aligned(rope->table, 16) || !aligned(rope->positions, 4))))
+    return fail(IDX_ERR_INVALID,
+                "q, k, v, out_q, the weights and the table must be 16-byte, slot_mapping 8-byte, "
+                "out_q_scale and positions 4-byte aligned");
+  rc = check_planes(k_pool, v_pool);
+  if (rc != IDX_OK) return rc;
+  idx::RopeArgs a = {};
+  a.src[0] = static_cast<const uint16_t*>(q);
+  a.src[1] = static_cast<const uint16_t*>(k);
+  a.src[2] = static_cast<const uint16_t*>(v);
+  a.stride[0] = q ? q_stride : 0;
+  a.stride[1] = k_stride;
+  a.stride[2] = v ? v_stride : 0;
+  a.weight[0] = static_cast<const uint16_t*>(q_weight);
+  a.weight[1] = static_cast<const uint16_t*>(k_weight);
+  a.payload[0] = static_cast<uint8_t*>(k_pool->payload);
+  a.payload[1] = v_pool ? static_cast<uint8_t*>(v_pool->payload) : nullptr;
+  a.scale[0] = k_pool->scale;
+  a.scale[1] = v_pool ? v_pool->scale : nullptr;
+  a.up[0] = 1.f / k_outer;
+  a.up[1] = 1.f / v_outer;
+  a.slots = slot_mapping;
+  a.out_q = out_q;
+  a.out_q_scale = out_q_scale;
+  a.tokens = num_tokens;
+  a.num_slots = k_pool->num_pages / kv_heads * IDX_PAGE_SIZE;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.rows = rows;
+  a.eps = eps;
+  if (rope) {
+    a.table = rope->table;
+    a.positions = rope->positions;
+    a.num_positions = (int)rope->num_positions;
+    a.rotary_dim = rope->rotary_dim;
+    a.interleaved = rope->interleaved != 0;
+    a.axes = rope->axes;
+    for (int i = 0; rope->axes > 1 && i < rope->rotary_dim / 2; ++i)
+      a.pair_axis[i / 16] |= (uint32_t)rope->pair_axis[i] << (2 * (i % 16));
+  }
+  const cudaError_t e = idx::launch_norm_rope_store(dtype, a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "launching the norm, rotation and store kernel");
+  return IDX_OK;
 }
 
 int idx_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual,

@@ -51,7 +51,7 @@ struct Divisor {
 struct AttnArgs {
   const uint16_t* q;           // bf16 [R][P][q_heads][128]
   const uint8_t* k_payload;    // plane rows (page * kv_heads + head) * 64 + token % 64
-  const float* k_scale;        // one a row (fp8) or nullptr
+  const float* k_scale;        // one a row (fp8), 8 E4M3 bytes a row (NVFP4), or nullptr
   const uint8_t* v_payload;
   const float* v_scale;
   const int32_t* page_table;   // [n_slots][max_pages]
@@ -78,7 +78,8 @@ struct AttnArgs {
   int shift;                   // pieces of a position: 2^shift
   int unit_cost;               // positions that stand for a unit's end
   float dealt_ends, dealt_piece;  // estimate of units dealt whole (up to 16 rows, no lists)
-  float scale_log2;            // softmax scale times log2(e)
+  float scale_log2;            // softmax scale (NVFP4: times the keys' outer scale) times log2(e)
+  float out_scale;             // the values' outer scale (NVFP4), or 1
   unsigned long long wait_ns;
   int stall_test;
 };

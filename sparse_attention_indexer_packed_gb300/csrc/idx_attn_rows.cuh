@@ -289,6 +289,15 @@ __device__ __forceinline__ float4 plane_f32(const uint8_t* payload, const float*
     const uint2 u = __ldg(reinterpret_cast<const uint2*>(payload + row * 256) + lane);
     return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
   }
+  if (KF == kNvfp4) {   // without the outer scale
+    uint32_t d[4], s, unused;
+    e2m1x8_to_f16x2x4(__ldg(reinterpret_cast<const uint16_t*>(payload + row * 64) + lane), d);
+    e4m3x4_to_f16x2x2(__ldg(reinterpret_cast<const uint8_t*>(scale) + row * 8 + lane / 4), s, unused);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&d[0]));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&d[1]));
+    const float f = __half22float2(*reinterpret_cast<const __half2*>(&s)).x;
+    return make_float4(x.x * f, x.y * f, y.x * f, y.y * f);
+  }
   uint32_t lo, hi;
   e4m3x4_to_f16x2x2(__ldg(reinterpret_cast<const uint32_t*>(payload + row * 128) + lane), lo, hi);
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
@@ -405,7 +414,7 @@ __device__ __forceinline__ bool finite4(float4 o) {
 // Write a finished row: lane = four dims.
 __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, float m, float l, float4 o,
                                           int lane) {
-  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  const float inv = m == -INFINITY ? 0.f : a.out_scale / l;
   uint2 u;
   u.x = m == -INFINITY ? 0u : pack_bf16(o.x * inv, o.y * inv);
   u.y = m == -INFINITY ? 0u : pack_bf16(o.z * inv, o.w * inv);

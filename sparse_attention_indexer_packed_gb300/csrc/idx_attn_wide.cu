@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         const float f1 = ex2_approx((KF == kFp8 ? e1.z : e1.x) - ref);
         const bool complete = s.o0 == 0 && s.o1 == s.cap;
         const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
-        const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+        const float inv = M == -INFINITY ? 0.f : a.out_scale / sum;
         bool odd = false;
 #pragma unroll 1
         for (int ch = g * (kDim / 2); ch < (g + 1) * (kDim / 2); ch += 32) {

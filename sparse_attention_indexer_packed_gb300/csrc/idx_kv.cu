@@ -2,7 +2,8 @@
 //
 // What it computes: token i of head h goes to plane row
 // (slot / 64 * heads + h) * 64 + slot % 64 of the keys' and the values' plane.
-// bf16 planes take the bits; e4m3 planes take codes and one fp32 scale a row
+// bf16 planes take the bits; NVFP4 planes codes and a scale for each 16 elements
+// (idx_rows.cuh); e4m3 planes take codes and one fp32 scale a row
 // (the rule in idx_ops.cuh; the reciprocal and the products are single fp32
 // roundings, so the stored bytes are the same wherever they are computed).
 //
@@ -19,6 +20,7 @@
 
 #include "idx_internal.cuh"
 #include "idx_ops.cuh"
+#include "idx_rows.cuh"
 
 namespace idx {
 
@@ -64,6 +66,12 @@ __global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int ch
       if (write) reinterpret_cast<uint4*>(payload + r * 256)[lane] = u[j];
       continue;
     }
+    if (KF == kNvfp4) {
+      float x[8];
+      bf16x8_to_f32(u[j], x);
+      put_row<kNvfp4>(x, plane ? a.up[1] : a.up[0], payload, plane ? a.scale[1] : a.scale[0], r, lane, write);
+      continue;
+    }
     const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
     // the row's largest magnitude on bf16 pairs, a NaN kept
     __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(magnitudes(w[0]), magnitudes(w[1])),
@@ -79,7 +87,7 @@ __global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int ch
       c[e] = e4m3x2(__fmul_rn(__uint_as_float(w[e] << 16), up),
                     __fmul_rn(__uint_as_float(w[e] & 0xffff0000u), up));
     reinterpret_cast<uint2*>(payload + r * 128)[lane] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    if (lane == 0) (plane ? a.scale[1] : a.scale[0])[r] = __fdiv_rn(amax, kE4m3Max);
+    if (lane == 0) static_cast<float*>(plane ? a.scale[1] : a.scale[0])[r] = __fdiv_rn(amax, kE4m3Max);
   }
 }
 
@@ -97,7 +105,9 @@ cudaError_t launch(const StoreArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_store_kv(int key_format, const StoreArgs& a, cudaStream_t stream) {
-  const cudaError_t e = key_format == kBf16 ? launch<kBf16>(a, stream) : launch<kFp8>(a, stream);
+  const cudaError_t e = key_format == kBf16   ? launch<kBf16>(a, stream)
+                        : key_format == kFp8 ? launch<kFp8>(a, stream)
+                                             : launch<kNvfp4>(a, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -48,11 +48,34 @@ struct StoreArgs {
   const uint16_t* src[2];    // bf16 keys / values [tokens][heads][128]
   long long stride[2];       // elements between tokens
   uint8_t* payload[2];
-  float* scale[2];
+  void* scale[2];            // fp32 a row, or 8 E4M3 bytes a row (NVFP4)
+  float up[2];               // 1 / the planes' outer scales (NVFP4)
   const int64_t* slots;      // [tokens]: page * 64 + offset
   long long tokens, num_slots;
   int heads, planes;
 };
 cudaError_t launch_store_kv(int key_format, const StoreArgs& args, cudaStream_t stream);
+
+// Queries, keys and values of new tokens: norm and rotation, then the keys and values
+// into the cache (planes 0 and 1 as for the store).
+struct RopeArgs {
+  const uint16_t* src[3];    // bf16 q, k, v [tokens][heads][128]; q, v may be nullptr
+  long long stride[3];       // elements between tokens
+  const uint16_t* weight[2]; // bf16 [128] of the queries', the keys' norm; nullptr: no norm
+  uint8_t* payload[2];
+  void* scale[2];
+  float up[2];
+  const int64_t* slots;
+  void* out_q;               // [tokens][q_heads][128]: bf16, or e4m3 codes
+  float* out_q_scale;        // [tokens][q_heads] with e4m3 codes, else nullptr
+  const float* table;        // [num_positions][rotary_dim]: cosines, then sines; or nullptr
+  const int32_t* positions;  // [axes][tokens]
+  uint32_t pair_axis[4];     // axis of pair i: bits 2 (i % 16) of word i / 16
+  long long tokens, num_slots;
+  int q_heads, kv_heads, rows;   // rows of a token: q_heads and one or two times kv_heads
+  int num_positions, rotary_dim, interleaved, axes;
+  float eps;
+};
+cudaError_t launch_norm_rope_store(int key_format, const RopeArgs& args, cudaStream_t stream);
 
 }  // namespace idx

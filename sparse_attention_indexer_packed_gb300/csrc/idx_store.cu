@@ -12,60 +12,19 @@
 // rounded fp32 quotient x / scale; a negative value that rounds to zero keeps
 // its sign.
 //
-// The codes come from the hardware e2m1 conversion (round to nearest, ties to
-// the even code, saturating at 6, the sign kept) of a quotient q2 that equals
-// x / s where that is on the e2m1 grid's midpoints and is within two ulps of it
-// elsewhere: q1 = x * r with r = 1 / s, the residual e = x - q1 * s (exact in
-// one fma), q2 = q1 + e * r (one correction step of a reciprocal-based
-// quotient, after Markstein, "IA-64 and Elementary Functions", 2000).  This is
-// enough: every midpoint t of the grid has at most three significant bits and
-// s at most four, so t * s is a bf16 value, and a bf16 x either equals t * s
-// (then the residual is exact and q2 = t) or lies a bf16 spacing away from it,
-// far beyond the quotient's error, on the same side as fl(x / s).
+// (How the codes are found without a division each: idx_rows.cuh.)
 //
 // One thread per (key, group of 16): eight threads cover a key, a warp four.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
-#include <string.h>
 
 #include "idx_internal.cuh"
+#include "idx_rows.cuh"
 
 namespace idx {
 
 namespace {
-
-// Value of an E4M3 byte with the sign bit clear (scales are never negative):
-// exponent field 0 -> m * 2^-9; otherwise (8 + m) * 2^(e - 10).
-__device__ __forceinline__ float e4m3_magnitude(uint32_t b) {
-  const uint32_t e = (b >> 3) & 0xfu, m = b & 7u;
-  if (e == 0) return (float)m * 0.001953125f;
-  return __uint_as_float(((e + 120u) << 23) | (m << 20));
-}
-
-__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t u) {
-  __nv_bfloat162 v;
-  memcpy(&v, &u, sizeof(v));
-  return v;
-}
-
-// x / s on the e2m1 midpoints, within two ulps elsewhere (see above), with
-// x's sign (the fma steps would turn -0 into +0).
-__device__ __forceinline__ float grid_quotient(float x, float s, float r) {
-  const float q1 = x * r;
-  return copysignf(fmaf(fmaf(-q1, s, x), r, q1), x);
-}
-
-// Byte of two e2m1 codes: the code of lo in the low nibble, of hi in the high.
-__device__ __forceinline__ uint32_t e2m1x2_byte(float lo, float hi) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
-      : "=r"(d)
-      : "f"(hi), "f"(lo));
-  return d;
-}
 
 // Quantise one group (its 16 bf16 values in w) and write it.
 __device__ __forceinline__ void store_group(const uint32_t (&w)[8], int64_t row, int grp,
