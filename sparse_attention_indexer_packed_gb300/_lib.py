@@ -698,11 +698,12 @@ def idx_add_rmsnorm_fp8(x, residual, weight, eps: float, group: int, out, out_sc
         _check(rc, "idx_add_rmsnorm_fp8")
 
 
-NATIVE_CALLS = ("idx_attn_paged", "idx_attn_blocks", "idx_store_kv", "idx_add_rmsnorm_fp8")
+NATIVE_CALLS = ("idx_attn_paged", "idx_attn_blocks", "idx_store_kv", "idx_add_rmsnorm_fp8",
+                "idx_attn_paged_nvfp4", "idx_attn_blocks_nvfp4", "idx_store_kv_nvfp4", "idx_norm_rope_store")
 
 
 def _native_calls():
-    """The four small-call operators of the CPython module, or these functions themselves
+    """The small-call operators of the CPython module, or these functions themselves
     where it has not been built (or torch lacks the bare stream call): the same checks and
     the same library calls, slower on the host."""
     here = tuple(globals()[name] for name in NATIVE_CALLS)
