@@ -628,6 +628,8 @@ int store_impl(const void* k_src, const void* v_src, int64_t k_stride, int64_t v
   s.num_slots = k_pool->num_pages / kv_heads * IDX_PAGE_SIZE;
   s.heads = kv_heads;
   s.planes = v_pool ? 2 : 1;
+  s.outer[0] = k_outer;
+  s.outer[1] = v_outer;
   s.up[0] = 1.f / k_outer;
   s.up[1] = 1.f / v_outer;
   const cudaError_t e = idx::launch_store_kv(dtype, s, static_cast<cudaStream_t>(stream));
@@ -1024,6 +1026,8 @@ int idx_norm_rope_store(const void* q, int64_t q_stride, int q_heads, const void
   a.payload[1] = v_pool ? static_cast<uint8_t*>(v_pool->payload) : nullptr;
   a.scale[0] = k_pool->scale;
   a.scale[1] = v_pool ? v_pool->scale : nullptr;
+  a.outer[0] = k_outer;
+  a.outer[1] = v_outer;
   a.up[0] = 1.f / k_outer;
   a.up[1] = 1.f / v_outer;
   a.slots = slot_mapping;

@@ -11,27 +11,6 @@
 namespace idx {
 namespace attn {
 
-// Two fp32 sums, or fused multiply-adds, in one instruction (see fmul2_rn).
-__device__ __forceinline__ float2 fadd2_rn(float2 a, float2 b) {
-  unsigned long long pa, pb, pd;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(pa) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(pb) : "f"(b.x), "f"(b.y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(pd) : "l"(pa), "l"(pb));
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(pd));
-  return d;
-}
-__device__ __forceinline__ float2 ffma2_rn(float2 a, float2 b, float2 c) {
-  unsigned long long pa, pb, pc, pd;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(pa) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(pb) : "f"(b.x), "f"(b.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(pc) : "f"(c.x), "f"(c.y));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pd) : "l"(pa), "l"(pb), "l"(pc));
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(pd));
-  return d;
-}
-
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxList = kMaxTopk * kMaxDrafts;  // joined block list of a group
 constexpr int kMaxBlockWords = 65536 / 2 / 32;   // bits for every block of a request

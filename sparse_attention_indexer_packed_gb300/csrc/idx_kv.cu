@@ -66,12 +66,6 @@ __global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int ch
       if (write) reinterpret_cast<uint4*>(payload + r * 256)[lane] = u[j];
       continue;
     }
-    if (KF == kNvfp4) {
-      float x[8];
-      bf16x8_to_f32(u[j], x);
-      put_row<kNvfp4>(x, plane ? a.up[1] : a.up[0], payload, plane ? a.scale[1] : a.scale[0], r, lane, write);
-      continue;
-    }
     const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
     // the row's largest magnitude on bf16 pairs, a NaN kept
     __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(magnitudes(w[0]), magnitudes(w[1])),
@@ -91,6 +85,65 @@ __global__ void __launch_bounds__(256) store_kv_kernel(const StoreArgs a, int ch
   }
 }
 
+// NVFP4: a lane holds a group of 16, so that its scale's divisions are made once; 8 lanes a
+// row.  (8 elements a lane, 16 lanes a row: 22.0 us on 32,001 tokens x 4 heads.)
+template <int kTokens>
+__global__ void __launch_bounds__(256) store_kv4_kernel(const StoreArgs a, int chunks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int hp = blockIdx.x / chunks, chunk = blockIdx.x - hp * chunks;
+  const int plane = hp >= a.heads, h = hp - (plane ? a.heads : 0);
+  const int lane = threadIdx.x & 7;
+  const uint16_t* src = (plane ? a.src[1] : a.src[0]) + h * kDim;
+  const long long stride = plane ? a.stride[1] : a.stride[0];
+  uint8_t* payload = plane ? a.payload[1] : a.payload[0];
+  uint8_t* scale = static_cast<uint8_t*>(plane ? a.scale[1] : a.scale[0]);
+  const float outer = plane ? a.outer[1] : a.outer[0], up = plane ? a.up[1] : a.up[0];
+  const long long tok0 = (long long)chunk * (2 * kRowsAtOnce * kTokens) + threadIdx.x / 8;
+  uint4 u[kTokens][2];
+  long long row[kTokens];
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    const long long tok = tok0 + j * 2 * kRowsAtOnce;
+    u[j][0] = u[j][1] = make_uint4(0, 0, 0, 0);
+    row[j] = -1;
+    if (tok < a.tokens) {
+      const uint4* p = reinterpret_cast<const uint4*>(src + tok * stride) + 2 * lane;
+      u[j][0] = __ldcs(p);
+      u[j][1] = __ldcs(p + 1);
+      row[j] = __ldg(reinterpret_cast<const long long*>(a.slots) + tok);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTokens; ++j) {
+    const unsigned long long slot = (unsigned long long)row[j];   // negative: past every slot
+    if (slot >= (unsigned long long)a.num_slots) continue;
+    const unsigned long long r = ((slot >> 6) * a.heads + h) * kPage + (slot & (kPage - 1));
+    const uint32_t w[8] = {u[j][0].x, u[j][0].y, u[j][0].z, u[j][0].w, u[j][1].x, u[j][1].y, u[j][1].z, u[j][1].w};
+    // the group's largest magnitude on bf16 pairs, a NaN kept
+    __nv_bfloat162 m2 = magnitudes(w[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) m2 = __hmax2_nan(m2, magnitudes(w[e]));
+    const float m = fmax_nan(__low2float(m2), __high2float(m2)) * up;
+    float2 neg_x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) neg_x[e] = neg_bf16x2(w[e]);
+    const uint32_t s_code = nvfp4_scale(m);
+    uint32_t c[2];
+    nvfp4_codes(neg_x, s_code, m, outer, up, c);
+    reinterpret_cast<uint2*>(payload + r * 64)[lane] = make_uint2(c[0], c[1]);
+    scale[r * 8 + lane] = (uint8_t)s_code;
+  }
+}
+
+cudaError_t launch4(const StoreArgs& a, cudaStream_t stream) {
+  const bool many = a.tokens * a.heads * a.planes >= 16384;
+  const int per = 2 * kRowsAtOnce * (many ? 2 : 1);
+  const int chunks = (int)((a.tokens + per - 1) / per);
+  const int grid = chunks * a.heads * a.planes;
+  return many ? launch_pdl(store_kv4_kernel<2>, grid, 256, 0, stream, a, chunks)
+              : launch_pdl(store_kv4_kernel<1>, grid, 256, 0, stream, a, chunks);
+}
+
 template <int KF>
 cudaError_t launch(const StoreArgs& a, cudaStream_t stream) {
   // four rows a thread once that still gives every SM a CTA or two
@@ -107,7 +160,7 @@ cudaError_t launch(const StoreArgs& a, cudaStream_t stream) {
 cudaError_t launch_store_kv(int key_format, const StoreArgs& a, cudaStream_t stream) {
   const cudaError_t e = key_format == kBf16   ? launch<kBf16>(a, stream)
                         : key_format == kFp8 ? launch<kFp8>(a, stream)
-                                             : launch<kNvfp4>(a, stream);
+                                             : launch4(a, stream);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

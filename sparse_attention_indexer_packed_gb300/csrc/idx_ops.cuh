@@ -49,7 +49,7 @@ struct StoreArgs {
   long long stride[2];       // elements between tokens
   uint8_t* payload[2];
   void* scale[2];            // fp32 a row, or 8 E4M3 bytes a row (NVFP4)
-  float up[2];               // 1 / the planes' outer scales (NVFP4)
+  float outer[2], up[2];     // the planes' outer scales (NVFP4), and 1 / them
   const int64_t* slots;      // [tokens]: page * 64 + offset
   long long tokens, num_slots;
   int heads, planes;
@@ -64,7 +64,7 @@ struct RopeArgs {
   const uint16_t* weight[2]; // bf16 [128] of the queries', the keys' norm; nullptr: no norm
   uint8_t* payload[2];
   void* scale[2];
-  float up[2];
+  float outer[2], up[2];
   const int64_t* slots;
   void* out_q;               // [tokens][q_heads][128]: bf16, or e4m3 codes
   float* out_q_scale;        // [tokens][q_heads] with e4m3 codes, else nullptr

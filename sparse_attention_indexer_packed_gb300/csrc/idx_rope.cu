@@ -26,55 +26,86 @@ namespace {
 
 constexpr int kTokens = 16;   // of a 256-thread CTA, a half warp each
 
-// kRows rows of a token a half warp: their loads all go out before any is used, and the
-// token's cosines and sines are loaded once for them.
+// The rows of a token in chunks of kRows: the queries', the keys', the values'.
+struct Chunks {
+  int q, k, all;
+};
+
+// kRows rows of one kind of a token a half warp: their loads all go out before any is used,
+// and what the rows are multiplied by, cos and sin times the norm's weights, is made once
+// for them: out = rstd (x A + y B), y the other half of x's pair.
 template <int KF, int kRows>
-__global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, int chunks) {
+__global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, Chunks chunks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int chunk = blockIdx.x % chunks, lane = threadIdx.x & 15;
-  const long long want = (long long)(blockIdx.x / chunks) * kTokens + threadIdx.x / 16;
+  int chunk = blockIdx.x % chunks.all;
+  const int lane = threadIdx.x & 15;
+  const long long want = (long long)(blockIdx.x / chunks.all) * kTokens + threadIdx.x / 16;
   const bool live = want < a.tokens;     // lanes past the last token only take part in the shuffles
   const long long tok = live ? want : a.tokens - 1;
-  const int first = chunk * kRows;
+  const int kind = chunk < chunks.q ? 0 : chunk < chunks.k ? 1 : 2;
+  chunk -= kind == 0 ? 0 : kind == 1 ? chunks.q : chunks.k;
+  const int heads = kind ? a.kv_heads : a.q_heads, first = chunk * kRows;
+  const uint16_t* src = (kind == 0 ? a.src[0] + tok * a.stride[0]
+                         : kind == 1 ? a.src[1] + tok * a.stride[1] : a.src[2] + tok * a.stride[2]) + first * kDim;
   uint4 u[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
-    const int row = first + j;
     u[j] = make_uint4(0, 0, 0, 0);
-    if (row < a.rows) {
-      const int kind = row < a.q_heads ? 0 : row < a.q_heads + a.kv_heads ? 1 : 2;
-      const int head = row - (kind == 0 ? 0 : kind == 1 ? a.q_heads : a.q_heads + a.kv_heads);
-      const uint16_t* src = kind == 0 ? a.src[0] : kind == 1 ? a.src[1] : a.src[2];
-      const long long stride = kind == 0 ? a.stride[0] : kind == 1 ? a.stride[1] : a.stride[2];
-      u[j] = __ldcs(reinterpret_cast<const uint4*>(src + tok * stride + head * kDim) + lane);
-    }
+    if (first + j < heads) u[j] = __ldcs(reinterpret_cast<const uint4*>(src + j * kDim) + lane);
   }
-  unsigned long long slot = ~0ull;
-  if (first + kRows > a.q_heads) slot = (unsigned long long)__ldg(reinterpret_cast<const long long*>(a.slots) + tok);
+  unsigned long long at0, at_step;       // output row of the chunk's first row; to the next
+  bool write = live;
+  if (kind == 0) {
+    at0 = (unsigned long long)tok * a.q_heads + first;
+    at_step = 1;
+  } else {
+    const unsigned long long slot = (unsigned long long)__ldg(reinterpret_cast<const long long*>(a.slots) + tok);
+    write = live && slot < (unsigned long long)a.num_slots;   // negative: past every slot
+    at0 = ((slot >> 6) * a.kv_heads + first) * kPage + (slot & (kPage - 1));
+    at_step = kPage;
+  }
+  uint8_t* payload = kind == 1 ? a.payload[0] : a.payload[1];
+  void* scale = kind == 1 ? a.scale[0] : a.scale[1];
+  const float outer = kind == 1 ? a.outer[0] : a.outer[1], up = kind == 1 ? a.up[0] : a.up[1];
+  if (kind == 2) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (first + j >= heads) break;
+      if (KF == kBf16) {
+        if (write) reinterpret_cast<uint4*>(payload + (at0 + j * at_step) * 256)[lane] = u[j];
+        continue;
+      }
+      float x[8];
+      bf16x8_to_f32(u[j], x);
+      put_row<KF>(x, outer, up, payload, scale, at0 + j * at_step, lane, write);
+    }
+    return;
+  }
 
-  // cos and sin of the lane's eight elements; the sine negative for a pair's first
-  float c[8], s[8];
+  // A and B of the lane's eight elements
+  const uint16_t* weight = kind ? a.weight[1] : a.weight[0];
   const int half = a.rotary_dim / 2;
-  const bool turned = lane * 8 < a.rotary_dim && first < a.q_heads + a.kv_heads;
-  int other = lane;                      // the lane with the other halves of the lane's pairs
+  const bool turned = lane * 8 < a.rotary_dim;
+  const bool second = !a.interleaved && lane * 8 >= half;
+  // the lane with the other halves of the lane's pairs
+  const int other = !turned || a.interleaved ? lane : second ? lane - half / 8 : lane + half / 8;
+  float A[8], B[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) A[e] = 1.f, B[e] = 0.f;
   if (turned) {
-    const bool second = !a.interleaved && lane * 8 >= half;
     const int pair0 = a.interleaved ? lane * 4 : lane * 8 - (second ? half : 0);
-    if (!a.interleaved) other = second ? lane - half / 8 : lane + half / 8;
     const float nan = __int_as_float(0x7fffffff);
-    const int n = a.interleaved ? 4 : 8;
     // axes of the lane's pairs, two bits each (pair0 is a multiple of four, or of eight)
     const uint32_t axes = a.axes > 1 ? a.pair_axis[pair0 / 16] >> (2 * (pair0 % 16)) : 0u;
-    const uint32_t same = (axes & 3u) * 0x5555u;
-    const uint32_t mask = n == 8 ? 0xffffu : 0xffu;
+    const uint32_t mask = a.interleaved ? 0xffu : 0xffffu;
     float cs[8], sn[8];
-    if (((axes ^ same) & mask) == 0u) {
+    if (((axes ^ ((axes & 3u) * 0x5555u)) & mask) == 0u) {
       const int p = __ldg(a.positions + (long long)(axes & 3u) * a.tokens + tok);
       const bool ok = p >= 0 && p < a.num_positions;
       const float* t = a.table + (long long)(ok ? p : 0) * a.rotary_dim + pair0;
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
-        if (e >= n) break;
+        if (e == 4 && a.interleaved) break;
         const float4 x = __ldg(reinterpret_cast<const float4*>(t + e));
         const float4 z = __ldg(reinterpret_cast<const float4*>(t + half + e));
         cs[e] = ok ? x.x : nan, cs[e + 1] = ok ? x.y : nan, cs[e + 2] = ok ? x.z : nan, cs[e + 3] = ok ? x.w : nan;
@@ -83,7 +114,7 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (e >= n) break;
+        if (e == 4 && a.interleaved) break;
         const int p = __ldg(a.positions + (long long)((axes >> (2 * e)) & 3u) * a.tokens + tok);
         const bool ok = p >= 0 && p < a.num_positions;
         const float* t = a.table + (long long)(ok ? p : 0) * a.rotary_dim + pair0 + e;
@@ -93,74 +124,71 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      c[e] = a.interleaved ? cs[e / 2] : cs[e];
-      s[e] = a.interleaved ? ((e & 1) ? sn[e / 2] : -sn[e / 2]) : second ? sn[e] : -sn[e];
+      A[e] = a.interleaved ? cs[e / 2] : cs[e];
+      B[e] = a.interleaved ? ((e & 1) ? sn[e / 2] : -sn[e / 2]) : second ? sn[e] : -sn[e];
     }
-  } else {
+  }
+  if (weight) {
+    float w[8], v[8];
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(weight) + lane), w);
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(weight) + other), v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+    for (int e = 0; e < 8; ++e) A[e] *= w[e], B[e] *= a.interleaved ? w[e ^ 1] : v[e];
   }
 
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
-    const int row = first + j;
-    if (row >= a.rows) break;
-    const int kind = row < a.q_heads ? 0 : row < a.q_heads + a.kv_heads ? 1 : 2;
-    const int head = row - (kind == 0 ? 0 : kind == 1 ? a.q_heads : a.q_heads + a.kv_heads);
+    if (first + j >= heads) break;
     float x[8];
     bf16x8_to_f32(u[j], x);
-    if (kind < 2) {
-      const uint16_t* weight = kind ? a.weight[1] : a.weight[0];
-      if (weight) {
-        float w[8], sum = 0.f;
-        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(weight) + lane), w);
+    float rstd = 1.f;
+    if (weight) {
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int e = 0; e < 8; e += 2) sum = ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), sum);
+      float all = sum.x + sum.y;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float rstd = rsqrtf(sum / (float)kDim + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * w[e];
-      }
-      if (a.table) {
-        float y[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], other, 16);
-        }
-        if (turned) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], c[e], y[e] * s[e]);
-        }
-      }
+      for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      rstd = rsqrtf(fmaf(all, 1.f / kDim, a.eps));
     }
-    if (kind == 0) {
-      const unsigned long long at = (unsigned long long)tok * a.q_heads + head;
-      if (a.out_q_scale)
-        put_row<kFp8>(x, 1.f, static_cast<uint8_t*>(a.out_q), a.out_q_scale, at, lane, live);
-      else
-        put_row<kBf16>(x, 1.f, static_cast<uint8_t*>(a.out_q), nullptr, at, lane, live);
-    } else {
-      const bool write = live && slot < (unsigned long long)a.num_slots;   // negative: past every slot
-      const unsigned long long at = ((slot >> 6) * a.kv_heads + head) * kPage + (slot & (kPage - 1));
-      put_row<KF>(x, kind == 1 ? a.up[0] : a.up[1], kind == 1 ? a.payload[0] : a.payload[1],
-                  kind == 1 ? a.scale[0] : a.scale[1], at, lane, write);
+    float y[8];
+    if (a.table) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = a.interleaved ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], other, 16);
     }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float2 z = fmul2_rn(make_float2(x[e], x[e + 1]), make_float2(A[e], A[e + 1]));
+      if (turned) z = ffma2_rn(make_float2(y[e], y[e + 1]), make_float2(B[e], B[e + 1]), z);
+      z = fmul2_rn(z, make_float2(rstd, rstd));
+      x[e] = z.x, x[e + 1] = z.y;
+    }
+    const unsigned long long at = at0 + j * at_step;
+    if (kind == 1)
+      put_row<KF>(x, outer, up, payload, scale, at, lane, write);
+    else if (a.out_q_scale)
+      put_row<kFp8>(x, 1.f, 1.f, static_cast<uint8_t*>(a.out_q), a.out_q_scale, at, lane, write);
+    else
+      put_row<kBf16>(x, 1.f, 1.f, static_cast<uint8_t*>(a.out_q), nullptr, at, lane, write);
   }
+}
+
+template <int KF, int kRows>
+cudaError_t launch_rows(const RopeArgs& a, cudaStream_t stream) {
+  auto chunks_of = [](int rows) { return (rows + kRows - 1) / kRows; };
+  Chunks c;
+  c.q = chunks_of(a.q_heads);
+  c.k = c.q + chunks_of(a.kv_heads);
+  c.all = c.k + (a.src[2] ? chunks_of(a.kv_heads) : 0);
+  const int grid = (int)((a.tokens + kTokens - 1) / kTokens * c.all);
+  return launch_pdl(norm_rope_store_kernel<KF, kRows>, grid, 256, 0, stream, a, c);
 }
 
 template <int KF>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   // four rows a half warp once that still gives every SM a CTA or two
   const long long groups = (a.tokens + kTokens - 1) / kTokens;
-  const bool many = groups * a.rows >= 152 * 8;
-  const int per = many ? 4 : 1, chunks = (a.rows + per - 1) / per;
-  const int grid = (int)(groups * chunks);
-  return many ? launch_pdl(norm_rope_store_kernel<KF, 4>, grid, 256, 0, stream, a, chunks)
-              : launch_pdl(norm_rope_store_kernel<KF, 1>, grid, 256, 0, stream, a, chunks);
+  return groups * a.rows >= 152 * 8 ? launch_rows<KF, 4>(a, stream) : launch_rows<KF, 1>(a, stream);
 }
 
 }  // namespace

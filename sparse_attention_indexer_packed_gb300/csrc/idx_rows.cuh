@@ -9,6 +9,7 @@
 
 #include "idx_internal.cuh"
 #include "idx_ops.cuh"
+#include "idx_ptx.cuh"
 
 namespace idx {
 
@@ -39,32 +40,72 @@ __device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t u) {
   return v;
 }
 
-// x / s on the e2m1 midpoints, within two ulps elsewhere (see above), with
-// x's sign (the fma steps would turn -0 into +0).
-__device__ __forceinline__ float grid_quotient(float x, float s, float r) {
-  const float q1 = x * r;
-  return copysignf(fmaf(fmaf(-q1, s, x), r, q1), x);
+// x / s on the e2m1 midpoints, within two ulps elsewhere (see above), of two elements from
+// -x: q1 = (-x) (-r), the residual q1 s - x, q2 = q1 - residual r.  In this form a zero keeps
+// its sign.  nr = -1 / s.
+__device__ __forceinline__ float2 grid_quotient(float2 neg_x, float s, float nr) {
+  const float2 r2 = make_float2(nr, nr), q1 = fmul2_rn(neg_x, r2);
+  return ffma2_rn(ffma2_rn(q1, make_float2(s, s), neg_x), r2, q1);
 }
 
-// Byte of two e2m1 codes: the code of lo in the low nibble, of hi in the high.
-__device__ __forceinline__ uint32_t e2m1x2_byte(float lo, float hi) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
-      : "=r"(d)
-      : "f"(hi), "f"(lo));
-  return d;
+// Eight e2m1 codes (half to even, saturating, the sign kept), the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return w;
+}
+
+// The scale code of a group whose largest magnitude is m, in units of the outer scale; NaN
+// (0x7f) for a NaN.
+__device__ __forceinline__ uint32_t nvfp4_scale(float m) { return e4m3x2(__fdiv_rn(m, 6.0f), 0.f) & 0x7fu; }
+
+// Codes of 2 N elements of a group, given as -x; s_code as above, m > 2^120: an element's
+// quotient may not be finite.  The outer scale goes with the group's scale: a power of two,
+// it changes no quotient.
+template <int N>
+__device__ __forceinline__ void nvfp4_codes(float2 (&neg_x)[N], uint32_t s_code, float m, float outer, float up,
+                                            uint32_t (&c)[N / 4]) {
+  const float s0 = e4m3_magnitude(s_code);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) c[i] = 0u;
+  if (!(s0 > 0.f && m == m)) return;
+  const float s = s0 * outer, nr = -__frcp_rn(s0) * up;
+  if (m > 0x1p120f) {
+    const float most = fminf(0x1p120f * outer, 0x1p126f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      neg_x[e].x = fmaxf(fminf(neg_x[e].x, most), -most);
+      neg_x[e].y = fmaxf(fminf(neg_x[e].y, most), -most);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) neg_x[e] = grid_quotient(neg_x[e], s, nr);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    c[i] = e2m1x8(neg_x[4 * i], neg_x[4 * i + 1], neg_x[4 * i + 2], neg_x[4 * i + 3]);
+}
+
+// Two bf16 as -x.
+__device__ __forceinline__ float2 neg_bf16x2(uint32_t w) {
+  w ^= 0x80008000u;
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // One row to a plane of format KF, eight fp32 values x a lane (16 lanes a row, every lane
-// of the warp takes part).  up: 1 / outer scale (NVFP4; a power of two, so the product is
-// exact).  `write` is the same in the row's lanes.
+// of the warp takes part).  up: 1 / outer scale (NVFP4).  `write` is the same in the row's
+// lanes.
 //  e4m3: one fp32 scale a row, the rule in idx_ops.cuh; a NaN makes scale and codes NaN.
 //  NVFP4: a NaN makes its group's scale NaN; an infinity, and what lies past 6 * 448, is
 //  held as 6 * 448.
 template <int KF>
-__device__ __forceinline__ void put_row(float (&x)[8], float up, uint8_t* payload, void* scale,
+__device__ __forceinline__ void put_row(float (&x)[8], float outer, float up, uint8_t* payload, void* scale,
                                         unsigned long long row, int lane, bool write) {
   if (KF == kBf16) {
     uint32_t w[4];
@@ -77,10 +118,6 @@ __device__ __forceinline__ void put_row(float (&x)[8], float up, uint8_t* payloa
     return;
   }
   float m = 0.f;
-  if (KF == kNvfp4) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= up;
-  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = fmax_nan(m, fabsf(x[e]));
 #pragma unroll
@@ -96,19 +133,13 @@ __device__ __forceinline__ void put_row(float (&x)[8], float up, uint8_t* payloa
     }
     return;
   }
-  const uint32_t s_code = e4m3x2(__fdiv_rn(m, 6.0f), 0.f) & 0x7fu;
-  const float s = e4m3_magnitude(s_code);
-  uint32_t c = 0;
-  if (s > 0.f && m == m) {
-    const float r = __frcp_rn(s);
-    if (m > 0x1p120f) {   // no quotient of it is finite
+  m *= up;
+  const uint32_t s_code = nvfp4_scale(m);
+  uint32_t c[1];
+  float2 neg_x[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaxf(fminf(x[e], 0x1p120f), -0x1p120f);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c |= e2m1x2_byte(grid_quotient(x[2 * e], s, r), grid_quotient(x[2 * e + 1], s, r)) << (8 * e);
-  }
+  for (int e = 0; e < 4; ++e) neg_x[e] = make_float2(-x[2 * e], -x[2 * e + 1]);
+  nvfp4_codes(neg_x, s_code, m, outer, up, c);
   // the row's eight scales in its first lane
   uint2 all;
   {
@@ -119,7 +150,7 @@ __device__ __forceinline__ void put_row(float (&x)[8], float up, uint8_t* payloa
     all = make_uint2(b, __shfl_xor_sync(0xffffffffu, b, 8));
   }
   if (write) {
-    reinterpret_cast<uint32_t*>(payload + row * 64)[lane] = c;
+    reinterpret_cast<uint32_t*>(payload + row * 64)[lane] = c[0];
     if (lane == 0) reinterpret_cast<uint2*>(scale)[row] = all;
   }
 }

@@ -40,15 +40,12 @@ __device__ __forceinline__ void store_group(const uint32_t (&w)[8], int64_t row,
   const float s = e4m3_magnitude(s_code);
   uint32_t lo = 0, hi = 0;
   if (s > 0.f) {
-    const float r = __frcp_rn(s);
-    uint32_t byte[8];
+    const float nr = -__frcp_rn(s);
+    float2 q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
-      byte[e] = e2m1x2_byte(grid_quotient(x0, s, r), grid_quotient(x1, s, r));
-    }
-    lo = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
-    hi = byte[4] | (byte[5] << 8) | (byte[6] << 16) | (byte[7] << 24);
+    for (int e = 0; e < 8; ++e) q[e] = grid_quotient(neg_bf16x2(w[e]), s, nr);
+    lo = e2m1x8(q[0], q[1], q[2], q[3]);
+    hi = e2m1x8(q[4], q[5], q[6], q[7]);
   }
   *reinterpret_cast<uint2*>(payload + row * 64 + grp * 8) = make_uint2(lo, hi);
   scale[row * 8 + grp] = (uint8_t)s_code;
