@@ -137,10 +137,10 @@ __global__ void __launch_bounds__(256) store_kv4_kernel(const StoreArgs a, int c
 
 cudaError_t launch4(const StoreArgs& a, cudaStream_t stream) {
   const bool many = a.tokens * a.heads * a.planes >= 16384;
-  const int per = 2 * kRowsAtOnce * (many ? 2 : 1);
+  const int per = 2 * kRowsAtOnce * (many ? 4 : 1);
   const int chunks = (int)((a.tokens + per - 1) / per);
   const int grid = chunks * a.heads * a.planes;
-  return many ? launch_pdl(store_kv4_kernel<2>, grid, 256, 0, stream, a, chunks)
+  return many ? launch_pdl(store_kv4_kernel<4>, grid, 256, 0, stream, a, chunks)
               : launch_pdl(store_kv4_kernel<1>, grid, 256, 0, stream, a, chunks);
 }
 

@@ -26,16 +26,17 @@ namespace {
 
 constexpr int kTokens = 16;   // of a 256-thread CTA, a half warp each
 
-// The rows of a token in chunks of kRows: the queries', the keys', the values'.
+// The rows of a token in chunks of `rows` of one kind: the queries', the keys', the values'.
 struct Chunks {
-  int q, k, all;
+  int q, k, all, rows;
 };
 
-// kRows rows of one kind of a token a half warp: their loads all go out before any is used,
-// and what the rows are multiplied by, cos and sin times the norm's weights, is made once
-// for them: out = rstd (x A + y B), y the other half of x's pair.
-template <int KF, int kRows>
-__global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, Chunks chunks) {
+// A chunk of a token a half warp, kRows rows at a time: their loads all go out before any is
+// used; kMore: the chunk may have more than kRows, loaded under the arithmetic before.  What the rows are multiplied by, cos
+// and sin times the norm's weights, is made once for the chunk: out = rstd (x A + y B), y
+// the other half of x's pair.
+template <int KF, int kRows, bool kMore>
+__global__ void __launch_bounds__(256, kMore ? 3 : 4) norm_rope_store_kernel(const RopeArgs a, Chunks chunks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int chunk = blockIdx.x % chunks.all;
   const int lane = threadIdx.x & 15;
@@ -44,15 +45,19 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
   const long long tok = live ? want : a.tokens - 1;
   const int kind = chunk < chunks.q ? 0 : chunk < chunks.k ? 1 : 2;
   chunk -= kind == 0 ? 0 : kind == 1 ? chunks.q : chunks.k;
-  const int heads = kind ? a.kv_heads : a.q_heads, first = chunk * kRows;
+  const int first = chunk * chunks.rows;
+  const int rows = min((kind ? a.kv_heads : a.q_heads) - first, chunks.rows);
   const uint16_t* src = (kind == 0 ? a.src[0] + tok * a.stride[0]
                          : kind == 1 ? a.src[1] + tok * a.stride[1] : a.src[2] + tok * a.stride[2]) + first * kDim;
   uint4 u[kRows];
+  auto load = [&](uint4(&v)[kRows], int j0) {
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    u[j] = make_uint4(0, 0, 0, 0);
-    if (first + j < heads) u[j] = __ldcs(reinterpret_cast<const uint4*>(src + j * kDim) + lane);
-  }
+    for (int j = 0; j < kRows; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (j0 + j < rows) v[j] = __ldcs(reinterpret_cast<const uint4*>(src + (j0 + j) * kDim) + lane);
+    }
+  };
+  load(u, 0);
   unsigned long long at0, at_step;       // output row of the chunk's first row; to the next
   bool write = live;
   if (kind == 0) {
@@ -67,18 +72,34 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
   uint8_t* payload = kind == 1 ? a.payload[0] : a.payload[1];
   void* scale = kind == 1 ? a.scale[0] : a.scale[1];
   const float outer = kind == 1 ? a.outer[0] : a.outer[1], up = kind == 1 ? a.up[0] : a.up[1];
-  if (kind == 2) {
+  // f(row of the chunk, its words) for each row
+  auto each = [&](auto&& f) {
+    if constexpr (kMore) {
+      for (int j0 = 0; j0 < rows; j0 += kRows) {
+        uint4 next[kRows];
+        load(next, j0 + kRows);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      if (first + j >= heads) break;
+        for (int j = 0; j < kRows; ++j)
+          if (j0 + j < rows) f(j0 + j, u[j]);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) u[j] = next[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (j < rows) f(j, u[j]);
+    }
+  };
+  if (kind == 2) {
+    each([&](int j, uint4 v) {
       if (KF == kBf16) {
-        if (write) reinterpret_cast<uint4*>(payload + (at0 + j * at_step) * 256)[lane] = u[j];
-        continue;
+        if (write) reinterpret_cast<uint4*>(payload + (at0 + j * at_step) * 256)[lane] = v;
+        return;
       }
       float x[8];
-      bf16x8_to_f32(u[j], x);
+      bf16x8_to_f32(v, x);
       put_row<KF>(x, outer, up, payload, scale, at0 + j * at_step, lane, write);
-    }
+    });
     return;
   }
 
@@ -136,11 +157,9 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
     for (int e = 0; e < 8; ++e) A[e] *= w[e], B[e] *= a.interleaved ? w[e ^ 1] : v[e];
   }
 
-#pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    if (first + j >= heads) break;
+  each([&](int j, uint4 words) {
     float x[8];
-    bf16x8_to_f32(u[j], x);
+    bf16x8_to_f32(words, x);
     float rstd = 1.f;
     if (weight) {
       float2 sum = make_float2(0.f, 0.f);
@@ -170,25 +189,27 @@ __global__ void __launch_bounds__(256) norm_rope_store_kernel(const RopeArgs a, 
       put_row<kFp8>(x, 1.f, 1.f, static_cast<uint8_t*>(a.out_q), a.out_q_scale, at, lane, write);
     else
       put_row<kBf16>(x, 1.f, 1.f, static_cast<uint8_t*>(a.out_q), nullptr, at, lane, write);
-  }
+  });
 }
 
-template <int KF, int kRows>
-cudaError_t launch_rows(const RopeArgs& a, cudaStream_t stream) {
-  auto chunks_of = [](int rows) { return (rows + kRows - 1) / kRows; };
+template <int KF, int kRows, bool kMore>
+cudaError_t launch_rows(const RopeArgs& a, int rows, cudaStream_t stream) {
+  auto chunks_of = [&](int heads) { return (heads + rows - 1) / rows; };
   Chunks c;
   c.q = chunks_of(a.q_heads);
   c.k = c.q + chunks_of(a.kv_heads);
   c.all = c.k + (a.src[2] ? chunks_of(a.kv_heads) : 0);
+  c.rows = rows;
   const int grid = (int)((a.tokens + kTokens - 1) / kTokens * c.all);
-  return launch_pdl(norm_rope_store_kernel<KF, kRows>, grid, 256, 0, stream, a, c);
+  return launch_pdl(norm_rope_store_kernel<KF, kRows, kMore>, grid, 256, 0, stream, a, c);
 }
 
 template <int KF>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
-  // four rows a half warp once that still gives every SM a CTA or two
-  const long long groups = (a.tokens + kTokens - 1) / kTokens;
-  return groups * a.rows >= 152 * 8 ? launch_rows<KF, 4>(a, stream) : launch_rows<KF, 1>(a, stream);
+  const long long rows = (a.tokens + kTokens - 1) / kTokens * a.rows;
+  if (rows < 152 * 8) return launch_rows<KF, 1, false>(a, 1, stream);
+  if (rows < 152 * 64) return launch_rows<KF, 4, false>(a, 4, stream);
+  return launch_rows<KF, 4, true>(a, 16, stream);
 }
 
 }  // namespace
