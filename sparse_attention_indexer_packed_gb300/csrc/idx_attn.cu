@@ -412,12 +412,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(w));
   return d;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // One 32-token piece of an NVFP4 cache (kMask as above).  A lane's 16 bytes of a key are 32
 // dims, two groups; its 8 bytes of a value one group, whose dims are the 16 product tiles,
 // so a scale serves all of them.  A code times its scale is exact in f16.  The weights are

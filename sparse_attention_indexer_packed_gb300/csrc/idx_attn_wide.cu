@@ -73,6 +73,10 @@ using namespace attn;
 constexpr int kTok = kPage;          // tokens of a tile
 constexpr int kLanes = 128;          // tensor-memory lanes, product rows
 constexpr float kSlack = 8.f;        // log2 units a score may pass the running maximum by
+// NVFP4: the weights' unit lies 2^7 below the running maximum, the most that f16 allows a
+// weight that may pass it by 2^8
+template <int KF>
+constexpr float kHeadWide = KF == kNvfp4 ? 7.f : 0.f;
 // Tensor-memory columns: the queries; S of each group, and in its place P (bf16
 // caches), or P of its own, 32 columns a group (e4m3); O of each group.
 constexpr int kColQ = 0, kColS = 64, kColP = 192, kColO = 256, kCols = 512;
@@ -96,20 +100,30 @@ struct AWCfg<kFp8> {
   static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);   // f16
 };
 
+template <>
+struct AWCfg<kNvfp4> {
+  static constexpr int kRowBytes = 64;
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kIdQK = instr_desc(0u, kLanes, kTok);                // f16
+  static constexpr uint32_t kIdPV = instr_desc(0u, kLanes, kDim) | (1u << 16);
+};
+
 template <int KF, int F>
 struct AWLayout {
   static constexpr int NS = AWCfg<KF>::kStages;
   // Whether the softmax groups take registers from the other warps: 200 and more
   // instead of 168.  128 rows (64 scores a lane) 76 -> 67 us on 8 x 64K bf16, e4m3
   // 169 -> 162 on 16 x 131K; without it 64 rows of bf16 are 1% faster.
-  static constexpr bool kSplitRegs = KF == kFp8 || F == 1;
+  static constexpr bool kSplitRegs = KF != kBf16 || F == 1;
   // two softmax groups; producer, issuer (and two idle warps: whole warpgroups)
   static constexpr int kThreads = kSplitRegs ? 384 : 320;
   static constexpr int kTile = kTok * AWCfg<KF>::kRowBytes;  // keys or values of a page
-  static constexpr int kV16 = KF == kFp8 ? kTok * 256 : 0;   // decoded values, two a group
-  static constexpr int kScale = KF == kFp8 ? kTok * 4 : 0;
+  static constexpr int kV16 = KF != kBf16 ? kTok * 256 : 0;   // decoded values, two a group
+  static constexpr int kK16 = KF == kNvfp4 ? kTok * 256 : 0;  // decoded keys, one a group
+  static constexpr int kScale = KF == kFp8 ? kTok * 4 : KF == kNvfp4 ? kTok * 8 : 0;
   static constexpr int kV16Off = NS * 2 * kTile;
-  static constexpr int kScaleOff = kV16Off + 4 * kV16;
+  static constexpr int kK16Off = kV16Off + 4 * kV16;
+  static constexpr int kScaleOff = kK16Off + 2 * kK16;
   static constexpr int kBitsOff = kScaleOff + NS * 2 * kScale;     // block bits while lists are joined
   static constexpr int kMlOff = kBitsOff + 2 * kMaxBlockWords * 4;  // (max, sum, output unit) of each lane
   static constexpr int kInfoOff = kMlOff + 2 * kLanes * 16;         // valid tokens of each stage
@@ -214,6 +228,31 @@ __device__ __forceinline__ void tm_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// A page of NVFP4 codes (64 rows of 64 bytes) and their scales to f16 operand rows: two
+// halves of 64 dims, the 128-byte swizzle, as TMA would leave a 16-bit page; rows from
+// `valid` on as zeros.  128 threads, a group of 16 codes at a time.  Either half's lanes
+// write their two pieces in another order, which keeps the writes off one bank.
+__device__ __forceinline__ void decode_page4(const uint8_t* codes, const uint8_t* scales, uint8_t* out, int valid) {
+  const int t = threadIdx.x & 127, ch = t & 7, late = ch >> 2;
+  const int c0 = (ch & 3) * 2 + late;   // the piece written first, the other is c0 ^ 1
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int tok = (t >> 3) + 16 * e;
+    uint2 u = *reinterpret_cast<const uint2*>(codes + tok * 64 + ch * 8);
+    uint32_t s = scales[tok * 8 + ch], unused;
+    if (tok >= valid) u = make_uint2(0, 0), s = 0u;
+    e4m3x4_to_f16x2x2(s * 0x101u, s, unused);
+    uint32_t x[4], y[4];
+    e2m1x8_to_f16x2x4(late ? u.y : u.x, x);
+    e2m1x8_to_f16x2x4(late ? u.x : u.y, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], s), y[i] = hmul2(y[i], s);
+    uint8_t* base = out + late * (kTok * 128) + tok * 128;
+    *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(base + (((c0 ^ 1) ^ (tok & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -253,14 +292,15 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
   const uint32_t q_full = bars + 8 * (4 * NS + 8), stall_bar = q_full + 8, drain = q_full + 16;
   auto k_tile = [&](int s) { return sbase + s * 2 * L::kTile; };
   auto v_tile = [&](int s) { return sbase + s * 2 * L::kTile + L::kTile; };
+  auto scales_at = [&](int s) { return L::kScaleOff + s * 2 * L::kScale; };   // the keys', then the values'
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full_k(s), 1);
       mbar_init(full_v(s), 1);
-      mbar_init(empty_k(s), 1);
-      mbar_init(empty_v(s), KF == kFp8 ? 4 : 1);
+      mbar_init(empty_k(s), KF == kNvfp4 ? 4 : 1);
+      mbar_init(empty_v(s), KF != kBf16 ? 4 : 1);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(s_full(g), 1);
@@ -375,8 +415,11 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           const int row = (pg * a.kv_heads + it.kv_head) * kPage;
           if (!wait(empty_k(st), ph)) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile);
-            if (pg >= 0) {
+            mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile + (KF == kNvfp4 ? L::kScale : 0));
+            if (pg >= 0 && KF == kNvfp4) {   // a head page lies in one piece
+              bulk_load(k_tile(st), a.k_payload + (size_t)row * 64, L::kTile, full_k(st));
+              bulk_load(sbase + scales_at(st), a.k_scale + (size_t)row * 2, L::kScale, full_k(st));
+            } else if (pg >= 0) {
               tma_load_2d(k_tile(st), &k_map, 0, row, full_k(st));
               if (KF == kBf16) tma_load_2d(k_tile(st) + L::kTile / 2, &k_map, 64, row, full_k(st));
             }
@@ -385,15 +428,18 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           if (!wait(empty_v(st), ph)) break;
           if (lane == 0) {
             info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
-            // both planes' scales come with the values: the group reads them, and
+            // e4m3: both planes' scales come with the values: the group reads them, and
             // it gives the values' stage back itself
-            mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + 2 * L::kScale);
-            if (pg >= 0) {
+            mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + (KF == kNvfp4 ? 1 : 2) * L::kScale);
+            if (pg >= 0 && KF == kNvfp4) {
+              bulk_load(v_tile(st), a.v_payload + (size_t)row * 64, L::kTile, full_v(st));
+              bulk_load(sbase + scales_at(st) + L::kScale, a.v_scale + (size_t)row * 2, L::kScale, full_v(st));
+            } else if (pg >= 0) {
               tma_load_2d(v_tile(st), &v_map, 0, row, full_v(st));
               if (KF == kBf16) {
                 tma_load_2d(v_tile(st) + L::kTile / 2, &v_map, 64, row, full_v(st));
               } else {
-                const uint32_t sc = sbase + L::kScaleOff + st * 2 * L::kScale;
+                const uint32_t sc = sbase + scales_at(st);
                 bulk_load(sc, a.k_scale + row, L::kScale, full_v(st));
                 bulk_load(sc + L::kScale, a.v_scale + row, L::kScale, full_v(st));
               }
@@ -407,14 +453,16 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         constexpr uint32_t kIdQK = AWCfg<KF>::kIdQK, kIdPV = AWCfg<KF>::kIdPV;
         auto qk = [&](int b) -> bool {
           const int tile = tile0 + b, st = tile % NS, g = b & 1;
-          if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
+          if (KF != kNvfp4 && !wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
           tc_fence_after();
           const uint32_t d = tmem + kColS + 64 * g;
-          if (KF == kBf16) {
+          if (KF != kFp8) {
+            // (NVFP4: the keys that group g has decoded, which it has told by s_free)
+            const uint32_t k = KF == kBf16 ? k_tile(st) : sbase + L::kK16Off + g * L::kK16;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               mma_ts_f16(d, tmem + kColQ + ks * 8,
-                         desc_kmajor_sw128(k_tile(st) + (ks >> 2) * (L::kTile / 2) + (ks & 3) * 32),
+                         desc_kmajor_sw128(k + (ks >> 2) * (kTok * 128) + (ks & 3) * 32),
                          kIdQK, ks > 0);
           } else {
 #pragma unroll
@@ -422,7 +470,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               mma_ts_f8(d, tmem + kColQ + ks * 8, desc_kmajor_sw128(k_tile(st) + (ks & 3) * 32),
                         ks < 4 ? kIdQK : AWCfg<kFp8>::kIdQKLow, ks > 0);
           }
-          tc_commit_warp(empty_k(st));
+          if (KF != kNvfp4) tc_commit_warp(empty_k(st));
           tc_commit_warp(s_full(g));
           return true;
         };
@@ -430,16 +478,19 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         if (ok && a.stall_test && segs == 0) ok = wait(stall_bar, 0);
         ok = ok && wait(q_full, (uint32_t)(segs & 1));
         tc_fence_after();
+        if (KF == kNvfp4) ok = ok && wait(s_free(0), (uint32_t)(cnt0 & 1));
         ok = ok && qk(0);
+        if (KF == kNvfp4 && n > 1) ok = ok && wait(s_free(1), (uint32_t)(cnt1 & 1));
         if (n > 1) ok = ok && qk(1);
         int k0 = cnt0, k1 = cnt1;
         for (int b = 0; b < n && ok; ++b) {
           const int tile = tile0 + b, st = tile % NS, g = b & 1;
           const int cnt = g ? k1++ : k0++;
           const uint32_t ph = (uint32_t)(cnt & 1);
-          // e4m3: the group's next scores as soon as it has read these
-          if (KF == kFp8 && b + 2 < n) ok = wait(s_free(g), ph) && qk(b + 2);
-          ok = ok && wait(p_full(g), ph) && (KF == kFp8 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
+          // e4m3: the group's next scores as soon as it has read these (NVFP4: and decoded the
+          // next keys, the ones of its page number cnt + 1)
+          if (KF != kBf16 && b + 2 < n) ok = wait(s_free(g), KF == kNvfp4 ? ph ^ 1u : ph) && qk(b + 2);
+          ok = ok && wait(p_full(g), ph) && (KF != kBf16 || wait(full_v(st), (uint32_t)((tile / NS) & 1)));
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + kColO + kDim * g;
@@ -512,6 +563,12 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             const int ex = to_2_7(amax);
             const float up = ldexpf(1.f, ex);
             post = fmaxf(post * ldexpf(1.f, -ex), kLeastPost);
+            if constexpr (KF == kNvfp4) {
+              // as f16: exact for elements within 2^21 of the row's largest
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = pack_f16(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+              tm_st<32>(tl + kColQ + 32 * g, w);
+            } else {
             uint32_t lo[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -522,6 +579,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             }
             tm_st<16>(tl + kColQ + 16 * g, w);
             tm_st<16>(tl + kColQ + 32 + 16 * g, lo);
+            }
           }
           tm_wait_st();
           tc_fence_before();
@@ -532,6 +590,18 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         int cnt = g ? cnt1 : cnt0;
         const uint32_t sp = tl + kColS + 64 * g, oc = tl + kColO + kDim * g;
         const uint32_t pp = KF == kBf16 ? sp : tl + kColP + 32 * g;
+        // NVFP4: the keys of the group's page b as operand rows, in the place of those of its
+        // page before, whose product has ended; and S is free: the scores may come
+        auto next_keys = [&](int b) {
+          const int tile = tile0 + b, st = tile % NS;
+          if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
+          decode_page4(smem + (k_tile(st) - sbase), smem + scales_at(st), smem + L::kK16Off + g * L::kK16, kTok);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty_k(st));
+          return true;
+        };
+        if (KF == kNvfp4 && g < n && next_keys(g) && lane == 0) mbar_arrive(s_free(g));
         for (int b = g; b < n; b += 2, ++cnt) {
           const int tile = tile0 + b, st = tile % NS;
           int tb;
@@ -539,7 +609,13 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, members);
           if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
           const int valid = info[st];
-          if (KF == kFp8) {
+          if (KF == kNvfp4) {
+            // as below; codes and scales have then been read
+            decode_page4(smem + (v_tile(st) - sbase), smem + scales_at(st) + L::kScale,
+                         smem + L::kV16Off + (2 * g + (cnt & 1)) * L::kV16, valid);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_v(st));
+          } else if (KF == kFp8) {
             // this page's values as f16, rows past the request's tokens as zeros, in
             // the buffer of the group's page before the last (whose product has
             // ended: that was waited for before the last page's weights)
@@ -571,6 +647,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           if (!wait(s_full(g), (uint32_t)(cnt & 1))) break;
           tc_fence_after();
+          if (KF == kNvfp4 && b + 2 < n && !next_keys(b + 2)) break;
           // the lane's scores
           uint32_t raw[kPart];
           if constexpr (F == 1) {
@@ -589,7 +666,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               for (int f = 1; f < F; ++f) raw[j] = part == f ? all[f][j] : raw[j];
             }
           }
-          if (KF == kFp8) {
+          if (KF == kFp8 || (KF == kNvfp4 && b + 2 < n)) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free(g));
@@ -597,7 +674,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           // y: the scores before the row's factor, two tokens at a time
           constexpr int kHalf = kPart / 2;
           float2 y[kHalf];
-          const float* ks = reinterpret_cast<const float*>(smem + L::kScaleOff + st * 2 * L::kScale) + part * kPart;
+          const float* ks = reinterpret_cast<const float*>(smem + scales_at(st)) + part * kPart;   // e4m3
 #pragma unroll
           for (int j = 0; j < kHalf; ++j)
             y[j] = make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
@@ -627,10 +704,10 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           const float top = fmaxf(t0, t1) * post;   // post is positive: the order is kept
           float shrink = 1.f;     // what the output gathered so far is to be multiplied by
-          if (top > m + (m == -INFINITY ? 0.f : kSlack)) {
-            shrink = ex2_approx(m - top);
+          if (top > m + (m == -INFINITY ? 0.f : kSlack + kHeadWide<KF>)) {
+            shrink = ex2_approx(m - (top - kHeadWide<KF>));
             l *= shrink;
-            m = top;
+            m = top - kHeadWide<KF>;
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const float2 pp2 = make_float2(post, post), rr2 = make_float2(-ref, -ref);
@@ -678,8 +755,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           // e4m3: the output is still, and P's columns free, once the last product
           // has ended (bf16: its scores came after that)
-          if (KF == kFp8 && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
-          if (KF == kFp8) tc_fence_after();
+          if (KF != kBf16 && cnt > 0 && !wait(pv_done(g), (uint32_t)((cnt - 1) & 1))) break;
+          if (KF != kBf16) tc_fence_after();
           if (b >= 2 && __any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll
             for (int ch = 0; ch < kDim; ch += 32) {
@@ -716,7 +793,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           tm_wait_st();
           tc_fence_before();
-          if (KF == kFp8 || valid < kTok) fence_async();
+          if (KF != kBf16 || valid < kTok) fence_async();
           mbar_arrive(p_full(g));
           if (KF == kFp8) {
             // codes and scales of the page have been read
@@ -892,8 +969,9 @@ cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtenso
 
 cudaError_t launch_attn_wide(int key_format, const AttnArgs& a, const CUtensorMap& k_map,
                              const CUtensorMap& v_map, int grid, int dev, cudaStream_t stream) {
-  return key_format == kBf16 ? launch_kf<kBf16>(a, k_map, v_map, grid, dev, stream)
-                             : launch_kf<kFp8>(a, k_map, v_map, grid, dev, stream);
+  return key_format == kBf16  ? launch_kf<kBf16>(a, k_map, v_map, grid, dev, stream)
+         : key_format == kFp8 ? launch_kf<kFp8>(a, k_map, v_map, grid, dev, stream)
+                              : launch_kf<kNvfp4>(a, k_map, v_map, grid, dev, stream);
 }
 
 }  // namespace idx

@@ -188,6 +188,13 @@ __device__ __forceinline__ float2 ffma2_rn(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// Two f16 products.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Four E4M3 bytes -> two f16x2 registers of their exact values:
 // lo = {byte0, byte1}, hi = {byte2, byte3}.
 __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
