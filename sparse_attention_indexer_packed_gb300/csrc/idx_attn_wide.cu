@@ -235,18 +235,25 @@ __device__ __forceinline__ void tm_wait_st() {
 __device__ __forceinline__ void decode_page4(const uint8_t* codes, const uint8_t* scales, uint8_t* out, int valid) {
   const int t = threadIdx.x & 127, ch = t & 7, late = ch >> 2;
   const int c0 = (ch & 3) * 2 + late;   // the piece written first, the other is c0 ^ 1
+  // every read goes out before a write that may, for all the compiler knows, change it
+  uint2 u[4];
+  uint32_t s[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int tok = (t >> 3) + 16 * e;
-    uint2 u = *reinterpret_cast<const uint2*>(codes + tok * 64 + ch * 8);
-    uint32_t s = scales[tok * 8 + ch], unused;
-    if (tok >= valid) u = make_uint2(0, 0), s = 0u;
-    e4m3x4_to_f16x2x2(s * 0x101u, s, unused);
-    uint32_t x[4], y[4];
-    e2m1x8_to_f16x2x4(late ? u.y : u.x, x);
-    e2m1x8_to_f16x2x4(late ? u.x : u.y, y);
+    u[e] = *reinterpret_cast<const uint2*>(codes + tok * 64 + ch * 8);
+    s[e] = scales[tok * 8 + ch];
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], s), y[i] = hmul2(y[i], s);
+  for (int e = 0; e < 4; ++e) {
+    const int tok = (t >> 3) + 16 * e;
+    if (tok >= valid) u[e] = make_uint2(0, 0), s[e] = 0u;
+    uint32_t sc, unused, x[4], y[4];
+    e4m3x4_to_f16x2x2(s[e] * 0x101u, sc, unused);
+    e2m1x8_to_f16x2x4(late ? u[e].y : u[e].x, x);
+    e2m1x8_to_f16x2x4(late ? u[e].x : u[e].y, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = hmul2(x[i], sc), y[i] = hmul2(y[i], sc);
     uint8_t* base = out + late * (kTok * 128) + tok * 128;
     *reinterpret_cast<uint4*>(base + ((c0 ^ (tok & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<uint4*>(base + (((c0 ^ 1) ^ (tok & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
