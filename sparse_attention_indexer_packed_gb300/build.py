@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libidx.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["idx_api.cu", "idx_score.cu", "idx_wide.cu", "idx_topk.cu", "idx_store.cu", "idx_noalloc.cu",
-           "idx_attn.cu", "idx_attn_wide.cu", "idx_kv.cu", "idx_norm.cu",
+           "idx_attn.cu", "idx_attn4.cu", "idx_attn_wide.cu", "idx_kv.cu", "idx_norm.cu",
            "idx_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

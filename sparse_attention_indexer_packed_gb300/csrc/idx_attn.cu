@@ -71,8 +71,8 @@ namespace {
 
 using namespace attn;
 
-constexpr int kTile = 16;                              // packed rows of a group here
 constexpr int kItem = 32;                              // tokens of a piece
+constexpr int kMergeStride = kDim + 8;                 // floats: keeps row writes off one bank
 
 template <int KF>
 struct ACfg;
@@ -88,12 +88,6 @@ struct ACfg<kFp8> {
   static constexpr int kWarps = 8;
   static constexpr int kDepth = 2;
 };
-template <>
-struct ACfg<kNvfp4> {
-  static constexpr int kRowBytes = 64;
-  static constexpr int kWarps = 8;
-  static constexpr int kDepth = 4;
-};
 
 template <int KF>
 struct ALayout {
@@ -102,10 +96,7 @@ struct ALayout {
   static constexpr int kThreads = 32 * NW;
   static constexpr int kTileBytes = kItem * ACfg<KF>::kRowBytes;  // keys or values of a piece
   static constexpr int kStage = 2 * kTileBytes;
-  static constexpr int kScaleBytes = 2 * kItem * (KF == kFp8 ? 4 : KF == kNvfp4 ? 8 : 0);
-  // floats of a row of a warp's part: keeps row writes off one bank.  NVFP4: a lane has 32
-  // dims in a row, each run of 32 is four floats apart from the next
-  static constexpr int kMergeStride = kDim + (KF == kNvfp4 ? 16 : 8);
+  static constexpr int kScaleBytes = KF == kFp8 ? 2 * kItem * 4 : 0;
   static constexpr int kScaleOff = NW * D * kStage;
   static constexpr int kMergeOff = kScaleOff + NW * D * kScaleBytes;
   static constexpr int kMlOff = kMergeOff + NW / 2 * kTile * kMergeStride * 4;
@@ -134,9 +125,7 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& r0, u
 //  the row's largest magnitude into [2^7, 2^8) (exact for every element within
 //  2^21 of it, undone by post): e4m3 values are exact in f16, so each product is
 //  exact.  k order: step c takes d = 16c + 4t + {0,1} and + {2,3}, the order in
-//  which a lane's four bytes of an ldmatrix'ed key arrive.
-//  NVFP4 keys: scaled f16 queries too (every code times its E4M3 scale is exact in f16).
-//  k order: step c takes d = 32t + 4c + {0,1} and + {2,3}: a lane's 16 bytes of a key.  (Two e4m3 query terms
+//  which a lane's four bytes of an ldmatrix'ed key arrive.  (Two e4m3 query terms
 //  on m16n8k32 would spare the keys' conversion; measured on the 16 x 131K decode
 //  134 us against 113: the warp-level e4m3 product is the slower one here.)
 template <int KF>
@@ -155,17 +144,17 @@ struct QRows {
         a[c][2] = r0 ? __ldg(reinterpret_cast<const uint32_t*>(r0 + o + 8)) : 0u;
         a[c][3] = r1 ? __ldg(reinterpret_cast<const uint32_t*>(r1 + o + 8)) : 0u;
       } else {
-        const int o = KF == kFp8 ? 16 * c + 4 * t : 32 * t + 4 * c;
+        const int o = 16 * c + 4 * t;
         const uint2 u = r0 ? __ldg(reinterpret_cast<const uint2*>(r0 + o)) : make_uint2(0, 0);
         const uint2 v = r1 ? __ldg(reinterpret_cast<const uint2*>(r1 + o)) : make_uint2(0, 0);
         a[c][0] = u.x, a[c][2] = u.y, a[c][1] = v.x, a[c][3] = v.y;
       }
     }
   }
-  // what the scores are to be multiplied by; e4m3 and NVFP4 keys: the rows to scaled f16
+  // what the scores are to be multiplied by; e4m3 keys: the rows to scaled f16
   __device__ __forceinline__ void finish(float scale_log2) {
     post0 = post1 = scale_log2;
-    if (KF != kBf16) {
+    if (KF == kFp8) {
       post0 = fmaxf(post0 * to_f16(0), kLeastPost);
       post1 = fmaxf(post1 * to_f16(1), kLeastPost);
     }
@@ -402,151 +391,6 @@ __device__ __forceinline__ void piece(const QRows<KF>& q, State& st, uint32_t st
   }
 }
 
-// The token of an NVFP4 piece's 8-token tile that is column 2t + e of the scores' tile and
-// row 2t + e of the values' operand.  The order keeps the reads off one bank: the keys'
-// (tokens 2t, 2t + 1 side by side) and the values' (four tokens 2t + e at once).
-__device__ __forceinline__ int token4(int t, int e) { return 4 * (t >> 1) + ((t & 1) ^ (3 * e)); }
-
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(w));
-  return d;
-}
-// One 32-token piece of an NVFP4 cache (kMask as above).  A lane's 16 bytes of a key are 32
-// dims, two groups; its 8 bytes of a value one group, whose dims are the 16 product tiles,
-// so a scale serves all of them.  A code times its scale is exact in f16.  The weights are
-// held against the maximum's 2^kHead, the most that f16 allows a weight of 1: 11 bits of
-// each, down to 2^-28 of the row's largest, and 2^-39 of that below.
-constexpr float kHead = 14.f;
-template <bool kMask>
-__device__ __forceinline__ void piece4(const QRows<kNvfp4>& q, State& st, const uint8_t* stage,
-                                       const uint8_t* scales, int lane, int tb, int len0, int len1,
-                                       int glen) {
-  const int t = lane & 3, g = lane >> 2;
-  constexpr int TB = ALayout<kNvfp4>::kTileBytes;
-  float s[4][4];
-  {
-    const int tok = token4(g >> 1, g & 1);
-    const uint8_t* krow = stage + tok * 64 + ((t ^ (tok >> 1)) << 4);
-    const uint8_t* ks = scales + tok * 8 + 2 * t;
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      const uint4 u = *reinterpret_cast<const uint4*>(krow + nt * 512);
-      const uint32_t sc = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + nt * 64));
-      const uint32_t sc2[2] = {prmt(sc, 0u, 0x1010), prmt(sc, 0u, 0x3232)};
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t d[4];
-        e2m1x8_to_f16x2x4(w[e], d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = hmul2(d[i], sc2[e >> 1]);
-        mma_f16_16816(s[nt], q.a[2 * e], d[0], d[1]);
-        mma_f16_16816(s[nt], q.a[2 * e + 1], d[2], d[3]);
-      }
-    }
-  }
-  const int ta = token4(t, 0), tc = token4(t, 1);   // the lane's tokens of each tile
-  float2 y0[4], y1[4];
-  float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    y0[nt] = make_float2(s[nt][0], s[nt][1]);
-    y1[nt] = make_float2(s[nt][2], s[nt][3]);
-    if (kMask) {
-      const int t0 = tb + nt * 8 + ta, t1 = tb + nt * 8 + tc;
-      if (t0 >= len0) y0[nt].x = -INFINITY;
-      if (t1 >= len0) y0[nt].y = -INFINITY;
-      if (t0 >= len1) y1[nt].x = -INFINITY;
-      if (t1 >= len1) y1[nt].y = -INFINITY;
-    }
-    mx0 = fmaxf(mx0, fmaxf(y0[nt].x, y0[nt].y));
-    mx1 = fmaxf(mx1, fmaxf(y1[nt].x, y1[nt].y));
-  }
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-  }
-  const float mn0 = fmaxf(st.m0, fmaf(mx0, q.post0, -kHead)), mn1 = fmaxf(st.m1, fmaf(mx1, q.post1, -kHead));
-  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
-  const float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
-  st.m0 = mn0, st.m1 = mn1;
-  const float2 p0 = make_float2(q.post0, q.post0), p1 = make_float2(q.post1, q.post1);
-  const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
-  float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    y0[nt] = ffma2_rn(y0[nt], p0, r0);
-    y1[nt] = ffma2_rn(y1[nt], p1, r1);
-    y0[nt].x = ex2_approx(y0[nt].x), y0[nt].y = ex2_approx(y0[nt].y);
-    y1[nt].x = ex2_approx(y1[nt].x), y1[nt].y = ex2_approx(y1[nt].y);
-    l0 = fadd2_rn(l0, y0[nt]);
-    l1 = fadd2_rn(l1, y1[nt]);
-  }
-  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
-  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
-  if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      st.o[j][0] *= c0, st.o[j][1] *= c0;
-      st.o[j][2] *= c1, st.o[j][3] *= c1;
-    }
-  }
-  // (the two tokens' rows differ in the bits that the swizzle goes by)
-  const uint8_t* va = stage + TB + ta * 64 + (((g >> 1) ^ (ta >> 1)) << 4) + (g & 1) * 8;
-  const uint8_t* vc = stage + TB + tc * 64 + (((g >> 1) ^ (tc >> 1)) << 4) + (g & 1) * 8;
-  const uint8_t* vs = scales + kItem * 8 + g;
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    const uint32_t p[4] = {pack_f16(y0[2 * ks].x, y0[2 * ks].y), pack_f16(y1[2 * ks].x, y1[2 * ks].y),
-                           pack_f16(y0[2 * ks + 1].x, y0[2 * ks + 1].y),
-                           pack_f16(y1[2 * ks + 1].x, y1[2 * ks + 1].y)};
-    uint2 a[2], c[2];
-    uint32_t sc[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int nt = 2 * ks + h;
-      a[h] = *reinterpret_cast<const uint2*>(va + nt * 512);
-      c[h] = *reinterpret_cast<const uint2*>(vc + nt * 512);
-      uint32_t x = vs[(nt * 8 + ta) * 8], y = vs[(nt * 8 + tc) * 8];
-      if (kMask) {   // what lies past the request's tokens is zero: any scale is dropped
-        if (tb + nt * 8 + ta >= glen) x = 0u;
-        if (tb + nt * 8 + tc >= glen) y = 0u;
-      }
-      sc[h] = e4m3x2_to_f16x2(x | (y << 8));
-    }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      // two tokens' codes of a dim side by side: the even dims, then the odd ones
-      constexpr uint32_t kLow = 0x0f0f0f0fu;
-      uint32_t even[2][4], odd[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t x = w ? a[h].y : a[h].x, y = w ? c[h].y : c[h].x;
-        e2m1x8_to_f16x2x4((x & kLow) | ((y << 4) & ~kLow), even[h]);
-        e2m1x8_to_f16x2x4(((x >> 4) & kLow) | (y & ~kLow), odd[h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) even[h][i] = hmul2(even[h][i], sc[h]), odd[h][i] = hmul2(odd[h][i], sc[h]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mma_f16_16816(st.o[8 * w + 2 * i], p, even[0][i], even[1][i]);
-        mma_f16_16816(st.o[8 * w + 2 * i + 1], p, odd[0][i], odd[1][i]);
-      }
-    }
-  }
-}
-
-// A part of a shared unit's row: (running max, sum) and the unnormalised output.
-__device__ __forceinline__ void put_part(const AttnArgs& a, int slot, int i, float m, float l,
-                                         float4 o, int lane) {
-  const size_t at = (size_t)slot * kTile + i;
-  if (lane == 0) a.part_ml[at] = make_float2(m, l);
-  reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
-}
-
 // What the estimates below count in: the time in which an SM at its full rate takes a
 // piece (bf16 0.38 us, HBM's share; e4m3 0.23, the warps' own).  A warp alone needs
 // kAlone of it for a piece; kEnd and kEndAlone are a team's and a warp's cost of a unit
@@ -604,20 +448,7 @@ __device__ __forceinline__ void write_rows(const AttnArgs& a, const Items& it, c
   for (int j = 0; j < 8; ++j) {
     const float* x = st.o[2 * j];
     const float* y = st.o[2 * j + 1];
-    if (KF == kNvfp4) {
-      if (j & 1) continue;
-      const float* z = st.o[2 * j + 2];
-      const float* w = st.o[2 * j + 3];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (has0)
-          *reinterpret_cast<uint2*>(o0 + 32 * t + 16 * e + 2 * j) =
-              make_uint2(two(see0, x[e], y[e], f0), two(see0, z[e], w[e], f0));
-        if (has1)
-          *reinterpret_cast<uint2*>(o1 + 32 * t + 16 * e + 2 * j) =
-              make_uint2(two(see1, x[e + 2], y[e + 2], f1), two(see1, z[e + 2], w[e + 2], f1));
-      }
-    } else if (KF == kBf16) {
+    if (KF == kBf16) {
       if (has0) {
         *reinterpret_cast<uint32_t*>(o0 + 16 * j + 2 * t) = two(see0, x[0], x[1], f0);
         *reinterpret_cast<uint32_t*>(o0 + 16 * j + 8 + 2 * t) = two(see0, y[0], y[1], f0);
@@ -757,12 +588,11 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
         tma_load_2d(stage + L::kTileBytes, &v_map, 0, row, bar);
         tma_load_2d(stage + L::kTileBytes + L::kTileBytes / 2, &v_map, 64, row, bar);
       } else {
-        constexpr int kEach = L::kScaleBytes / 2, kWords = kEach / kItem / 4;   // a plane's scales
         const uint32_t sc = sbase + scales_of(issued);
         tma_load_2d(stage, &k_map, 0, row, bar);
-        bulk_load(sc, a.k_scale + (size_t)row * kWords, kEach, bar);
+        bulk_load(sc, a.k_scale + row, kItem * 4, bar);
         tma_load_2d(stage + L::kTileBytes, &v_map, 0, row, bar);
-        bulk_load(sc + kEach, a.v_scale + (size_t)row * kWords, kEach, bar);
+        bulk_load(sc + kItem * 4, a.v_scale + row, kItem * 4, bar);
       }
     }
     ++issued;
@@ -830,19 +660,11 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       const bool whole = __all_sync(0xffffffffu, (!has0 || cur.tb + kItem <= e0) &&
                                                      (!has1 || cur.tb + kItem <= e1));
       const uint32_t stage = stage_of(used);
-      if constexpr (KF == kNvfp4) {
-        const uint8_t* tiles = smem + (stage - sbase);
-        if (whole)
-          piece4<false>(q, st, tiles, smem + scales_of(used), lane, cur.tb, e0, e1, it.glen);
-        else
-          piece4<true>(q, st, tiles, smem + scales_of(used), lane, cur.tb, e0, e1, it.glen);
-      } else {
-        const float* scales = reinterpret_cast<const float*>(smem + scales_of(used));
-        if (whole)
-          piece<KF, false>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
-        else
-          piece<KF, true>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
-      }
+      const float* scales = reinterpret_cast<const float*>(smem + scales_of(used));
+      if (whole)
+        piece<KF, false>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
+      else
+        piece<KF, true>(q, st, stage, scales, lane, cur.tb, e0, e1, it.glen);
       ++used;
       // every lane's reads of the stage come before the copies that refill it
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -881,8 +703,8 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
     }
     constexpr int nh = TW > 1 ? TW / 2 : 1;
     const int first = team * nh, place = first + (member < nh ? member : member - nh);
-    float* w0 = merge + (size_t)(place * kTile + g) * L::kMergeStride;
-    float* w1 = w0 + 8 * L::kMergeStride;
+    float* w0 = merge + (size_t)(place * kTile + g) * kMergeStride;
+    float* w1 = w0 + 8 * kMergeStride;
     float2* ml0 = ml + place * kTile + g;
     auto put = [&]() {
       if (t == 0) {
@@ -895,16 +717,6 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
           *reinterpret_cast<float2*>(w0 + 8 * j + 2 * t) = make_float2(st.o[j][0], st.o[j][1]);
           *reinterpret_cast<float2*>(w1 + 8 * j + 2 * t) = make_float2(st.o[j][2], st.o[j][3]);
         }
-      } else if (KF == kNvfp4) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            *reinterpret_cast<float4*>(w0 + 36 * t + 16 * e + j) =
-                make_float4(st.o[j][e], st.o[j + 1][e], st.o[j + 2][e], st.o[j + 3][e]);
-            *reinterpret_cast<float4*>(w1 + 36 * t + 16 * e + j) =
-                make_float4(st.o[j][e + 2], st.o[j + 1][e + 2], st.o[j + 2][e + 2], st.o[j + 3][e + 2]);
-          }
       } else {
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
@@ -942,20 +754,6 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
           st.o[j][2] = fold(has_a1, st.o[j][2], a1, has_b1, y1.x, b1);
           st.o[j][3] = fold(has_a1, st.o[j][3], a1, has_b1, y1.y, b1);
         }
-      } else if (KF == kNvfp4) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 y0 = *reinterpret_cast<const float4*>(w0 + 36 * t + 16 * e + j);
-            const float4 y1 = *reinterpret_cast<const float4*>(w1 + 36 * t + 16 * e + j);
-            const float v0[4] = {y0.x, y0.y, y0.z, y0.w}, v1[4] = {y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              st.o[j + i][e] = fold(has_a0, st.o[j + i][e], a0, has_b0, v0[i], b0);
-              st.o[j + i][e + 2] = fold(has_a1, st.o[j + i][e + 2], a1, has_b1, v1[i], b1);
-            }
-          }
       } else {
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
@@ -997,8 +795,7 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
           const float2 x = ml[(first + w) * kTile + i];
           const float f = ex2_approx(x.x - m);
           if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
-          const float4 v = *reinterpret_cast<const float4*>(
-              merge + (size_t)((first + w) * kTile + i) * L::kMergeStride + 4 * lane + (KF == kNvfp4 ? 4 * (lane / 8) : 0));
+          const float4 v = *reinterpret_cast<const float4*>(merge + (size_t)((first + w) * kTile + i) * kMergeStride + 4 * lane);
           l = fmaf(x.y, f, l);
           o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
         }
@@ -1341,14 +1138,14 @@ cudaError_t launch_attn(int key_format, const AttnArgs& a, const CUtensorMap& k_
   bool whole = false;
   if (wide)
     e = launch_attn_wide(key_format, a, k_map, v_map, grid, dev, stream);
+  else if (key_format == kNvfp4)
+    e = launch_attn4(a, k_map, v_map, grid, dev, stream, whole);
   else if (blocks)
-    e = key_format == kBf16   ? launch_lists<kBf16>(a, k_map, v_map, grid, dev, stream, whole)
-        : key_format == kFp8 ? launch_lists<kFp8>(a, k_map, v_map, grid, dev, stream, whole)
-                             : launch_lists<kNvfp4>(a, k_map, v_map, grid, dev, stream, whole);
+    e = key_format == kBf16 ? launch_lists<kBf16>(a, k_map, v_map, grid, dev, stream, whole)
+                            : launch_lists<kFp8>(a, k_map, v_map, grid, dev, stream, whole);
   else
-    e = key_format == kBf16   ? launch_paged<kBf16>(a, k_map, v_map, grid, dev, stream)
-        : key_format == kFp8 ? launch_paged<kFp8>(a, k_map, v_map, grid, dev, stream)
-                             : launch_paged<kNvfp4>(a, k_map, v_map, grid, dev, stream);
+    e = key_format == kBf16 ? launch_paged<kBf16>(a, k_map, v_map, grid, dev, stream)
+                            : launch_paged<kFp8>(a, k_map, v_map, grid, dev, stream);
   if (e != cudaSuccess || whole) return e;
   const int rows = a.P * a.nq < a.group_rows ? a.P * a.nq : a.group_rows;
   e = units * 16 <= grid && a.most > 32 * 8

@@ -242,6 +242,9 @@ __device__ __forceinline__ int owner(int x, int W, int C) {
 
 cudaError_t launch_attn(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
                         const CUtensorMap& v_map, cudaStream_t stream);
+// NVFP4 caches, up to 16 packed rows a unit.  whole: no unit is cut, there is nothing to join.
+cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                         int grid, int dev, cudaStream_t stream, bool& whole);
 cudaError_t launch_attn_wide(int key_format, const AttnArgs& args, const CUtensorMap& k_map,
                              const CUtensorMap& v_map, int grid, int dev, cudaStream_t stream);
 // CTAs launch_attn uses on the current device (0: the device cannot be asked).

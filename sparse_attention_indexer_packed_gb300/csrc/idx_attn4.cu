@@ -1,0 +1,767 @@
+// Attention over an NVFP4 cache with up to 16 packed rows a unit: the mathematics, the
+// split and the dealing are idx_attn.cu's.
+//
+// What bounds it: 144 bytes a token and head, half of what an e4m3 cache has, against the same
+// products and a decode of both operands, so it is the warps' own work that bounds it, not
+// HBM.  A 32-token piece costs a warp 128 conversions, 128 f16x2 products and 64 matrix
+// products; on each of an SM's four schedulers the conversions (2 cycles each) come to 256
+// cycles, the matrix products (8 each) to 512, all instructions together to ~600, where
+// HBM's share of the piece is 215.
+//
+// How (sm_103a):
+//  * 16 warps of 128 registers, four a scheduler: with 8 (of 255) the warps' chains leave
+//    two thirds of the issue slots empty.  So the 16 queries lie in shared memory in the
+//    order of the product's operand (read once for four token tiles), the output alone in
+//    registers, and what feeds the warps in the last warp: its lane w walks warp w's
+//    units, looks its pieces' pages up and asks for their copies (walked by the warps
+//    themselves, that state is spilled: 146 us on 16 x 131K).  The other 15 are teams of 15,
+//    5 or 3;
+//  * a warp owns two stages of one piece (keys, values and their scales).  Its area, 9 KB, is
+//    also where a warp of the upper half of a team leaves its state at a unit's end, so
+//    those warps get the next unit's pieces only after it;
+//  * a lane's 16 bytes of a key are 32 dims of it, two groups; its 8 bytes of a value are one
+//    group, whose dims are the 16 product tiles, so one scale serves all of them.  Two
+//    tokens' codes of one dim are put side by side by masks, without a permutation.  A code
+//    times its scale is exact in f16, the queries are f16 as for e4m3 keys;
+//  * the weights are f16 against 2^kHead below the maximum's 2^m, the most that f16 allows a
+//    weight of 1: 11 bits of each, down to 2^-28 of the row's largest, 2^-39 of it below.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "idx_attn.cuh"
+#include "idx_attn_rows.cuh"
+#include "idx_ptx.cuh"
+
+namespace idx {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kItem = 32;      // tokens of a piece
+constexpr int NW = 15;         // warps that have units
+constexpr int D = 2;           // stages of a warp
+constexpr float kHead = 14.f;
+constexpr int kColdWords = 28;
+
+// What a piece needs to know of a packed row, in shared memory: the scores' factor, the
+// visible length (0: no such row) and the bit of its draft row.
+struct Row {
+  float post;
+  int len;
+  uint32_t bit;
+};
+
+struct L {
+  static constexpr int kThreads = 32 * (NW + 1);     // and the warp that feeds them
+  static constexpr int kTileBytes = kItem * 64;      // keys or values of a piece
+  static constexpr int kScaleBytes = kItem * 8;
+  static constexpr int kArea = D * 2 * (kTileBytes + kScaleBytes);   // of a warp: tiles, then scales
+  // floats of a row of a warp's state: a lane has 32 dims in a row, each run of 32 is four
+  // floats apart from the next, which keeps row writes off one bank
+  static constexpr int kStateStride = kDim + 16;
+  static_assert(kTile * kStateStride * 4 <= kArea, "a state in a warp's area");
+  static_assert(kArea % 512 == 0, "the 64-byte swizzle's period");
+  static constexpr int kTeams = NW / 3;
+  static constexpr int kQOff = NW * kArea;           // a team's queries, in operand order
+  static constexpr int kPostOff = kQOff + kTeams * kTile * 256;
+  static constexpr int kMlOff = kPostOff + kTeams * kTile * sizeof(Row);   // (max, sum) of a warp's rows
+  static constexpr int kInfoOff = kMlOff + NW * kTile * 8;       // whether a piece in flight exists
+  // (and the items of a team's list); full, empty [warp][stage], go [warp], stall
+  static constexpr int kBarOff = (kInfoOff + (NW * D + kTeams) * 4 + 7) & ~7;
+  static constexpr int kNumBars = 2 * NW * D + NW + 1;
+  static constexpr int kColdOff = kBarOff + kNumBars * 8;        // what a warp does not need in its loop
+  static constexpr int kCtlOff = kColdOff + NW * kColdWords * 4;  // flags, longest unit, abort, one int a warp
+  static constexpr int kPreOff = (kCtlOff + 12 + (NW + 1) * 4 + 15) & ~15;
+  static constexpr int kListOff = kPreOff + kRequestsBytes;
+  static constexpr int kBytes = kListOff + kMaxList * 4;
+  static constexpr int kSmem = kBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  // the bits that lists are joined with lie in the team's areas, where nothing is in flight then
+  static_assert(2 * kMaxBlockWords * 4 <= 3 * kArea, "block bits");
+};
+
+// The token of an NVFP4 piece's 8-token tile that is column 2t + e of the scores' tile and
+// row 2t + e of the values' operand.  The order keeps the reads off one bank: the keys'
+// (tokens 2t, 2t + 1 side by side) and the values' (four tokens 2t + e at once).
+__device__ __forceinline__ int token4(int t, int e) { return 4 * (t >> 1) + ((t & 1) ^ (3 * e)); }
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
+
+// Softmax state of the two rows a lane holds (g and g + 8), and its part of the
+// unnormalised output: dims 32t + j of o[j][0] (row g) and o[j][2] (row g + 8), 32t + 16 + j
+// of o[j][1] and o[j][3].  m in log2 units, kHead below the running maximum.
+struct State {
+  float m0, m1, l0, l1;
+  float o[16][4];
+  __device__ __forceinline__ void reset() {
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
+};
+
+// One 32-token piece.  q: the queries in operand order, step c takes the dims 32t + 4c + {0, 1}
+// and + {2, 3}.  kMask: some token of the piece lies outside some row (past its length, or
+// the row's draft does not list the block) or at or past glen, where the cache holds anything:
+// such values are dropped by selection, not by a product with zero.
+// (The lane is asked for anew: what follows from it is cheaper made again than kept or
+// spilled.)
+template <bool kMask>
+__device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, uint32_t stage,
+                                      uint32_t scales, int tb, uint32_t members, int glen) {
+  int lane;
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+  const int t = lane & 3, g = lane >> 2;
+  float s[4][4];
+  {
+    const int tok = token4(g >> 1, g & 1);
+    const uint32_t krow = stage + tok * 64 + ((t ^ (tok >> 1)) << 4), ks = scales + tok * 8 + 2 * t;
+#pragma unroll
+    for (int n2 = 0; n2 < 4; n2 += 2) {
+      uint32_t w[2][4], sc[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int nt = n2 + h;
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        const uint4 u = lds128(krow + nt * 512);
+        w[h][0] = u.x, w[h][1] = u.y, w[h][2] = u.z, w[h][3] = u.w;
+        sc[h] = e4m3x2_to_f16x2(lds16(ks + nt * 64));
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 u = lds128(q + c * 512 + lane * 16);
+        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t d0, d1;
+          if (c & 1) e2m1x4_to_f16x2x2<1>(w[h][c / 2], d0, d1);
+          else e2m1x4_to_f16x2x2<0>(w[h][c / 2], d0, d1);
+          const uint32_t f = prmt(sc[h], 0u, c < 4 ? 0x1010 : 0x3232);
+          mma_f16_16816(s[n2 + h], a, hmul2(d0, f), hmul2(d1, f));
+        }
+      }
+    }
+  }
+  const int ta = token4(t, 0), tc = token4(t, 1);   // the lane's tokens of each tile
+  const float post0 = rows[g].post, post1 = rows[g + 8].post;
+  const int len0 = kMask && (members & rows[g].bit) ? rows[g].len : 0;
+  const int len1 = kMask && (members & rows[g + 8].bit) ? rows[g + 8].len : 0;
+  float2 y0[4], y1[4];
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    y0[nt] = make_float2(s[nt][0], s[nt][1]);
+    y1[nt] = make_float2(s[nt][2], s[nt][3]);
+    if (kMask) {
+      const int t0 = tb + nt * 8 + ta, t1 = tb + nt * 8 + tc;
+      if (t0 >= len0) y0[nt].x = -INFINITY;
+      if (t1 >= len0) y0[nt].y = -INFINITY;
+      if (t0 >= len1) y1[nt].x = -INFINITY;
+      if (t1 >= len1) y1[nt].y = -INFINITY;
+    }
+    mx0 = fmaxf(mx0, fmaxf(y0[nt].x, y0[nt].y));
+    mx1 = fmaxf(mx1, fmaxf(y1[nt].x, y1[nt].y));
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+  }
+  const float mn0 = fmaxf(st.m0, fmaf(mx0, post0, -kHead)), mn1 = fmaxf(st.m1, fmaf(mx1, post1, -kHead));
+  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
+  const float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
+  st.m0 = mn0, st.m1 = mn1;
+  const float2 p0 = make_float2(post0, post0), p1 = make_float2(post1, post1);
+  const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
+  float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+  uint32_t p[2][4];
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+    y0[nt] = ffma2_rn(y0[nt], p0, r0);
+    y1[nt] = ffma2_rn(y1[nt], p1, r1);
+    y0[nt].x = ex2_approx(y0[nt].x), y0[nt].y = ex2_approx(y0[nt].y);
+    y1[nt].x = ex2_approx(y1[nt].x), y1[nt].y = ex2_approx(y1[nt].y);
+    l0 = fadd2_rn(l0, y0[nt]);
+    l1 = fadd2_rn(l1, y1[nt]);
+    p[nt / 2][2 * (nt % 2)] = pack_f16(y0[nt].x, y0[nt].y);
+    p[nt / 2][2 * (nt % 2) + 1] = pack_f16(y1[nt].x, y1[nt].y);
+  }
+  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
+  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
+  if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      st.o[j][0] *= c0, st.o[j][1] *= c0;
+      st.o[j][2] *= c1, st.o[j][3] *= c1;
+    }
+  }
+  // (the two tokens' rows differ in the bits that the swizzle goes by)
+  const uint32_t va = stage + L::kTileBytes + ta * 64 + (((g >> 1) ^ (ta >> 1)) << 4) + (g & 1) * 8;
+  const uint32_t vc = stage + L::kTileBytes + tc * 64 + (((g >> 1) ^ (tc >> 1)) << 4) + (g & 1) * 8;
+  const uint32_t sa = scales + L::kScaleBytes + g + ta * 8, sb = scales + L::kScaleBytes + g + tc * 8;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    uint2 a[2], c[2];
+    uint32_t sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int nt = 2 * ks + h;
+      a[h] = lds64(va + nt * 512);
+      c[h] = lds64(vc + nt * 512);
+      uint32_t x = lds8(sa + nt * 64), y = lds8(sb + nt * 64);
+      if (kMask) {   // what lies past the request's tokens is zero: any scale is dropped
+        if (tb + nt * 8 + ta >= glen) x = 0u;
+        if (tb + nt * 8 + tc >= glen) y = 0u;
+      }
+      sc[h] = e4m3x2_to_f16x2(x | (y << 8));
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      // two tokens' codes of a dim side by side: the even dims, then the odd ones
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        uint32_t v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = w ? a[h].y : a[h].x, y = w ? c[h].y : c[h].x;
+          e2m1x8_to_f16x2x4(odd ? ((x >> 4) & kLow) | (y & ~kLow) : (x & kLow) | ((y << 4) & ~kLow), v[h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[h][i] = hmul2(v[h][i], sc[h]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f16_16816(st.o[8 * w + 2 * i + odd], p[ks], v[0][i], v[1][i]);
+      }
+    }
+  }
+}
+
+// A lane's part of a state: 16 dims of a row at a time, four floats a write.
+template <class F>
+__device__ __forceinline__ void each_quad(float* w0, int t, F&& f) {
+  float* w1 = w0 + 8 * L::kStateStride;
+#pragma unroll
+  for (int j = 0; j < 16; j += 4)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      f(reinterpret_cast<float4*>(w0 + 36 * t + 16 * e + j), j, e);
+      f(reinterpret_cast<float4*>(w1 + 36 * t + 16 * e + j), j, e + 2);
+    }
+}
+
+// As in idx_attn.cu, in units of 0.13 us, an SM's time for a piece.
+struct Cost {
+  static constexpr float kAlone = 8.f, kEnd = 20.f, kStretch = 24.f, kCut = 26.f, kList = 18.f;
+};
+
+// Whether the units of the call are dealt whole to teams of TW warps: as in idx_attn.cu.
+template <int TW>
+__device__ __forceinline__ bool whole_units(const AttnArgs& a, const Requests& rq, int longest, int C) {
+  if (a.shift > 0) return false;
+  const int per = (int)a.by_per.d;
+  const float units = (float)(a.R * per), each = __fdividef(1.f, (float)C);
+  const float total = (float)((rq.pre[a.R] - a.R * a.unit_cost) * per), mean = __fdividef(total, units);
+  const float whole = a.dealt_ends + fmaxf(mean, (float)TW) * a.dealt_piece +
+                      ((float)longest - mean) * (Cost::kAlone / TW);
+  const float cut = fmaxf(total * each, Cost::kAlone) + Cost::kStretch * units * each + Cost::kCut;
+  return whole <= cut;
+}
+
+// Words of a team's joined list.
+__host__ __device__ constexpr int team_list_words(int tw) { return kMaxList / (NW / tw); }
+
+// The units of a team, as its warps and the lane that feeds each of them walk them: the CTA's
+// stretch of the line (kCut, TW = NW), or whole units dealt in turn to the teams of all CTAs.
+template <bool kBlocks, int TW, bool kCut>
+struct Team {
+  static_assert(NW % TW == 0 && TW % 2 == 1 && (!kCut || TW == NW), "teams");
+  // At a unit's end members nh .. TW - 1 leave their states in their areas, the first nh add
+  // theirs to those of the members nh + 1 on.
+  static constexpr int nh = TW / 2;
+  Walk walk;
+  __device__ __forceinline__ Team(const AttnArgs& a, const Requests& rq, int team, int W, int C) {
+    const int c = blockIdx.x;
+    if (kCut)
+      walk.begin(a, rq.pre, c < C ? W * c / C : 0, c < C ? W * (c + 1) / C : 0);
+    else
+      walk.begin_units(a, team * (int)gridDim.x + c, (NW / TW) * (int)gridDim.x);
+  }
+  __device__ __forceinline__ Segment next(const AttnArgs& a, const Requests& rq) {
+    return kCut ? walk.next(a, rq.pre) : walk.next_unit(a, rq.pre);
+  }
+  // Items member, member + TW, ... of the stretch.
+  static __device__ __forceinline__ int pieces(const Items& it, int member) {
+    return max(0, (it.i1 - it.i0 - member + TW - 1) / TW);
+  }
+};
+
+__device__ __forceinline__ uint32_t full_bar(uint32_t sbase, int warp, int k) { return sbase + L::kBarOff + (warp * D + k % D) * 8; }
+__device__ __forceinline__ uint32_t empty_bar(uint32_t sbase, int warp, int k) { return full_bar(sbase, NW + warp, k); }
+__device__ __forceinline__ uint32_t go_bar(uint32_t sbase, int warp) { return sbase + L::kBarOff + (2 * NW * D + warp) * 8; }
+__device__ __forceinline__ uint32_t stall_bar(uint32_t sbase) { return go_bar(sbase, NW); }
+__device__ __forceinline__ int tiles_of(int warp, int k) { return warp * L::kArea + (k % D) * 2 * L::kTileBytes; }
+__device__ __forceinline__ int scales_of(int warp, int k) {
+  return warp * L::kArea + D * 2 * L::kTileBytes + (k % D) * 2 * L::kScaleBytes;
+}
+
+// Lane w of the feeding warp: warp w's pieces.  It asks for one as soon as a stage is free
+// and, where the warp's area or list was in use between two units (`gated`), the warp has
+// said go.  The page id is loaded a piece ahead.  Nothing here waits: a lane that cannot go
+// on is passed over, and all give up when none has for the wait's limit.
+template <bool kBlocks, int TW, bool kCut>
+__device__ __forceinline__ void feed_warps(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                           uint8_t* smem, const Requests& rq, int W, int C) {
+  using T = Team<kBlocks, TW, kCut>;
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* ctl = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
+  volatile unsigned int* abort_flag = ctl + 2;
+  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
+  const int lane = threadIdx.x & 31, w = lane < NW ? lane : 0, member = w % TW;
+  const uint32_t* list = reinterpret_cast<const uint32_t*>(smem + L::kListOff) + team_list_words(TW) * (w / TW);
+  const bool gated = kBlocks || member >= T::nh;
+  T team(a, rq, w / TW, W, C);
+  Items it = {};
+  Segment s = {};
+  int left = 0, i = 0, units = 0, issued = 0, page = 0, tb = 0;
+  bool more = lane < NW, waiting = false;   // waiting: for the warp to say go
+  auto look_up = [&]() {
+    uint32_t unused;
+    page = -1;
+    if (item_tokens<kItem, kBlocks>(it, list, i, tb, unused))
+      page = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
+    else
+      tb = -1;
+  };
+  uint64_t t0 = global_timer_ns();
+  bool gave_up = false;
+  while (__any_sync(0xffffffffu, more) && !gave_up) {
+    bool did = false;
+    if (more && left == 0 && !waiting) {       // the next stretch
+      if (!team.walk.more()) {
+        more = false;
+      } else {
+        s = team.next(a, rq);
+        did = true;
+        if (s.live) {
+          if (kBlocks) {
+            waiting = true;
+          } else {
+            it = make_items<kItem, kBlocks>(a, rq, s, 0);
+            left = T::pieces(it, member);
+            i = it.i0 + member;
+            waiting = gated;
+            if (left > 0) look_up();
+          }
+        }
+      }
+    }
+    if (waiting && mbar_test_wait(go_bar(sbase, w), (uint32_t)(units & 1))) {
+      ++units;
+      waiting = false;
+      did = true;
+      if (kBlocks) {
+        it = make_items<kItem, kBlocks>(a, rq, s, infos[NW * D + w / TW]);
+        left = T::pieces(it, member);
+        i = it.i0 + member;
+        if (left > 0) look_up();
+      }
+    }
+    if (more && left > 0 && !waiting &&
+        (issued < D || mbar_test_wait(empty_bar(sbase, w, issued), (uint32_t)((issued / D - 1) & 1)))) {
+      const uint32_t bar = full_bar(sbase, w, issued);
+      const bool there = page >= 0 && page < a.num_pages;
+      if (tb >= 0 && !there) atomicOr(ctl, kErrBadPage);
+      infos[w * D + issued % D] = there;
+      mbar_arrive_expect_tx(bar, there ? 2 * (L::kTileBytes + L::kScaleBytes) : 0);
+      if (there) {
+        const int row = (page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
+        const uint32_t to = sbase + tiles_of(w, issued), sc = sbase + scales_of(w, issued);
+        tma_load_2d(to, &k_map, 0, row, bar);
+        bulk_load(sc, a.k_scale + (size_t)row * 2, L::kScaleBytes, bar);
+        tma_load_2d(to + L::kTileBytes, &v_map, 0, row, bar);
+        bulk_load(sc + L::kScaleBytes, a.v_scale + (size_t)row * 2, L::kScaleBytes, bar);
+      }
+      ++issued;
+      i += TW;
+      if (--left > 0) look_up();
+      did = true;
+    }
+    if (__any_sync(0xffffffffu, did))
+      t0 = global_timer_ns();
+    else
+      gave_up = global_timer_ns() - t0 > a.wait_ns + a.wait_ns / 2;
+    gave_up = __any_sync(0xffffffffu, gave_up || *abort_flag);
+  }
+  if (gave_up && lane == 0) {
+    atomicOr(ctl, kErrTimeout);
+    *abort_flag = 1;
+  }
+  // after a timeout: the copies in flight land before the block ends
+  if (gave_up && lane < NW)
+    for (int k = max(0, issued - D); k < issued; ++k)
+      (void)mbar_wait_bounded(full_bar(sbase, w, k), (uint32_t)((k / D) & 1), 200000000ull);
+  __syncwarp();
+}
+
+// Every word of a walk and of a stretch.
+template <class F>
+__device__ __forceinline__ void each_word(F&& f, Walk& w, Segment& s, Items& it) {
+  f(w.pos), f(w.end), f(w.start), f(w.r), f(w.head), f(w.group), f(w.unit), f(w.wt), f(w.step);
+  f(s.unit), f(s.r), f(s.head), f(s.group), f(s.o0), f(s.o1), f(s.cap), f(s.start);
+  f(it.r), f(it.head), f(it.slot), f(it.glen), f(it.kv_head), f(it.i0), f(it.i1);
+  static_assert(kColdWords >= 24, "room for them");
+}
+
+// A warp's share of the CTA's units, TW warps a unit.  record: the unit the CTA started and
+// did not end.
+template <bool kBlocks, int TW, bool kCut>
+__device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, const Requests& rq, int W, int C,
+                                          SplitRecord& record) {
+  using T = Team<kBlocks, TW, kCut>;
+  constexpr int nh = T::nh;
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
+  volatile unsigned int* abort_flag = cta_flags + 2;
+  // (one value a warp, and the compiler knows it)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int team = warp / TW, member = warp % TW, c = blockIdx.x;
+  uint32_t* list = reinterpret_cast<uint32_t*>(smem + L::kListOff) + team_list_words(TW) * team;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + team * TW * L::kArea);
+  uint8_t* q_rows = smem + L::kQOff + team * (kTile * 256);
+  Row* rows = reinterpret_cast<Row*>(smem + L::kPostOff) + team * kTile;
+  float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
+  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TW * 32) : "memory"); };
+  int* cold = reinterpret_cast<int*>(smem + L::kColdOff) + warp * kColdWords;
+  bool dead = false;
+  int used = 0;          // pieces this warp has waited for
+  T units(a, rq, team, W, C);
+  while (units.walk.more()) {
+    Segment s = units.next(a, rq);
+    if (!s.live) continue;
+    const int row_first = s.group * kTile;
+    const int nrows = min(kTile, a.P * a.nq - row_first);
+    const int p0 = a.by_nq.div(row_first);
+    int n_items = 0;
+    if (kBlocks) {
+      n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits,
+                           threadIdx.x % (32 * TW), 32 * TW, team_sync) *
+                (kBlock / kItem);
+      if (threadIdx.x % (32 * TW) == 0) infos[NW * D + team] = n_items;
+      // the areas that held the bits get copies again
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      team_sync();
+    }
+    if ((kBlocks || member >= nh) && lane == 0) mbar_arrive(go_bar(sbase, warp));
+    Items it = make_items<kItem, kBlocks>(a, rq, s, n_items);
+    auto q_index = [&](int pk, int p) {   // packed row pk of the unit head, draft row p = pk / nq
+      return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
+    };
+    // ---- the unit's queries: the warp's rows, to f16 scaled a row by the power of two that
+    // brings the row's largest magnitude into [2^7, 2^8) (undone by post) ----------
+    constexpr int kMine = (kTile + TW - 1) / TW;
+    uint2 qw[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = member + k * TW, pk = row_first + i;
+      qw[k] = make_uint2(0, 0);
+      if (i < nrows) qw[k] = __ldg(reinterpret_cast<const uint2*>(a.q + q_index(pk, a.by_nq.div(pk)) * kDim) + lane);
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = member + k * TW;
+      if (i >= kTile) break;
+      float top = fmaxf(fmaxf(fabsf(bf16_lo(qw[k].x)), fabsf(bf16_hi(qw[k].x))),
+                        fmaxf(fabsf(bf16_lo(qw[k].y)), fabsf(bf16_hi(qw[k].y))));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int x = to_2_7(top);
+      const float up = ldexpf(1.f, x);
+      // dims 4 lane ..: step lane % 8, the operand's lane (row % 8, lane / 8), its words of row / 8
+      uint32_t* to = reinterpret_cast<uint32_t*>(q_rows + (lane & 7) * 512 + ((i & 7) * 4 + lane / 8) * 16) + i / 8;
+      to[0] = pack_f16(bf16_lo(qw[k].x) * up, bf16_hi(qw[k].x) * up);
+      to[2] = pack_f16(bf16_lo(qw[k].y) * up, bf16_hi(qw[k].y) * up);
+      if (lane == 0) {
+        const int p = a.by_nq.div(row_first + i);
+        const bool has = i < nrows && it.glen > 0;
+        // with one draft row the request's longest row is the row
+        rows[i] = {fmaxf(a.scale_log2 * ldexpf(1.f, -x), kLeastPost),
+                   !has ? 0 : a.P == 1 ? it.glen : row_len(a, s.r, p), kBlocks && has ? 1u << (p - p0) : has ? 1u : 0u};
+      }
+    }
+    team_sync();
+    // pieces up to here, whose blocks all of these list, need no mask
+    int safe;
+    uint32_t drafts;
+    {
+      const Row r = rows[lane & 15];
+      safe = __reduce_min_sync(0xffffffffu, r.bit ? r.len : 0x7fffffff);
+      drafts = __reduce_or_sync(0xffffffffu, r.bit);
+    }
+    // ---- the walk and the stretch wait in shared memory: 128 registers are the loop's ------
+    const int n = T::pieces(it, member), glen = it.glen;
+    int i = it.i0 + member;
+    if (lane == 0) {
+      int* k = cold;
+      each_word([&](int& x) { *k++ = x; }, units.walk, s, it);
+    }
+    __syncwarp();
+    State st;
+    st.reset();
+    // ---- its pieces -----------------------------------------------------------
+    for (int k = 0; k < n && !dead; ++k, i += TW) {
+      int tb;
+      uint32_t members;
+      item_tokens<kItem, kBlocks>(glen, list, i, tb, members);
+      const bool stall = a.stall_test && warp == 0 && used == 0;
+      bool ok = mbar_try_wait(stall ? stall_bar(sbase) : full_bar(sbase, warp, used), stall ? 0u : (uint32_t)((used / D) & 1));
+      const uint64_t t0 = ok ? 0 : global_timer_ns();
+      while (!ok) {
+        ok = mbar_try_wait(stall ? stall_bar(sbase) : full_bar(sbase, warp, used), stall ? 0u : (uint32_t)((used / D) & 1));
+        if (!ok && (*abort_flag || global_timer_ns() - t0 > a.wait_ns)) break;
+      }
+      dead = __any_sync(0xffffffffu, !ok);
+      if (dead) {
+        if (lane == 0) {
+          atomicOr(cta_flags, kErrTimeout);
+          *abort_flag = 1;
+          // the unit's copies in flight land: the area is written to below
+          for (int j = 0; j < D && k + j < n; ++j)
+            (void)mbar_wait_bounded(full_bar(sbase, warp, used + j), (uint32_t)(((used + j) / D) & 1), 200000000ull);
+        }
+        __syncwarp();
+        break;
+      }
+      if (infos[warp * D + used % D]) {
+        const uint32_t tiles = sbase + tiles_of(warp, used), scales = sbase + scales_of(warp, used);
+        if (tb + kItem <= safe && (!kBlocks || (members & drafts) == drafts))
+          piece<false>(smem_u32(q_rows), rows, st, tiles, scales, tb, members, glen);
+        else
+          piece<true>(smem_u32(q_rows), rows, st, tiles, scales, tb, members, glen);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(sbase, warp, used));
+      ++used;
+    }
+    {
+      volatile const int* k = cold;
+      each_word([&](int& x) { x = *k++; }, units.walk, s, it);
+    }
+    // ---- join the warps: the upper half into the lower, then those by rows -----
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
+      st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, o);
+    }
+    st.m0 = not_empty(st.m0, st.l0);
+    st.m1 = not_empty(st.m1, st.l1);
+    const int place = warp + (member < nh ? nh + 1 : 0);   // whose area takes the state
+    float* w0 = reinterpret_cast<float*>(smem + place * L::kArea) + g * L::kStateStride;
+    float2* ml0 = ml + place * kTile + g;
+    auto put = [&]() {
+      if (t == 0) {
+        ml0[0] = make_float2(st.m0, st.l0);
+        ml0[8] = make_float2(st.m1, st.l1);
+      }
+      each_quad(w0, t, [&](float4* to, int j, int e) {
+        *to = make_float4(st.o[j][e], st.o[j + 1][e], st.o[j + 2][e], st.o[j + 3][e]);
+      });
+    };
+    if (member >= nh) put();
+    team_sync();
+    if (member < nh) {
+      const float2 x0 = ml0[0], x1 = ml0[8];
+      const float n0 = fmaxf(st.m0, x0.x), n1 = fmaxf(st.m1, x1.x);
+      const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+      // a half with nothing visible in the row holds zeros (or 0 * NaN: dropped)
+      const bool ha0 = st.m0 != -INFINITY, ha1 = st.m1 != -INFINITY;
+      const bool hb0 = x0.x != -INFINITY, hb1 = x1.x != -INFINITY;
+      const float a0 = ex2_approx(st.m0 - r0), a1 = ex2_approx(st.m1 - r1);
+      const float b0 = ex2_approx(x0.x - r0), b1 = ex2_approx(x1.x - r1);
+      st.l0 = (ha0 ? st.l0 * a0 : 0.f) + (hb0 ? x0.y * b0 : 0.f);
+      st.l1 = (ha1 ? st.l1 * a1 : 0.f) + (hb1 ? x1.y * b1 : 0.f);
+      st.m0 = n0, st.m1 = n1;
+      each_quad(w0, t, [&](float4* from, int j, int e) {
+        const float4 v = *from;
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        const bool ha = e < 2 ? ha0 : ha1, hb = e < 2 ? hb0 : hb1;
+        const float fa = e < 2 ? a0 : a1, fb = e < 2 ? b0 : b1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st.o[j + i][e] = (ha ? st.o[j + i][e] * fa : 0.f) + (hb ? x[i] * fb : 0.f);
+      });
+      __syncwarp();
+      put();
+    }
+    team_sync();
+    const int first_row = s.group * kTile, rows_here = min(kTile, a.P * a.nq - first_row), draft0 = a.by_nq.div(first_row);
+    const bool complete = !kCut || (s.o0 == 0 && s.o1 == s.cap);
+    const int slot_out = 2 * c + (s.o0 == 0 ? 1 : 0);
+    if (s.o0 == 0 && !complete) {
+      record.unit = s.unit;
+      record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
+    }
+    const int first = team * TW + nh;
+    for (int i = member; i < rows_here; i += TW) {
+      const int pk = first_row + i, p = a.by_nq.div(pk);
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < TW - nh; ++w) m = fmaxf(m, ml[(first + w) * kTile + i].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < TW - nh; ++w) {
+          const float2 x = ml[(first + w) * kTile + i];
+          const float f = ex2_approx(x.x - m);
+          if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
+          const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (first + w) * L::kArea) +
+                                                            i * L::kStateStride + 4 * lane + 4 * (lane / 8));
+          l = fmaf(x.y, f, l);
+          o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+        }
+      }
+      if (__any_sync(0xffffffffu, !finite4(o)))
+        careful_row<kNvfp4, kItem, kBlocks>(a, it, list, a.q + q_index(pk, p) * kDim,
+                                            it.glen > 0 ? row_len(a, s.r, p) : 0, p - draft0, lane, m, l, o);
+      if (complete)
+        write_row(a, q_index(pk, p), m, l, o, lane);
+      else
+        put_part(a, slot_out, i, m, l, o, lane);
+    }
+    // the states' places get copies again
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    team_sync();
+  }
+}
+
+template <bool kBlocks, int TW, bool kCut>
+__device__ __forceinline__ void run_cta(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                        uint8_t* smem, const Requests& rq, int W, int C, SplitRecord& record) {
+  if (threadIdx.x / 32 == NW)
+    feed_warps<kBlocks, TW, kCut>(a, k_map, v_map, smem, rq, W, C);
+  else
+    run_units<kBlocks, TW, kCut>(a, smem, rq, W, C, record);
+}
+
+enum class Deal { kCut, kWhole, kEither };
+template <bool kBlocks, int TW, Deal kDeal>
+__global__ void __launch_bounds__(L::kThreads, 1)
+    attn4_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
+  const Requests rq = requests_at(smem + L::kPreOff);
+
+  if (threadIdx.x < L::kNumBars) {
+    mbar_init(sbase + L::kBarOff + threadIdx.x * 8, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    cta_flags[2] = 0u;   // abort
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 3), cta_flags);
+
+  const int W = rq.pre[a.R] * (int)a.by_per.d;
+  const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
+  SplitRecord record = {-1, 0};
+  if constexpr (kDeal == Deal::kCut) {
+    run_cta<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
+  } else if constexpr (kDeal == Deal::kWhole) {
+    run_cta<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
+  } else {
+    if (whole_units<TW>(a, rq, (int)cta_flags[1], C))
+      run_cta<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
+    else
+      run_cta<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.records[blockIdx.x] = record;
+    a.err_bytes[blockIdx.x] = (uint8_t)*cta_flags;
+    if (blockIdx.x == 0) *a.err_count = gridDim.x;
+  }
+}
+
+template <bool kBlocks, int TW, Deal kDeal>
+cudaError_t launch_one(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                       int grid, int dev, cudaStream_t stream) {
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_limit_once(attn4_kernel<kBlocks, TW, kDeal>, L::kSmem, dev, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn4_kernel<kBlocks, TW, kDeal>, grid, L::kThreads, L::kSmem, stream, a, k_map, v_map);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+// The team size for units dealt whole, of so many pieces: as in idx_attn.cu.
+template <bool kBlocks>
+int team_for(AttnArgs& a, int grid, float pieces, float& least) {
+  const int units = a.R * (int)a.by_per.d;
+  int team = 0;
+  for (int tw : {15, 5, 3}) {
+    if (kBlocks && (a.P < kMaxDrafts ? a.P : kMaxDrafts) * a.topk > team_list_words(tw)) break;
+    const int teams = grid * (NW / tw), full = units / teams, rest = units - full * teams;
+    const float busy = (float)(rest * tw) / (float)grid;
+    const float last = rest == 0 ? 0.f : busy > Cost::kAlone ? busy : Cost::kAlone;
+    const float ends = (float)(full + (rest > 0)) * (Cost::kEnd + (kBlocks ? Cost::kList : 0.f));
+    const float piece = ((float)NW * (float)full + last) / (float)tw;
+    const float cost = ends + pieces * piece;
+    if (team > 0 && cost >= least) continue;
+    team = tw;
+    least = cost;
+    a.dealt_ends = ends;
+    a.dealt_piece = piece;
+  }
+  return team;
+}
+
+}  // namespace
+
+cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                         int grid, int dev, cudaStream_t stream, bool& whole) {
+  AttnArgs a = args;
+  float least;
+  if (!a.block_ids) {
+    // units of 16 pieces are assumed for the team; how long they are is known on the device
+    // only, which decides whether they are dealt whole at all
+    whole = false;
+    switch (team_for<false>(a, grid, 16.f, least)) {
+      case 3: return launch_one<false, 3, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 5: return launch_one<false, 5, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      default: return launch_one<false, 15, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+    }
+  }
+  // the lists' length bounds the units', so the host decides, and a call that deals needs no join
+  const float full = (float)(a.topk * (kBlock / kItem)) * (1.f + (float)(a.P - 1) / 8.f);
+  const float pieces = full < (float)a.most ? full : (float)a.most;
+  const float share = (float)(a.R * (int)a.by_per.d) / (float)grid;
+  const int team = team_for<true>(a, grid, pieces, least);
+  const float cut = (share * pieces > Cost::kAlone ? share * pieces : Cost::kAlone) +
+                    (Cost::kStretch + Cost::kList) * share + Cost::kCut + Cost::kList;
+  whole = least <= 0.83f * cut;
+  if (!whole) return launch_one<true, 15, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
+  switch (team) {
+    case 3: return launch_one<true, 3, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 5: return launch_one<true, 5, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_one<true, 15, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+  }
+}
+
+}  // namespace idx

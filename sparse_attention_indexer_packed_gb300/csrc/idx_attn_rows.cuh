@@ -322,7 +322,7 @@ __device__ __forceinline__ Items make_items(const AttnArgs& a, const Requests& r
 // list its block (bit p - p0, below kMaxDrafts; a group of the whole cache may have
 // more draft rows than the word has bits, and they all see it).  False: nothing there.
 template <int IT, bool kBlocks>
-__device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
+__device__ __forceinline__ bool item_tokens(int glen, const uint32_t* list, int i, int& tb,
                                             uint32_t& members) {
   if (kBlocks) {
     constexpr int kPer = kBlock / IT;
@@ -333,7 +333,12 @@ __device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* lis
     tb = i * IT;
     members = 0xffffffffu;
   }
-  return tb < it.glen;
+  return tb < glen;
+}
+template <int IT, bool kBlocks>
+__device__ __forceinline__ bool item_tokens(const Items& it, const uint32_t* list, int i, int& tb,
+                                            uint32_t& members) {
+  return item_tokens<IT, kBlocks>(it.glen, list, i, tb, members);
 }
 
 // Plane row of the item's first token, -1 if its page id is out of range.
@@ -399,6 +404,16 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, float m
   u.y = m == -INFINITY ? 0u : pack_bf16(o.z * inv, o.w * inv);
   reinterpret_cast<uint2*>(a.out + row * kDim)[lane] = u;
   if (lane == 0 && a.lse) a.lse[row] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+}
+
+constexpr int kTile = 16;   // packed rows of a group of the warp-level kernels
+
+// A part of a shared unit's row: (running max, sum) and the unnormalised output.
+__device__ __forceinline__ void put_part(const AttnArgs& a, int slot, int i, float m, float l,
+                                         float4 o, int lane) {
+  const size_t at = (size_t)slot * kTile + i;
+  if (lane == 0) a.part_ml[at] = make_float2(m, l);
+  reinterpret_cast<float4*>(a.part_o + at * kDim)[lane] = o;
 }
 
 }  // namespace attn
