@@ -10,21 +10,22 @@
 //
 // How (sm_103a):
 //  * 16 warps of 128 registers, four a scheduler: with 8 (of 255) the warps' chains leave
-//    two thirds of the issue slots empty.  So the 16 queries lie in shared memory in the
-//    order of the product's operand (read once for four token tiles), the output alone in
-//    registers, and what feeds the warps in the last warp: its lane w walks warp w's
-//    units, looks its pieces' pages up and asks for their copies (walked by the warps
-//    themselves, that state is spilled: 146 us on 16 x 131K).  The other 15 are teams of 15,
-//    5 or 3;
-//  * a warp owns two stages of one piece (keys, values and their scales).  Its area, 9 KB, is
-//    also where a warp of the upper half of a team leaves its state at a unit's end, so
-//    those warps get the next unit's pieces only after it;
+//    two thirds of the issue slots empty (120 us on 16 x 131K).  So the 16 queries lie in
+//    shared memory in the order of the product's operand, the output alone in registers, and
+//    what a warp does not need in its loop (the walk, the stretch) waits in shared memory;
+//  * a warp owns two stages of one piece (keys, values and their scales) and refills each as
+//    soon as it has been used.  Its copies end with the unit: a stage's 9 KB are then where
+//    the warp leaves its state, and a row's 16 states are joined by one warp.  (A warp that
+//    feeds the 15 others, across units: its copies, one lane after the other, took 3800
+//    cycles a round: 100 us);
 //  * a lane's 16 bytes of a key are 32 dims of it, two groups; its 8 bytes of a value are one
 //    group, whose dims are the 16 product tiles, so one scale serves all of them.  Two
 //    tokens' codes of one dim are put side by side by masks, without a permutation.  A code
 //    times its scale is exact in f16, the queries are f16 as for e4m3 keys;
-//  * the weights are f16 against 2^kHead below the maximum's 2^m, the most that f16 allows a
-//    weight of 1: 11 bits of each, down to 2^-28 of the row's largest, 2^-39 of it below.
+//  * the weights are f16 in units of 2^m, which is only raised, to 2^kHead below the row's
+//    maximum, when a score passes it by 2^(kHead + kSlack), the most that f16 holds: 11 bits of
+//    each, or 2^-32 of the row's largest.  So the output is seldom rescaled (raised with
+//    every new maximum, nearly every piece of 16 rows did).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,9 +42,9 @@ namespace {
 using namespace attn;
 
 constexpr int kItem = 32;      // tokens of a piece
-constexpr int NW = 15;         // warps that have units
+constexpr int NW = 16;         // warps
 constexpr int D = 2;           // stages of a warp
-constexpr float kHead = 14.f;
+constexpr float kHead = 7.f, kSlack = 8.f;   // log2 units
 constexpr int kColdWords = 28;
 
 // What a piece needs to know of a packed row, in shared memory: the scores' factor, the
@@ -55,7 +56,7 @@ struct Row {
 };
 
 struct L {
-  static constexpr int kThreads = 32 * (NW + 1);     // and the warp that feeds them
+  static constexpr int kThreads = 32 * NW;
   static constexpr int kTileBytes = kItem * 64;      // keys or values of a piece
   static constexpr int kScaleBytes = kItem * 8;
   static constexpr int kArea = D * 2 * (kTileBytes + kScaleBytes);   // of a warp: tiles, then scales
@@ -64,23 +65,22 @@ struct L {
   static constexpr int kStateStride = kDim + 16;
   static_assert(kTile * kStateStride * 4 <= kArea, "a state in a warp's area");
   static_assert(kArea % 512 == 0, "the 64-byte swizzle's period");
-  static constexpr int kTeams = NW / 3;
+  static constexpr int kTeams = NW / 2;
   static constexpr int kQOff = NW * kArea;           // a team's queries, in operand order
   static constexpr int kPostOff = kQOff + kTeams * kTile * 256;
   static constexpr int kMlOff = kPostOff + kTeams * kTile * sizeof(Row);   // (max, sum) of a warp's rows
   static constexpr int kInfoOff = kMlOff + NW * kTile * 8;       // whether a piece in flight exists
-  // (and the items of a team's list); full, empty [warp][stage], go [warp], stall
-  static constexpr int kBarOff = (kInfoOff + (NW * D + kTeams) * 4 + 7) & ~7;
-  static constexpr int kNumBars = 2 * NW * D + NW + 1;
+  static constexpr int kBarOff = (kInfoOff + NW * D * 4 + 7) & ~7;
+  static constexpr int kNumBars = NW * D + 1;                    // a stage's, the stall test's
   static constexpr int kColdOff = kBarOff + kNumBars * 8;        // what a warp does not need in its loop
-  static constexpr int kCtlOff = kColdOff + NW * kColdWords * 4;  // flags, longest unit, abort, one int a warp
-  static constexpr int kPreOff = (kCtlOff + 12 + (NW + 1) * 4 + 15) & ~15;
+  static constexpr int kCtlOff = kColdOff + NW * kColdWords * 4;  // flags, longest unit, one int a warp
+  static constexpr int kPreOff = (kCtlOff + 8 + NW * 4 + 15) & ~15;
   static constexpr int kListOff = kPreOff + kRequestsBytes;
   static constexpr int kBytes = kListOff + kMaxList * 4;
   static constexpr int kSmem = kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   // the bits that lists are joined with lie in the team's areas, where nothing is in flight then
-  static_assert(2 * kMaxBlockWords * 4 <= 3 * kArea, "block bits");
+  static_assert(2 * kMaxBlockWords * 4 <= 2 * kArea, "block bits");
 };
 
 // The token of an NVFP4 piece's 8-token tile that is column 2t + e of the scores' tile and
@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 
 // Softmax state of the two rows a lane holds (g and g + 8), and its part of the
 // unnormalised output: dims 32t + j of o[j][0] (row g) and o[j][2] (row g + 8), 32t + 16 + j
-// of o[j][1] and o[j][3].  m in log2 units, kHead below the running maximum.
+// of o[j][1] and o[j][3].  m: the weights' unit, in log2 units.
 struct State {
   float m0, m1, l0, l1;
   float o[16][4];
@@ -108,22 +108,37 @@ struct State {
   }
 };
 
-// One 32-token piece.  q: the queries in operand order, step c takes the dims 32t + 4c + {0, 1}
-// and + {2, 3}.  kMask: some token of the piece lies outside some row (past its length, or
-// the row's draft does not list the block) or at or past glen, where the cache holds anything:
-// such values are dropped by selection, not by a product with zero.
-// (The lane is asked for anew: what follows from it is cheaper made again than kept or
-// spilled.)
+// Where a lane reads in a piece: its key (of a tile; the scores' column), that key's two
+// scales, its first value's codes and scale, packed so that they cost one register.  The
+// second value's (token4(t, 1) = token4(t, 0) ^ 3) follow from them.
+struct Places {
+  uint32_t w;
+  __device__ __forceinline__ explicit Places(int lane) {
+    const int t = lane & 3, g = lane >> 2;
+    const int tok = token4(g >> 1, g & 1), ta = token4(t, 0);
+    const uint32_t key = tok * 64 + ((t ^ (tok >> 1)) << 4), key_scale = tok * 8 + 2 * t;
+    const uint32_t value = ta * 64 + (((g >> 1) ^ (ta >> 1)) << 4) + (g & 1) * 8, value_scale = ta * 8 + g;
+    w = key | (key_scale << 9) | (value << 15) | (value_scale << 24);
+  }
+  __device__ __forceinline__ uint32_t key() const { return w & 511u; }
+  __device__ __forceinline__ uint32_t key_scale() const { return (w >> 9) & 63u; }
+  __device__ __forceinline__ uint32_t value() const { return (w >> 15) & 511u; }
+  __device__ __forceinline__ uint32_t value_scale() const { return w >> 24; }
+  static constexpr uint32_t kValue1 = (3u << 6) | (1u << 4), kScale1 = 3u << 3;
+};
+
+// One 32-token piece.  q: the queries in operand order (the lane's place in a step), step c
+// takes the dims 32t + 4c + {0, 1} and + {2, 3}.  kMask: some token of the piece lies outside some row
+// (past its length, or the row's draft does not list the block) or at or past glen, where
+// the cache holds anything: such values are dropped by selection, not by a product with zero.
 template <bool kMask>
 __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, uint32_t stage,
-                                      uint32_t scales, int tb, uint32_t members, int glen) {
-  int lane;
-  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+                                      uint32_t scales, const Places& at, int tb, uint32_t members, int glen) {
+  const int lane = threadIdx.x & 31;
   const int t = lane & 3, g = lane >> 2;
   float s[4][4];
   {
-    const int tok = token4(g >> 1, g & 1);
-    const uint32_t krow = stage + tok * 64 + ((t ^ (tok >> 1)) << 4), ks = scales + tok * 8 + 2 * t;
+    const uint32_t krow = stage + at.key(), ks = scales + at.key_scale();
 #pragma unroll
     for (int n2 = 0; n2 < 4; n2 += 2) {
       uint32_t w[2][4], sc[2];
@@ -137,7 +152,7 @@ __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, ui
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const uint4 u = lds128(q + c * 512 + lane * 16);
+        const uint4 u = lds128(q + c * 512);
         const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -175,10 +190,21 @@ __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, ui
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
   }
-  const float mn0 = fmaxf(st.m0, fmaf(mx0, post0, -kHead)), mn1 = fmaxf(st.m1, fmaf(mx1, post1, -kHead));
-  const float ref0 = mn0 == -INFINITY ? 0.f : mn0, ref1 = mn1 == -INFINITY ? 0.f : mn1;
-  const float c0 = ex2_approx(st.m0 - ref0), c1 = ex2_approx(st.m1 - ref1);
-  st.m0 = mn0, st.m1 = mn1;
+  // (where nothing has been seen yet m is -inf, and any score raises it)
+  const float top0 = mx0 * post0, top1 = mx1 * post1;
+  if (__any_sync(0xffffffffu, top0 > st.m0 + (kHead + kSlack) || top1 > st.m1 + (kHead + kSlack))) {
+    const float n0 = top0 > st.m0 + (kHead + kSlack) ? top0 - kHead : st.m0;
+    const float n1 = top1 > st.m1 + (kHead + kSlack) ? top1 - kHead : st.m1;
+    const float c0 = n0 == -INFINITY ? 1.f : ex2_approx(st.m0 - n0), c1 = n1 == -INFINITY ? 1.f : ex2_approx(st.m1 - n1);
+    st.m0 = n0, st.m1 = n1;
+    st.l0 *= c0, st.l1 *= c1;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      st.o[j][0] *= c0, st.o[j][1] *= c0;
+      st.o[j][2] *= c1, st.o[j][3] *= c1;
+    }
+  }
+  const float ref0 = st.m0 == -INFINITY ? 0.f : st.m0, ref1 = st.m1 == -INFINITY ? 0.f : st.m1;
   const float2 p0 = make_float2(post0, post0), p1 = make_float2(post1, post1);
   const float2 r0 = make_float2(-ref0, -ref0), r1 = make_float2(-ref1, -ref1);
   float2 l0 = make_float2(0.f, 0.f), l1 = l0;
@@ -194,19 +220,11 @@ __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, ui
     p[nt / 2][2 * (nt % 2)] = pack_f16(y0[nt].x, y0[nt].y);
     p[nt / 2][2 * (nt % 2) + 1] = pack_f16(y1[nt].x, y1[nt].y);
   }
-  st.l0 = fmaf(st.l0, c0, l0.x + l0.y);
-  st.l1 = fmaf(st.l1, c1, l1.x + l1.y);
-  if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      st.o[j][0] *= c0, st.o[j][1] *= c0;
-      st.o[j][2] *= c1, st.o[j][3] *= c1;
-    }
-  }
-  // (the two tokens' rows differ in the bits that the swizzle goes by)
-  const uint32_t va = stage + L::kTileBytes + ta * 64 + (((g >> 1) ^ (ta >> 1)) << 4) + (g & 1) * 8;
-  const uint32_t vc = stage + L::kTileBytes + tc * 64 + (((g >> 1) ^ (tc >> 1)) << 4) + (g & 1) * 8;
-  const uint32_t sa = scales + L::kScaleBytes + g + ta * 8, sb = scales + L::kScaleBytes + g + tc * 8;
+  st.l0 += l0.x + l0.y;
+  st.l1 += l1.x + l1.y;
+  const uint32_t va = stage + L::kTileBytes + at.value(), vc = stage + L::kTileBytes + (at.value() ^ Places::kValue1);
+  const uint32_t sa = scales + L::kScaleBytes + at.value_scale();
+  const uint32_t sb = scales + L::kScaleBytes + (at.value_scale() ^ Places::kScale1);
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     uint2 a[2], c[2];
@@ -278,139 +296,6 @@ __device__ __forceinline__ bool whole_units(const AttnArgs& a, const Requests& r
 // Words of a team's joined list.
 __host__ __device__ constexpr int team_list_words(int tw) { return kMaxList / (NW / tw); }
 
-// The units of a team, as its warps and the lane that feeds each of them walk them: the CTA's
-// stretch of the line (kCut, TW = NW), or whole units dealt in turn to the teams of all CTAs.
-template <bool kBlocks, int TW, bool kCut>
-struct Team {
-  static_assert(NW % TW == 0 && TW % 2 == 1 && (!kCut || TW == NW), "teams");
-  // At a unit's end members nh .. TW - 1 leave their states in their areas, the first nh add
-  // theirs to those of the members nh + 1 on.
-  static constexpr int nh = TW / 2;
-  Walk walk;
-  __device__ __forceinline__ Team(const AttnArgs& a, const Requests& rq, int team, int W, int C) {
-    const int c = blockIdx.x;
-    if (kCut)
-      walk.begin(a, rq.pre, c < C ? W * c / C : 0, c < C ? W * (c + 1) / C : 0);
-    else
-      walk.begin_units(a, team * (int)gridDim.x + c, (NW / TW) * (int)gridDim.x);
-  }
-  __device__ __forceinline__ Segment next(const AttnArgs& a, const Requests& rq) {
-    return kCut ? walk.next(a, rq.pre) : walk.next_unit(a, rq.pre);
-  }
-  // Items member, member + TW, ... of the stretch.
-  static __device__ __forceinline__ int pieces(const Items& it, int member) {
-    return max(0, (it.i1 - it.i0 - member + TW - 1) / TW);
-  }
-};
-
-__device__ __forceinline__ uint32_t full_bar(uint32_t sbase, int warp, int k) { return sbase + L::kBarOff + (warp * D + k % D) * 8; }
-__device__ __forceinline__ uint32_t empty_bar(uint32_t sbase, int warp, int k) { return full_bar(sbase, NW + warp, k); }
-__device__ __forceinline__ uint32_t go_bar(uint32_t sbase, int warp) { return sbase + L::kBarOff + (2 * NW * D + warp) * 8; }
-__device__ __forceinline__ uint32_t stall_bar(uint32_t sbase) { return go_bar(sbase, NW); }
-__device__ __forceinline__ int tiles_of(int warp, int k) { return warp * L::kArea + (k % D) * 2 * L::kTileBytes; }
-__device__ __forceinline__ int scales_of(int warp, int k) {
-  return warp * L::kArea + D * 2 * L::kTileBytes + (k % D) * 2 * L::kScaleBytes;
-}
-
-// Lane w of the feeding warp: warp w's pieces.  It asks for one as soon as a stage is free
-// and, where the warp's area or list was in use between two units (`gated`), the warp has
-// said go.  The page id is loaded a piece ahead.  Nothing here waits: a lane that cannot go
-// on is passed over, and all give up when none has for the wait's limit.
-template <bool kBlocks, int TW, bool kCut>
-__device__ __forceinline__ void feed_warps(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                                           uint8_t* smem, const Requests& rq, int W, int C) {
-  using T = Team<kBlocks, TW, kCut>;
-  const uint32_t sbase = smem_u32(smem);
-  unsigned int* ctl = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
-  volatile unsigned int* abort_flag = ctl + 2;
-  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
-  const int lane = threadIdx.x & 31, w = lane < NW ? lane : 0, member = w % TW;
-  const uint32_t* list = reinterpret_cast<const uint32_t*>(smem + L::kListOff) + team_list_words(TW) * (w / TW);
-  const bool gated = kBlocks || member >= T::nh;
-  T team(a, rq, w / TW, W, C);
-  Items it = {};
-  Segment s = {};
-  int left = 0, i = 0, units = 0, issued = 0, page = 0, tb = 0;
-  bool more = lane < NW, waiting = false;   // waiting: for the warp to say go
-  auto look_up = [&]() {
-    uint32_t unused;
-    page = -1;
-    if (item_tokens<kItem, kBlocks>(it, list, i, tb, unused))
-      page = __ldg(a.page_table + (size_t)it.slot * a.max_pages + tb / kPage);
-    else
-      tb = -1;
-  };
-  uint64_t t0 = global_timer_ns();
-  bool gave_up = false;
-  while (__any_sync(0xffffffffu, more) && !gave_up) {
-    bool did = false;
-    if (more && left == 0 && !waiting) {       // the next stretch
-      if (!team.walk.more()) {
-        more = false;
-      } else {
-        s = team.next(a, rq);
-        did = true;
-        if (s.live) {
-          if (kBlocks) {
-            waiting = true;
-          } else {
-            it = make_items<kItem, kBlocks>(a, rq, s, 0);
-            left = T::pieces(it, member);
-            i = it.i0 + member;
-            waiting = gated;
-            if (left > 0) look_up();
-          }
-        }
-      }
-    }
-    if (waiting && mbar_test_wait(go_bar(sbase, w), (uint32_t)(units & 1))) {
-      ++units;
-      waiting = false;
-      did = true;
-      if (kBlocks) {
-        it = make_items<kItem, kBlocks>(a, rq, s, infos[NW * D + w / TW]);
-        left = T::pieces(it, member);
-        i = it.i0 + member;
-        if (left > 0) look_up();
-      }
-    }
-    if (more && left > 0 && !waiting &&
-        (issued < D || mbar_test_wait(empty_bar(sbase, w, issued), (uint32_t)((issued / D - 1) & 1)))) {
-      const uint32_t bar = full_bar(sbase, w, issued);
-      const bool there = page >= 0 && page < a.num_pages;
-      if (tb >= 0 && !there) atomicOr(ctl, kErrBadPage);
-      infos[w * D + issued % D] = there;
-      mbar_arrive_expect_tx(bar, there ? 2 * (L::kTileBytes + L::kScaleBytes) : 0);
-      if (there) {
-        const int row = (page * a.kv_heads + it.kv_head) * kPage + tb % kPage;
-        const uint32_t to = sbase + tiles_of(w, issued), sc = sbase + scales_of(w, issued);
-        tma_load_2d(to, &k_map, 0, row, bar);
-        bulk_load(sc, a.k_scale + (size_t)row * 2, L::kScaleBytes, bar);
-        tma_load_2d(to + L::kTileBytes, &v_map, 0, row, bar);
-        bulk_load(sc + L::kScaleBytes, a.v_scale + (size_t)row * 2, L::kScaleBytes, bar);
-      }
-      ++issued;
-      i += TW;
-      if (--left > 0) look_up();
-      did = true;
-    }
-    if (__any_sync(0xffffffffu, did))
-      t0 = global_timer_ns();
-    else
-      gave_up = global_timer_ns() - t0 > a.wait_ns + a.wait_ns / 2;
-    gave_up = __any_sync(0xffffffffu, gave_up || *abort_flag);
-  }
-  if (gave_up && lane == 0) {
-    atomicOr(ctl, kErrTimeout);
-    *abort_flag = 1;
-  }
-  // after a timeout: the copies in flight land before the block ends
-  if (gave_up && lane < NW)
-    for (int k = max(0, issued - D); k < issued; ++k)
-      (void)mbar_wait_bounded(full_bar(sbase, w, k), (uint32_t)((k / D) & 1), 200000000ull);
-  __syncwarp();
-}
-
 // Every word of a walk and of a stretch.
 template <class F>
 __device__ __forceinline__ void each_word(F&& f, Walk& w, Segment& s, Items& it) {
@@ -420,16 +305,14 @@ __device__ __forceinline__ void each_word(F&& f, Walk& w, Segment& s, Items& it)
   static_assert(kColdWords >= 24, "room for them");
 }
 
-// A warp's share of the CTA's units, TW warps a unit.  record: the unit the CTA started and
-// did not end.
+// The CTA's units, TW warps a unit: its stretch of the line (kCut, TW = NW), or whole units
+// dealt in turn to the teams of all CTAs.  record: the unit the CTA started and did not end.
 template <bool kBlocks, int TW, bool kCut>
-__device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, const Requests& rq, int W, int C,
-                                          SplitRecord& record) {
-  using T = Team<kBlocks, TW, kCut>;
-  constexpr int nh = T::nh;
+__device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                          uint8_t* smem, const Requests& rq, int W, int C, SplitRecord& record) {
+  static_assert(TW >= 2 && NW % TW == 0 && (!kCut || TW == NW), "teams");
   const uint32_t sbase = smem_u32(smem);
   unsigned int* cta_flags = reinterpret_cast<unsigned int*>(smem + L::kCtlOff);
-  volatile unsigned int* abort_flag = cta_flags + 2;
   // (one value a warp, and the compiler knows it)
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -439,14 +322,31 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
   uint8_t* q_rows = smem + L::kQOff + team * (kTile * 256);
   Row* rows = reinterpret_cast<Row*>(smem + L::kPostOff) + team * kTile;
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
-  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff);
-  auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TW * 32) : "memory"); };
   int* cold = reinterpret_cast<int*>(smem + L::kColdOff) + warp * kColdWords;
+  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff) + warp * D;
+  auto team_sync = [&]() {
+    if (TW == NW)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TW * 32) : "memory");
+  };
+  // The warp's D stages are used in turn: its k-th piece lies in stage k % D.
+  auto tiles_of = [&](int k) { return sbase + warp * L::kArea + (k % D) * 2 * L::kTileBytes; };
+  auto scales_of = [&](int k) {
+    return sbase + warp * L::kArea + D * 2 * L::kTileBytes + (k % D) * 2 * L::kScaleBytes;
+  };
+  auto bar_of = [&](int k) { return sbase + L::kBarOff + (warp * D + k % D) * 8; };
+  const Places places(lane);
+  const uint32_t q_at = smem_u32(q_rows) + lane * 16;
   bool dead = false;
   int used = 0;          // pieces this warp has waited for
-  T units(a, rq, team, W, C);
-  while (units.walk.more()) {
-    Segment s = units.next(a, rq);
+  Walk walk;
+  if (kCut)
+    walk.begin(a, rq.pre, c < C ? W * c / C : 0, c < C ? W * (c + 1) / C : 0);
+  else
+    walk.begin_units(a, team * (int)gridDim.x + c, (NW / TW) * (int)gridDim.x);
+  while (walk.more()) {
+    Segment s = kCut ? walk.next(a, rq.pre) : walk.next_unit(a, rq.pre);
     if (!s.live) continue;
     const int row_first = s.group * kTile;
     const int nrows = min(kTile, a.P * a.nq - row_first);
@@ -456,46 +356,85 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
       n_items = join_lists(a, rq, s, p0, (row_first + nrows - 1) / a.nq, list, bits,
                            threadIdx.x % (32 * TW), 32 * TW, team_sync) *
                 (kBlock / kItem);
-      if (threadIdx.x % (32 * TW) == 0) infos[NW * D + team] = n_items;
       // the areas that held the bits get copies again
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       team_sync();
     }
-    if ((kBlocks || member >= nh) && lane == 0) mbar_arrive(go_bar(sbase, warp));
     Items it = make_items<kItem, kBlocks>(a, rq, s, n_items);
+    // ---- the warp's pieces: items member, member + TW, ... of the stretch.  Page ids 32
+    // pieces at a time, one a lane; -1: nothing to read there ------------------------
+    const int n = max(0, (it.i1 - it.i0 - member + TW - 1) / TW), first = it.i0 + member, glen = it.glen;
+    const int slot = it.slot, kv_head = it.kv_head;
+    auto ids_of = [&](int k) {
+      int tb = 0, page = -1;
+      uint32_t unused;
+      if (k < n && item_tokens<kItem, kBlocks>(glen, list, first + k * TW, tb, unused)) {
+        page = __ldg(a.page_table + (size_t)slot * a.max_pages + tb / kPage);
+        if (page < 0 || page >= a.num_pages) {
+          atomicOr(cta_flags, kErrBadPage);
+          page = -1;
+        }
+      }
+      return page;
+    };
+    int ids = ids_of(lane);
+    // ask for the copies of piece k of the unit, the warp's piece j of all
+    auto issue = [&](int k, int j) {
+      if (k > 0 && (k & 31) == 0) ids = ids_of(k + lane);
+      const int page = __shfl_sync(0xffffffffu, ids, k & 31);
+      if (lane == 0) {
+        int tb;
+        uint32_t unused;
+        item_tokens<kItem, kBlocks>(glen, list, first + k * TW, tb, unused);
+        const uint32_t bar = bar_of(j);
+        infos[j % D] = page >= 0;
+        mbar_arrive_expect_tx(bar, page >= 0 ? 2 * (L::kTileBytes + L::kScaleBytes) : 0);
+        if (page >= 0) {
+          const int row = (page * a.kv_heads + kv_head) * kPage + tb % kPage;
+          const uint32_t to = tiles_of(j), sc = scales_of(j);
+          tma_load_2d(to, &k_map, 0, row, bar);
+          bulk_load(sc, a.k_scale + (size_t)row * 2, L::kScaleBytes, bar);
+          tma_load_2d(to + L::kTileBytes, &v_map, 0, row, bar);
+          bulk_load(sc + L::kScaleBytes, a.v_scale + (size_t)row * 2, L::kScaleBytes, bar);
+        }
+      }
+      __syncwarp();      // the piece's word is there for every lane
+    };
     auto q_index = [&](int pk, int p) {   // packed row pk of the unit head, draft row p = pk / nq
       return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
     };
     // ---- the unit's queries: the warp's rows, to f16 scaled a row by the power of two that
     // brings the row's largest magnitude into [2^7, 2^8) (undone by post) ----------
-    constexpr int kMine = (kTile + TW - 1) / TW;
+    for (int k = 0; k < D && k < n && !dead; ++k) issue(k, used + k);
+    constexpr int kMine = kTile / TW;
     uint2 qw[kMine];
+    int lens[kMine];
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
       const int i = member + k * TW, pk = row_first + i;
       qw[k] = make_uint2(0, 0);
+      // with one draft row the request's longest row is the row
+      lens[k] = i < nrows && glen > 0 ? a.P == 1 ? glen : row_len(a, s.r, a.by_nq.div(pk)) : 0;
       if (i < nrows) qw[k] = __ldg(reinterpret_cast<const uint2*>(a.q + q_index(pk, a.by_nq.div(pk)) * kDim) + lane);
     }
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
       const int i = member + k * TW;
-      if (i >= kTile) break;
       float top = fmaxf(fmaxf(fabsf(bf16_lo(qw[k].x)), fabsf(bf16_hi(qw[k].x))),
                         fmaxf(fabsf(bf16_lo(qw[k].y)), fabsf(bf16_hi(qw[k].y))));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int x = to_2_7(top);
-      const float up = ldexpf(1.f, x);
+      auto power = [](int e) { return __uint_as_float((uint32_t)(e + 127) << 23); };   // -120 .. 120
+      const float up = power(x);
       // dims 4 lane ..: step lane % 8, the operand's lane (row % 8, lane / 8), its words of row / 8
       uint32_t* to = reinterpret_cast<uint32_t*>(q_rows + (lane & 7) * 512 + ((i & 7) * 4 + lane / 8) * 16) + i / 8;
       to[0] = pack_f16(bf16_lo(qw[k].x) * up, bf16_hi(qw[k].x) * up);
       to[2] = pack_f16(bf16_lo(qw[k].y) * up, bf16_hi(qw[k].y) * up);
       if (lane == 0) {
         const int p = a.by_nq.div(row_first + i);
-        const bool has = i < nrows && it.glen > 0;
-        // with one draft row the request's longest row is the row
-        rows[i] = {fmaxf(a.scale_log2 * ldexpf(1.f, -x), kLeastPost),
-                   !has ? 0 : a.P == 1 ? it.glen : row_len(a, s.r, p), kBlocks && has ? 1u << (p - p0) : has ? 1u : 0u};
+        const bool has = i < nrows && glen > 0;
+        rows[i] = {fmaxf(a.scale_log2 * power(-x), kLeastPost), lens[k], has ? kBlocks ? 1u << (p - p0) : 1u : 0u};
       }
     }
     team_sync();
@@ -508,55 +447,50 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
       drafts = __reduce_or_sync(0xffffffffu, r.bit);
     }
     // ---- the walk and the stretch wait in shared memory: 128 registers are the loop's ------
-    const int n = T::pieces(it, member), glen = it.glen;
-    int i = it.i0 + member;
     if (lane == 0) {
       int* k = cold;
-      each_word([&](int& x) { *k++ = x; }, units.walk, s, it);
+      each_word([&](int& x) { *k++ = x; }, walk, s, it);
     }
     __syncwarp();
     State st;
     st.reset();
     // ---- its pieces -----------------------------------------------------------
-    for (int k = 0; k < n && !dead; ++k, i += TW) {
+    for (int k = 0; k < n && !dead; ++k) {
       int tb;
       uint32_t members;
-      item_tokens<kItem, kBlocks>(glen, list, i, tb, members);
+      item_tokens<kItem, kBlocks>(glen, list, first + k * TW, tb, members);
       const bool stall = a.stall_test && warp == 0 && used == 0;
-      bool ok = mbar_try_wait(stall ? stall_bar(sbase) : full_bar(sbase, warp, used), stall ? 0u : (uint32_t)((used / D) & 1));
-      const uint64_t t0 = ok ? 0 : global_timer_ns();
-      while (!ok) {
-        ok = mbar_try_wait(stall ? stall_bar(sbase) : full_bar(sbase, warp, used), stall ? 0u : (uint32_t)((used / D) & 1));
-        if (!ok && (*abort_flag || global_timer_ns() - t0 > a.wait_ns)) break;
-      }
+      const bool ok = mbar_wait_bounded(stall ? sbase + L::kBarOff + NW * D * 8 : bar_of(used),
+                                        stall ? 0u : (uint32_t)((used / D) & 1), a.wait_ns);
       dead = __any_sync(0xffffffffu, !ok);
       if (dead) {
         if (lane == 0) {
           atomicOr(cta_flags, kErrTimeout);
-          *abort_flag = 1;
-          // the unit's copies in flight land: the area is written to below
+          // the copies in flight land
           for (int j = 0; j < D && k + j < n; ++j)
-            (void)mbar_wait_bounded(full_bar(sbase, warp, used + j), (uint32_t)(((used + j) / D) & 1), 200000000ull);
+            (void)mbar_wait_bounded(bar_of(used + j), (uint32_t)(((used + j) / D) & 1), 200000000ull);
         }
+        used += min(D, n - k);
         __syncwarp();
         break;
       }
-      if (infos[warp * D + used % D]) {
-        const uint32_t tiles = sbase + tiles_of(warp, used), scales = sbase + scales_of(warp, used);
+      if (infos[used % D]) {
         if (tb + kItem <= safe && (!kBlocks || (members & drafts) == drafts))
-          piece<false>(smem_u32(q_rows), rows, st, tiles, scales, tb, members, glen);
+          piece<false>(q_at, rows, st, tiles_of(used), scales_of(used), places, tb, members, glen);
         else
-          piece<true>(smem_u32(q_rows), rows, st, tiles, scales, tb, members, glen);
+          piece<true>(q_at, rows, st, tiles_of(used), scales_of(used), places, tb, members, glen);
       }
+      // every lane's reads of the stage come before the copies that refill it
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty_bar(sbase, warp, used));
+      if (k + D < n) issue(k + D, used + D);
       ++used;
     }
     {
       volatile const int* k = cold;
-      each_word([&](int& x) { x = *k++; }, units.walk, s, it);
+      each_word([&](int& x) { x = *k++; }, walk, s, it);
     }
-    // ---- join the warps: the upper half into the lower, then those by rows -----
+    // ---- join the warps: a state each, then by rows ------------------------------
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
       st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, o);
@@ -564,44 +498,14 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
     }
     st.m0 = not_empty(st.m0, st.l0);
     st.m1 = not_empty(st.m1, st.l1);
-    const int place = warp + (member < nh ? nh + 1 : 0);   // whose area takes the state
-    float* w0 = reinterpret_cast<float*>(smem + place * L::kArea) + g * L::kStateStride;
-    float2* ml0 = ml + place * kTile + g;
-    auto put = [&]() {
-      if (t == 0) {
-        ml0[0] = make_float2(st.m0, st.l0);
-        ml0[8] = make_float2(st.m1, st.l1);
-      }
-      each_quad(w0, t, [&](float4* to, int j, int e) {
-        *to = make_float4(st.o[j][e], st.o[j + 1][e], st.o[j + 2][e], st.o[j + 3][e]);
-      });
-    };
-    if (member >= nh) put();
-    team_sync();
-    if (member < nh) {
-      const float2 x0 = ml0[0], x1 = ml0[8];
-      const float n0 = fmaxf(st.m0, x0.x), n1 = fmaxf(st.m1, x1.x);
-      const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
-      // a half with nothing visible in the row holds zeros (or 0 * NaN: dropped)
-      const bool ha0 = st.m0 != -INFINITY, ha1 = st.m1 != -INFINITY;
-      const bool hb0 = x0.x != -INFINITY, hb1 = x1.x != -INFINITY;
-      const float a0 = ex2_approx(st.m0 - r0), a1 = ex2_approx(st.m1 - r1);
-      const float b0 = ex2_approx(x0.x - r0), b1 = ex2_approx(x1.x - r1);
-      st.l0 = (ha0 ? st.l0 * a0 : 0.f) + (hb0 ? x0.y * b0 : 0.f);
-      st.l1 = (ha1 ? st.l1 * a1 : 0.f) + (hb1 ? x1.y * b1 : 0.f);
-      st.m0 = n0, st.m1 = n1;
-      each_quad(w0, t, [&](float4* from, int j, int e) {
-        const float4 v = *from;
-        const float x[4] = {v.x, v.y, v.z, v.w};
-        const bool ha = e < 2 ? ha0 : ha1, hb = e < 2 ? hb0 : hb1;
-        const float fa = e < 2 ? a0 : a1, fb = e < 2 ? b0 : b1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st.o[j + i][e] = (ha ? st.o[j + i][e] * fa : 0.f) + (hb ? x[i] * fb : 0.f);
-      });
-      __syncwarp();
-      put();
+    float* w0 = reinterpret_cast<float*>(smem + warp * L::kArea) + g * L::kStateStride;
+    if (t == 0) {
+      ml[warp * kTile + g] = make_float2(st.m0, st.l0);
+      ml[warp * kTile + g + 8] = make_float2(st.m1, st.l1);
     }
+    each_quad(w0, t, [&](float4* to, int j, int e) {
+      *to = make_float4(st.o[j][e], st.o[j + 1][e], st.o[j + 2][e], st.o[j + 3][e]);
+    });
     team_sync();
     const int first_row = s.group * kTile, rows_here = min(kTile, a.P * a.nq - first_row), draft0 = a.by_nq.div(first_row);
     const bool complete = !kCut || (s.o0 == 0 && s.o1 == s.cap);
@@ -610,24 +514,29 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
       record.unit = s.unit;
       record.splits = owner(s.start + s.cap - 1, W, C) - c + 1;
     }
-    const int first = team * TW + nh;
     for (int i = member; i < rows_here; i += TW) {
       const int pk = first_row + i, p = a.by_nq.div(pk);
-      float m = -INFINITY, l = 0.f;
+      // one state a lane: their maximum, and what each is multiplied by (-1: a warp with
+      // nothing visible in the row, whose output is not read)
+      float2 x = make_float2(-INFINITY, 0.f);
+      if (lane < TW) x = ml[(team * TW + lane) * kTile + i];
+      float m = x.x;
 #pragma unroll
-      for (int w = 0; w < TW - nh; ++w) m = fmaxf(m, ml[(first + w) * kTile + i].x);
+      for (int d = TW / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = __shfl_sync(0xffffffffu, m, 0);
+      const float f = x.x == -INFINITY ? -1.f : ex2_approx(x.x - m);
+      float l = x.x == -INFINITY ? 0.f : x.y * f;
+#pragma unroll
+      for (int d = TW / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      l = __shfl_sync(0xffffffffu, l, 0);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < TW - nh; ++w) {
-          const float2 x = ml[(first + w) * kTile + i];
-          const float f = ex2_approx(x.x - m);
-          if (x.x == -INFINITY) continue;   // a warp with nothing visible in the row
-          const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (first + w) * L::kArea) +
-                                                            i * L::kStateStride + 4 * lane + 4 * (lane / 8));
-          l = fmaf(x.y, f, l);
-          o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
-        }
+      for (int w = 0; w < TW; ++w) {
+        const float fw = __shfl_sync(0xffffffffu, f, w);
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (team * TW + w) * L::kArea) +
+                                                          i * L::kStateStride + 4 * lane + 4 * (lane / 8));
+        if (fw != -1.f)
+          o = make_float4(fmaf(v.x, fw, o.x), fmaf(v.y, fw, o.y), fmaf(v.z, fw, o.z), fmaf(v.w, fw, o.w));
       }
       if (__any_sync(0xffffffffu, !finite4(o)))
         careful_row<kNvfp4, kItem, kBlocks>(a, it, list, a.q + q_index(pk, p) * kDim,
@@ -641,15 +550,6 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, uint8_t* smem, cons
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     team_sync();
   }
-}
-
-template <bool kBlocks, int TW, bool kCut>
-__device__ __forceinline__ void run_cta(const AttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                                        uint8_t* smem, const Requests& rq, int W, int C, SplitRecord& record) {
-  if (threadIdx.x / 32 == NW)
-    feed_warps<kBlocks, TW, kCut>(a, k_map, v_map, smem, rq, W, C);
-  else
-    run_units<kBlocks, TW, kCut>(a, smem, rq, W, C, record);
 }
 
 enum class Deal { kCut, kWhole, kEither };
@@ -669,27 +569,26 @@ __global__ void __launch_bounds__(L::kThreads, 1)
     fence_barrier_init();
   }
   if (threadIdx.x == 0) {
-    cta_flags[2] = 0u;   // abort
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 3), cta_flags);
+  build_requests<kItem, kBlocks, false>(a, rq, reinterpret_cast<int*>(cta_flags + 2), cta_flags);
 
   const int W = rq.pre[a.R] * (int)a.by_per.d;
   const int C = min((W + kLeast - 1) / kLeast, (int)gridDim.x);
   SplitRecord record = {-1, 0};
   if constexpr (kDeal == Deal::kCut) {
-    run_cta<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
+    run_units<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
   } else if constexpr (kDeal == Deal::kWhole) {
-    run_cta<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
+    run_units<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
   } else {
     if (whole_units<TW>(a, rq, (int)cta_flags[1], C))
-      run_cta<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
+      run_units<kBlocks, TW, false>(a, k_map, v_map, smem, rq, W, C, record);
     else
-      run_cta<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
+      run_units<kBlocks, NW, true>(a, k_map, v_map, smem, rq, W, C, record);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -715,7 +614,7 @@ template <bool kBlocks>
 int team_for(AttnArgs& a, int grid, float pieces, float& least) {
   const int units = a.R * (int)a.by_per.d;
   int team = 0;
-  for (int tw : {15, 5, 3}) {
+  for (int tw = NW; tw >= 2; tw /= 2) {
     if (kBlocks && (a.P < kMaxDrafts ? a.P : kMaxDrafts) * a.topk > team_list_words(tw)) break;
     const int teams = grid * (NW / tw), full = units / teams, rest = units - full * teams;
     const float busy = (float)(rest * tw) / (float)grid;
@@ -743,9 +642,10 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
     // only, which decides whether they are dealt whole at all
     whole = false;
     switch (team_for<false>(a, grid, 16.f, least)) {
-      case 3: return launch_one<false, 3, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
-      case 5: return launch_one<false, 5, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
-      default: return launch_one<false, 15, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 2: return launch_one<false, 2, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 4: return launch_one<false, 4, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 8: return launch_one<false, 8, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      default: return launch_one<false, 16, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
     }
   }
   // the lists' length bounds the units', so the host decides, and a call that deals needs no join
@@ -756,11 +656,12 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
   const float cut = (share * pieces > Cost::kAlone ? share * pieces : Cost::kAlone) +
                     (Cost::kStretch + Cost::kList) * share + Cost::kCut + Cost::kList;
   whole = least <= 0.83f * cut;
-  if (!whole) return launch_one<true, 15, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
+  if (!whole) return launch_one<true, 16, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
   switch (team) {
-    case 3: return launch_one<true, 3, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
-    case 5: return launch_one<true, 5, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
-    default: return launch_one<true, 15, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 2: return launch_one<true, 2, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 4: return launch_one<true, 4, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 8: return launch_one<true, 8, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_one<true, 16, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
   }
 }
 
