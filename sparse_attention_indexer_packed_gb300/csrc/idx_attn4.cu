@@ -42,7 +42,7 @@ namespace {
 using namespace attn;
 
 constexpr int kItem = 32;      // tokens of a piece
-constexpr int NW = 16;         // warps
+constexpr int NW = 12;         // warps
 constexpr int D = 2;           // stages of a warp
 constexpr float kHead = 7.f, kSlack = 8.f;   // log2 units
 constexpr int kColdWords = 28;
@@ -65,12 +65,11 @@ struct L {
   static constexpr int kStateStride = kDim + 16;
   static_assert(kTile * kStateStride * 4 <= kArea, "a state in a warp's area");
   static_assert(kArea % 512 == 0, "the 64-byte swizzle's period");
-  static constexpr int kTeams = NW / 2;
+  static constexpr int kTeams = NW / 3;
   static constexpr int kQOff = NW * kArea;           // a team's queries, in operand order
   static constexpr int kPostOff = kQOff + kTeams * kTile * 256;
   static constexpr int kMlOff = kPostOff + kTeams * kTile * sizeof(Row);   // (max, sum) of a warp's rows
-  static constexpr int kInfoOff = kMlOff + NW * kTile * 8;       // whether a piece in flight exists
-  static constexpr int kBarOff = (kInfoOff + NW * D * 4 + 7) & ~7;
+  static constexpr int kBarOff = kMlOff + NW * kTile * 8;
   static constexpr int kNumBars = NW * D + 1;                    // a stage's, the stall test's
   static constexpr int kColdOff = kBarOff + kNumBars * 8;        // what a warp does not need in its loop
   static constexpr int kCtlOff = kColdOff + NW * kColdWords * 4;  // flags, longest unit, one int a warp
@@ -141,7 +140,7 @@ __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, ui
     const uint32_t krow = stage + at.key(), ks = scales + at.key_scale();
 #pragma unroll
     for (int n2 = 0; n2 < 4; n2 += 2) {
-      uint32_t w[2][4], sc[2];
+      uint32_t w[2][4], sc[2], f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int nt = n2 + h;
@@ -156,11 +155,11 @@ __device__ __forceinline__ void piece(uint32_t q, const Row* rows, State& st, ui
         const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (c % 4 == 0) f[h] = prmt(sc[h], 0u, c == 0 ? 0x1010 : 0x3232);
           uint32_t d0, d1;
           if (c & 1) e2m1x4_to_f16x2x2<1>(w[h][c / 2], d0, d1);
           else e2m1x4_to_f16x2x2<0>(w[h][c / 2], d0, d1);
-          const uint32_t f = prmt(sc[h], 0u, c < 4 ? 0x1010 : 0x3232);
-          mma_f16_16816(s[n2 + h], a, hmul2(d0, f), hmul2(d1, f));
+          mma_f16_16816(s[n2 + h], a, hmul2(d0, f[h]), hmul2(d1, f[h]));
         }
       }
     }
@@ -323,7 +322,6 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
   Row* rows = reinterpret_cast<Row*>(smem + L::kPostOff) + team * kTile;
   float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
   int* cold = reinterpret_cast<int*>(smem + L::kColdOff) + warp * kColdWords;
-  volatile int* infos = reinterpret_cast<volatile int*>(smem + L::kInfoOff) + warp * D;
   auto team_sync = [&]() {
     if (TW == NW)
       __syncthreads();
@@ -378,35 +376,35 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       return page;
     };
     int ids = ids_of(lane);
-    // ask for the copies of piece k of the unit, the warp's piece j of all
-    auto issue = [&](int k, int j) {
+    // Ask for the copies of piece k of the unit, the warp's piece j of all.  exist: a bit for
+    // each piece in flight, the oldest lowest; pieces that do not exist arrive at once.
+    uint32_t exist = 0u;
+    auto issue = [&](int k, int j, int place) {
       if (k > 0 && (k & 31) == 0) ids = ids_of(k + lane);
       const int page = __shfl_sync(0xffffffffu, ids, k & 31);
+      int tb;
+      uint32_t unused;
+      item_tokens<kItem, kBlocks>(glen, list, first + k * TW, tb, unused);
+      const uint32_t bar = bar_of(j), to = tiles_of(j), sc = scales_of(j);
+      exist |= page >= 0 ? 1u << place : 0u;
+      const int row = (page * a.kv_heads + kv_head) * kPage + tb % kPage;
       if (lane == 0) {
-        int tb;
-        uint32_t unused;
-        item_tokens<kItem, kBlocks>(glen, list, first + k * TW, tb, unused);
-        const uint32_t bar = bar_of(j);
-        infos[j % D] = page >= 0;
         mbar_arrive_expect_tx(bar, page >= 0 ? 2 * (L::kTileBytes + L::kScaleBytes) : 0);
         if (page >= 0) {
-          const int row = (page * a.kv_heads + kv_head) * kPage + tb % kPage;
-          const uint32_t to = tiles_of(j), sc = scales_of(j);
           tma_load_2d(to, &k_map, 0, row, bar);
           bulk_load(sc, a.k_scale + (size_t)row * 2, L::kScaleBytes, bar);
           tma_load_2d(to + L::kTileBytes, &v_map, 0, row, bar);
           bulk_load(sc + L::kScaleBytes, a.v_scale + (size_t)row * 2, L::kScaleBytes, bar);
         }
       }
-      __syncwarp();      // the piece's word is there for every lane
     };
     auto q_index = [&](int pk, int p) {   // packed row pk of the unit head, draft row p = pk / nq
       return ((size_t)s.r * a.P + p) * a.q_heads + s.head * a.nq + (pk - p * a.nq);
     };
     // ---- the unit's queries: the warp's rows, to f16 scaled a row by the power of two that
     // brings the row's largest magnitude into [2^7, 2^8) (undone by post) ----------
-    for (int k = 0; k < D && k < n && !dead; ++k) issue(k, used + k);
-    constexpr int kMine = kTile / TW;
+    for (int k = 0; k < D && k < n && !dead; ++k) issue(k, used + k, k);
+    constexpr int kMine = (kTile + TW - 1) / TW;
     uint2 qw[kMine];
     int lens[kMine];
 #pragma unroll
@@ -420,6 +418,7 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
       const int i = member + k * TW;
+      if (i >= kTile) break;
       float top = fmaxf(fmaxf(fabsf(bf16_lo(qw[k].x)), fabsf(bf16_hi(qw[k].x))),
                         fmaxf(fabsf(bf16_lo(qw[k].y)), fabsf(bf16_hi(qw[k].y))));
 #pragma unroll
@@ -474,7 +473,7 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
         __syncwarp();
         break;
       }
-      if (infos[used % D]) {
+      if (exist & 1u) {
         if (tb + kItem <= safe && (!kBlocks || (members & drafts) == drafts))
           piece<false>(q_at, rows, st, tiles_of(used), scales_of(used), places, tb, members, glen);
         else
@@ -483,7 +482,8 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       // every lane's reads of the stage come before the copies that refill it
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (k + D < n) issue(k + D, used + D);
+      exist >>= 1;
+      if (k + D < n) issue(k + D, used + D, D - 1);
       ++used;
     }
     {
@@ -522,12 +522,12 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       if (lane < TW) x = ml[(team * TW + lane) * kTile + i];
       float m = x.x;
 #pragma unroll
-      for (int d = TW / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       m = __shfl_sync(0xffffffffu, m, 0);
       const float f = x.x == -INFINITY ? -1.f : ex2_approx(x.x - m);
       float l = x.x == -INFINITY ? 0.f : x.y * f;
 #pragma unroll
-      for (int d = TW / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
       l = __shfl_sync(0xffffffffu, l, 0);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -614,7 +614,7 @@ template <bool kBlocks>
 int team_for(AttnArgs& a, int grid, float pieces, float& least) {
   const int units = a.R * (int)a.by_per.d;
   int team = 0;
-  for (int tw = NW; tw >= 2; tw /= 2) {
+  for (int tw : {12, 6, 3}) {
     if (kBlocks && (a.P < kMaxDrafts ? a.P : kMaxDrafts) * a.topk > team_list_words(tw)) break;
     const int teams = grid * (NW / tw), full = units / teams, rest = units - full * teams;
     const float busy = (float)(rest * tw) / (float)grid;
@@ -642,10 +642,9 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
     // only, which decides whether they are dealt whole at all
     whole = false;
     switch (team_for<false>(a, grid, 16.f, least)) {
-      case 2: return launch_one<false, 2, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
-      case 4: return launch_one<false, 4, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
-      case 8: return launch_one<false, 8, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
-      default: return launch_one<false, 16, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 3: return launch_one<false, 3, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      case 6: return launch_one<false, 6, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
+      default: return launch_one<false, 12, Deal::kEither>(a, k_map, v_map, grid, dev, stream);
     }
   }
   // the lists' length bounds the units', so the host decides, and a call that deals needs no join
@@ -656,12 +655,11 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
   const float cut = (share * pieces > Cost::kAlone ? share * pieces : Cost::kAlone) +
                     (Cost::kStretch + Cost::kList) * share + Cost::kCut + Cost::kList;
   whole = least <= 0.83f * cut;
-  if (!whole) return launch_one<true, 16, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
+  if (!whole) return launch_one<true, 12, Deal::kCut>(a, k_map, v_map, grid, dev, stream);
   switch (team) {
-    case 2: return launch_one<true, 2, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
-    case 4: return launch_one<true, 4, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
-    case 8: return launch_one<true, 8, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
-    default: return launch_one<true, 16, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 3: return launch_one<true, 3, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    case 6: return launch_one<true, 6, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+    default: return launch_one<true, 12, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
   }
 }
 
