@@ -126,7 +126,11 @@ static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit t
 // 48 ragged requests x 4 heads 36.2 / 28.3 / 24.9 / 26.9 at 4 / 8 / 12 / 24; 24
 // ragged requests with lists 25.5 / 20.6 / 17.8 / 18.1 at 4 / 8 / 24 / 48; 16 x 131K
 // with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
-inline int unit_cost(int group_rows, bool blocks) {
+// NVFP4, whose pieces of 16 rows take half the time: paged 48 ragged x 4 heads 30.3 / 23.5 /
+// 19.9 / 20.0 at 6 / 12 / 20 / 28, 8 x 32K 23.6 / 23.1 / 21.6 / 20.9; lists 16 x 131K 34.8 / 33.8 /
+// 33.2 at 16 / 24 / 32.
+inline int unit_cost(int group_rows, bool blocks, bool nvfp4) {
+  if (nvfp4 && group_rows <= 16) return blocks ? 32 : 28;
   return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
 }
 

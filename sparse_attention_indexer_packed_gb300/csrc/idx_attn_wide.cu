@@ -137,6 +137,10 @@ struct AWLayout {
   static constexpr int kSmem = kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kV16Off % 1024 == 0, "operand tiles on 1024 bytes");
+  // NVFP4: a unit's end, the outputs of the parts behind the first, half the dims a group,
+  // where the values were
+  static constexpr int kSwapStride = kDim / 2 + 4;
+  static_assert(KF != kNvfp4 || 2 * (F - 1) * (kLanes / F) * kSwapStride * 4 <= 4 * kV16, "outputs that change hands");
 };
 
 // Shared-memory descriptor of an operand whose rows run along M or N: the
@@ -275,7 +279,11 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
   using L = AWLayout<KF, F>;
   constexpr int NS = L::NS;
   constexpr int kPart = kTok / F;      // tokens of a lane
-  constexpr int kWarpRows = 32 / F;    // rows of a softmax warp
+  // NVFP4: the parts of a row's tokens are warps (lanes would have to select their scores
+  // from all columns, and to write zeros for the other parts' weights)
+  constexpr bool kByWarp = KF == kNvfp4;
+  constexpr int kWarpRows = kByWarp ? 32 : 32 / F;    // rows of a softmax warp
+  constexpr int kRowWarps = 4 / F;                    // warps that hold all rows (kByWarp)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(s_full(g), 1);
-      mbar_init(p_full(g), kLanes);
+      mbar_init(p_full(g), kByWarp ? 4 : kLanes);
       mbar_init(pv_done(g), 1);
       mbar_init(s_free(g), 4);
     }
@@ -420,13 +428,28 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           uint32_t m;
           item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, m);
           const int row = (pg * a.kv_heads + it.kv_head) * kPage;
+          if constexpr (KF == kNvfp4) {
+            // one barrier a page: its keys are decoded two pages before its values
+            if (!wait(empty_v(st), ph)) break;
+            if (lane == 0) {
+              info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
+              mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : 2 * (L::kTile + L::kScale));
+              if (pg >= 0) {   // a head page lies in one piece
+                const uint32_t sc = sbase + scales_at(st), bar = full_k(st);
+                bulk_load(k_tile(st), a.k_payload + (size_t)row * 64, L::kTile, bar);
+                bulk_load(sc, a.k_scale + (size_t)row * 2, L::kScale, bar);
+                bulk_load(v_tile(st), a.v_payload + (size_t)row * 64, L::kTile, bar);
+                bulk_load(sc + L::kScale, a.v_scale + (size_t)row * 2, L::kScale, bar);
+              }
+            }
+            ++sent_k;
+            __syncwarp();
+            continue;
+          }
           if (!wait(empty_k(st), ph)) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile + (KF == kNvfp4 ? L::kScale : 0));
-            if (pg >= 0 && KF == kNvfp4) {   // a head page lies in one piece
-              bulk_load(k_tile(st), a.k_payload + (size_t)row * 64, L::kTile, full_k(st));
-              bulk_load(sbase + scales_at(st), a.k_scale + (size_t)row * 2, L::kScale, full_k(st));
-            } else if (pg >= 0) {
+            mbar_arrive_expect_tx(full_k(st), pg < 0 ? 0 : L::kTile);
+            if (pg >= 0) {
               tma_load_2d(k_tile(st), &k_map, 0, row, full_k(st));
               if (KF == kBf16) tma_load_2d(k_tile(st) + L::kTile / 2, &k_map, 64, row, full_k(st));
             }
@@ -435,13 +458,10 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           if (!wait(empty_v(st), ph)) break;
           if (lane == 0) {
             info[st] = pg < 0 ? 0 : min(kTok, it.glen - tb);
-            // e4m3: both planes' scales come with the values: the group reads them, and
+            // both planes' scales come with the values: the group reads them, and
             // it gives the values' stage back itself
-            mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + (KF == kNvfp4 ? 1 : 2) * L::kScale);
-            if (pg >= 0 && KF == kNvfp4) {
-              bulk_load(v_tile(st), a.v_payload + (size_t)row * 64, L::kTile, full_v(st));
-              bulk_load(sbase + scales_at(st) + L::kScale, a.v_scale + (size_t)row * 2, L::kScale, full_v(st));
-            } else if (pg >= 0) {
+            mbar_arrive_expect_tx(full_v(st), pg < 0 ? 0 : L::kTile + 2 * L::kScale);
+            if (pg >= 0) {
               tma_load_2d(v_tile(st), &v_map, 0, row, full_v(st));
               if (KF == kBf16) {
                 tma_load_2d(v_tile(st) + L::kTile / 2, &v_map, 64, row, full_v(st));
@@ -517,8 +537,8 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
       } else {
         // ---- softmax group g: pages g, g + 2, ... ------------------------------
         const int g = warp >> 2, quad = warp & 3;
-        const int part = lane / kWarpRows;
-        const int row = quad * kWarpRows + lane % kWarpRows;   // of the group
+        const int part = kByWarp ? quad / kRowWarps : lane / kWarpRows;
+        const int row = (kByWarp ? quad % kRowWarps : quad) * kWarpRows + lane % kWarpRows;   // of the group
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const bool live = row < nrows;
         const int pk = row_first + (live ? row : 0), p = a.by_nq.div(pk);
@@ -604,17 +624,27 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           if (!wait(full_k(st), (uint32_t)((tile / NS) & 1))) return false;
           decode_page4(smem + (k_tile(st) - sbase), smem + scales_at(st), smem + L::kK16Off + g * L::kK16, kTok);
           fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty_k(st));
           return true;
         };
-        if (KF == kNvfp4 && g < n && next_keys(g) && lane == 0) mbar_arrive(s_free(g));
+        // the weights of the other parts' tokens are zeros, which stay
+        if (kByWarp && F > 1 && segs == 0 && n > 0) {
+          uint32_t z[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = 0u;
+          tm_st<32>(pp, z);
+          tm_wait_st();
+        }
+        if (KF == kNvfp4 && g < n && next_keys(g)) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free(g));
+        }
         for (int b = g; b < n; b += 2, ++cnt) {
           const int tile = tile0 + b, st = tile % NS;
           int tb;
           uint32_t members;
           item_tokens<kTok, kBlocks>(it, list, it.i0 + b, tb, members);
-          if (!wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
+          // (NVFP4: the page is there, its keys have been decoded)
+          if (KF != kNvfp4 && !wait(full_v(st), (uint32_t)((tile / NS) & 1))) break;
           const int valid = info[st];
           if (KF == kNvfp4) {
             // as below; codes and scales have then been read
@@ -654,10 +684,16 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
           }
           if (!wait(s_full(g), (uint32_t)(cnt & 1))) break;
           tc_fence_after();
-          if (KF == kNvfp4 && b + 2 < n && !next_keys(b + 2)) break;
           // the lane's scores
           uint32_t raw[kPart];
-          if constexpr (F == 1) {
+          if constexpr (kByWarp) {
+#pragma unroll
+            for (int k = 0; k < kPart; k += 32) tm_ld<kPart < 32 ? kPart : 32>(sp + part * kPart + k, raw + k);
+            // (the next keys while they come)
+            const bool ok = b + 2 >= n || next_keys(b + 2);
+            tc_wait_ld();
+            if (!ok) break;
+          } else if constexpr (F == 1) {
             tm_ld<32>(sp, raw);
             tm_ld<32>(sp + 32, raw + 32);
             tc_wait_ld();
@@ -703,11 +739,21 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               if (2 * j + 1 >= visible) y[j].y = -INFINITY;
             }
           }
-          float t0 = fmaxf(y[0].x, y[0].y), t1 = fmaxf(y[1].x, y[1].y);
+          float t0, t1;
+          if constexpr (kByWarp) {
+            t0 = y[0].x, t1 = y[0].y;
 #pragma unroll
-          for (int j = 2; j < kHalf; j += 2) {
-            t0 = fmaxf(t0, fmaxf(y[j].x, y[j].y));
-            t1 = fmaxf(t1, fmaxf(y[j + 1].x, y[j + 1].y));
+            for (int j = 1; j < kHalf; j += 2) {
+              t0 = fmax3_finite(t0, y[j].x, y[j].y);
+              if (j + 1 < kHalf) t1 = fmax3_finite(t1, y[j + 1].x, y[j + 1].y);
+            }
+          } else {
+            t0 = fmaxf(y[0].x, y[0].y), t1 = fmaxf(y[1].x, y[1].y);
+#pragma unroll
+            for (int j = 2; j < kHalf; j += 2) {
+              t0 = fmaxf(t0, fmaxf(y[j].x, y[j].y));
+              t1 = fmaxf(t1, fmaxf(y[j + 1].x, y[j + 1].y));
+            }
           }
           const float top = fmaxf(t0, t1) * post;   // post is positive: the order is kept
           float shrink = 1.f;     // what the output gathered so far is to be multiplied by
@@ -786,6 +832,9 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               hi[j] = pack_f16(y[j].x, y[j].y);
             }
           }
+          if constexpr (kByWarp) {
+            tm_st<kPart / 2>(pp + part * (kPart / 2), hi);
+          } else {
 #pragma unroll
           for (int f = 0; f < F; ++f) {
             uint32_t z[kPart / 2];
@@ -798,10 +847,16 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
             }
           }
+          }
           tm_wait_st();
           tc_fence_before();
           if (KF != kBf16 || valid < kTok) fence_async();
-          mbar_arrive(p_full(g));
+          if (kByWarp) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(g));
+          } else {
+            mbar_arrive(p_full(g));
+          }
           if (KF == kFp8) {
             // codes and scales of the page have been read
             __syncwarp();
@@ -815,13 +870,17 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         ml[g * kLanes + quad * 32 + lane] = make_float4(m, l, unit, 0.f);
         group_sync();
         float M = -INFINITY, sum = 0.f;
+        // (max, sum) of part f of the row in group h
+        auto part_of = [&](int h, int f) {
+          return ml[h * kLanes + (kByWarp ? (f * kRowWarps + quad % kRowWarps) * 32 + lane
+                                          : quad * 32 + lane % kWarpRows + f * kWarpRows)];
+        };
 #pragma unroll
-        for (int f = 0; f < 2 * F; ++f)
-          M = fmaxf(M, ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows].x);
+        for (int f = 0; f < 2 * F; ++f) M = fmaxf(M, part_of(f / F, f % F).x);
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int f = 0; f < 2 * F; ++f) {
-          const float4 e = ml[(f / F) * kLanes + quad * 32 + lane % kWarpRows + (f % F) * kWarpRows];
+          const float4 e = part_of(f / F, f % F);
           if (e.x != -INFINITY) sum = fmaf(e.y, ex2_approx(e.x - ref), sum);
         }
         // Either group finishes half the dims: its warps see the tensor-memory lanes
@@ -834,20 +893,52 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
         const size_t at = (size_t)(2 * c + (s.o0 == 0 ? 1 : 0)) * a.group_rows + row;
         const float inv = M == -INFINITY ? 0.f : a.out_scale / sum;
         bool odd = false;
-#pragma unroll 1
-        for (int ch = g * (kDim / 2); ch < (g + 1) * (kDim / 2); ch += 32) {
+        // 32 dims of the row from ch on, in units of 2^ref: both groups', and the sum over the
+        // lanes that hold its parts
+        auto gather = [&](int ch, float(&v)[32]) {
           uint32_t o0[32], o1[32];
           tm_ld<32>(tl + kColO + ch, o0);
           tm_ld<32>(tl + kColO + kDim + ch, o1);
           tc_wait_ld();
-          float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             v[e] = (has0 ? __uint_as_float(o0[e]) * f0 : 0.f) + (has1 ? __uint_as_float(o1[e]) * f1 : 0.f);
 #pragma unroll
             for (int d = kWarpRows; d < 32; d <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], d);
-            odd |= !isfinite(v[e]);
           }
+        };
+        // NVFP4: parts are warps, those behind the first hand theirs over
+        [[maybe_unused]] float* swap = reinterpret_cast<float*>(smem + L::kV16Off) +
+                                       (g * (kLanes / F) + row) * L::kSwapStride;
+        [[maybe_unused]] constexpr int kSwapPart = 2 * (kLanes / F) * L::kSwapStride;
+        if constexpr (kByWarp && F > 1) {
+#pragma unroll 1
+          for (int ch = 0; part > 0 && ch < kDim / 2; ch += 32) {
+            float v[32];
+            gather(g * (kDim / 2) + ch, v);
+            float4* to = reinterpret_cast<float4*>(swap + (part - 1) * kSwapPart + ch);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+          group_sync();
+        }
+#pragma unroll 1
+        for (int ch = g * (kDim / 2); (!kByWarp || part == 0) && ch < (g + 1) * (kDim / 2); ch += 32) {
+          float v[32];
+          gather(ch, v);
+          if constexpr (kByWarp && F > 1) {
+#pragma unroll
+            for (int f = 1; f < F; ++f) {
+              const float4* from = reinterpret_cast<const float4*>(swap + (f - 1) * kSwapPart + ch - g * (kDim / 2));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 x = from[e];
+                v[4 * e] += x.x, v[4 * e + 1] += x.y, v[4 * e + 2] += x.z, v[4 * e + 3] += x.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) odd |= !isfinite(v[e]);
           if (part == 0 && live) {
             if (complete) {
               uint4* out = reinterpret_cast<uint4*>(a.out + q_row * kDim + ch);
