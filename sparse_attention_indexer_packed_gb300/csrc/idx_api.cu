@@ -270,7 +270,8 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   if (num_pages < 1 || num_pages > 0x7fffffffLL / idx::kPage / kv_heads)
     return fail(IDX_ERR_INVALID, "num_pages * kv_heads must be in [1, 2^31 / 64) (got %lld x %d)",
                 (long long)num_pages, kv_heads);
-  const int group = idx::attn::group_rows(P, q_heads / heads, blocks);
+  const int group = nvfp4 ? idx::attn::group_rows4(R, heads, P, q_heads / heads, max_pages, blocks ? topk : 0)
+                          : idx::attn::group_rows(P, q_heads / heads, blocks);
   const long long units = (long long)R * heads * (((long long)P * (q_heads / heads) + group - 1) / group);
   if (units > idx::attn::kMaxUnits)
     return fail(IDX_ERR_INVALID, "at most %lld (request, key head or list, row group) units a call (got %lld)",

@@ -147,6 +147,28 @@ inline int position_shift(int R, long long per, long long most, int unit_cost) {
   return shift;
 }
 
+// Packed rows of a group over an NVFP4 cache: 16, whose kernel is the faster one a token up to
+// 32 rows (two groups: 16 x 65K tokens 77.1 us, 82.1 with the wide kernel) and has the cheaper
+// start and end, so also where more rows meet few tokens in all, as the host can bound
+// them: 64 rows of 8 x 8K 20.3 / 23.7, of 64 x 1K 18.9 / 24.0, of 64 x 4K 47.5 / 36.7, 128 rows of
+// 8 x 8K 29.3 / 30.8, of 64 x 1K 31.0 / 29.5.  Lists, where a group of 16 joins those of fewer
+// drafts: 64 rows of 16 x 64 blocks 37.6 / 42.3, of 100 x 16 54.3 / 48.6.
+inline int group_rows4(int requests, int heads, int drafts, int nq, int max_pages, int topk) {
+  const bool blocks = topk > 0;
+  const int wide = group_rows(drafts, nq, blocks);
+  const long long groups = ((long long)drafts * nq + 15) / 16, units = (long long)requests * heads * groups;
+  if (wide == 16 || units > kMaxUnits) return wide;
+  if (groups <= 2) return 16;
+  long long tokens = (long long)max_pages * kPage;
+  if (blocks) {
+    // a further draft's list taken to add an eighth of its own
+    const int mine = 15 / nq + 1 < drafts ? 15 / nq + 1 : drafts;
+    const long long listed = (long long)topk * kBlock * (7 + mine) / 8;
+    if (listed < tokens) tokens = listed;
+  }
+  return units * tokens <= (blocks ? 700000 : 300000) ? 16 : wide;
+}
+
 struct Segment {
   int unit;          // (r * heads + unit head) * groups + group
   int r, head, group;

@@ -1057,7 +1057,9 @@ cudaError_t launch_kf(const AttnArgs& a, const CUtensorMap& k_map, const CUtenso
   (blocks ? launch_kfb<KF, F, true>(a, k_map, v_map, grid, dev, stream)            \
           : launch_kfb<KF, F, false>(a, k_map, v_map, grid, dev, stream))
   // (17 rows at least: launch_attn sends units of up to 16 to the other kernel)
-  if (rows <= 32) return IDX_LAUNCH(4);
+  // (NVFP4: nor up to 32, but for calls of more units than that kernel takes)
+  if constexpr (KF != kNvfp4)
+    if (rows <= 32) return IDX_LAUNCH(4);
   if (rows <= 64) return IDX_LAUNCH(2);
   return IDX_LAUNCH(1);
 #undef IDX_LAUNCH

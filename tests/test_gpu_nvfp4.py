@@ -96,22 +96,29 @@ def test_store_of_values_that_are_not_finite():
 
 
 # ---- attention -----------------------------------------------------------------------------
+# More than 32 packed rows go to the kernel of up to 16 where the page table, which bounds the
+# tokens, is narrow, and to the tensor-memory one where it is wide.
+TABLES = [None, 60000]
+
+
+@pytest.mark.parametrize("max_pages", TABLES)
 @pytest.mark.parametrize("P,Hq,Hkv", [(1, 1, 1), (1, 16, 2), (1, 4, 4), (2, 6, 2), (4, 16, 1),
                                       (4, 8, 2), (3, 10, 2), (1, 40, 1), (7, 24, 1), (8, 16, 1)])
-def test_whole_cache(P, Hq, Hkv):
+def test_whole_cache(P, Hq, Hkv, max_pages):
     lens = [drafts(L, P) for L in LENS]
-    c = _nvfp4.make(lens, Hkv, 11 + P + Hq, pads=(3, 8))
+    c = _nvfp4.make(lens, Hkv, 11 + P + Hq, pads=(3, 8), max_pages=max_pages)
     q = draws(len(lens), P, Hq, 5)
     out, l, flags = run(c, q)
     assert flags == 0
     _attn.check(out, l, _nvfp4.reference(c, q, SCALE))
 
 
+@pytest.mark.parametrize("max_pages", TABLES)
 @pytest.mark.parametrize("ctas", [1, 2, 7, 0])
 @pytest.mark.parametrize("P,Hq,Hkv", [(1, 8, 2), (4, 16, 1)])
-def test_splits_of_a_long_cache(ctas, P, Hq, Hkv):
+def test_splits_of_a_long_cache(ctas, P, Hq, Hkv, max_pages):
     lens = [drafts(L, P) for L in (5000, 3, 2049, 0, 777)]
-    c = _nvfp4.make(lens, Hkv, 21)
+    c = _nvfp4.make(lens, Hkv, 21, max_pages=max_pages)
     q = draws(len(lens), P, Hq, 6)
     idx.idx_set_grid_limit(ctas)
     try:
@@ -138,22 +145,27 @@ def test_many_units_dealt_whole(R, P, Hq, Hkv, L):
 
 def test_rows_of_very_different_lengths():
     lens = [[1, 700, 0, 64], [129, 128, 2000, 1]]
-    for Hq in (4, 8, 32):
-        c = _nvfp4.make(lens, 2, 31)
+    for Hq, max_pages in ((4, None), (8, None), (32, None), (32, 60000), (64, 60000)):
+        c = _nvfp4.make(lens, 2, 31, max_pages=max_pages)
         q = draws(2, 4, Hq, 7)
         out, l, flags = run(c, q)
         assert flags == 0
         _attn.check(out, l, _nvfp4.reference(c, q, SCALE))
 
 
+@pytest.mark.parametrize("more", [0, 200])
 @pytest.mark.parametrize("P,Hq,Hkv,lists,topk", [
     (1, 16, 1, 4, 8), (4, 16, 1, 4, 16), (4, 16, 4, 4, 5), (4, 16, 4, 2, 5), (2, 12, 2, 6, 3),
     (16, 4, 1, 4, 4), (5, 40, 1, 2, 6), (1, 1, 1, 1, 256), (17, 2, 1, 2, 3), (8, 16, 1, 1, 4)])
-def test_blocks(P, Hq, Hkv, lists, topk):
+def test_blocks(P, Hq, Hkv, lists, topk, more):
     lens = [drafts(L, P) for L in (0, 1, 64, 129, 1000, 2500, 4097)]
-    c = _nvfp4.make(lens, Hkv, 41 + P, pads=(2,))
+    c = _nvfp4.make(lens, Hkv, 41 + P, pads=(2,), max_pages=4000 if more else None)
     q = draws(len(lens), P, Hq, 8)
     ids = lists_for(lens, lists, topk, 9, P)
+    if more:      # longer lists with nothing more in them: the other kernel for many rows
+        if topk + more > 256:
+            pytest.skip("no list is that long")
+        ids = torch.cat([ids, torch.full((*ids.shape[:2], more), -1, dtype=torch.int32)], 2)
     # what a list may hold besides: a block twice, no block, blocks past the row's own
     ids[4, 0, 0] = ids[4, 0, topk // 2]
     ids[5, 1 % (P * lists), -1] = -7
@@ -164,22 +176,22 @@ def test_blocks(P, Hq, Hkv, lists, topk):
     _attn.check(out, l, _nvfp4.reference(c, q, SCALE, ids, lists))
 
 
-@pytest.mark.parametrize("P,Hq", [(1, 8), (3, 16)])
+@pytest.mark.parametrize("P,Hq,max_pages", [(1, 8, None), (3, 16, None), (3, 16, 60000)])
 @pytest.mark.parametrize("outers", [(1.0, 1.0), (2.0 ** -20, 2.0 ** 30), (2.0 ** 40, 2.0 ** -50)])
-def test_outer_scales_and_group_scales_of_every_size(P, Hq, outers):
+def test_outer_scales_and_group_scales_of_every_size(P, Hq, max_pages, outers):
     lens = [drafts(L, P) for L in (900, 65, 1)]
-    c = _nvfp4.make(lens, 1, 61, spread=9)
+    c = _nvfp4.make(lens, 1, 61, spread=9, max_pages=max_pages)
     q = draws(3, P, Hq, 11)
     out, l, flags = run(c, q, SCALE / outers[0], k_outer=outers[0], v_outer=outers[1])
     assert flags == 0
     _attn.check(out, l, _nvfp4.reference(c, q, SCALE / outers[0], k_outer=outers[0], v_outer=outers[1]))
 
 
-@pytest.mark.parametrize("Hq,P", [(4, 2), (16, 4)])
-def test_a_token_that_one_draft_row_sees_does_not_reach_the_others(Hq, P):
+@pytest.mark.parametrize("Hq,P,max_pages", [(4, 2, None), (16, 4, None), (16, 4, 300000 // 64 * 13), (16, 8, 60000)])
+def test_a_token_that_one_draft_row_sees_does_not_reach_the_others(Hq, P, max_pages):
     lens = [[70 + p for p in range(P)]]
     for plane in ("k", "v"):
-        c = _nvfp4.make(lens, 1, 71)
+        c = _nvfp4.make(lens, 1, 71, max_pages=max_pages)
         slot = int(c.slot_ids[0])
         row = int(c.page_table[slot, (70 + P - 2) // 64]) * 64 + (70 + P - 2) % 64   # the last draft's own
         getattr(c, plane)[1][row, 2] = 0x7f
@@ -193,8 +205,8 @@ def test_a_token_that_one_draft_row_sees_does_not_reach_the_others(Hq, P):
 
 def test_bad_pages_are_left_out_and_flagged():
     lens = [[500], [200]]
-    for Hq in (4, 32):
-        c = _nvfp4.make(lens, 1, 81)
+    for Hq, max_pages in ((4, None), (40, None), (40, 60000)):
+        c = _nvfp4.make(lens, 1, 81, max_pages=max_pages)
         slot = int(c.slot_ids[0])
         c.page_table[slot, 2], c.page_table[slot, 5] = c.num_pages, -9
         q = draws(2, 1, Hq, 13)
@@ -204,7 +216,7 @@ def test_bad_pages_are_left_out_and_flagged():
 
 
 def test_long_rows_are_clamped():
-    for Hq in (4, 32):
+    for Hq in (4, 40):
         c = _nvfp4.make([[128], [100]], 1, 83, max_pages=2)
         c.row_lens[0, 0] = 5000
         q = draws(2, 1, Hq, 14)
@@ -215,8 +227,8 @@ def test_long_rows_are_clamped():
 
 
 def test_queries_of_any_size():
-    c = _nvfp4.make([[300], [65]], 1, 85)
-    for Hq in (4, 32):
+    for Hq, max_pages in ((4, None), (40, 60000)):
+        c = _nvfp4.make([[300], [65]], 1, 85, max_pages=max_pages)
         q = draws(2, 1, Hq, 15)
         q[0, 0, 0] *= 2.0 ** 100
         q[0, 0, 1] *= 2.0 ** -110
@@ -264,12 +276,13 @@ def test_past_32_bit_offsets():
         for a, b in zip(want, small_pages):
             for dst, src in zip(big, p):
                 dst[a * 64:a * 64 + 64] = src[b * 64:b * 64 + 64].cuda()
-    for Hq in (4, 32):
+    for Hq, more in ((4, 0), (40, 60000)):
         q = draws(1, 1, Hq, 19)
         out, l = torch.empty_like(q, device="cuda"), torch.empty((1, 1, Hq), device="cuda")
         ws = idx.alloc_attn_workspace(1, Hq, 1)
         i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
-        idx.idx_attn_paged_nvfp4(q.cuda(), *k, *v, i32(want), i32(0), i32([190]), 1, SCALE, out, l, ws)
+        table = i32(want + [-1] * more)
+        idx.idx_attn_paged_nvfp4(q.cuda(), *k, *v, table, i32(0), i32([190]), 1, SCALE, out, l, ws)
         assert idx.idx_workspace_errors(ws) == 0
         _attn.check(out, l, _nvfp4.reference(small, q, SCALE))
     src = tokens(2, 1, 20)[:, :1]
@@ -279,8 +292,8 @@ def test_past_32_bit_offsets():
 
 
 def test_a_wait_that_runs_out_is_reported():
-    for Hq in (4, 32):
-        c = _nvfp4.make([[900]], 1, 97)
+    for Hq, max_pages in ((4, None), (40, 60000)):
+        c = _nvfp4.make([[900]], 1, 97, max_pages=max_pages)
         q = draws(1, 1, Hq, 21)
         idx.idx_set_wait_limit_ns(20_000_000)
         idx.idx_set_stall_test(1)
