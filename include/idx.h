@@ -464,7 +464,7 @@ IDX_API int idx_attn_blocks(const void* q, const void* k_payload, const void* k_
  * (device, 16-byte aligned) are E4M3 bytes [rows][8], k_outer, v_outer the planes' outer scales;
  * sm_scale * k_outer must be a normal fp32 number.  Codes times scales are exact in f16, where the
  * products are taken; a query element is exact within 2^21 of its row's largest; the weights
- * enter the product with the values as one f16: 2^-11 of the weight, or 2^-39 of the row's
+ * enter the product with the values as one f16: 2^-11 of the weight, or 2^-32 of the row's
  * largest weight.
  */
 IDX_API int idx_attn_paged_nvfp4(const void* q, const void* k_payload, const void* k_scale,

@@ -6,17 +6,20 @@
 // HBM.  A 32-token piece costs a warp 128 conversions, 128 f16x2 products and 64 matrix
 // products; on each of an SM's four schedulers the conversions (2 cycles each) come to 256
 // cycles, the matrix products (8 each) to 512, all instructions together to ~600, where
-// HBM's share of the piece is 215.
+// HBM's share of the piece is 215.  Measured, 16 x 131K tokens x 16 rows: 76.7 us, 0.53 of the
+// bytes' rate; issue slots 50% taken, tensor cores 37%, HBM 41%.
 //
 // How (sm_103a):
-//  * 16 warps of 128 registers, four a scheduler: with 8 (of 255) the warps' chains leave
-//    two thirds of the issue slots empty (120 us on 16 x 131K).  So the 16 queries lie in
-//    shared memory in the order of the product's operand, the output alone in registers, and
-//    what a warp does not need in its loop (the walk, the stretch) waits in shared memory;
+//  * 12 warps of 168 registers, three a scheduler, nothing spilled.  Eight of 255 leave two
+//    thirds of the issue slots empty (120 us), 16 of 128 spill in the loop, and a spill here
+//    goes past the L1 that shared memory takes (88 us).  So the 16 queries lie in shared memory
+//    in the order of the product's operand, the output alone in registers, and what a warp does
+//    not need in its loop (the walk, the stretch) waits in shared memory.  Four key tiles to a
+//    read of the queries instead of two 79.8, values loaded before the scores 79.1;
 //  * a warp owns two stages of one piece (keys, values and their scales) and refills each as
-//    soon as it has been used.  Its copies end with the unit: a stage's 9 KB are then where
-//    the warp leaves its state, and a row's 16 states are joined by one warp.  (A warp that
-//    feeds the 15 others, across units: its copies, one lane after the other, took 3800
+//    soon as it has been used (three stages: 81.2).  Its copies end with the unit: a stage's 9 KB
+//    are then where the warp leaves its state, and a row's 12 states are joined by one warp.  (A
+//    warp that feeds the 15 others, across units: its copies, one lane after the other, took 3800
 //    cycles a round: 100 us);
 //  * a lane's 16 bytes of a key are 32 dims of it, two groups; its 8 bytes of a value are one
 //    group, whose dims are the 16 product tiles, so one scale serves all of them.  Two
@@ -26,6 +29,8 @@
 //    maximum, when a score passes it by 2^(kHead + kSlack), the most that f16 holds: 11 bits of
 //    each, or 2^-32 of the row's largest.  So the output is seldom rescaled (raised with
 //    every new maximum, nearly every piece of 16 rows did).
+// Small calls: 1 x 1K tokens 9.5 us (11.8 with eight warps), 48 ragged requests x 4 heads 19.9,
+// 16 x 131K with four lists of 64 blocks each 44.5 (50.5).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -274,7 +279,7 @@ __device__ __forceinline__ void each_quad(float* w0, int t, F&& f) {
     }
 }
 
-// As in idx_attn.cu, in units of 0.13 us, an SM's time for a piece.
+// As in idx_attn.cu, in units of 0.18 us, an SM's time for a piece.
 struct Cost {
   static constexpr float kAlone = 8.f, kEnd = 20.f, kStretch = 24.f, kCut = 26.f, kList = 18.f;
 };
@@ -445,7 +450,7 @@ __device__ __forceinline__ void run_units(const AttnArgs& a, const CUtensorMap& 
       safe = __reduce_min_sync(0xffffffffu, r.bit ? r.len : 0x7fffffff);
       drafts = __reduce_or_sync(0xffffffffu, r.bit);
     }
-    // ---- the walk and the stretch wait in shared memory: 128 registers are the loop's ------
+    // ---- the walk and the stretch wait in shared memory: the registers are the loop's ------
     if (lane == 0) {
       int* k = cold;
       each_word([&](int& x) { *k++ = x; }, walk, s, it);
@@ -614,7 +619,7 @@ template <bool kBlocks>
 int team_for(AttnArgs& a, int grid, float pieces, float& least) {
   const int units = a.R * (int)a.by_per.d;
   int team = 0;
-  for (int tw : {12, 6, 3}) {
+  for (int tw : {12, 6, 3}) {   // (single warps: 256 x 8 x 100 tokens 35.3 us, 33.6 without)
     if (kBlocks && (a.P < kMaxDrafts ? a.P : kMaxDrafts) * a.topk > team_list_words(tw)) break;
     const int teams = grid * (NW / tw), full = units / teams, rest = units - full * teams;
     const float busy = (float)(rest * tw) / (float)grid;

@@ -37,6 +37,21 @@
 // values are decoded to f16, exactly, by the group that uses them, and the weights
 // times the value's scale are one f16 (11 bits; raise_unit).
 //
+// NVFP4 cache: neither a code times its scale (6 significant bits, exact in f16) nor the group
+// of 16 along the values' dims fits a product of codes, so both operands are decoded to f16
+// tiles in shared memory, by the group that uses them: its keys two pages ahead of the scores it
+// waits for, its values while the scores of another page are made.  The queries are f16 scaled a
+// row by a power of two; the weights are f16 in units that lie 2^7 below the running maximum
+// (raised when a score passes it by 2^8 more: 2^-11 of each weight, or 2^-32 of the row's largest).
+// The parts of a row's tokens are warps, not lanes, so a warp skips what its part does not see and
+// a page costs one barrier; a unit's end joins them through the values' tiles.  Measured: 16 x
+// 131K with 64 rows 147.5 us (378 as four groups of the 16-row kernel's first form, 168 with
+// lanes as parts), 0.28 of the copy peak; 8 x 64K with 128 rows 66.5.  A group needs ~2900 cycles a
+// page: decoding keys and values 600 to 750 each, weights 450, the products' end 300; two
+// alternate, issue slots 47% taken, tensor cores 38%, shared memory 38%.  Tried and slower:
+// warps of their own for decoding (192 us), 16 softmax warps (203), a look at the barriers ahead
+// of the products (150).
+//
 // Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 162 to
 // 167 us, 0.87 to 0.90 of the copy peak from one GPU to another (the warp-level kernel, four groups of 16 rows:
 // 548); 32 rows 157 us, 0.93.  128 rows, 8 x 64K: 72 to 74 us, 0.51: a lane's 64
