@@ -619,7 +619,7 @@ template <bool kBlocks>
 int team_for(AttnArgs& a, int grid, float pieces, float& least) {
   const int units = a.R * (int)a.by_per.d;
   int team = 0;
-  for (int tw : {12, 6, 3}) {   // (single warps: 256 x 8 x 100 tokens 35.3 us, 33.6 without)
+  for (int tw : {12, 6, 3}) {   // (single warps: 256 x 8 x 100 tokens 35.3 us, 33.8 without)
     if (kBlocks && (a.P < kMaxDrafts ? a.P : kMaxDrafts) * a.topk > team_list_words(tw)) break;
     const int teams = grid * (NW / tw), full = units / teams, rest = units - full * teams;
     const float busy = (float)(rest * tw) / (float)grid;
@@ -642,8 +642,24 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
                          int grid, int dev, cudaStream_t stream, bool& whole) {
   AttnArgs a = args;
   float least;
+  const float share = (float)(a.R * (int)a.by_per.d) / (float)grid;
   if (!a.block_ids) {
-    // units of 16 pieces are assumed for the team; how long they are is known on the device
+    // A table that holds short units only: where dealing them whole costs about what cutting them
+    // does, the call deals and needs no join (us, cut / dealt: 1 request x 2 key heads x 200 tokens
+    // 7.5 / 6.0, x 600 9.8 / 8.4, x 1000 9.3 / 10.3; 16 x 8 x 200 8.6 / 6.8, x 1000 12.4 / 10.6; 64 x 8
+    // x 1K 30.0 / 28.3).
+    if (a.most <= 40 && a.shift == 0) {
+      const int team = team_for<false>(a, grid, (float)a.most, least);
+      const float piece = share * (float)a.most;
+      const float cut = (piece > Cost::kAlone ? piece : Cost::kAlone) + Cost::kStretch * share + Cost::kCut;
+      whole = least <= 1.1f * cut;
+      if (whole) switch (team) {
+          case 3: return launch_one<false, 3, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+          case 6: return launch_one<false, 6, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+          default: return launch_one<false, 12, Deal::kWhole>(a, k_map, v_map, grid, dev, stream);
+        }
+    }
+    // else units of 16 pieces are assumed for the team; how long they are is known on the device
     // only, which decides whether they are dealt whole at all
     whole = false;
     switch (team_for<false>(a, grid, 16.f, least)) {
@@ -655,7 +671,6 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
   // the lists' length bounds the units', so the host decides, and a call that deals needs no join
   const float full = (float)(a.topk * (kBlock / kItem)) * (1.f + (float)(a.P - 1) / 8.f);
   const float pieces = full < (float)a.most ? full : (float)a.most;
-  const float share = (float)(a.R * (int)a.by_per.d) / (float)grid;
   const int team = team_for<true>(a, grid, pieces, least);
   const float cut = (share * pieces > Cost::kAlone ? share * pieces : Cost::kAlone) +
                     (Cost::kStretch + Cost::kList) * share + Cost::kCut + Cost::kList;
