@@ -593,7 +593,8 @@ def _attn_args(q, k_payload, k_scale, v_payload, v_scale, kv_dtype, page_table, 
         raise IdxError("page_table must be [n_slots, max_pages]")
     n_slots, max_pages = table
     return (_want(q, "q", _BF16, shape), kp, ks, vp, vs,
-            *(() if kv_dtype is None else (DTYPES[kv_dtype],)), k_pages // kv_heads, kv_heads, _want(page_table, "page_table", _I32, table), n_slots, max_pages,
+            *(() if kv_dtype is None else (DTYPES[kv_dtype],)), k_pages // kv_heads, kv_heads,
+            _want(page_table, "page_table", _I32, table), n_slots, max_pages,
             _want(slot_ids, "slot_ids", _I32, (R,)),
             _want(row_lens, "row_lens", _I32, (R, P))), R, P, Hq
 

@@ -50,7 +50,9 @@
 // page: decoding keys and values 600 to 750 each, weights 450, the products' end 300; two
 // alternate, issue slots 47% taken, tensor cores 38%, shared memory 38%.  Tried and slower:
 // warps of their own for decoding (192 us), 16 softmax warps (203), a look at the barriers ahead
-// of the products (150).
+// of the products (150), the keys as the rows of the products in tiles of 128 tokens, decoded
+// straight into tensor memory, a lane a token (152; 128 rows as two groups 95): a row's factor and
+// unit are then read from shared memory by every lane.
 //
 // Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 162 to
 // 167 us, 0.87 to 0.90 of the copy peak from one GPU to another (the warp-level kernel, four groups of 16 rows:
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
     for (int s = 0; s < NS; ++s) {
       mbar_init(full_k(s), 1);
       mbar_init(full_v(s), 1);
-      mbar_init(empty_k(s), KF == kNvfp4 ? 4 : 1);
+      mbar_init(empty_k(s), 1);   // (not NVFP4's, which gives its stage back by empty_v)
       mbar_init(empty_v(s), KF != kBf16 ? 4 : 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -611,16 +613,16 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
               for (int e = 0; e < 32; ++e) w[e] = pack_f16(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
               tm_st<32>(tl + kColQ + 32 * g, w);
             } else {
-            uint32_t lo[16];
+              uint32_t lo[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
-                            bf16_hi(w[2 * e + 1]) * up};
-              w[e] = e4m3x4_take(x);
-              lo[e] = e5m2x4(x);
-            }
-            tm_st<16>(tl + kColQ + 16 * g, w);
-            tm_st<16>(tl + kColQ + 32 + 16 * g, lo);
+              for (int e = 0; e < 16; ++e) {
+                float x[4] = {bf16_lo(w[2 * e]) * up, bf16_hi(w[2 * e]) * up, bf16_lo(w[2 * e + 1]) * up,
+                              bf16_hi(w[2 * e + 1]) * up};
+                w[e] = e4m3x4_take(x);
+                lo[e] = e5m2x4(x);
+              }
+              tm_st<16>(tl + kColQ + 16 * g, w);
+              tm_st<16>(tl + kColQ + 32 + 16 * g, lo);
             }
           }
           tm_wait_st();
@@ -851,17 +853,17 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
             tm_st<kPart / 2>(pp + part * (kPart / 2), hi);
           } else {
 #pragma unroll
-          for (int f = 0; f < F; ++f) {
-            uint32_t z[kPart / 2];
+            for (int f = 0; f < F; ++f) {
+              uint32_t z[kPart / 2];
 #pragma unroll
-            for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
-            tm_st<kPart / 2>(pp + f * (kPart / 2), z);
-            if (KF == kBf16) {
+              for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? hi[j] : 0u;
+              tm_st<kPart / 2>(pp + f * (kPart / 2), z);
+              if (KF == kBf16) {
 #pragma unroll
-              for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
-              tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
+                for (int j = 0; j < kPart / 2; ++j) z[j] = F == 1 || part == f ? lo[j] : 0u;
+                tm_st<kPart / 2>(pp + 32 + f * (kPart / 2), z);
+              }
             }
-          }
           }
           tm_wait_st();
           tc_fence_before();
