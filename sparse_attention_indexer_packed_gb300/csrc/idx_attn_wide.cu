@@ -49,10 +49,11 @@
 // lanes as parts), 0.28 of the copy peak; 8 x 64K with 128 rows 66.5.  A group needs ~2900 cycles a
 // page: decoding keys and values 600 to 750 each, weights 450, the products' end 300; two
 // alternate, issue slots 47% taken, tensor cores 38%, shared memory 38%.  Tried and slower:
-// warps of their own for decoding (192 us), 16 softmax warps (203), a look at the barriers ahead
-// of the products (150), the keys as the rows of the products in tiles of 128 tokens, decoded
-// straight into tensor memory, a lane a token (152; 128 rows as two groups 95): a row's factor and
-// unit are then read from shared memory by every lane.
+// warps of their own for decoding both operands (192 us) or the values (174; the softmax groups
+// then have 168 registers), 16 softmax warps (203), ten warps without the split of registers (149),
+// a look at the barriers ahead of the products (150), the keys as the rows of the products in tiles
+// of 128 tokens, decoded straight into tensor memory, a lane a token (152; 128 rows as two groups
+// 95): a row's factor and unit are then read from shared memory by every lane.
 //
 // Measured (one GB300, calls back to back): bf16 16 x 131K with 64 rows 162 to
 // 167 us, 0.87 to 0.90 of the copy peak from one GPU to another (the warp-level kernel, four groups of 16 rows:
