@@ -64,8 +64,9 @@
 // 152 us against 122 at the time, 1 x 1K 12.8 against 9.3).
 // Registers: 168 a thread at launch, and every instantiation spills; bytes of stores /
 // loads (-Xptxas -v) for 17 to 32, 33 to 64, 65 to 128 rows: bf16 4 / 4, 92 / 48, 148 /
-// 552, with lists 72 / 24, 216 / 224, 164 / 324; e4m3 156 / 224, 152 / 232, 128 / 232,
-// with lists 124 / 236, 160 / 280, 160 / 276.
+// 552, with lists 24 / 16, 216 / 224, 164 / 324; e4m3 156 / 224, 152 / 232, 128 / 232,
+// with lists 132 / 260, 160 / 280, 160 / 276; NVFP4 from 33 rows on 156 / 224, 156 / 220, with
+// lists 164 / 332, 164 / 324.
 // Tried and slower: the values decoded by four warps of their own (161 -> 189); each
 // group finishing a slice through shared memory at a unit's end (166 -> 183).
 //
