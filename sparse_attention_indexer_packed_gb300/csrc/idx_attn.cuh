@@ -128,9 +128,14 @@ static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit t
 // with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
 // NVFP4, whose pieces of 16 rows take half the time: paged 48 ragged x 4 heads 30.3 / 23.5 /
 // 19.9 / 20.0 at 6 / 12 / 20 / 28, 8 x 32K 23.6 / 23.1 / 21.6 / 20.9; lists 16 x 131K 34.8 / 33.8 /
-// 33.2 at 16 / 24 / 32.
-inline int unit_cost(int group_rows, bool blocks, bool nvfp4) {
-  if (nvfp4 && group_rows <= 16) return blocks ? 32 : 28;
+// 33.2 at 16 / 24 / 32.  A unit's lots count the lists of all its draft rows (four at most are
+// counted here), which share most blocks, so the end counts as often: four rows 44.5 / 43.3 / 41.4 /
+// 43.0 at 32 / 64 / 128 / 192, one row 16.5 / 16.7 / 17.5 at 32 / 64 / 128.
+inline int unit_cost(int group_rows, bool blocks, bool nvfp4, int drafts, long long units) {
+  if (nvfp4 && group_rows <= 16) {
+    const int cost = 32 * (drafts < 4 ? drafts : 4);
+    return !blocks ? 28 : units * (cost + 1) <= kMaxPositions ? cost : 32;
+  }
   return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
 }
 
