@@ -127,14 +127,16 @@ static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit t
 // ragged requests with lists 25.5 / 20.6 / 17.8 / 18.1 at 4 / 8 / 24 / 48; 16 x 131K
 // with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
 // NVFP4, whose pieces of 16 rows take half the time: paged 48 ragged x 4 heads 30.3 / 23.5 /
-// 19.9 / 20.0 at 6 / 12 / 20 / 28, 8 x 32K 23.6 / 23.1 / 21.6 / 20.9; lists 16 x 131K 34.8 / 33.8 /
+// 19.9 / 20.0 at 6 / 12 / 20 / 28 (21.9 at 40), 64 ragged 18.5 / 17.6 / 18.2 at 20 / 28 / 40; where
+// few units are cut among many CTAs, 16 x 32K 31.6 / 30.4 / 30.1 / 30.3 at 28 / 36 / 44 / 52, 40 x 32K
+// 55.3 / 54.0 / 53.6 / 54.3, 16 x 131K 76.6 / 75.3 / 75.2 / 75.2; lists 16 x 131K 34.8 / 33.8 /
 // 33.2 at 16 / 24 / 32.  A unit's lots count the lists of all its draft rows (four at most are
 // counted here), which share most blocks, so the end counts as often: four rows 44.5 / 43.3 / 41.4 /
 // 43.0 at 32 / 64 / 128 / 192, one row 16.5 / 16.7 / 17.5 at 32 / 64 / 128.
 inline int unit_cost(int group_rows, bool blocks, bool nvfp4, int drafts, long long units) {
   if (nvfp4 && group_rows <= 16) {
     const int cost = 32 * (drafts < 4 ? drafts : 4);
-    return !blocks ? 28 : units * (cost + 1) <= kMaxPositions ? cost : 32;
+    return !blocks ? (units <= 40 ? 44 : 28) : units * (cost + 1) <= kMaxPositions ? cost : 32;
   }
   return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
 }

@@ -6,7 +6,7 @@
 // HBM.  A 32-token piece costs a warp 128 conversions, 128 f16x2 products and 64 matrix
 // products; on each of an SM's four schedulers the conversions (2 cycles each) come to 256
 // cycles, the matrix products (8 each) to 512, all instructions together to ~600, where
-// HBM's share of the piece is 215.  Measured, 16 x 131K tokens x 16 rows: 76.7 us, 0.53 of the
+// HBM's share of the piece is 215.  Measured, 16 x 131K tokens x 16 rows: 75.3 us, 0.54 of the
 // bytes' rate; issue slots 50% taken, tensor cores 37%, HBM 41%.
 //
 // How (sm_103a):
