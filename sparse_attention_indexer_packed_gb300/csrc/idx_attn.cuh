@@ -133,12 +133,17 @@ static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit t
 // 33.2 at 16 / 24 / 32.  A unit's lots count the lists of all its draft rows (four at most are
 // counted here), which share most blocks, so the end counts as often: four rows 44.5 / 43.3 / 41.4 /
 // 43.0 at 32 / 64 / 128 / 192, one row 16.5 / 16.7 / 17.5 at 32 / 64 / 128.
+// Above 16 rows (pages): 16 x 131K x 64 rows 148.4 / 145.9 / 145.0 / 145.6 at 8 / 12 / 16 / 24, 64 ragged
+// 28.8 / 27.7 / 29.3 / 30.6; lists of four draft rows 57.9 / 53.8 / 52.4 / 53.6 at 16 / 32 / 48 / 64, of
+// 16 (eight a group) 70.5 / 68.4 / 64.1 / 64.3 at 16 / 32 / 64 / 96, of one 93.3 / 95.3 at 16 / 32.
 inline int unit_cost(int group_rows, bool blocks, bool nvfp4, int drafts, long long units) {
-  if (nvfp4 && group_rows <= 16) {
-    const int cost = 32 * (drafts < 4 ? drafts : 4);
-    return !blocks ? (units <= 40 ? 44 : 28) : units * (cost + 1) <= kMaxPositions ? cost : 32;
+  const bool wide = group_rows > 16;
+  if (nvfp4) {
+    const int one = wide ? 16 : 32, cost = one * (drafts < 4 ? drafts : 4);
+    if (blocks) return units * (cost + 1) <= kMaxPositions ? cost : one;
+    return wide ? 12 : units <= 40 ? 44 : 28;
   }
-  return group_rows > 16 ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
+  return wide ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
 }
 
 // The most half-page pieces a unit of the call may have, from what the host knows:

@@ -45,8 +45,8 @@
 // (raised when a score passes it by 2^8 more: 2^-11 of each weight, or 2^-32 of the row's largest).
 // The parts of a row's tokens are warps, not lanes, so a warp skips what its part does not see and
 // a page costs one barrier; a unit's end joins them through the values' tiles.  Measured: 16 x
-// 131K with 64 rows 147.5 us (378 as four groups of the 16-row kernel's first form, 168 with
-// lanes as parts), 0.28 of the copy peak; 8 x 64K with 128 rows 66.5.  A group needs ~2900 cycles a
+// 131K with 64 rows 145.8 us (378 as four groups of the 16-row kernel's first form, 168 with
+// lanes as parts), 0.28 of the copy peak; 8 x 64K with 128 rows 64.5.  A group needs ~2900 cycles a
 // page: decoding keys and values 600 to 750 each, weights 450, the products' end 300; two
 // alternate, issue slots 47% taken, tensor cores 38%, shared memory 38%.  Tried and slower:
 // warps of their own for decoding both operands (192 us) or the values (174; the softmax groups
