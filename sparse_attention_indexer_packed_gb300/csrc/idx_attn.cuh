@@ -160,11 +160,12 @@ inline int position_shift(int R, long long per, long long most, int unit_cost) {
 }
 
 // Packed rows of a group over an NVFP4 cache: 16, whose kernel is the faster one a token up to
-// 32 rows (two groups: 16 x 65K tokens 77.1 us, 82.1 with the wide kernel) and has the cheaper
+// 32 rows (two groups: 16 x 65K tokens 76.0 us, 85.2 with the wide kernel) and has the cheaper
 // start and end, so also where more rows meet few tokens in all, as the host can bound
-// them: 64 rows of 8 x 8K 20.3 / 23.7, of 64 x 1K 18.9 / 24.0, of 64 x 4K 47.5 / 36.7, 128 rows of
-// 8 x 8K 29.3 / 30.8, of 64 x 1K 31.0 / 29.5.  Lists, where a group of 16 joins those of fewer
-// drafts: 64 rows of 16 x 64 blocks 37.6 / 42.3, of 100 x 16 54.3 / 48.6.
+// them: 64 rows of 8 x 8K 19.9 / 23.5, of 64 x 1K 17.4 / 22.9, of 64 x 4K 47.2 / 35.4, 128 rows of
+// 8 x 1K 11.8 / 18.8, of 64 x 1K 29.4 / 27.4, of 128 x 256 26.6 / 19.9 (a unit's own cost is that of
+// 256 tokens).  Lists, where a group of 16 joins those of fewer drafts: 64 rows of 16 x 64 blocks
+// 34.8 / 37.0, of 100 x 16 54.1 / 50.0.
 inline int group_rows4(int requests, int heads, int drafts, int nq, int max_pages, int topk) {
   const bool blocks = topk > 0;
   const int wide = group_rows(drafts, nq, blocks);
@@ -178,7 +179,7 @@ inline int group_rows4(int requests, int heads, int drafts, int nq, int max_page
     const long long listed = (long long)topk * kBlock * (7 + mine) / 8;
     if (listed < tokens) tokens = listed;
   }
-  return units * tokens <= (blocks ? 700000 : 300000) ? 16 : wide;
+  return (blocks ? units * tokens <= 700000 : units * (tokens + 256) <= 340000) ? 16 : wide;
 }
 
 struct Segment {
