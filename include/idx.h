@@ -111,6 +111,8 @@ IDX_API int idx_pool_free(idx_pool* pool);
  * at 448; codes = e2m1(x / scale) with a correctly rounded fp32 division, rounded
  * half-to-even, saturating at 6, sign kept (a negative value rounding to 0 is 0x8);
  * a scale of 0 writes all-zero codes; element 2b goes to the low nibble of byte b.
+ * Infinities saturate like any value past 6 * 448.  A NaN is left out of amax and takes the code
+ * of 6; only a group of nothing but NaNs has the scale NaN (0x7f).
  *   src_bf16 (device):     bf16 [num_tokens][128], token-major staging buffer.
  *   slot_mapping (device): int64 [num_tokens], physical pool row of each key
  *                          (page * 64 + offset); a negative entry skips the key; an
@@ -327,9 +329,10 @@ IDX_API int idx_store_kv(const void* k_src, const void* v_src, int64_t k_stride,
 /*
  * idx_store_kv_nvfp4 — idx_store_kv into NVFP4 planes.  Per group of 16 elements y = x / outer:
  * scale = E4M3(max |y| / 6), half to even, at most 448; codes e2m1(y / scale), half to even,
- * saturating at 6, the sign kept; a scale of 0 gives codes of 0.  With an outer scale of 1 the
- * bytes are idx_store_nvfp4's.  A NaN makes its group's scale NaN (0x7f, codes 0); an infinity is
- * held as the largest value, 6 * 448 * outer, of its sign.
+ * saturating at 6, the sign kept; a scale of 0 gives codes of 0.  An infinity is held as the
+ * largest value, 6 * 448 * outer, of its sign.  With an outer scale of 1 the bytes are
+ * idx_store_nvfp4's, but for groups with a NaN: here its scale is NaN (0x7f, codes 0), so that
+ * the attention's rows that see it are NaN.
  *   k_pool, v_pool (host): NVFP4 planes (IDX_ERR_UNSUPPORTED for others), the scale planes 8-byte
  *                          aligned
  *   k_outer, v_outer:      the planes' outer scales (v_outer is checked without values too)

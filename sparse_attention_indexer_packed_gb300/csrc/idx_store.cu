@@ -10,7 +10,8 @@
 // correctly rounded division; the scale rounds half-to-even and saturates at
 // 448; a zero scale writes all-zero codes; codes are those of the correctly
 // rounded fp32 quotient x / scale; a negative value that rounds to zero keeps
-// its sign.
+// its sign.  An infinity counts as the largest finite value of its sign; a NaN is left out of
+// amax and takes the code of 6 (the conversion's).
 //
 // (How the codes are found without a division each: idx_rows.cuh.)
 //
@@ -25,6 +26,12 @@
 namespace idx {
 
 namespace {
+
+// Two bf16 with infinities as the largest finite value of their sign; a NaN stays.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  const __nv_bfloat162 v = __hmax2_nan(__hmin2_nan(as_bf16x2(w), as_bf16x2(0x7f7f7f7fu)), as_bf16x2(0xff7fff7fu));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // Quantise one group (its 16 bf16 values in w) and write it.
 __device__ __forceinline__ void store_group(const uint32_t (&w)[8], int64_t row, int grp,
@@ -41,9 +48,16 @@ __device__ __forceinline__ void store_group(const uint32_t (&w)[8], int64_t row,
   uint32_t lo = 0, hi = 0;
   if (s > 0.f) {
     const float nr = -__frcp_rn(s);
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = w[e];
+    if (amax == INFINITY) {   // an infinity's residual would be inf - inf: the largest finite value saturates too
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = finite_bf16x2(v[e]);
+    }
     float2 q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = grid_quotient(neg_bf16x2(w[e]), s, nr);
+    for (int e = 0; e < 8; ++e) q[e] = grid_quotient(neg_bf16x2(v[e]), s, nr);
     lo = e2m1x8(q[0], q[1], q[2], q[3]);
     hi = e2m1x8(q[4], q[5], q[6], q[7]);
   }
