@@ -597,7 +597,7 @@ int store_impl(const void* k_src, const void* v_src, int64_t k_stride, int64_t v
                bool nvfp4, void* stream) {
   if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
   // (no tokens: an empty source's pointer may be NULL)
-  if (num_tokens != 0 && (v_src != nullptr) != (v_pool != nullptr))
+  if (v_src ? !v_pool : v_pool && num_tokens != 0)
     return fail(IDX_ERR_INVALID, "v_src and v_pool come together or not at all");
   int rc = check_pools(k_pool, v_pool, kv_heads, nvfp4, k_outer, v_outer);
   if (rc != IDX_OK) return rc;
@@ -966,7 +966,7 @@ int idx_norm_rope_store(const void* q, int64_t q_stride, int q_heads, const void
                         const idx_pool* v_pool, float k_outer, float v_outer, void* stream) {
   if (!k_pool) return fail(IDX_ERR_INVALID, "k_pool is NULL");
   // (no tokens: an empty tensor's pointer may be NULL)
-  if (num_tokens != 0 && (v != nullptr) != (v_pool != nullptr))
+  if (v ? !v_pool : v_pool && num_tokens != 0)
     return fail(IDX_ERR_INVALID, "v and v_pool come together or not at all");
   if (num_tokens != 0 && ((q != nullptr) != (out_q != nullptr) || (q != nullptr) != (q_heads > 0) ||
                           (!q && out_q_scale)))
