@@ -345,12 +345,15 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   a.part_ml = reinterpret_cast<float2*>(ws);
   ws += idx::attn::part_ml_bytes(idx::attn::kMaxCtas, a.group_rows);
   a.part_o = reinterpret_cast<float*>(ws);
-  CUtensorMap k_map, v_map;
-  const int64_t plane_rows = num_pages * kv_heads * idx::kPage;
-  const int box_rows = a.group_rows > 16 ? idx::kPage : idx::kPage / 2;
-  int rc = make_plane_map(kv_dtype, k_payload, plane_rows, box_rows, &k_map);
-  if (rc == IDX_OK) rc = make_plane_map(kv_dtype, v_payload, plane_rows, box_rows, &v_map);
-  if (rc != IDX_OK) return rc;
+  CUtensorMap k_map = {}, v_map = {};
+  const bool wide = a.group_rows > 16;
+  if (!(nvfp4 && wide)) {   // that kernel takes its pages by plain bulk copies
+    const int64_t plane_rows = num_pages * kv_heads * idx::kPage;
+    const int box_rows = wide ? idx::kPage : idx::kPage / 2;
+    int rc = make_plane_map(kv_dtype, k_payload, plane_rows, box_rows, &k_map);
+    if (rc == IDX_OK) rc = make_plane_map(kv_dtype, v_payload, plane_rows, box_rows, &v_map);
+    if (rc != IDX_OK) return rc;
+  }
   const cudaError_t e = idx::launch_attn(kv_dtype, a, k_map, v_map, st);
   if (e != cudaSuccess) return cuda_fail(e, "launching the attention kernels");
   return IDX_OK;

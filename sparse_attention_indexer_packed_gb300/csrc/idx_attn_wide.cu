@@ -347,8 +347,10 @@ __global__ void __launch_bounds__(AWLayout<KF, F>::kThreads, 1)
     mbar_init(drain, 1);
     fence_barrier_init();
     *abort_flag = 0;
-    prefetch_tensormap(&k_map);
-    prefetch_tensormap(&v_map);
+    if constexpr (KF != kNvfp4) {   // (whose maps are not made)
+      prefetch_tensormap(&k_map);
+      prefetch_tensormap(&v_map);
+    }
   }
   if (warp == 9) {
     tmem_alloc(sbase + L::kCtlOff + 12, kCols);
