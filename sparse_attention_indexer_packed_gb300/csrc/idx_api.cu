@@ -330,7 +330,7 @@ int attn_impl(const void* q, const void* k_payload, const void* k_scale, const v
   a.by_topk = idx::attn::Divisor::of(blocks ? topk : 1);
   a.by_kv = idx::attn::Divisor::of(heads / kv_heads > 1 ? heads / kv_heads : 1);
   a.by_list = idx::attn::Divisor::of(heads / a.lists > 1 ? heads / a.lists : 1);
-  a.unit_cost = idx::attn::unit_cost(a.group_rows, blocks, nvfp4, P, units);
+  a.unit_cost = idx::attn::unit_cost(a.group_rows, blocks, nvfp4, P, units, idx::attn_ctas());
   a.most = idx::attn::most_pieces(max_pages, blocks ? (long long)topk * P : 0);
   a.shift = idx::attn::position_shift(R, (long long)heads * a.groups, a.most, a.unit_cost);
   a.scale_log2 = scale_log2;

@@ -77,7 +77,7 @@ struct AttnArgs {
   long long most;              // pieces a unit may have at most, as the host knows it
   int shift;                   // pieces of a position: 2^shift
   int unit_cost;               // positions that stand for a unit's end
-  float dealt_ends, dealt_piece;  // estimate of units dealt whole (up to 16 rows, no lists)
+  float dealt_ends, dealt_piece;  // estimate of units dealt whole (up to 16 rows)
   float scale_log2;            // softmax scale (NVFP4: times the keys' outer scale) times log2(e)
   float out_scale;             // the values' outer scale (NVFP4), or 1
   unsigned long long wait_ns;
@@ -116,8 +116,10 @@ inline size_t part_o_bytes(int ctas, int group_rows) {
 constexpr int kLeast = 8, kLeastWide = 4;   // positions a CTA takes at least
 constexpr long long kMaxPositions = 0x7fffffffll / (kMaxCtas + 1);
 constexpr long long kMaxUnits = 1 << 18;
-constexpr int kMaxUnitCost = 32;
-static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit the line");
+// What a unit's end may take in a call of any size; of calls with fewer units it may take
+// more, as long as ends and one lot each fit the line (unit_cost).
+constexpr int kSureUnitCost = 32;
+static_assert(kMaxUnits * (kSureUnitCost + 1) <= kMaxPositions, "units must fit the line");
 
 // Positions that stand for a unit's end, in pieces of its kernel.  A stretch of a
 // unit costs a CTA about 2.5 us beside its pieces (queries, join, output; 5 with
@@ -126,24 +128,27 @@ static_assert(kMaxUnits * (kMaxUnitCost + 1) <= kMaxPositions, "units must fit t
 // 48 ragged requests x 4 heads 36.2 / 28.3 / 24.9 / 26.9 at 4 / 8 / 12 / 24; 24
 // ragged requests with lists 25.5 / 20.6 / 17.8 / 18.1 at 4 / 8 / 24 / 48; 16 x 131K
 // with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
-// NVFP4, whose pieces of 16 rows take half the time: paged 48 ragged x 4 heads 30.3 / 23.5 /
-// 19.9 / 20.0 at 6 / 12 / 20 / 28 (21.9 at 40), 64 ragged 18.5 / 17.6 / 18.2 at 20 / 28 / 40; where
-// few units are cut among many CTAs, 16 x 32K 31.6 / 30.4 / 30.1 / 30.3 at 28 / 36 / 44 / 52, 40 x 32K
-// 55.3 / 54.0 / 53.6 / 54.3, 16 x 131K 76.6 / 75.3 / 75.2 / 75.2; lists 16 x 131K 34.8 / 33.8 /
-// 33.2 at 16 / 24 / 32.  A unit's lots count the lists of all its draft rows (four at most are
-// counted here), which share most blocks, so the end counts as often: four rows 44.5 / 43.3 / 41.4 /
-// 43.0 at 32 / 64 / 128 / 192, one row 16.5 / 16.7 / 17.5 at 32 / 64 / 128.
+// NVFP4, whose pieces of 16 rows take half the time: paged at 20 / 24 / 28 / 32 / 36 / 40, 48 requests
+// x 4 heads of log-uniform lengths 27.6 / 26.5 / 26.9 / 27.7 / 28.3 / 28.8, 140 x 1 24.9 / 23.6 / 23.4 / 24.2 /
+// 24.6 / 24.9, of uniform lengths 77.6 / 74.8 / 73.4 / 72.5 / 72.2 / 72.4.  Units that four CTAs or more
+// could share are cut among several, and one request of 1K tokens, whose line this also makes
+// longer, gets more CTAs: at 28 / 36 / 44 on 152 CTAs 1 x 1K 10.3 / 9.9 / 9.6, 16 x 131K 76.6 / 75.9 /
+// 75.3, 24 x 32K 40.2 / 39.2 / 39.8, 32 x 32K 49.2 / 48.2 / 48.2, 24 of uniform lengths to 64K 38.8 /
+// 38.0 / 38.2, to 4K 13.7 / 13.5 / 13.1; on 76 16 x 16K 29.0 / 28.5 / 28.9, on 38 8 x 16K 28.6 / 28.2 /
+// 28.5.  Past that short contexts lose what long ones gain: 50 of uniform lengths to 4K 15.3 / 15.7 /
+// 16.6, 12 x 4 heads 15.3 / 15.7 / 16.5, 48 x 32K 66.3 / 65.1 / 65.2.
+// Lists 16 x 131K 34.8 / 33.8 / 33.2 at 16 / 24 / 32.  A unit's lots count the lists of all its draft
+// rows (four at most are counted here), which share most blocks, so the end counts as often: four rows
+// 44.5 / 43.3 / 41.4 / 43.0 at 32 / 64 / 128 / 192, one row 16.5 / 16.7 / 17.5 at 32 / 64 / 128.
 // Above 16 rows (pages): 16 x 131K x 64 rows 148.4 / 145.9 / 145.0 / 145.6 at 8 / 12 / 16 / 24, 64 ragged
 // 28.8 / 27.7 / 29.3 / 30.6; lists of four draft rows 57.9 / 53.8 / 52.4 / 53.6 at 16 / 32 / 48 / 64, of
 // 16 (eight a group) 70.5 / 68.4 / 64.1 / 64.3 at 16 / 32 / 64 / 96, of one 93.3 / 95.3 at 16 / 32.
-inline int unit_cost(int group_rows, bool blocks, bool nvfp4, int drafts, long long units) {
+inline int unit_cost(int group_rows, bool blocks, bool nvfp4, int drafts, long long units, int ctas) {
   const bool wide = group_rows > 16;
-  if (nvfp4) {
-    const int one = wide ? 16 : 32, cost = one * (drafts < 4 ? drafts : 4);
-    if (blocks) return units * (cost + 1) <= kMaxPositions ? cost : one;
-    return wide ? 12 : units <= 40 ? 44 : 28;
-  }
-  return wide ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
+  if (!nvfp4) return wide ? (blocks ? 16 : 8) : (blocks ? 32 : 12);
+  const int cost = blocks ? (wide ? 16 : 32) * (drafts < 4 ? drafts : 4) : wide ? 12 : 4 * units <= ctas ? 44 : 28;
+  const long long room = kMaxPositions / units - 1;
+  return cost < room ? cost : (int)room;
 }
 
 // The most half-page pieces a unit of the call may have, from what the host knows:
