@@ -468,7 +468,8 @@ IDX_API int idx_attn_blocks(const void* q, const void* k_payload, const void* k_
  * sm_scale * k_outer must be a normal fp32 number.  Codes times scales are exact in f16, where the
  * products are taken; a query element is exact within 2^21 of its row's largest; the weights
  * enter the product with the values as one f16: 2^-11 of the weight, or 2^-32 of the row's
- * largest weight.
+ * largest weight.  Short requests are faster under a page table about as wide as the longest of
+ * them: max_pages is all that the host knows of the lengths.
  */
 IDX_API int idx_attn_paged_nvfp4(const void* q, const void* k_payload, const void* k_scale,
                                  const void* v_payload, const void* v_scale, int64_t num_pages,

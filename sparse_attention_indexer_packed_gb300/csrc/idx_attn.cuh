@@ -130,7 +130,7 @@ static_assert(kMaxUnits * (kSureUnitCost + 1) <= kMaxPositions, "units must fit 
 // with lists 66.5 / 65.3 / 64.2 at 4 / 32 / 64.
 // NVFP4, whose pieces of 16 rows take half the time: paged at 20 / 24 / 28 / 32 / 36 / 40, 48 requests
 // x 4 heads of log-uniform lengths 27.6 / 26.5 / 26.9 / 27.7 / 28.3 / 28.8, 140 x 1 24.9 / 23.6 / 23.4 / 24.2 /
-// 24.6 / 24.9, of uniform lengths 77.6 / 74.8 / 73.4 / 72.5 / 72.2 / 72.4.  Units that four CTAs or more
+// 24.6 / 24.9, 48 x 4 of uniform lengths 77.6 / 74.8 / 73.4 / 72.5 / 72.2 / 72.4.  Units that four CTAs or more
 // could share are cut among several, and one request of 1K tokens, whose line this also makes
 // longer, gets more CTAs: at 28 / 36 / 44 on 152 CTAs 1 x 1K 10.3 / 9.9 / 9.6, 16 x 131K 76.6 / 75.9 /
 // 75.3, 24 x 32K 40.2 / 39.2 / 39.8, 32 x 32K 49.2 / 48.2 / 48.2, 24 of uniform lengths to 64K 38.8 /
@@ -166,11 +166,18 @@ inline int position_shift(int R, long long per, long long most, int unit_cost) {
 
 // Packed rows of a group over an NVFP4 cache: 16, whose kernel is the faster one a token up to
 // 32 rows (two groups: 16 x 65K tokens 76.0 us, 85.2 with the wide kernel) and has the cheaper
-// start and end, so also where more rows meet few tokens in all, as the host can bound
-// them: 64 rows of 8 x 8K 19.9 / 23.5, of 64 x 1K 17.4 / 22.9, of 64 x 4K 47.2 / 35.4, 128 rows of
-// 8 x 1K 11.8 / 18.8, of 64 x 1K 29.4 / 27.4, of 128 x 256 26.6 / 19.9 (a unit's own cost is that of
-// 256 tokens).  Lists, where a group of 16 joins those of fewer drafts: 64 rows of 16 x 64 blocks
-// 34.8 / 37.0, of 100 x 16 54.1 / 50.0.
+// start and end, so also where more rows meet few tokens in all (a unit's own cost is that of 256
+// tokens).  Us with groups of 16 / with the wide kernel, either side of the limit, in thousands of
+// units * (tokens + 256): 64 rows of 32 x 1K (164) 11.8 / 19.0, 8 x 8K (270) 21.1 / 23.9, 16 x 4K (279)
+// 21.7 / 21.7, 64 x 1K (328) 17.4 / 23.0, 20 x 4K (348) 28.2 / 22.1, 72 x 1K (369) 17.4 / 24.3, 40 x 2K (369)
+// 28.3 / 23.0, 80 x 1K (410) 27.9 / 25.2, 16 x 8K (541) 30.5 / 26.2; 128 rows of 64 x 256 (262) 14.5 / 20.0,
+// 32 x 1K (328) 17.7 / 21.8, 80 x 256 (328) 22.9 / 19.7, 40 x 1K (410) 28.0 / 23.4, 64 x 1K (655) 29.2 / 27.2.
+// Lists, where a group of 16 joins those of fewer drafts, in thousands of units * tokens: 64 rows, 64
+// lists of 16 blocks (524) 29.7 / 36.3, 16 of 64 (524) 33.9 / 32.4, 80 of 16 (655) 49.1 / 41.5, 16 drafts' 32 of
+// 32 (721) 43.4 / 46.4, 24 of 64 (786) 44.2 / 37.4, 40 of 64 (1311) 62.2 / 51.6; 128 rows, 8 of 64 (524) 33.9 /
+// 38.3, 24 of 32 (786) 47.9 / 36.2.
+// The host bounds the tokens by the page table's width, so a table as wide as the longest context that
+// may come gets the wide kernel for short ones too.
 inline int group_rows4(int requests, int heads, int drafts, int nq, int max_pages, int topk) {
   const bool blocks = topk > 0;
   const int wide = group_rows(drafts, nq, blocks);

@@ -644,7 +644,8 @@ cudaError_t launch_attn4(const AttnArgs& args, const CUtensorMap& k_map, const C
   float least;
   const float share = (float)(a.R * (int)a.by_per.d) / (float)grid;
   if (!a.block_ids) {
-    // A table that holds short units only: where dealing them whole costs about what cutting them
+    // A table that holds short units only (the host knows its width, not the lengths: under a table
+    // as wide as the longest context that may come, short units take the first figures): where dealing them whole costs about what cutting them
     // does, the call deals and needs no join (us, cut / dealt: 1 request x 2 key heads x 200 tokens
     // 7.5 / 6.0, x 600 9.8 / 8.4, x 1000 9.3 / 10.3; 16 x 8 x 200 8.6 / 6.8, x 1000 12.4 / 10.6; 64 x 8
     // x 1K 30.0 / 28.3).

@@ -37,10 +37,13 @@
 // values are decoded to f16, exactly, by the group that uses them, and the weights
 // times the value's scale are one f16 (11 bits; raise_unit).
 //
-// NVFP4 cache: neither a code times its scale (6 significant bits, exact in f16) nor the group
-// of 16 along the values' dims fits a product of codes, so both operands are decoded to f16
-// tiles in shared memory, by the group that uses them: its keys two pages ahead of the scores it
-// waits for, its values while the scores of another page are made.  The queries are f16 scaled a
+// NVFP4 cache: both operands are decoded to f16 tiles (a code times its scale has 6 significant
+// bits, exact there) in shared memory, by the group that uses them: its keys two pages ahead of
+// the scores it waits for, its values while the scores of another page are made.  The values have
+// to be: their groups of 16 lie along the product's columns, where no product of codes takes a
+// scale.  The keys' groups lie along its sum, as in the block-scaled product of e2m1 operands, but
+// that wants the queries as e2m1 terms too, about six of them for the precision below; it has not
+// been built or timed.  The queries are f16 scaled a
 // row by a power of two; the weights are f16 in units that lie 2^7 below the running maximum
 // (raised when a score passes it by 2^8 more: 2^-11 of each weight, or 2^-32 of the row's largest).
 // The parts of a row's tokens are warps, not lanes, so a warp skips what its part does not see and

@@ -26,6 +26,7 @@ namespace idx {
 // (then the residual is exact and q2 = t) or lies a bf16 spacing away from it,
 // far beyond the quotient's error, on the same side as fl(x / s).  (An fp32 x, as of a
 // key that was normed and rotated, may get the code of a neighbour two ulps away.)
+
 // Value of an E4M3 byte with the sign bit clear (scales are never negative):
 // exponent field 0 -> m * 2^-9; otherwise (8 + m) * 2^(e - 10).
 __device__ __forceinline__ float e4m3_magnitude(uint32_t b) {
